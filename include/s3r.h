@@ -529,6 +529,135 @@ int s3r_mx_backward_dw(const s3r_qdesc* desc, const uint8_t* Qt, int64_t ld_qt,
                        const float* ec_row_t, const float* ec_col_t, const float* ec_mean_t,
                        float* dW, int64_t ld_dw, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- routing to experts --------------------------------------------------
+ * The router of a mixture-of-experts layer: which experts a token takes, with
+ * which weights, and the expert-sorted order of the rows that the grouped calls
+ * above (and s3r_mx_product) take.  The S3R page trains MoE models (Table IV and
+ * the paragraph after it) and leaves the router open.
+ *   scores   s = softmax of the row of logits, or 1 / (1 + exp(-l));
+ *   keys     s + bias (a bias steers the experts' load; it enters no weight and
+ *            has no gradient);
+ *   groups   the experts in `groups` equal runs; a run's score is its largest
+ *            key (group_top 1) or the sum of its two largest (2); the `keep`
+ *            best runs stay, the others' keys become -inf;
+ *   choice   the top_k largest keys in descending order.  Every tie, of keys or
+ *            of runs, goes to the lower index.  Keys are compared as fp64 values
+ *            (without a bias and without sums: by the logits, the same order).
+ *            A logit of -inf (a masked expert) or NaN, and a NaN key, rank as -inf:
+ *            such experts are taken only when no others are left;
+ *   weights  scale * s_j, or with renorm scale * s_j / sum of the chosen s
+ *            (0 where that sum is 0, so a fully masked token has weights 0).  A
+ *            softmax row with a NaN or +inf logit has NaN weights.
+ *   order    slot t * top_k + j is choice j of token t; the rows are the slots
+ *            sorted by expert, in slot order within an expert.  No row is dropped.
+ * Limits: experts 1 .. 1024, top_k 1 .. min(experts, 64), groups 1 .. 64 dividing
+ * experts, group_top <= experts / groups, top_k <= keep * experts / groups,
+ * tokens * top_k < 2^31, scale finite.
+ */
+typedef enum { S3R_SOFTMAX = 0, S3R_SIGMOID = 1 } s3r_score;
+typedef struct s3r_route_desc {
+  int64_t  tokens;            /* T (>= 0) */
+  int32_t  experts, top_k;
+  int32_t  groups, keep, group_top;   /* 1, 1, 1: no groups */
+  int32_t  score;             /* s3r_score */
+  int32_t  renorm;            /* 0 or 1 */
+  float    scale;
+  uint32_t reserved;          /* must be 0 */
+} s3r_route_desc;
+
+/* s3r_route: logits [T x E] F32 or BF16 (ld >= E), bias [E] f32 or NULL ->
+ * ids [T x top_k] int32, weights [T x top_k] f32, offsets [E + 1] int64 (expert
+ * e owns rows offsets[e] .. offsets[e+1]), slot_row [T x top_k] int32 (the row of
+ * each slot) and row_slot [T * top_k] int32 (the slot of each row).
+ *   ws: s3r_route_workspace(desc) bytes, 256-byte aligned. */
+size_t s3r_route_workspace(const s3r_route_desc* desc);
+int s3r_route(const s3r_route_desc* desc, const void* logits, int32_t dtype, int64_t ld, const float* bias,
+              int32_t* ids, float* weights, int64_t* offsets, int32_t* slot_row, int32_t* row_slot,
+              void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* s3r_route_backward: the logits' gradient dlogits [T x E] (the logits' dtype,
+ * ld_d >= E) of weights with the gradient dweights [T x top_k] f32, at the choice
+ * ids of s3r_route (an index outside 0 .. E-1 takes no part; the choice itself has
+ * no gradient).  With g = scale * dweights, p_j = s_j / sum of the chosen s:
+ *   renorm:   dl_j = p_j (g_j - sum_i p_i g_i), times 1 - s_j for the sigmoid;
+ *   sigmoid:  dl_j = g_j s_j (1 - s_j);
+ *   softmax:  dl_e = s_e (g_e - sum_i g_i s_i) for every expert (g_e 0 where not chosen);
+ * and 0 elsewhere.  groups, keep and group_top are not used. */
+int s3r_route_backward(const s3r_route_desc* desc, const void* logits, int32_t dtype, int64_t ld, const int32_t* ids,
+                       const float* dweights, void* dlogits, int64_t ld_d, hipStream_t stream);
+
+/* ---- tokens to the experts' rows and back ---------------------------------
+ * Rows of D elements, all F32 or all BF16 (dtype), any alignment (16-byte-aligned
+ * bases, leading dims and widths take the vector path).  slot_row [T x k] int32
+ * as s3r_route writes it; an index outside 0 .. R-1 is no row: it is skipped, and
+ * its weight's gradient is 0.  k >= 1.
+ *   s3r_dispatch:          rows[slot_row[t,j]] = X[t].  Its gradient is
+ *                          s3r_combine without weights.
+ *   s3r_combine:           y[t] = sum_j w[t,j] Y[slot_row[t,j]] (fp32, j ascending;
+ *                          w NULL: 1), rounded once.
+ *   s3r_combine_backward:  dY[slot_row[t,j]] = w[t,j] dy[t], dw[t,j] = <dy[t], Y[slot_row[t,j]]>.
+ */
+int s3r_dispatch(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dtype, const void* X, int64_t ld_x,
+                 const int32_t* slot_row, void* rows, int64_t ld_rows, hipStream_t stream);
+int s3r_combine(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dtype, const void* Y, int64_t ld_rows,
+                const int32_t* slot_row, const float* weights, void* y, int64_t ld_y, hipStream_t stream);
+int s3r_combine_backward(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dtype, const void* dy, int64_t ld_y,
+                         const void* Y, const int32_t* slot_row, const float* weights, void* dY, int64_t ld_rows,
+                         float* dweights, hipStream_t stream);
+
+/* ---- MXFP4 rows and forward products ---------------------------------------
+ * The forward side of the MXFP4 variant: rows of any number and any length K,
+ * RTNE, in the format of that section (E2M1 codes, E8M0 scales, the 256-row block
+ * layout), blocked along the row.  K is padded to steps of 128 elements with zero
+ * codes: ld >= 16384 * ceil(K / 128), scales [ceil(K/128)][rows][4]; the scale of a
+ * padding block is byte 0.  Codes buffers hold ceil(rows / 256) * ld bytes, below
+ * 2^32.  The backward of a product is s3r_mx_backward_dx / _dw, over the experts
+ * s3r_grouped_backward_dx / _dw.
+ */
+
+/* s3r_mx_rows: `groups` matrices of rows x K elements (a_stride elements, c_stride
+ * and s_stride bytes apart; weights of all experts in one call) to codes and scales.
+ *   A        F32 or BF16, ld >= K;  up: NULL, or a second matrix of A's layout: the
+ *            elements are then silu(A) * up, in fp32 with the glue's exponential and
+ *            not rounded in between (the down projection's input);
+ *   index    NULL, or int32 [rows] on the device: row r is row index[r] / index_div of
+ *            A (row_slot with index_div top_k gathers the tokens of the experts' rows);
+ *            an index outside 0 .. a_rows - 1 gives a row of zeros.  groups must be 1;
+ *   a_rows   rows that A has (rows without an index);
+ *   flags    S3R_FLAG_NONFINITE is raised for a block with a non-finite element (its
+ *            scale is NaN, and so are the products with it). */
+int s3r_mx_rows(int64_t groups, int64_t rows, int64_t K, const void* A, const void* up, int32_t dtype, int64_t ld,
+                int64_t a_stride, int64_t a_rows, const int32_t* index, int64_t index_div,
+                uint8_t* codes, int64_t ld_c, int64_t c_stride, uint8_t* scales, int64_t ld_s, int64_t s_stride,
+                uint32_t* flags, hipStream_t stream);
+
+/* Shape and weights' layout of a product. */
+typedef struct s3r_mx_pdesc {
+  int64_t rows, cols, depth;        /* M (or R), N, K; each >= 0 and below 2^24 */
+  int64_t groups;                   /* 0: one weight; else 1 .. 4096, offsets required */
+  int64_t ld_b, ld_bs;              /* bytes: codes of 256 rows, scales of one step */
+  int64_t b_stride, bs_stride;      /* bytes between the groups' codes and scales */
+  int32_t out_dtype;                /* S3R_F32 or S3R_BF16 */
+  uint32_t reserved;                /* must be 0 */
+} s3r_mx_pdesc;
+
+/* s3r_mx_product: out [M x N] = dq(A) dq(B)^T, fp32 accumulation in the matrix cores,
+ * rounded once; B [N x K] as s3r_mx_rows wrote it.  With groups, the rows of A and out
+ * are sorted by group and offsets is as in the grouped calls above (invalid offsets
+ * raise S3R_FLAG_BAD_GROUPS and nothing is computed). */
+int s3r_mx_product(const s3r_mx_pdesc* desc, const uint8_t* A, int64_t ld_a, const uint8_t* A_scales, int64_t ld_as,
+                   const int64_t* offsets, const uint8_t* B, const uint8_t* B_scales,
+                   void* out, int64_t ld_out, uint32_t* flags, hipStream_t stream);
+
+/* s3r_mx_linear: s3r_mx_rows on A (one group; up and index as there) and
+ * s3r_mx_product of the result, which lives in the workspace.
+ *   ws: s3r_mx_linear_workspace(rows, K) bytes, 256-byte aligned. */
+size_t s3r_mx_linear_workspace(int64_t rows, int64_t K);
+int s3r_mx_linear(const s3r_mx_pdesc* desc, const void* A, const void* up, int32_t dtype, int64_t ld, int64_t a_rows,
+                  const int32_t* index, int64_t index_div, const int64_t* offsets, const uint8_t* B,
+                  const uint8_t* B_scales, void* out, int64_t ld_out, uint32_t* flags,
+                  void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- measurement aid --------------------------------------------------
  * s3r_time_next_gemm: record `start` immediately before and `stop` immediately
  * after the GEMM kernel launched by the next s3r_backward_dx / s3r_backward_dw

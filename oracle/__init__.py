@@ -25,9 +25,10 @@ Modules:
   backward  -- exact integer GEMMs, dequantised and corrected dX and dW
   swiglu    -- the SwiGLU FFN block's backward glue between the down and the
                gate / up projections (fp32 in a fixed order, bf16 results)
+  route     -- routing to experts, its gradient, the rows' way there and back
 
 Parity status: every function here is pinned by a test in
-``tests/test_oracle_pins.py`` or ``tests/test_oracle_swiglu_pins.py`` (against torch's Philox header, exact rational
+``tests/test_oracle_pins.py``, ``tests/test_oracle_swiglu_pins.py`` or ``tests/test_oracle_route_pins.py`` (against torch's Philox header, exact rational
 arithmetic, closed forms, library routines or brute force); none is marked
 "parity unpinned".
 """

@@ -181,3 +181,16 @@ def backward(G, X, W, *, mode: int, ec: int, rows_per_example: int, seed: int = 
         dW = dW - out["ebar_t"][:, dw_rows].T @ xs - u[None, :]
     out["dX"], out["dW"] = dX, dW
     return out
+
+
+def rows(M: np.ndarray) -> dict:
+    """RTNE MXFP4 of the rows of M [R x K], K of any length: K padded to steps of 128 with zeros.
+
+    "deq" [R x K] float64, "codes" and "scale" over the padded length.
+    """
+    M = np.asarray(M, F32)
+    R, K = M.shape
+    P = np.zeros((R, (K + 127) // 128 * 128), F32)
+    P[:, :K] = M
+    q = quantize(P, axis=1)
+    return {"deq": q["deq"][:, :K], "codes": q["codes"], "scale": q["scale"], "flag": q["flag"]}

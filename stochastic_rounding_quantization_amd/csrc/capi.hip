@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "s3r_internal.h"
@@ -621,6 +622,235 @@ int s3r_mx_backward_dw(const s3r_qdesc* d, const uint8_t* Qt, int64_t ld_qt, con
   a.vcol = xs; a.ec_row = ec_row_t; a.ec_col = ec_col_t; a.ec_mean = ec_mean_t;
   a.out = dW; a.ld_out = ld_dw; a.ws = (char*)ws;
   return finish(launch_mx_backward_dw(a, stream));
+}
+
+// ---- routing
+static int check_route(const s3r_route_desc* d) {
+  if (!d || d->tokens < 0 || d->reserved != 0) return S3R_ERR_INVALID_ARG;
+  if (d->experts < 1 || d->top_k < 1 || d->top_k > d->experts) return S3R_ERR_INVALID_ARG;
+  if (d->experts > 1024 || d->top_k > 64 || d->groups > 64) return S3R_ERR_UNSUPPORTED;
+  if (d->groups < 1 || d->experts % d->groups || d->keep < 1 || d->keep > d->groups) return S3R_ERR_INVALID_ARG;
+  if (d->score != S3R_SOFTMAX && d->score != S3R_SIGMOID) return S3R_ERR_UNSUPPORTED;
+  if (d->group_top != 1 && d->group_top != 2) return S3R_ERR_UNSUPPORTED;
+  const int per = d->experts / d->groups;
+  if (d->group_top > per && d->groups > 1) return S3R_ERR_INVALID_ARG;
+  if (d->top_k > (int64_t)d->keep * per) return S3R_ERR_INVALID_ARG;
+  if (d->renorm != 0 && d->renorm != 1) return S3R_ERR_INVALID_ARG;
+  if (!std::isfinite(d->scale)) return S3R_ERR_INVALID_ARG;
+  if (d->tokens > 0x7FFFFFFF || d->tokens * d->top_k > 0x7FFFFFFF) return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
+static bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+// Rows of `dtype` elements: known type, pointer aligned to an element.
+static int check_rows(const void* p, int32_t dtype, int64_t ld, int64_t cols, bool nonempty) {
+  if (dtype != S3R_F32 && dtype != S3R_BF16) return S3R_ERR_UNSUPPORTED;
+  if (ld < cols || ((uintptr_t)p & (dtype == S3R_BF16 ? 1u : 3u)) || (nonempty && !p)) return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
+size_t s3r_route_workspace(const s3r_route_desc* d) {
+  return check_route(d) == S3R_OK ? route_workspace(d->tokens, d->experts) : 0;
+}
+
+int s3r_route(const s3r_route_desc* d, const void* logits, int32_t dtype, int64_t ld, const float* bias, int32_t* ids,
+              float* weights, int64_t* offsets, int32_t* slot_row, int32_t* row_slot, void* ws, size_t ws_bytes,
+              hipStream_t stream) {
+  int rc = check_route(d);
+  if (rc) return rc;
+  const bool any = d->tokens > 0;
+  if ((rc = check_rows(logits, dtype, ld, d->experts, any))) return rc;
+  if (!offsets || ((uintptr_t)offsets & 7u) || (any && (!ids || !weights || !slot_row || !row_slot)))
+    return S3R_ERR_INVALID_ARG;
+  if (!al4(bias) || !al4(ids) || !al4(weights) || !al4(slot_row) || !al4(row_slot)) return S3R_ERR_INVALID_ARG;
+  if (ws_bytes < route_workspace(d->tokens, d->experts)) return S3R_ERR_WORKSPACE;
+  if (!ws || ((uintptr_t)ws & 255u)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  RouteArgs a{};
+  a.logits = logits; a.dtype = dtype; a.ld = ld; a.bias = bias; a.ids = ids; a.weights = weights; a.offsets = offsets;
+  a.slot_row = slot_row; a.row_slot = row_slot; a.T = d->tokens; a.E = d->experts; a.K = d->top_k;
+  a.groups = d->groups; a.keep = d->keep; a.group_top = d->group_top; a.sigmoid = d->score == S3R_SIGMOID;
+  a.renorm = d->renorm; a.scale = d->scale; a.ws = (char*)ws;
+  return finish(launch_route(a, stream));
+}
+
+int s3r_route_backward(const s3r_route_desc* d, const void* logits, int32_t dtype, int64_t ld, const int32_t* ids,
+                       const float* dweights, void* dlogits, int64_t ld_d, hipStream_t stream) {
+  int rc = check_route(d);
+  if (rc) return rc;
+  const bool any = d->tokens > 0;
+  if ((rc = check_rows(logits, dtype, ld, d->experts, any))) return rc;
+  if ((rc = check_rows(dlogits, dtype, ld_d, d->experts, any))) return rc;
+  if ((any && (!ids || !dweights)) || !al4(ids) || !al4(dweights)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  RouteBwdArgs a{};
+  a.logits = logits; a.dtype = dtype; a.ld = ld; a.ids = ids; a.dweights = dweights; a.dlogits = dlogits; a.ld_d = ld_d;
+  a.T = d->tokens; a.E = d->experts; a.K = d->top_k; a.sigmoid = d->score == S3R_SIGMOID; a.renorm = d->renorm;
+  a.scale = d->scale;
+  return finish(launch_route_backward(a, stream));
+}
+
+// ---- tokens to the experts' rows and back
+static int check_move(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dtype, const void* tok, int64_t ld_tok,
+                      const void* rows, int64_t ld_rows, const int32_t* slot_row) {
+  if (T < 0 || k < 1 || R < 0 || D < 0 || k > 0x7FFFFFFF || T > 0x7FFFFFFF || R > 0x7FFFFFFF || D > 0x7FFFFFFF ||
+      T * k > 0x7FFFFFFF || T * D >= ((int64_t)1 << 39))
+    return S3R_ERR_INVALID_ARG;
+  int rc;
+  if ((rc = check_rows(tok, dtype, ld_tok, D, T > 0 && D > 0))) return rc;
+  if ((rc = check_rows(rows, dtype, ld_rows, D, R > 0 && D > 0 && T > 0))) return rc;
+  if ((T > 0 && !slot_row) || !al4(slot_row)) return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
+int s3r_dispatch(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dtype, const void* X, int64_t ld_x,
+                 const int32_t* slot_row, void* rows, int64_t ld_rows, hipStream_t stream) {
+  int rc = check_move(T, k, R, D, dtype, X, ld_x, rows, ld_rows, slot_row);
+  if (rc) return rc;
+  if ((rc = check_arch())) return rc;
+  RowMoveArgs a{};
+  a.T = T; a.K = k; a.R = R; a.D = D; a.dtype = dtype; a.in = X; a.ld_in = ld_x; a.out = rows; a.ld_out = ld_rows;
+  a.slot_row = slot_row;
+  return finish(launch_dispatch(a, stream));
+}
+
+int s3r_combine(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dtype, const void* Y, int64_t ld_rows,
+                const int32_t* slot_row, const float* weights, void* y, int64_t ld_y, hipStream_t stream) {
+  int rc = check_move(T, k, R, D, dtype, y, ld_y, Y, ld_rows, slot_row);
+  if (rc) return rc;
+  if (!al4(weights)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  RowMoveArgs a{};
+  a.T = T; a.K = k; a.R = R; a.D = D; a.dtype = dtype; a.in = Y; a.ld_in = ld_rows; a.out = y; a.ld_out = ld_y;
+  a.slot_row = slot_row; a.weights = weights;
+  return finish(launch_combine(a, stream));
+}
+
+int s3r_combine_backward(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dtype, const void* dy, int64_t ld_y,
+                         const void* Y, const int32_t* slot_row, const float* weights, void* dY, int64_t ld_rows,
+                         float* dweights, hipStream_t stream) {
+  int rc = check_move(T, k, R, D, dtype, dy, ld_y, Y, ld_rows, slot_row);
+  if (rc) return rc;
+  if ((rc = check_rows(dY, dtype, ld_rows, D, R > 0 && D > 0 && T > 0))) return rc;
+  if ((T > 0 && (!weights || !dweights)) || !al4(weights) || !al4(dweights)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  RowMoveArgs a{};
+  a.T = T; a.K = k; a.R = R; a.D = D; a.dtype = dtype; a.in = Y; a.ld_in = ld_rows; a.out = dY; a.ld_out = ld_rows;
+  a.slot_row = slot_row; a.weights = weights; a.dy = dy; a.ld_dy = ld_y; a.dweights = dweights;
+  return finish(launch_combine_backward(a, stream));
+}
+
+// ---- MXFP4 rows and forward products
+static int64_t mx_steps(int64_t K) { return (K + 127) / 128; }
+static bool mx_size_ok(int64_t x) { return x >= 0 && x < ((int64_t)1 << 24); }
+// Codes and scales of rows x K elements, K padded to whole steps.
+static int check_mx_padded(const uint8_t* p, int64_t ld, const uint8_t* s, int64_t lds, int64_t rows, int64_t K) {
+  if (rows == 0 || K == 0) return S3R_OK;
+  if (!mx_codes_ok(p, ld, rows, 128 * mx_steps(K)) || !s || !al4(s) || (lds & 3) || lds < 4 * rows ||
+      lds >= ((int64_t)1 << 32) || (mx_steps(K) + 1) * lds >= ((int64_t)1 << 32))
+    return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
+// The source of s3r_mx_rows and s3r_mx_linear.
+static int check_mx_source(int64_t rows, int64_t K, const void* A, const void* up, int32_t dtype, int64_t ld,
+                           int64_t a_rows, const int32_t* index, int64_t index_div) {
+  const bool any = rows > 0 && K > 0 && (!index || a_rows > 0);
+  int rc;
+  if ((rc = check_rows(A, dtype, ld, K, any))) return rc;
+  if ((rc = check_rows(up, dtype, ld, K, false))) return rc;
+  if (a_rows < 0 || a_rows > 0x7FFFFFFF || index_div < 1 || index_div > 0x7FFFFFFF || !al4(index))
+    return S3R_ERR_INVALID_ARG;
+  if (!index && a_rows != rows) return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
+int s3r_mx_rows(int64_t groups, int64_t rows, int64_t K, const void* A, const void* up, int32_t dtype, int64_t ld,
+                int64_t a_stride, int64_t a_rows, const int32_t* index, int64_t index_div, uint8_t* codes, int64_t ld_c,
+                int64_t c_stride, uint8_t* scales, int64_t ld_s, int64_t s_stride, uint32_t* flags,
+                hipStream_t stream) {
+  if (groups < 1 || groups > kMaxGroups || !mx_size_ok(rows) || !mx_size_ok(K)) return S3R_ERR_INVALID_ARG;
+  if (index && groups != 1) return S3R_ERR_UNSUPPORTED;
+  int rc = check_mx_source(rows, K, A, up, dtype, ld, a_rows, index, index_div);
+  if (rc) return rc;
+  if ((rc = check_mx_padded(codes, ld_c, scales, ld_s, rows, K))) return rc;
+  if (groups > 1 && rows > 0 && K > 0 &&
+      (a_stride < (rows - 1) * ld + K || c_stride % 16 || c_stride < (rows + 255) / 256 * ld_c || (s_stride & 3) ||
+       s_stride < mx_steps(K) * ld_s))
+    return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  MxRowsArgs a{};
+  a.A = A; a.up = up; a.dtype = dtype; a.ld = ld; a.a_stride = a_stride; a.a_rows = a_rows; a.index = index;
+  a.index_div = index_div; a.G = groups; a.R = rows; a.K = K; a.codes = codes; a.ld_c = ld_c; a.c_stride = c_stride;
+  a.scales = scales; a.ld_s = ld_s; a.s_stride = s_stride; a.flags = flags;
+  return finish(launch_mx_rows(a, stream));
+}
+
+static int check_pdesc(const s3r_mx_pdesc* d, const int64_t* offsets, const uint8_t* B, const uint8_t* Bs,
+                       const void* out, int64_t ld_out) {
+  if (!d || d->reserved != 0 || !mx_size_ok(d->rows) || !mx_size_ok(d->cols) || !mx_size_ok(d->depth))
+    return S3R_ERR_INVALID_ARG;
+  if (d->groups < 0 || d->groups > kMaxGroups) return S3R_ERR_INVALID_ARG;
+  if ((d->groups > 0) != (offsets != nullptr) || ((uintptr_t)offsets & 7u)) return S3R_ERR_INVALID_ARG;
+  if (d->out_dtype != S3R_F32 && d->out_dtype != S3R_BF16) return S3R_ERR_UNSUPPORTED;
+  int rc = check_rows(out, d->out_dtype, ld_out, d->cols, d->rows > 0 && d->cols > 0);
+  if (rc) return rc;
+  if (ld_out >= kMaxLdOut) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_mx_padded(B, d->ld_b, Bs, d->ld_bs, d->cols, d->depth))) return rc;
+  if (d->groups > 1 && d->cols > 0 && d->depth > 0 &&
+      (d->b_stride % 16 || d->b_stride < (d->cols + 255) / 256 * d->ld_b || (d->bs_stride & 3) ||
+       d->bs_stride < mx_steps(d->depth) * d->ld_bs))
+    return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
+static MxProductArgs product_args(const s3r_mx_pdesc* d, const uint8_t* A, int64_t ld_a, const uint8_t* As,
+                                  int64_t ld_as, const int64_t* offsets, const uint8_t* B, const uint8_t* Bs,
+                                  void* out, int64_t ld_out, uint32_t* flags) {
+  MxProductArgs a{};
+  a.A = A; a.lda = ld_a; a.As = As; a.ldas = ld_as; a.B = B; a.ldb = d->ld_b; a.Bs = Bs; a.ldbs = d->ld_bs;
+  a.b_stride = d->b_stride; a.bs_stride = d->bs_stride; a.offsets = offsets; a.G = d->groups;
+  a.M = d->rows; a.N = d->cols; a.K = d->depth; a.out = out; a.out_dt = d->out_dtype; a.ld_out = ld_out;
+  a.flags = flags;
+  return a;
+}
+
+int s3r_mx_product(const s3r_mx_pdesc* d, const uint8_t* A, int64_t ld_a, const uint8_t* As, int64_t ld_as,
+                   const int64_t* offsets, const uint8_t* B, const uint8_t* Bs, void* out, int64_t ld_out,
+                   uint32_t* flags, hipStream_t stream) {
+  int rc = check_pdesc(d, offsets, B, Bs, out, ld_out);
+  if (rc) return rc;
+  if ((rc = check_mx_padded(A, ld_a, As, ld_as, d->rows, d->depth))) return rc;
+  if ((rc = check_arch())) return rc;
+  return finish(launch_mx_product(product_args(d, A, ld_a, As, ld_as, offsets, B, Bs, out, ld_out, flags), stream));
+}
+
+size_t s3r_mx_linear_workspace(int64_t rows, int64_t K) {
+  if (!mx_size_ok(rows) || !mx_size_ok(K)) return 0;
+  return std::max<size_t>(256, align_up(mx_rows_codes_bytes(rows, K), 256) + align_up(mx_rows_scales_bytes(rows, K), 256));
+}
+
+int s3r_mx_linear(const s3r_mx_pdesc* d, const void* A, const void* up, int32_t dtype, int64_t ld, int64_t a_rows,
+                  const int32_t* index, int64_t index_div, const int64_t* offsets, const uint8_t* B, const uint8_t* Bs,
+                  void* out, int64_t ld_out, uint32_t* flags, void* ws, size_t ws_bytes, hipStream_t stream) {
+  int rc = check_pdesc(d, offsets, B, Bs, out, ld_out);
+  if (rc) return rc;
+  if ((rc = check_mx_source(d->rows, d->depth, A, up, dtype, ld, a_rows, index, index_div))) return rc;
+  const size_t codes = align_up(mx_rows_codes_bytes(d->rows, d->depth), 256);
+  if (codes >= ((size_t)1 << 32) || (mx_steps(d->depth) + 1) * 4 * d->rows >= ((int64_t)1 << 32))
+    return S3R_ERR_INVALID_ARG;
+  if (ws_bytes < s3r_mx_linear_workspace(d->rows, d->depth)) return S3R_ERR_WORKSPACE;
+  if (!ws || ((uintptr_t)ws & 255u)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  uint8_t* c = (uint8_t*)ws;
+  uint8_t* s = c + codes;
+  MxRowsArgs r{};
+  r.A = A; r.up = up; r.dtype = dtype; r.ld = ld; r.a_rows = a_rows; r.index = index; r.index_div = index_div;
+  r.G = 1; r.R = d->rows; r.K = d->depth; r.codes = c; r.ld_c = mx_steps(d->depth) * 16384;
+  r.scales = s; r.ld_s = 4 * d->rows; r.flags = flags;
+  rc = finish(launch_mx_rows(r, stream));
+  if (rc) return rc;
+  return finish(launch_mx_product(product_args(d, c, r.ld_c, s, r.ld_s, offsets, B, Bs, out, ld_out, flags), stream));
 }
 
 int s3r_time_next_gemm(hipEvent_t start, hipEvent_t stop) {

@@ -190,6 +190,54 @@ hipError_t launch_mx_operand(const MxOperandArgs& a, hipStream_t st);
 hipError_t launch_mx_backward_dx(const MxBwArgs& a, hipStream_t st);
 hipError_t launch_mx_backward_dw(const MxBwArgs& a, hipStream_t st);
 
+// Routing (route.hip).
+struct RouteArgs {
+  const void* logits; int dtype; int64_t ld; const float* bias;
+  int32_t* ids; float* weights; int64_t* offsets; int32_t* slot_row; int32_t* row_slot;
+  int64_t T; int E, K, groups, keep, group_top, sigmoid, renorm; float scale;
+  char* ws;
+};
+struct RouteBwdArgs {
+  const void* logits; int dtype; int64_t ld; const int32_t* ids; const float* dweights;
+  void* dlogits; int64_t ld_d;
+  int64_t T; int E, K, sigmoid, renorm; float scale;
+};
+size_t route_workspace(int64_t T, int E);
+hipError_t launch_route(const RouteArgs& a, hipStream_t st);
+hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st);
+
+// Tokens to the experts' rows and back (rows.hip): `in` holds token rows (dispatch) or expert rows,
+// `out` expert rows (dispatch, backward) or token rows (combine).
+struct RowMoveArgs {
+  int64_t T, K, R, D; int dtype;
+  const void* in; int64_t ld_in; void* out; int64_t ld_out;
+  const int32_t* slot_row; const float* weights;
+  const void* dy; int64_t ld_dy; float* dweights;
+};
+hipError_t launch_dispatch(const RowMoveArgs& a, hipStream_t st);
+hipError_t launch_combine(const RowMoveArgs& a, hipStream_t st);
+hipError_t launch_combine_backward(const RowMoveArgs& a, hipStream_t st);
+
+// MXFP4 rows and forward products (mx_linear.hip).
+struct MxRowsArgs {
+  const void* A; const void* up; int dtype; int64_t ld, a_stride, a_rows;
+  const int32_t* index; int64_t index_div;
+  int64_t G, R, K;
+  uint8_t* codes; int64_t ld_c, c_stride; uint8_t* scales; int64_t ld_s, s_stride;
+  uint32_t* flags; int vec;
+};
+struct MxProductArgs {       // out [M x N] = A [M x K] . B [N x K]^T, B + e * stride for the rows of group e
+  const uint8_t* A; int64_t lda; const uint8_t* As; int64_t ldas;
+  const uint8_t* B; int64_t ldb; const uint8_t* Bs; int64_t ldbs; int64_t b_stride, bs_stride;
+  const int64_t* offsets; int64_t G;
+  int64_t M, N, K;
+  void* out; int out_dt; int64_t ld_out; uint32_t* flags;
+};
+size_t mx_rows_codes_bytes(int64_t R, int64_t K);
+size_t mx_rows_scales_bytes(int64_t R, int64_t K);
+hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st);
+hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st);
+
 // SwiGLU backward glue (swiglu.hip).
 hipError_t launch_swiglu_backward(int64_t T, int64_t F, const float* dH, int64_t ld_dh, const uint16_t* Ag,
                                   const uint16_t* Au, int64_t ld_a, uint16_t* Gg, uint16_t* Gu, int64_t ld_g,

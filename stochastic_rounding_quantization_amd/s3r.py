@@ -25,6 +25,7 @@ S3R_F32, S3R_BF16, S3R_I32_RAW, S3R_F32_ACC = 0, 1, 2, 3
 RTNE, SR, S3R, S3R_BCAST = 0, 1, 2, 3
 EC_NONE, EC_DX_ONLY, EC_TWO_WAY, EC_DW_ONLY = 0, 1, 2, 3
 PER_TENSOR, PER_TOKEN = 0, 1
+SOFTMAX, SIGMOID = 0, 1
 FLAG_NONFINITE, FLAG_TINY_STEP, FLAG_BAD_GROUPS = 1, 2, 8
 S3R_NOALLOC_SCRATCH_BYTES = 32 << 20    # include/s3r.h: the no-alloc quantizer's device array
 
@@ -32,7 +33,9 @@ EXPORTED = ["s3r_quantize_workspace", "s3r_quantize", "s3r_quantize_with_amax", 
             "s3r_backward_dw", "s3r_backward_dw_pair", "s3r_backward_dw_pair_workspace", "s3r_backward_workspace", "s3r_swiglu_backward", "s3r_swiglu_amax_workspace",
             "s3r_swiglu_backward_amax", "s3r_swiglu_quantize_workspace", "s3r_swiglu_quantize", "s3r_grouped_workspace", "s3r_grouped_quantize",
             "s3r_grouped_backward_dx", "s3r_grouped_backward_dw", "s3r_mx_workspace", "s3r_mx_operand_workspace",
-            "s3r_mx_operand", "s3r_mx_quantize", "s3r_mx_backward_dx", "s3r_mx_backward_dw", "s3r_time_next_gemm",
+            "s3r_mx_operand", "s3r_mx_quantize", "s3r_mx_backward_dx", "s3r_mx_backward_dw", "s3r_route_workspace", "s3r_route",
+            "s3r_route_backward", "s3r_dispatch", "s3r_combine", "s3r_combine_backward", "s3r_mx_rows",
+            "s3r_mx_product", "s3r_mx_linear_workspace", "s3r_mx_linear", "s3r_time_next_gemm",
             "s3r_status_string", "s3r_version"]
 
 
@@ -46,6 +49,25 @@ class QDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("rows_per_example", ctypes.c_int64),
                 ("mode", ctypes.c_int32), ("ec", ctypes.c_int32), ("scale", ctypes.c_int32),
                 ("layer_id", ctypes.c_uint32), ("seed", ctypes.c_uint64), ("stream", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("keep", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
+def route_desc(tokens, experts, top_k, *, score=SOFTMAX, groups=1, keep=1, group_top=1, renorm=True,
+               scale=1.0) -> RouteDesc:
+    return RouteDesc(tokens, experts, top_k, groups, keep, group_top, score, 1 if renorm else 0, scale, 0)
+
+
+class MxPDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("depth", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("ld_b", ctypes.c_int64), ("ld_bs", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("bs_stride", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_uint32)]
 
 
@@ -116,6 +138,22 @@ def lib() -> ctypes.CDLL:
     L.s3r_mx_quantize.argtypes = [DP, P, I32, I64, P, I64, P, I64, P, I64, P, I64, P, P, P, P, P, P, P, P, SZ, P]
     L.s3r_mx_backward_dx.argtypes = [DP, P, I64, P, I64, P, I64, P, I64, I64, P, P, P, P, P, I64, P, SZ, P]
     L.s3r_mx_backward_dw.argtypes = [DP, P, I64, P, I64, P, I64, P, I64, I64, P, P, P, P, P, I64, P, SZ, P]
+    RP, MP = ctypes.POINTER(RouteDesc), ctypes.POINTER(MxPDesc)
+    L.s3r_route_workspace.argtypes = [RP]
+    L.s3r_route_workspace.restype = SZ
+    L.s3r_route.argtypes = [RP, P, I32, I64, P, P, P, P, P, P, P, SZ, P]
+    L.s3r_route_backward.argtypes = [RP, P, I32, I64, P, P, P, I64, P]
+    L.s3r_dispatch.argtypes = [I64, I64, I64, I64, I32, P, I64, P, P, I64, P]
+    L.s3r_combine.argtypes = [I64, I64, I64, I64, I32, P, I64, P, P, P, I64, P]
+    L.s3r_combine_backward.argtypes = [I64, I64, I64, I64, I32, P, I64, P, P, P, P, I64, P, P]
+    L.s3r_mx_rows.argtypes = [I64, I64, I64, P, P, I32, I64, I64, I64, P, I64, P, I64, I64, P, I64, I64, P, P]
+    L.s3r_mx_product.argtypes = [MP, P, I64, P, I64, P, P, P, P, I64, P, P]
+    L.s3r_mx_linear_workspace.argtypes = [I64, I64]
+    L.s3r_mx_linear_workspace.restype = SZ
+    L.s3r_mx_linear.argtypes = [MP, P, P, I32, I64, I64, P, I64, P, P, P, P, I64, P, P, SZ, P]
+    for f in ("s3r_route", "s3r_route_backward", "s3r_dispatch", "s3r_combine", "s3r_combine_backward",
+              "s3r_mx_rows", "s3r_mx_product", "s3r_mx_linear"):
+        getattr(L, f).restype = ctypes.c_int
     L.s3r_time_next_gemm.argtypes = [P, P]
     L.s3r_time_next_gemm.restype = ctypes.c_int
     L.s3r_status_string.argtypes = [ctypes.c_int]
@@ -426,6 +464,224 @@ def s3r_mx_backward_dw(desc: QDesc, Qt, Qt_scales, Xt, Xt_scales, xs, ec_row_t, 
     _check("s3r_mx_backward_dw", rc)
 
 
+def _contig(what, *ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"expected a contiguous {what}")
+
+
+def _typed(t, dtype, what):
+    if t is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+
+
+def _shaped(t, shape, what):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def s3r_route_workspace(desc: RouteDesc) -> int:
+    return lib().s3r_route_workspace(ctypes.byref(desc))
+
+
+def s3r_route(desc: RouteDesc, logits, bias, ids, weights, offsets, slot_row, row_slot, ws, stream=None, *,
+              rc_only=False):
+    """logits [T x E] f32/bf16, bias f32 [E] or None -> ids int32 [T x k], weights f32 [T x k], offsets int64
+    [E + 1], slot_row int32 [T x k], row_slot int32 [T * k]."""
+    import torch
+    T, E, k = desc.tokens, desc.experts, desc.top_k
+    _shaped(logits, (T, E), "logits")
+    for t, dt, n, what in ((bias, torch.float32, E, "bias"), (ids, torch.int32, T * k, "ids"),
+                           (weights, torch.float32, T * k, "weights"), (offsets, torch.int64, E + 1, "offsets"),
+                           (slot_row, torch.int32, T * k, "slot_row"), (row_slot, torch.int32, T * k, "row_slot")):
+        if t is not None and (t.dtype != dt or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{what}: expected {n} contiguous elements of {dt}")
+    rc = lib().s3r_route(ctypes.byref(desc), _ptr(logits), _gdtype(logits), _ld(logits, E), _ptr(bias), _ptr(ids),
+                         _ptr(weights), _ptr(offsets), _ptr(slot_row), _ptr(row_slot), _ptr(ws), _nbytes(ws),
+                         _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_route", rc)
+
+
+def s3r_route_backward(desc: RouteDesc, logits, ids, dweights, dlogits, stream=None, *, rc_only=False):
+    """dlogits [T x E], of the logits' dtype, from dweights f32 [T x k] at the choice ids int32 [T x k]."""
+    import torch
+    T, E, k = desc.tokens, desc.experts, desc.top_k
+    _shaped(logits, (T, E), "logits")
+    _shaped(dlogits, (T, E), "dlogits")
+    _typed(dlogits, logits.dtype, "dlogits")
+    for t, dt, what in ((ids, torch.int32, "ids"), (dweights, torch.float32, "dweights")):
+        if t.dtype != dt or t.numel() != T * k or not t.is_contiguous():
+            raise ValueError(f"{what}: expected {T * k} contiguous elements of {dt}")
+    rc = lib().s3r_route_backward(ctypes.byref(desc), _ptr(logits), _gdtype(logits), _ld(logits, E), _ptr(ids),
+                                  _ptr(dweights), _ptr(dlogits), _ld(dlogits, E), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_route_backward", rc)
+
+
+def _slots(slot_row, tokens):
+    import torch
+    if slot_row.dtype != torch.int32 or slot_row.dim() != 2 or slot_row.shape[0] != tokens.shape[0] or \
+            not slot_row.is_contiguous():
+        raise ValueError("slot_row: expected a contiguous int32 [T x k]")
+    return slot_row.shape
+
+
+def s3r_dispatch(X, slot_row, rows, stream=None, *, rc_only=False):
+    """rows[slot_row[t, j]] = X[t]; rows [R x D] of X's dtype."""
+    T, k = _slots(slot_row, X)
+    _typed(rows, X.dtype, "rows")
+    _shaped(rows, (rows.shape[0], X.shape[1]), "rows")
+    rc = lib().s3r_dispatch(T, k, rows.shape[0], X.shape[1], _gdtype(X), _ptr(X), _ld(X), _ptr(slot_row), _ptr(rows),
+                            _ld(rows), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_dispatch", rc)
+
+
+def s3r_combine(rows, slot_row, weights, y, stream=None, *, rc_only=False):
+    """y[t] = sum_j weights[t, j] rows[slot_row[t, j]] (weights f32 [T x k], or None: 1)."""
+    import torch
+    T, k = _slots(slot_row, y)
+    _typed(y, rows.dtype, "y")
+    _shaped(y, (T, rows.shape[1]), "y")
+    _typed(weights, torch.float32, "weights")
+    _shaped(weights, (T, k), "weights")
+    _contig("weights", weights)
+    rc = lib().s3r_combine(T, k, rows.shape[0], rows.shape[1], _gdtype(rows), _ptr(rows), _ld(rows), _ptr(slot_row),
+                           _ptr(weights), _ptr(y), _ld(y), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_combine", rc)
+
+
+def s3r_combine_backward(dy, rows, slot_row, weights, drows, dweights, stream=None, *, rc_only=False):
+    """drows[slot_row[t, j]] = weights[t, j] dy[t]; dweights[t, j] = <dy[t], rows[slot_row[t, j]]>."""
+    import torch
+    T, k = _slots(slot_row, dy)
+    D = dy.shape[1]
+    for t, what in ((rows, "rows"), (drows, "drows")):
+        _typed(t, dy.dtype, what)
+        _shaped(t, (rows.shape[0], D), what)
+    if _ld(drows) != _ld(rows):
+        raise ValueError("rows and drows must share their layout")
+    for t, what in ((weights, "weights"), (dweights, "dweights")):
+        _typed(t, torch.float32, what)
+        _shaped(t, (T, k), what)
+        _contig(what, t)
+    rc = lib().s3r_combine_backward(T, k, rows.shape[0], D, _gdtype(dy), _ptr(dy), _ld(dy), _ptr(rows), _ptr(slot_row),
+                                    _ptr(weights), _ptr(drows), _ld(rows), _ptr(dweights), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_combine_backward", rc)
+
+
+@dataclass
+class MxRows:
+    """MXFP4 matrices of rows x K elements in the library's block layout, K padded to steps of 128:
+    codes uint8 [groups x ceil(rows/256) x 16384 steps], scales uint8 [groups x steps x 4 rows]."""
+    codes: object
+    scales: object
+    rows: int
+    K: int
+    groups: int = 1
+
+
+def mx_rows_buffer(rows: int, K: int, device, groups: int = 1) -> MxRows:
+    import torch
+    steps = (K + 127) // 128
+    u8 = dict(dtype=torch.uint8, device=device)
+    return MxRows(torch.empty(groups, (rows + 255) // 256, 16384 * steps, **u8),
+                  torch.empty(groups, steps, 4 * rows, **u8), rows, K, groups)
+
+
+def _index(index, rows):
+    import torch
+    if index is not None and (index.dtype != torch.int32 or index.numel() != rows or not index.is_contiguous()):
+        raise ValueError(f"index: expected {rows} contiguous int32")
+
+
+def _like(A, up):
+    if up is not None and (up.dtype != A.dtype or up.shape != A.shape or up.stride() != A.stride()):
+        raise ValueError("up must have A's type, shape and layout")
+
+
+def s3r_mx_rows(A, out: MxRows, up=None, index=None, index_div=1, flags=None, stream=None, *, rc_only=False):
+    """A [rows x K], or [groups x rows x K], f32/bf16 (silu(A) * up with up) -> out; with index, row r of out is
+    row index[r] // index_div of the 2-D A."""
+    if A.dim() not in (2, 3) or A.stride(-1) != 1:
+        raise ValueError("expected row-major matrices (unit column stride)")
+    G, a_rows, K = (1, *A.shape) if A.dim() == 2 else A.shape
+    if (out.groups, out.K) != (G, K) or (index is None and out.rows != a_rows):
+        raise ValueError("out does not fit A")
+    _index(index, out.rows)
+    _like(A, up)
+    steps, blocks = (K + 127) // 128, (out.rows + 255) // 256
+    rc = lib().s3r_mx_rows(G, out.rows, K, _ptr(A), _ptr(up), _gdtype(A), A.stride(-2), A.stride(0) if A.dim() == 3 else 0,
+                           a_rows, _ptr(index), index_div, _ptr(out.codes), 16384 * steps, blocks * 16384 * steps,
+                           _ptr(out.scales), 4 * out.rows, steps * 4 * out.rows, _ptr(flags), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_mx_rows", rc)
+
+
+def _mx_pdesc(rows, w: MxRows, out, offsets):
+    import torch
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported output dtype {out.dtype}")
+    _shaped(out, (rows, w.rows), "out")
+    if offsets is None:
+        if w.groups != 1:
+            raise ValueError("several weights need the rows' offsets")
+    elif offsets.dtype != torch.int64 or offsets.numel() != w.groups + 1 or not offsets.is_contiguous():
+        raise ValueError(f"offsets: expected {w.groups + 1} contiguous int64")
+    steps, blocks = (w.K + 127) // 128, (w.rows + 255) // 256
+    return MxPDesc(rows, w.rows, w.K, 0 if offsets is None else w.groups, 16384 * steps, 4 * w.rows,
+                   blocks * 16384 * steps, steps * 4 * w.rows, S3R_BF16 if out.dtype == torch.bfloat16 else S3R_F32, 0)
+
+
+def s3r_mx_product(a: MxRows, w: MxRows, out, offsets=None, flags=None, stream=None, *, rc_only=False):
+    """out [rows x w.rows] (f32/bf16) = a w^T; with offsets int64 [groups + 1], a's rows are sorted by group and
+    group e takes w's matrix e."""
+    if a.groups != 1 or a.K != w.K:
+        raise ValueError("a and w do not fit")
+    d = _mx_pdesc(a.rows, w, out, offsets)
+    rc = lib().s3r_mx_product(ctypes.byref(d), _ptr(a.codes), 16384 * ((a.K + 127) // 128), _ptr(a.scales), 4 * a.rows,
+                              _ptr(offsets), _ptr(w.codes), _ptr(w.scales), _ptr(out), _ld(out), _ptr(flags),
+                              _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_mx_product", rc)
+
+
+def s3r_mx_linear_workspace(rows: int, K: int) -> int:
+    return lib().s3r_mx_linear_workspace(rows, K)
+
+
+def mx_linear_buffer(rows: int, K: int, device):
+    """A workspace for s3r_mx_linear on that many rows."""
+    return _workspace(s3r_mx_linear_workspace(rows, K), device)
+
+
+def s3r_mx_linear(A, w: MxRows, out, *, up=None, offsets=None, index=None, index_div=1, ws=None, flags=None,
+                  stream=None, rc_only=False):
+    """out = mx(A) w^T in one call (A as in s3r_mx_rows, the product as in s3r_mx_product)."""
+    rows = out.shape[0]
+    if A.dim() != 2 or A.shape[1] != w.K or (index is None and A.shape[0] != rows):
+        raise ValueError("A, w and out do not fit")
+    _index(index, rows)
+    _like(A, up)
+    d = _mx_pdesc(rows, w, out, offsets)
+    rc = lib().s3r_mx_linear(ctypes.byref(d), _ptr(A), _ptr(up), _gdtype(A), _ld(A), A.shape[0], _ptr(index), index_div,
+                             _ptr(offsets), _ptr(w.codes), _ptr(w.scales), _ptr(out), _ld(out), _ptr(flags), _ptr(ws),
+                             _nbytes(ws), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_mx_linear", rc)
+
+
 def swiglu_backward(dH, A_gate, A_up, stream=None):
     """Allocate G_gate, G_up (bf16, like A_gate) and run s3r_swiglu_backward."""
     import torch
@@ -640,3 +896,94 @@ def mx_backward_dw(q: MxQuantized, Xt, Xt_scales, xs=None, stream=None):
     ws = _workspace(s3r_mx_workspace(q.desc, d_in), Xt.device)
     s3r_mx_backward_dw(q.desc, q.Qt, q.Qt_scales, Xt, Xt_scales, xs, *q.ec_t, dW, ws, stream)
     return dW
+
+
+# ------------------------------------------- routing and expert-row helpers ----
+
+@dataclass
+class Routed:
+    """A router's answer: the choice, its weights and the expert-sorted order of the rows."""
+    ids: object          # int32 [T x k]
+    weights: object      # f32 [T x k]
+    offsets: object      # int64 [E + 1]: expert e owns rows offsets[e] .. offsets[e + 1]
+    slot_row: object     # int32 [T x k]: the row of each slot
+    row_slot: object     # int32 [T * k]: the slot of each row
+    desc: RouteDesc = None
+    ws: object = None
+
+
+def routed_buffers(desc: RouteDesc, device) -> Routed:
+    """Outputs and workspace for s3r_route, to be kept between calls."""
+    import torch
+    T, E, k = desc.tokens, desc.experts, desc.top_k
+    i32 = dict(dtype=torch.int32, device=device)
+    return Routed(torch.empty(T, k, **i32), torch.empty(T, k, dtype=torch.float32, device=device),
+                  torch.empty(E + 1, dtype=torch.int64, device=device), torch.empty(T, k, **i32),
+                  torch.empty(T * k, **i32), desc, _workspace(s3r_route_workspace(desc), device))
+
+
+def route(logits, top_k, *, score=SOFTMAX, bias=None, groups=1, keep=1, group_top=1, renorm=True, scale=1.0,
+          stream=None) -> Routed:
+    """Choose top_k experts for every row of the logits [T x E]."""
+    d = route_desc(*logits.shape, top_k, score=score, groups=groups, keep=keep, group_top=group_top, renorm=renorm,
+                   scale=scale)
+    r = routed_buffers(d, logits.device)
+    s3r_route(d, logits, bias, r.ids, r.weights, r.offsets, r.slot_row, r.row_slot, r.ws, stream)
+    return r
+
+
+def route_backward(r: Routed, logits, dweights, stream=None):
+    """The logits' gradient from the weights'."""
+    import torch
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    s3r_route_backward(r.desc, logits, r.ids, dweights, dlogits, stream)
+    return dlogits
+
+
+def dispatch(X, r: Routed, stream=None):
+    """The tokens' rows in the experts' order: [T * k x D]."""
+    import torch
+    rows = torch.empty(r.row_slot.numel(), X.shape[1], dtype=X.dtype, device=X.device)
+    s3r_dispatch(X, r.slot_row, rows, stream)
+    return rows
+
+
+def combine(rows, r: Routed, weighted=True, stream=None):
+    """The experts' rows summed back into the tokens, weighted (or not: dispatch's gradient)."""
+    import torch
+    y = torch.empty(r.ids.shape[0], rows.shape[1], dtype=rows.dtype, device=rows.device)
+    s3r_combine(rows, r.slot_row, r.weights if weighted else None, y, stream)
+    return y
+
+
+def combine_backward(dy, rows, r: Routed, stream=None):
+    """(drows, dweights) of combine(rows, r)."""
+    import torch
+    drows, dw = torch.empty_strided(rows.shape, rows.stride(), dtype=rows.dtype, device=rows.device), torch.empty_like(r.weights)
+    s3r_combine_backward(dy, rows, r.slot_row, r.weights, drows, dw, stream)
+    return drows, dw
+
+
+def mx_rows(A, *, up=None, index=None, index_div=1, flags=None, stream=None) -> MxRows:
+    """RTNE MXFP4 of the rows of A ([rows x K], or [groups x rows x K]: weights [N x K] of every expert)."""
+    G = 1 if A.dim() == 2 else A.shape[0]
+    out = mx_rows_buffer(A.shape[-2] if index is None else index.numel(), A.shape[-1], A.device, G)
+    s3r_mx_rows(A, out, up, index, index_div, flags, stream)
+    return out
+
+
+def mx_product(a: MxRows, w: MxRows, *, offsets=None, out_dtype=None, flags=None, stream=None):
+    import torch
+    out = torch.empty(a.rows, w.rows, dtype=out_dtype or torch.float32, device=a.codes.device)
+    s3r_mx_product(a, w, out, offsets, flags, stream)
+    return out
+
+
+def mx_linear(A, w: MxRows, *, up=None, offsets=None, index=None, index_div=1, out_dtype=None, flags=None, stream=None):
+    """A's rows in MXFP4 times the weights w (mx_rows): [rows x w.rows], of A's dtype unless out_dtype is given."""
+    import torch
+    rows = A.shape[0] if index is None else index.numel()
+    out = torch.empty(rows, w.rows, dtype=out_dtype or A.dtype, device=A.device)
+    s3r_mx_linear(A, w, out, up=up, offsets=offsets, index=index, index_div=index_div,
+                  ws=mx_linear_buffer(rows, w.K, A.device), flags=flags, stream=stream)
+    return out
