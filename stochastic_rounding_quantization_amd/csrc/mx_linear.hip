@@ -247,6 +247,303 @@ __global__ __launch_bounds__(kSkThreads) void mx_few_rows_kernel(MxProdK p) {
   }
 }
 
+// Many rows: BM x BN tiles, WM x WN waves of (32 MI) x (32 NI) each, operands staged through LDS by
+// buffer-load DMA in a ring of NS steps of 128 elements.  A stage holds the tile's rows of both
+// operands, 64 bytes a row with the four 16-byte chunks of a row at permuted places (chunk q of row r
+// at q ^ ((r >> 2) & 3), so a quarter-wave's reads hit 16 bank groups), and the rows' scale words.
+// v_mfma_scale_f32_32x32x64_f8f6f4: lane l holds row or column l % 32, K elements 32 (l / 32) .. + 31;
+// result register r is row (r / 4) 8 + (l / 32) 4 + r % 4, column l % 32.
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+constexpr int kRsrcWord3 = 0x00020000;   // raw buffer, 32-bit dword format
+
+#define S3R_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (((n) >> 4) << 14) | 0x70 | 0xF00)
+#define S3R_WAIT_LGKM0() __builtin_amdgcn_s_waitcnt(0xC07F)
+constexpr int kSgMfma = 0x008, kSgDsRead = 0x100, kSgVmem = 0x010;
+
+template <int MI_, int NI_, int WM_, int WN_, int NS_>
+struct Tile {
+  static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr int Waves = WM * WN, Threads = 64 * Waves;
+  static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN;
+  static constexpr int PA = BM / 16 / Waves, PB = BN / 16 / Waves;        // 1 KiB pieces per wave
+  static constexpr int SW = (BM + BN) / 64;                               // 64-word scale loads of a step
+  static constexpr int PS = (SW + Waves - 1) / Waves;                     // per wave; surplus ones go to a spare place
+  static constexpr int Loads = PA + PB + PS;
+  static constexpr int OffB = BM * 64, OffS = OffB + BN * 64;
+  static constexpr int StageBytes = OffS + Waves * PS * 256;
+  static constexpr int EpiLd = 32 * NI + 4;                               // floats per row of the epilogue's staging
+  static_assert(BM % (16 * Waves) == 0 && BN % (16 * Waves) == 0, "whole pieces per wave");
+};
+
+// One LDS object per stage: the compiler then sees that a stage's reads and the DMA into another touch
+// different memory, and does not drain the loads in flight before the reads.
+template <typename T, int S>
+__device__ __forceinline__ uint8_t* ring() {
+  __shared__ __attribute__((aligned(1024))) uint8_t stage[T::StageBytes];
+  return stage;
+}
+
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ int chunk_pos(int r, int q) { return q ^ ((r >> 2) & 3); }
+
+template <typename T>
+struct TileSrc {
+  __amdgpu_buffer_rsrc_t a, b, sa, sb, z;
+  uint32_t va[T::PA], vb[T::PB], vs[T::PS];   // this lane's byte offsets in step 0
+  uint32_t ldas, ldbs;
+  int nk;
+};
+
+// Step kt into stage st; past the last step every load reads zeros, so the wait counts stay the same.
+template <typename T>
+__device__ __forceinline__ void tile_load(const TileSrc<T>& s, uint8_t* st, int kt) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool live = kt < s.nk;
+  const __amdgpu_buffer_rsrc_t ra = live ? s.a : s.z, rb = live ? s.b : s.z;
+  const uint32_t koff = (uint32_t)kt * (uint32_t)kMxBlkBytes;
+#pragma unroll
+  for (int q = 0; q < T::PA; ++q)
+    dma16(ra, st + (wave * T::PA + q) * 1024, s.va[q], koff);
+#pragma unroll
+  for (int q = 0; q < T::PB; ++q)
+    dma16(rb, st + T::OffB + (wave * T::PB + q) * 1024, s.vb[q], koff);
+#pragma unroll
+  for (int q = 0; q < T::PS; ++q) {
+    const int w = q * T::Waves + wave;                       // 64-word run w: A's runs, then B's, then surplus
+    const bool is_a = w < T::BM / 64 || w >= T::SW;
+    const __amdgpu_buffer_rsrc_t rs = live ? (is_a ? s.sa : s.sb) : s.z;
+    dma4(rs, st + T::OffS + w * 256, s.vs[q], (uint32_t)kt * (is_a ? s.ldas : s.ldbs));
+  }
+}
+
+template <typename T>
+struct TileFrag { v8i a[T::MI], b[T::NI]; };
+
+template <typename T>
+__device__ __forceinline__ void tile_frag(const uint8_t* st, int h, TileFrag<T>& f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  const int r31 = lane & 31, c = h * 2 + (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i) {
+    const int r = (wm * T::MI + i) * 32 + r31;
+    const uint4 x = *reinterpret_cast<const uint4*>(st + r * 64 + (chunk_pos(r, c) << 4));
+    f.a[i] = v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int j = 0; j < T::NI; ++j) {
+    const int r = (wn * T::NI + j) * 32 + r31;
+    const uint4 x = *reinterpret_cast<const uint4*>(st + T::OffB + r * 64 + (chunk_pos(r, c) << 4));
+    f.b[j] = v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+  }
+}
+
+// The scale words of this lane's rows and columns, shifted so that bytes 0 and 2 are its blocks in the
+// two half-steps (the instruction picks the byte).
+template <typename T>
+__device__ __forceinline__ void tile_scales(const uint8_t* st, uint32_t (&sa)[T::MI], uint32_t (&sb)[T::NI]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  const int r31 = lane & 31, sh = (lane >> 5) * 8;
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i)
+    sa[i] = *reinterpret_cast<const uint32_t*>(st + T::OffS + ((wm * T::MI + i) * 32 + r31) * 4) >> sh;
+#pragma unroll
+  for (int j = 0; j < T::NI; ++j)
+    sb[j] = *reinterpret_cast<const uint32_t*>(st + T::OffS + T::BM * 4 + ((wn * T::NI + j) * 32 + r31) * 4) >> sh;
+}
+
+template <typename T, int H>
+__device__ __forceinline__ void tile_mfma(const TileFrag<T>& f, const uint32_t (&sa)[T::MI], const uint32_t (&sb)[T::NI],
+                                          v16f (&acc)[T::MI][T::NI]) {
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[i], f.b[j], acc[i][j], 4, 4, 2 * H, (int)sa[i],
+                                                                  2 * H, (int)sb[j]);
+}
+
+// Step kt on stage S = kt % NS.  Its loads were issued NS - 1 steps ago; the wait leaves the later steps'
+// in flight.  The barrier makes every wave's loads visible and retires the stage of step kt - 1, which
+// takes step kt + NS - 1.
+template <typename T, int S>
+__device__ __forceinline__ void tile_step(const TileSrc<T>& src, int kt, v16f (&acc)[T::MI][T::NI]) {
+  S3R_WAIT_VM(T::Loads * (T::NS - 2));
+  S3R_WAIT_LGKM0();
+  __builtin_amdgcn_s_barrier();
+  const uint8_t* st = ring<T, S>();
+  uint32_t sa[T::MI], sb[T::NI];
+  TileFrag<T> f0, f1;
+  tile_frag<T>(st, 0, f0);
+  tile_scales<T>(st, sa, sb);
+  tile_load<T>(src, ring<T, (S + T::NS - 1) % T::NS>(), kt + T::NS - 1);
+  tile_frag<T>(st, 1, f1);
+  tile_mfma<T, 0>(f0, sa, sb, acc);
+  tile_mfma<T, 1>(f1, sa, sb, acc);
+  __builtin_amdgcn_sched_group_barrier(kSgVmem, T::Loads, 0);
+  __builtin_amdgcn_sched_group_barrier(kSgDsRead, 2 * (T::MI + T::NI), 0);
+#pragma unroll
+  for (int x = 0; x < T::MI * T::NI; ++x) {
+    __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+    if (x < T::MI + T::NI) __builtin_amdgcn_sched_group_barrier(kSgDsRead, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(kSgMfma, T::MI * T::NI, 0);
+}
+
+template <typename T, int S>
+__device__ __forceinline__ void tile_steps(const TileSrc<T>& src, int kt, v16f (&acc)[T::MI][T::NI]) {
+  if constexpr (S < T::NS) {
+    if (kt + S < src.nk) {
+      tile_step<T, S>(src, kt + S, acc);
+      tile_steps<T, S + 1>(src, kt, acc);
+    }
+  }
+}
+
+// The wave's results, 32 rows at a time through its own part of the (now free) ring, so that whole
+// 16-byte words of consecutive columns are stored.
+template <typename T, typename TOut>
+__device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t m1, int64_t n0, bool vec,
+                                           const v16f (&acc)[T::MI][T::NI]) {
+  constexpr int kBuf = 32 * T::EpiLd * 4;
+  constexpr int kPer = T::StageBytes / kBuf;                  // waves' buffers in one stage
+  static_assert(kPer > 0 && kPer * T::NS >= T::Waves, "the epilogue's staging fits the ring");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  uint8_t* stage = ring<T, 0>();
+  if (wave / kPer == 1) stage = ring<T, 1 % T::NS>();
+  if (wave / kPer == 2) stage = ring<T, 2 % T::NS>();
+  if (T::NS > 3 && wave / kPer == 3) stage = ring<T, 3 % T::NS>();
+  float* buf = reinterpret_cast<float*>(stage + (wave % kPer) * kBuf);
+  constexpr int W = 16 / (int)sizeof(TOut);                   // elements of a store
+  constexpr int LR = 32 * T::NI / W;                          // lanes of a row
+  const int lr = lane / LR, lc = (lane % LR) * W;
+  const int64_t n = n0 + wn * (32 * T::NI) + lc;
+  TOut* out = (TOut*)p.out;
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i) {
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        buf[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * T::EpiLd + j * 32 + (lane & 31)] = acc[i][j][r];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (int q = 0; q < 32; q += 64 / LR) {
+      const int64_t m = m0 + (wm * T::MI + i) * 32 + q + lr;
+      float v[W];
+#pragma unroll
+      for (int x = 0; x < W; x += 4) {
+        const float4 t = *reinterpret_cast<const float4*>(buf + (q + lr) * T::EpiLd + lc + x);
+        v[x] = t.x; v[x + 1] = t.y; v[x + 2] = t.z; v[x + 3] = t.w;
+      }
+      if (m >= m1) continue;
+      TOut* o = out + m * p.ld_out + n;
+      if (vec && n + W <= p.N) {
+        if constexpr (sizeof(TOut) == 2) {
+          typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+          typedef float f2 __attribute__((ext_vector_type(2)));
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * x], v[2 * x + 1]}), bf2));
+          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < W; ++x)
+          if (n + x < p.N) store_out(o + x, v[x]);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <typename T, typename TOut>
+__global__ __launch_bounds__(T::Threads, T::BN == 128 ? 2 : 1) void mx_tile_kernel(MxProdK p, int tiles_m, int vec) {
+  int bid = blockIdx.x;
+  const int nblocks = tiles_m * p.tiles_n;
+  if (nblocks % 8 == 0) bid = (bid % 8) * (nblocks / 8) + bid / 8;   // a contiguous range of tiles per XCD
+  const int group = 8 * p.tiles_n;
+  const int first_m = (bid / group) * 8;
+  const int gsz = min(tiles_m - first_m, 8);
+  const int tm = first_m + (bid % group) % gsz, tn = (bid % group) / gsz;
+  int64_t m0 = (int64_t)tm * T::BM, m1 = p.M;
+  const int64_t n0 = (int64_t)tn * T::BN;
+  const uint8_t *B = p.B, *Bs = p.Bs;
+  if (p.G) {
+    const GroupTile h = find_group_tile(p.offsets, p.G, p.M, tm, T::BM);
+    if (h.bad) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_BAD_GROUPS);
+      return;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(h.e);
+    if (e < 0) return;
+    m0 = h.r0;
+    m1 = h.r1;
+    B += e * p.b_stride;
+    Bs += e * p.bs_stride;
+  }
+  TileSrc<T> src;
+  src.nk = p.ksteps;
+  src.ldas = (uint32_t)p.ldas;
+  src.ldbs = (uint32_t)p.ldbs;
+  // whole operands, every 256-row block of codes: rows past the end inside the last block reach only
+  // outputs that are not stored, and their scale words are the last row's
+  src.a = __builtin_amdgcn_make_buffer_rsrc((void*)p.A, (short)0, (int)(uint32_t)(((p.M + 255) >> 8) * p.lda), kRsrcWord3);
+  src.b = __builtin_amdgcn_make_buffer_rsrc((void*)B, (short)0, (int)(uint32_t)(((p.N + 255) >> 8) * p.ldb), kRsrcWord3);
+  src.sa = __builtin_amdgcn_make_buffer_rsrc((void*)p.As, (short)0, (int)(uint32_t)(((int64_t)p.ksteps - 1) * p.ldas + 4 * p.M), kRsrcWord3);
+  src.sb = __builtin_amdgcn_make_buffer_rsrc((void*)Bs, (short)0, (int)(uint32_t)(((int64_t)p.ksteps - 1) * p.ldbs + 4 * p.N), kRsrcWord3);
+  src.z = __builtin_amdgcn_make_buffer_rsrc((void*)p.A, (short)0, 0, kRsrcWord3);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int q = 0; q < T::PA; ++q) {
+    const int r = (wave * T::PA + q) * 16 + (lane >> 2);
+    const int64_t m = m0 + r;
+    src.va[q] = (uint32_t)((m >> 8) * p.lda + (m & 255) * 64 + chunk_pos(r, lane & 3) * 16);
+  }
+#pragma unroll
+  for (int q = 0; q < T::PB; ++q) {
+    const int r = (wave * T::PB + q) * 16 + (lane >> 2);
+    const int64_t n = n0 + r;
+    src.vb[q] = (uint32_t)((n >> 8) * p.ldb + (n & 255) * 64 + chunk_pos(r, lane & 3) * 16);
+  }
+#pragma unroll
+  for (int q = 0; q < T::PS; ++q) {
+    const int w = q * T::Waves + wave;
+    src.vs[q] = w < T::BM / 64 ? (uint32_t)(min(m0 + w * 64 + lane, p.M - 1) * 4)
+                : w < T::SW    ? (uint32_t)(min(n0 + (w - T::BM / 64) * 64 + lane, p.N - 1) * 4)
+                               : 0u;
+  }
+  v16f acc[T::MI][T::NI];
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  tile_load<T>(src, ring<T, 0>(), 0);
+  tile_load<T>(src, ring<T, 1>(), 1);
+  if constexpr (T::NS > 3) tile_load<T>(src, ring<T, 2>(), 2);
+  for (int kt = 0; kt < p.ksteps; kt += T::NS) tile_steps<T, 0>(src, kt, acc);
+  S3R_WAIT_VM(0);
+  S3R_WAIT_LGKM0();
+  __builtin_amdgcn_s_barrier();
+  tile_store<T, TOut>(p, m0, m1, n0, vec != 0, acc);
+}
+
 }  // namespace
 
 size_t mx_rows_codes_bytes(int64_t R, int64_t K) { return (size_t)((R + 255) / 256) * (size_t)((K + 127) / 128) * kMxBlkBytes; }
@@ -265,6 +562,20 @@ hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+namespace {
+using BigTile = Tile<4, 2, 2, 2, 3>;
+
+template <typename T, typename TOut>
+hipError_t run_tiles(const MxProductArgs& a, MxProdK p, hipStream_t st) {
+  const int64_t mt = a.G ? a.M / T::BM + std::min(a.G, a.M) : (a.M + T::BM - 1) / T::BM;
+  p.tiles_n = (int)((a.N + T::BN - 1) / T::BN);
+  if (mt * p.tiles_n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const int vec = ((uintptr_t)a.out & 15u) == 0 && (a.ld_out * (int64_t)sizeof(TOut)) % 16 == 0;
+  hipLaunchKernelGGL((mx_tile_kernel<T, TOut>), dim3((unsigned)(mt * p.tiles_n)), dim3(T::Threads), 0, st, p, (int)mt, vec);
+  return hipGetLastError();
+}
+}  // namespace
+
 hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   MxProdK p{};
@@ -272,13 +583,21 @@ hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
   p.B = a.B; p.ldb = a.ldb; p.Bs = a.Bs; p.ldbs = a.ldbs; p.b_stride = a.b_stride; p.bs_stride = a.bs_stride;
   p.offsets = a.offsets; p.G = a.G; p.M = a.M; p.N = a.N; p.ksteps = (int)((a.K + 127) / 128);
   p.out = a.out; p.ld_out = a.ld_out; p.flags = a.flags;
-  // grouped: the tiles of every group, at most one partial tile each
-  const int64_t mt = a.G ? a.M / 16 + std::min(a.G, a.M) : (a.M + 15) / 16;
-  p.tiles_n = (int)((a.N + 31) / 32);
-  if (mt * p.tiles_n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(mt * p.tiles_n));
-  if (a.out_dt == S3R_BF16) hipLaunchKernelGGL((mx_few_rows_kernel<uint16_t, 2>), grid, dim3(kSkThreads), 0, st, p);
-  else hipLaunchKernelGGL((mx_few_rows_kernel<float, 2>), grid, dim3(kSkThreads), 0, st, p);
+  const bool bf16 = a.out_dt == S3R_BF16;
+  // rows per weight, on average (only the device knows the groups' own)
+  const int64_t rows = a.G ? (a.M + a.G - 1) / a.G : a.M;
+  if (rows <= 32) {
+    // grouped: the tiles of every group, at most one partial tile each
+    const int64_t mt = a.G ? a.M / 16 + std::min(a.G, a.M) : (a.M + 15) / 16;
+    p.tiles_n = (int)((a.N + 31) / 32);
+    if (mt * p.tiles_n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(mt * p.tiles_n));
+    if (bf16) hipLaunchKernelGGL((mx_few_rows_kernel<uint16_t, 2>), grid, dim3(kSkThreads), 0, st, p);
+    else hipLaunchKernelGGL((mx_few_rows_kernel<float, 2>), grid, dim3(kSkThreads), 0, st, p);
+  } else {
+    if (bf16) return run_tiles<BigTile, uint16_t>(a, p, st);
+    return run_tiles<BigTile, float>(a, p, st);
+  }
   return hipGetLastError();
 }
 

@@ -167,7 +167,7 @@ def lib() -> ctypes.CDLL:
 # ------------------------------------------------------------ marshalling ----
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()      # the argument's declared type makes it a pointer
 
 
 def _ld(t, default=0):
@@ -180,9 +180,9 @@ def _ld(t, default=0):
 
 def _stream(stream):
     if stream is not None:
-        return ctypes.c_void_p(stream)
+        return stream
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(fn, rc):
