@@ -15,35 +15,55 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------ rows ----
-// A block of 256 threads takes 16 rows x one 128-element step at a time: 16 lanes
-// per row, 8 elements a lane (16 bytes of bf16), so a block of 32 elements is
-// four lanes.  Codes leave as 1 KiB and scales as 64 bytes in one run.  With
+// A block of 256 threads takes 16 rows x kMrSteps 128-element steps: 16 lanes per
+// row, 8 elements a lane and step (16 bytes of bf16), so a block of 32 elements
+// is four lanes.  Codes leave as 1 KiB and scales as 64 bytes in one run.  With
 // `up` the element is silu(A) * up in fp32, not rounded in between.
-constexpr int kMrThreads = 256, kMrRows = 16;
+// The arithmetic is what bounded the first version (28 instructions an element:
+// 35 us for 8192 x 4096 bf16, whose bytes need 15); now two elements convert in
+// one instruction, and the maximum of bf16 runs on packed magnitudes.
+constexpr int kMrThreads = 256, kMrRows = 16, kMrSteps = 4;
 
+// 8 consecutive elements of a row as they lie in memory: packed bf16, or fp32.
+template <typename TIn> struct Raw8;
+template <> struct Raw8<uint16_t> { uint32_t w[4]; };
+template <> struct Raw8<float> { float w[8]; };
+
+// Elements past the first n are zero.
 template <typename TIn>
-__device__ __forceinline__ void mr_load8(const TIn* p, int64_t n, bool vec, float (&v)[8]) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(TIn) == 2) {
+__device__ __forceinline__ Raw8<TIn> mr_load8(const TIn* p, int64_t n, bool vec) {
+  Raw8<TIn> r;
+  if constexpr (sizeof(TIn) == 2) {
+    if (vec && n >= 8) {
       const uint4 w = *reinterpret_cast<const uint4*>(p);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(ww[i] << 16);
-        v[2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
-      }
+      r.w[0] = w.x; r.w[1] = w.y; r.w[2] = w.z; r.w[3] = w.w;
     } else {
-      const float4 w0 = reinterpret_cast<const float4*>(p)[0], w1 = reinterpret_cast<const float4*>(p)[1];
-      v[0] = w0.x; v[1] = w0.y; v[2] = w0.z; v[3] = w0.w;
-      v[4] = w1.x; v[5] = w1.y; v[6] = w1.z; v[7] = w1.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
     }
   } else {
+    if (vec && n >= 8) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+      r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (sizeof(TIn) == 2) v[i] = i < n ? bf16_to_f32(*reinterpret_cast<const uint16_t*>(p + i)) : 0.f;
-      else v[i] = i < n ? p[i] : 0.f;
+      for (int i = 0; i < 8; ++i) r.w[i] = i < n ? p[i] : 0.f;
     }
   }
+  return r;
+}
+
+__device__ __forceinline__ Raw8<float> mr_float8(const Raw8<float>& r) { return r; }
+__device__ __forceinline__ Raw8<float> mr_float8(const Raw8<uint16_t>& r) {
+  Raw8<float> f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f.w[2 * i] = __uint_as_float(r.w[i] << 16);
+    f.w[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+  }
+  return f;
 }
 
 // silu(a) * u in fp32 with the glue's exponential and reciprocal.
@@ -53,61 +73,130 @@ __device__ __forceinline__ float mr_swiglu(float a, float u) {
   return (a * s) * u;
 }
 
-// The codes of this lane's 8 elements (one word) and, in every lane of the row's 16, its step's four
-// scale bytes; lanes 4 b .. 4 b + 3 hold block b.
-__device__ __forceinline__ uint32_t mr_encode(const float (&v)[8], uint32_t& scales) {
+// Largest magnitude of the 8 elements, as fp32 bits.
+__device__ __forceinline__ uint32_t mr_amax(const Raw8<float>& r) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 2, 64));
-  const int sb = block_scale_byte(m);
-  uint32_t w = 0;
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(r.w[i]) & 0x7FFFFFFFu);
+  return m;
+}
+__device__ __forceinline__ uint32_t mr_amax(const Raw8<uint16_t>& r) {
+  typedef unsigned short u2 __attribute__((ext_vector_type(2)));
+  u2 m = __builtin_bit_cast(u2, r.w[0] & 0x7FFF7FFFu);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    int n, M;
-    w |= e2m1_round<true>(v[i], sb - 126, 0, n, M) << (4 * i);
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u2, r.w[i] & 0x7FFF7FFFu));
+  return (uint32_t)(m.x > m.y ? m.x : m.y) << 16;
+}
+
+// Codes of 8 elements in a block of scale 2^(sb - 127), 1 <= sb <= 254: the hardware's conversion divides
+// by the scale and rounds to nearest, ties to even.  Its sign survives a magnitude of 0; the format here
+// has one zero.
+__device__ __forceinline__ uint32_t mr_one_zero(uint32_t w) {
+  const uint32_t mag = w & 0x77777777u;
+  return mag | (w & (mag + 0x77777777u) & 0x88888888u);
+}
+__device__ __forceinline__ uint32_t mr_codes(const Raw8<float>& r, int sb) {
+  const float scale = __uint_as_float((uint32_t)sb << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.w[0], r.w[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.w[2], r.w[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.w[4], r.w[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r.w[6], r.w[7], scale, 3);
+  return mr_one_zero(w);
+}
+__device__ __forceinline__ uint32_t mr_codes(const Raw8<uint16_t>& r, int sb) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const float scale = __uint_as_float((uint32_t)sb << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf2, r.w[0]), scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf2, r.w[1]), scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf2, r.w[2]), scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf2, r.w[3]), scale, 3);
+  return mr_one_zero(w);
+}
+
+template <int Ctrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, 0xF, 0xF, true);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppRor4 = 0x124, kDppRor8 = 0x128;
+
+// The codes of this lane's 8 elements (one word) and, in every lane of the row's 16, its step's four
+// scale bytes; lanes 4 b .. 4 b + 3 hold block b.
+template <typename TRaw>
+__device__ __forceinline__ uint32_t mr_encode(const TRaw& v, uint32_t& scales) {
+  uint32_t m = mr_amax(v);
+  m = max(m, dpp<kDppXor1>(m));
+  m = max(m, dpp<kDppXor2>(m));
+  const int sb = block_scale_byte(m);
+  uint32_t w = mr_codes(v, sb);
+  if (sb == 0 || sb == 255) {                  // below the conversion's scales, or not finite
+    w = 0;
+    if (sb == 0 && m != 0) {
+      const Raw8<float> f = mr_float8(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        int n, M;
+        w |= e2m1_round<true>(f.w[i], sb - 126, 0, n, M) << (4 * i);
+      }
+    }
   }
   uint32_t s = (uint32_t)sb << (8 * ((threadIdx.x >> 2) & 3));
-  s |= (uint32_t)__shfl_xor((int)s, 4, 64);
-  s |= (uint32_t)__shfl_xor((int)s, 8, 64);
+  s |= dpp<kDppRor4>(s);
+  s |= dpp<kDppRor8>(s);
   scales = s;
-  return sb == 255 ? 0u : w;
+  return w;
 }
 
 __device__ __forceinline__ bool mr_nan_scale(uint32_t s) {
   return (s & 0xFFu) == 0xFFu || (s & 0xFF00u) == 0xFF00u || (s & 0xFF0000u) == 0xFF0000u || (s >> 24) == 0xFFu;
 }
 
-template <typename TIn>
+// The source row of row r, or -1: none (past the end, or an index outside the source).
+__device__ __forceinline__ int64_t mr_source(const MxRowsArgs& a, int64_t r) {
+  if (r >= a.R) return -1;
+  if (!a.index) return r;
+  const int i = a.index[r];
+  if (i < 0) return -1;
+  const int s = (int)((uint32_t)i / (uint32_t)a.index_div);
+  return s < a.a_rows ? s : -1;
+}
+
+template <typename TIn, bool UP>
 __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int ksteps) {
   const int sub = threadIdx.x & 15;
-  const int64_t r = (int64_t)blockIdx.x * kMrRows + (threadIdx.x >> 4);
-  const int64_t g = blockIdx.z;
-  const TIn* A = (const TIn*)a.A + g * a.a_stride;
-  const TIn* U = a.up ? (const TIn*)a.up + g * a.a_stride : nullptr;
+  const int kblocks = (ksteps + kMrSteps - 1) / kMrSteps;
+  const int rb = blockIdx.x / kblocks;
+  const int64_t r = (int64_t)rb * kMrRows + (threadIdx.x >> 4);
+  const int64_t g = blockIdx.y;
   uint8_t* codes = a.codes + g * a.c_stride;
   uint8_t* scales = a.scales + g * a.s_stride;
-  int64_t src = r;
-  bool live = r < a.R;
-  if (a.index && live) {
-    src = (int64_t)a.index[r] / a.index_div;
-    live = a.index[r] >= 0 && src < a.a_rows;     // an index outside the source is a row of zeros
-  }
-  if (!live) src = 0;
-  for (int kt = blockIdx.y; kt < ksteps; kt += gridDim.y) {
-    const int64_t c = (int64_t)kt * 128 + sub * 8;
-    const int64_t n = live ? a.K - c : 0;
-    float v[8];
-    mr_load8<TIn>(A + src * a.ld + c, n, a.vec != 0, v);
-    if (U) {
-      float u[8];
-      mr_load8<TIn>(U + src * a.ld + c, n, a.vec != 0, u);
+  const int64_t src = mr_source(a, r);
+  const TIn* A = (const TIn*)a.A + g * a.a_stride + (src < 0 ? 0 : src) * a.ld;
+  const TIn* U = UP ? (const TIn*)a.up + g * a.a_stride + (src < 0 ? 0 : src) * a.ld : nullptr;
+  const int k0 = (blockIdx.x - rb * kblocks) * kMrSteps;
+  Raw8<TIn> v[kMrSteps], u[UP ? kMrSteps : 1];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? mr_swiglu(v[i], u[i]) : 0.f;
+  for (int q = 0; q < kMrSteps; ++q) {           // every load before the first conversion
+    const int64_t c = (int64_t)(k0 + q) * 128 + sub * 8;
+    const int64_t n = src >= 0 ? a.K - c : 0;
+    v[q] = mr_load8<TIn>(A + c, n, a.vec != 0);
+    if constexpr (UP) u[q] = mr_load8<TIn>(U + c, n, a.vec != 0);
+  }
+#pragma unroll
+  for (int q = 0; q < kMrSteps; ++q) {
+    const int kt = k0 + q;
+    if (kt >= ksteps) break;
+    uint32_t s, w;
+    if constexpr (UP) {
+      const Raw8<float> x = mr_float8(v[q]), y = mr_float8(u[q]);
+      Raw8<float> h;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h.w[i] = mr_swiglu(x.w[i], y.w[i]);        // 0 * 0 past the end
+      w = mr_encode(h, s);
+    } else {
+      w = mr_encode(v[q], s);
     }
-    uint32_t s;
-    const uint32_t w = mr_encode(v, s);
     if (r < a.R) {
       *reinterpret_cast<uint32_t*>(codes + mx_code_off(r, (int64_t)kt * 64 + sub * 4, a.ld_c)) = w;
       if (sub == 0) {
@@ -261,8 +350,9 @@ constexpr int kRsrcWord3 = 0x00020000;   // raw buffer, 32-bit dword format
 #define S3R_WAIT_LGKM0() __builtin_amdgcn_s_waitcnt(0xC07F)
 constexpr int kSgMfma = 0x008, kSgDsRead = 0x100, kSgVmem = 0x010;
 
-template <int MI_, int NI_, int WM_, int WN_, int NS_>
+template <int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
 struct Tile {
+  static constexpr int WavesPerSimd = WavesPerSimd_;
   static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr int Waves = WM * WN, Threads = 64 * Waves;
   static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN;
@@ -371,39 +461,55 @@ __device__ __forceinline__ void tile_mfma(const TileFrag<T>& f, const uint32_t (
                                                                   2 * H, (int)sb[j]);
 }
 
-// Step kt on stage S = kt % NS.  Its loads were issued NS - 1 steps ago; the wait leaves the later steps'
-// in flight.  The barrier makes every wave's loads visible and retires the stage of step kt - 1, which
-// takes step kt + NS - 1.
+// What a wave holds at the start of a step: the fragments of its first half and its scales.
+template <typename T>
+struct TileHead {
+  TileFrag<T> f0;
+  uint32_t sa[T::MI], sb[T::NI];
+};
+
+template <typename T>
+__device__ __forceinline__ void tile_head(const uint8_t* st, TileHead<T>& h) {
+  tile_frag<T>(st, 0, h.f0);
+  tile_scales<T>(st, h.sa, h.sb);
+}
+
+// Step kt on stage S = kt % NS.  The first half's products cover the reads of the second half's
+// fragments; the barrier in the middle then makes step kt + 1 visible and retires stage S, which takes
+// step kt + NS; the second half's products cover the reads of step kt + 1's head.  So the matrix cores
+// wait for no LDS read, and a load has NS - 1 steps and a half to arrive.
 template <typename T, int S>
-__device__ __forceinline__ void tile_step(const TileSrc<T>& src, int kt, v16f (&acc)[T::MI][T::NI]) {
+__device__ __forceinline__ void tile_step(const TileSrc<T>& src, int kt, TileHead<T>& h, v16f (&acc)[T::MI][T::NI]) {
+  TileFrag<T> f1;
+  tile_frag<T>(ring<T, S>(), 1, f1);
+  tile_mfma<T, 0>(h.f0, h.sa, h.sb, acc);
+  __builtin_amdgcn_sched_group_barrier(kSgDsRead, T::MI + T::NI, 0);
+  __builtin_amdgcn_sched_group_barrier(kSgMfma, T::MI * T::NI, 0);
+  __builtin_amdgcn_sched_barrier(0);
   S3R_WAIT_VM(T::Loads * (T::NS - 2));
   S3R_WAIT_LGKM0();
   __builtin_amdgcn_s_barrier();
-  const uint8_t* st = ring<T, S>();
-  uint32_t sa[T::MI], sb[T::NI];
-  TileFrag<T> f0, f1;
-  tile_frag<T>(st, 0, f0);
-  tile_scales<T>(st, sa, sb);
-  tile_load<T>(src, ring<T, (S + T::NS - 1) % T::NS>(), kt + T::NS - 1);
-  tile_frag<T>(st, 1, f1);
-  tile_mfma<T, 0>(f0, sa, sb, acc);
-  tile_mfma<T, 1>(f1, sa, sb, acc);
-  __builtin_amdgcn_sched_group_barrier(kSgVmem, T::Loads, 0);
-  __builtin_amdgcn_sched_group_barrier(kSgDsRead, 2 * (T::MI + T::NI), 0);
+  __builtin_amdgcn_sched_barrier(0);
+  TileHead<T> n;
+  tile_load<T>(src, ring<T, S>(), kt + T::NS);
+  tile_head<T>(ring<T, (S + 1) % T::NS>(), n);
+  tile_mfma<T, 1>(f1, h.sa, h.sb, acc);
 #pragma unroll
   for (int x = 0; x < T::MI * T::NI; ++x) {
     __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
-    if (x < T::MI + T::NI) __builtin_amdgcn_sched_group_barrier(kSgDsRead, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, (2 * (T::MI + T::NI) + T::MI * T::NI - 1) / (T::MI * T::NI), 0);
+    __builtin_amdgcn_sched_group_barrier(kSgVmem, (T::Loads + T::MI * T::NI - 1) / (T::MI * T::NI), 0);
   }
-  __builtin_amdgcn_sched_group_barrier(kSgMfma, T::MI * T::NI, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  h = n;
 }
 
 template <typename T, int S>
-__device__ __forceinline__ void tile_steps(const TileSrc<T>& src, int kt, v16f (&acc)[T::MI][T::NI]) {
+__device__ __forceinline__ void tile_steps(const TileSrc<T>& src, int kt, TileHead<T>& h, v16f (&acc)[T::MI][T::NI]) {
   if constexpr (S < T::NS) {
     if (kt + S < src.nk) {
-      tile_step<T, S>(src, kt + S, acc);
-      tile_steps<T, S + 1>(src, kt, acc);
+      tile_step<T, S>(src, kt + S, h, acc);
+      tile_steps<T, S + 1>(src, kt, h, acc);
     }
   }
 }
@@ -455,9 +561,9 @@ __device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             w[x] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * x], v[2 * x + 1]}), bf2));
-          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+          __builtin_nontemporal_store((v4u32{w[0], w[1], w[2], w[3]}), reinterpret_cast<v4u32*>(o));
         } else {
-          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+          __builtin_nontemporal_store((v4f32{v[0], v[1], v[2], v[3]}), reinterpret_cast<v4f32*>(o));
         }
       } else {
 #pragma unroll
@@ -471,7 +577,7 @@ __device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t
 }
 
 template <typename T, typename TOut>
-__global__ __launch_bounds__(T::Threads, T::BN == 128 ? 2 : 1) void mx_tile_kernel(MxProdK p, int tiles_m, int vec) {
+__global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void mx_tile_kernel(MxProdK p, int tiles_m, int vec) {
   int bid = blockIdx.x;
   const int nblocks = tiles_m * p.tiles_n;
   if (nblocks % 8 == 0) bid = (bid % 8) * (nblocks / 8) + bid / 8;   // a contiguous range of tiles per XCD
@@ -536,8 +642,13 @@ __global__ __launch_bounds__(T::Threads, T::BN == 128 ? 2 : 1) void mx_tile_kern
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   tile_load<T>(src, ring<T, 0>(), 0);
   tile_load<T>(src, ring<T, 1>(), 1);
-  if constexpr (T::NS > 3) tile_load<T>(src, ring<T, 2>(), 2);
-  for (int kt = 0; kt < p.ksteps; kt += T::NS) tile_steps<T, 0>(src, kt, acc);
+  tile_load<T>(src, ring<T, 2>(), 2);
+  if constexpr (T::NS > 3) tile_load<T>(src, ring<T, 3>(), 3);
+  S3R_WAIT_VM(T::Loads * (T::NS - 1));
+  __builtin_amdgcn_s_barrier();
+  TileHead<T> head;
+  tile_head<T>(ring<T, 0>(), head);
+  for (int kt = 0; kt < p.ksteps; kt += T::NS) tile_steps<T, 0>(src, kt, head, acc);
   S3R_WAIT_VM(0);
   S3R_WAIT_LGKM0();
   __builtin_amdgcn_s_barrier();
@@ -556,14 +667,32 @@ hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st) {
   b.vec = ((uintptr_t)a.A & 15u) == 0 && ((uintptr_t)a.up & 15u) == 0 && (a.ld * esize) % 16 == 0 &&
           (a.a_stride * esize) % 16 == 0;
   const int ksteps = (int)((a.K + 127) / 128);
-  const dim3 grid((unsigned)((a.R + kMrRows - 1) / kMrRows), (unsigned)std::min(ksteps, 65535), (unsigned)a.G);
-  if (a.dtype == S3R_BF16) hipLaunchKernelGGL((mx_rows_kernel<uint16_t>), grid, dim3(kMrThreads), 0, st, b, ksteps);
-  else hipLaunchKernelGGL((mx_rows_kernel<float>), grid, dim3(kMrThreads), 0, st, b, ksteps);
+  const int64_t kblocks = (ksteps + kMrSteps - 1) / kMrSteps, blocks = kblocks * ((a.R + kMrRows - 1) / kMrRows);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)a.G);
+  const dim3 block(kMrThreads);
+  if (a.dtype == S3R_BF16) {
+    if (a.up) hipLaunchKernelGGL((mx_rows_kernel<uint16_t, true>), grid, block, 0, st, b, ksteps);
+    else hipLaunchKernelGGL((mx_rows_kernel<uint16_t, false>), grid, block, 0, st, b, ksteps);
+  } else {
+    if (a.up) hipLaunchKernelGGL((mx_rows_kernel<float, true>), grid, block, 0, st, b, ksteps);
+    else hipLaunchKernelGGL((mx_rows_kernel<float, false>), grid, block, 0, st, b, ksteps);
+  }
   return hipGetLastError();
 }
 
 namespace {
-using BigTile = Tile<4, 2, 2, 2, 3>;
+#ifndef BIGTILE
+#define BIGTILE 4, 2, 2, 4, 3, 2
+#endif
+#ifndef MIDTILE
+#define MIDTILE 2, 2, 4, 2, 3, 4
+#endif
+#ifndef FEW
+#define FEW 32
+#endif
+using BigTile = Tile<BIGTILE>;
+using MidTile = Tile<MIDTILE>;
 
 template <typename T, typename TOut>
 hipError_t run_tiles(const MxProductArgs& a, MxProdK p, hipStream_t st) {
@@ -586,7 +715,7 @@ hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
   const bool bf16 = a.out_dt == S3R_BF16;
   // rows per weight, on average (only the device knows the groups' own)
   const int64_t rows = a.G ? (a.M + a.G - 1) / a.G : a.M;
-  if (rows <= 32) {
+  if (rows <= FEW) {
     // grouped: the tiles of every group, at most one partial tile each
     const int64_t mt = a.G ? a.M / 16 + std::min(a.G, a.M) : (a.M + 15) / 16;
     p.tiles_n = (int)((a.N + 31) / 32);
@@ -595,8 +724,9 @@ hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
     if (bf16) hipLaunchKernelGGL((mx_few_rows_kernel<uint16_t, 2>), grid, dim3(kSkThreads), 0, st, p);
     else hipLaunchKernelGGL((mx_few_rows_kernel<float, 2>), grid, dim3(kSkThreads), 0, st, p);
   } else {
-    if (bf16) return run_tiles<BigTile, uint16_t>(a, p, st);
-    return run_tiles<BigTile, float>(a, p, st);
+    const int64_t big = ((a.M + BigTile::BM - 1) / BigTile::BM) * ((a.N + BigTile::BN - 1) / BigTile::BN);
+    if (!a.G && big >= 256) return bf16 ? run_tiles<BigTile, uint16_t>(a, p, st) : run_tiles<BigTile, float>(a, p, st);
+    return bf16 ? run_tiles<MidTile, uint16_t>(a, p, st) : run_tiles<MidTile, float>(a, p, st);
   }
   return hipGetLastError();
 }
