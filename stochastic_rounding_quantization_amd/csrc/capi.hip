@@ -848,9 +848,7 @@ int s3r_mx_linear(const s3r_mx_pdesc* d, const void* A, const void* up, int32_t 
   r.A = A; r.up = up; r.dtype = dtype; r.ld = ld; r.a_rows = a_rows; r.index = index; r.index_div = index_div;
   r.G = 1; r.R = d->rows; r.K = d->depth; r.codes = c; r.ld_c = mx_steps(d->depth) * 16384;
   r.scales = s; r.ld_s = 4 * d->rows; r.flags = flags;
-  rc = finish(launch_mx_rows(r, stream));
-  if (rc) return rc;
-  return finish(launch_mx_product(product_args(d, c, r.ld_c, s, r.ld_s, offsets, B, Bs, out, ld_out, flags), stream));
+  return finish(launch_mx_linear(r, product_args(d, c, r.ld_c, s, r.ld_s, offsets, B, Bs, out, ld_out, flags), stream));
 }
 
 int s3r_time_next_gemm(hipEvent_t start, hipEvent_t stop) {

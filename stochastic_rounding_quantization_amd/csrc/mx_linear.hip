@@ -5,6 +5,8 @@
 //
 // The contraction K is padded to whole steps of 128 elements with zero codes, so
 // K, like the rows and the columns, can have any size.
+#include <type_traits>
+
 #include "mx_math.h"
 #include "swiglu_math.h"
 
@@ -29,13 +31,15 @@ template <typename TIn> struct Raw8;
 template <> struct Raw8<uint16_t> { uint32_t w[4]; };
 template <> struct Raw8<float> { float w[8]; };
 
-// Elements past the first n are zero.
-template <typename TIn>
-__device__ __forceinline__ Raw8<TIn> mr_load8(const TIn* p, int64_t n, bool vec) {
+// Elements past the first n are zero.  Words: 16-byte aligned rows with K a multiple of 8, so that n is 8
+// or more, or 0 or less (the element path in an unrolled loop is code that has to be fetched, whether it
+// runs or not: a kernel of few instructions per byte was twice as slow with it).
+template <typename TIn, bool Words>
+__device__ __forceinline__ Raw8<TIn> mr_load8(const TIn* p, int64_t n) {
   Raw8<TIn> r;
   if constexpr (sizeof(TIn) == 2) {
-    if (vec && n >= 8) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p);
+    if constexpr (Words) {
+      const uint4 w = n > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
       r.w[0] = w.x; r.w[1] = w.y; r.w[2] = w.z; r.w[3] = w.w;
     } else {
 #pragma unroll
@@ -43,8 +47,9 @@ __device__ __forceinline__ Raw8<TIn> mr_load8(const TIn* p, int64_t n, bool vec)
         r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
     }
   } else {
-    if (vec && n >= 8) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    if constexpr (Words) {
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 a = n > 0 ? reinterpret_cast<const float4*>(p)[0] : z, b = n > 0 ? reinterpret_cast<const float4*>(p)[1] : z;
       r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
       r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
     } else {
@@ -121,6 +126,20 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
 }
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppRor4 = 0x124, kDppRor8 = 0x128;
 
+// Codes of 8 elements of a block with the scale byte sb, any of them: 0 is below the conversion's scales
+// (2^-127 is no normal fp32 number), so there elements and scale are taken times 2^64, which is exact.
+template <typename TRaw>
+__device__ __forceinline__ uint32_t mr_word(const TRaw& v, int sb) {
+  uint32_t w = mr_codes(v, sb);
+  if (sb == 0) {
+    Raw8<float> f = mr_float8(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.w[i] *= 0x1p64f;
+    w = mr_codes(f, 64);
+  }
+  return sb == 255 ? 0u : w;                   // a block with a non-finite element
+}
+
 // The codes of this lane's 8 elements (one word) and, in every lane of the row's 16, its step's four
 // scale bytes; lanes 4 b .. 4 b + 3 hold block b.
 template <typename TRaw>
@@ -129,18 +148,7 @@ __device__ __forceinline__ uint32_t mr_encode(const TRaw& v, uint32_t& scales) {
   m = max(m, dpp<kDppXor1>(m));
   m = max(m, dpp<kDppXor2>(m));
   const int sb = block_scale_byte(m);
-  uint32_t w = mr_codes(v, sb);
-  if (sb == 0 || sb == 255) {                  // below the conversion's scales, or not finite
-    w = 0;
-    if (sb == 0 && m != 0) {
-      const Raw8<float> f = mr_float8(v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        int n, M;
-        w |= e2m1_round<true>(f.w[i], sb - 126, 0, n, M) << (4 * i);
-      }
-    }
-  }
+  const uint32_t w = mr_word(v, sb);
   uint32_t s = (uint32_t)sb << (8 * ((threadIdx.x >> 2) & 3));
   s |= dpp<kDppRor4>(s);
   s |= dpp<kDppRor8>(s);
@@ -162,7 +170,7 @@ __device__ __forceinline__ int64_t mr_source(const MxRowsArgs& a, int64_t r) {
   return s < a.a_rows ? s : -1;
 }
 
-template <typename TIn, bool UP>
+template <typename TIn, bool UP, bool Words>
 __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int ksteps) {
   const int sub = threadIdx.x & 15;
   const int kblocks = (ksteps + kMrSteps - 1) / kMrSteps;
@@ -180,8 +188,8 @@ __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int k
   for (int q = 0; q < kMrSteps; ++q) {           // every load before the first conversion
     const int64_t c = (int64_t)(k0 + q) * 128 + sub * 8;
     const int64_t n = src >= 0 ? a.K - c : 0;
-    v[q] = mr_load8<TIn>(A + c, n, a.vec != 0);
-    if constexpr (UP) u[q] = mr_load8<TIn>(U + c, n, a.vec != 0);
+    v[q] = mr_load8<TIn, Words>(A + c, n);
+    if constexpr (UP) u[q] = mr_load8<TIn, Words>(U + c, n);
   }
 #pragma unroll
   for (int q = 0; q < kMrSteps; ++q) {
@@ -212,31 +220,37 @@ __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int k
 // found by one wave from the offsets themselves (prefix sums of the groups' tile counts, 64 groups a
 // round).  e = -1 past the last tile.  bad: the offsets are not a non-decreasing sequence from 0 to R.
 struct GroupTile { int e; int64_t r0, r1; bool bad; };
-__device__ __forceinline__ GroupTile find_group_tile(const int64_t* __restrict__ offsets, int64_t G, int64_t R, int64_t i,
+__device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
+                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
+}
+__device__ __forceinline__ GroupTile find_group_tile(const int64_t* __restrict__ offsets, int64_t G, int64_t R, int i,
                                                      int tile) {
   const int lane = threadIdx.x & 63;
   GroupTile h{-1, 0, 0, false};
-  int64_t carry = 0;                          // tiles of the groups before this round's
-  bool bad = lane == 0 && (offsets[0] != 0 || offsets[G] != R);
+  int carry = 0;                              // tiles of the groups before this round's
+  bool bad = false;
   for (int64_t g0 = 0; g0 < G; g0 += 64) {
     const int64_t g = g0 + lane;
-    const int64_t o0 = g < G ? offsets[g] : 0, o1 = g < G ? offsets[g + 1] : 0;
-    bad |= o1 < o0 || o0 < 0 || o1 > R;
-    const int64_t n = bad ? 0 : (o1 - o0 + tile - 1) / tile;
-    int64_t s = n;
+    const bool in = g < G;
+    const int64_t o0 = in ? offsets[g] : 0, o1 = in ? offsets[g + 1] : 0;
+    const bool odd = in && (o1 < o0 || o0 < 0 || o1 > R || (g == 0 && o0 != 0) || (g == G - 1 && o1 != R));
+    bad |= odd;
+    const int n = odd ? 0 : ((int)(o1 - o0) + tile - 1) / tile;
+    int s = n;
+#pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int64_t b = __shfl_up(s, o, 64);
+      const int b = __shfl_up(s, o, 64);
       if (lane >= o) s += b;
     }
-    const bool hit = carry + s > i && carry + s - n <= i;
-    const uint64_t m = __builtin_amdgcn_ballot_w64(hit);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(carry + s > i && carry + s - n <= i);
     if (m && h.e < 0) {
       const int w = __builtin_ctzll(m);
       h.e = (int)g0 + w;
-      h.r1 = __shfl(o1, w, 64);
-      h.r0 = __shfl(o0 + (i - (carry + s - n)) * tile, w, 64);
+      h.r1 = read_lane(o1, w);
+      h.r0 = read_lane(o0, w) + (int64_t)(i - (carry + __builtin_amdgcn_readlane(s - n, w))) * tile;
     }
-    carry += __shfl(s, 63, 64);
+    carry += __builtin_amdgcn_readlane(s, 63);
   }
   h.bad = __builtin_amdgcn_ballot_w64(bad) != 0;
   return h;
@@ -262,36 +276,61 @@ __device__ __forceinline__ void store_out(uint16_t* p, float v) {
 // joined in LDS in wave order.  Fragments go straight from memory to the matrix cores
 // (v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds row or column l % 16, K elements 32 (l / 16) .. + 31,
 // 16 bytes, and that block's scale; the result's register r is row 4 (l / 16) + r, column l % 16): 16
-// rows of a step are one contiguous KiB of the code layout.
+// rows of a step are one contiguous KiB of the code layout.  The weights' bytes are the bound, so a wave
+// issues the loads of `Depth` steps before its first product.
+// With TIn the rows come unquantized (s3r_mx_linear): the workgroup rounds its rows into LDS, as
+// mx_rows_kernel does into memory, while its first weights are on the way, so there is no second launch
+// and no codes go through memory (every column tile rounds the rows again, from the caches).  Rounding in
+// each lane's own fragment instead did the work of 16 rows for one row: 12 us against 9 (N = 14336, K = 4096).
+// TIn void: rows already in codes.
 constexpr int kSkThreads = 256;
-template <typename TOut, int NJ>
-__global__ __launch_bounds__(kSkThreads) void mx_few_rows_kernel(MxProdK p) {
-  __shared__ float part[3][NJ][256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+constexpr size_t kSkLdsMax = 65536;               // a workgroup's dynamic LDS
+// LDS of the rounded rows: a row's codes (64 bytes a step, 16 to spread the rows over the banks), then
+// every row's scale words
+__host__ __device__ inline size_t sk_row_bytes(int ksteps) { return (size_t)ksteps * 64 + 16; }
+__host__ __device__ inline size_t sk_lds_bytes(int rows, int ksteps) { return rows * (sk_row_bytes(ksteps) + (size_t)ksteps * 4); }
+
+template <typename TOut, typename TIn, bool Words, int MI, int NJ, int Depth>
+__global__ __launch_bounds__(kSkThreads) void mx_few_rows_kernel(MxProdK p, MxRowsArgs q, int tile_rows) {
+  constexpr bool kFused = !std::is_void<TIn>::value;
+  static_assert(!kFused || MI == 1, "rounded rows of one 16-row tile");
+  __shared__ float part[3][MI * NJ][256];
+  extern __shared__ __attribute__((aligned(16))) uint8_t sk_rows[];
+  // The wave's index in a scalar register: the loop over its steps has to branch, since the matrix
+  // instructions run whatever the execution mask says.
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t m0, m1;
   const uint8_t *B = p.B, *Bs = p.Bs;
   const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
   if (p.G) {
-    const GroupTile h = find_group_tile(p.offsets, p.G, p.M, mt, 16);
+    const GroupTile h = find_group_tile(p.offsets, p.G, p.M, mt, 16 * MI);
     if (h.bad) {
       if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_BAD_GROUPS);
       return;
     }
-    if (h.e < 0) return;
+    const int e = __builtin_amdgcn_readfirstlane(h.e);
+    if (e < 0) return;
     m0 = h.r0;
-    m1 = min(h.r1, m0 + 16);
-    B += h.e * p.b_stride;
-    Bs += h.e * p.bs_stride;
+    m1 = min(h.r1, m0 + 16 * MI);
+    B += e * p.b_stride;
+    Bs += e * p.bs_stride;
   } else {
-    m0 = (int64_t)mt * 16;
-    m1 = min(p.M, m0 + 16);
+    m0 = (int64_t)mt * (16 * MI);
+    m1 = min(p.M, m0 + 16 * MI);
   }
   const int64_t n0 = (int64_t)nt * (16 * NJ);
   const int r15 = lane & 15, kb = lane >> 4;
   // rows and columns past the end repeat the last one; their results are not stored
-  const int64_t ar = min(m0 + r15, m1 - 1);
-  const uint8_t* pa = p.A + (ar >> 8) * p.lda + (ar & 255) * 64 + kb * 16;
-  const uint8_t* psa = p.As + 4 * ar + kb;
+  const int rows = (int)(m1 - m0), lr = min(r15, rows - 1);
+  const uint8_t *pa[MI], *psa[MI];
+  if constexpr (!kFused) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t ar = m0 + min(16 * i + r15, rows - 1);
+      pa[i] = p.A + (ar >> 8) * p.lda + (ar & 255) * 64 + kb * 16;
+      psa[i] = p.As + 4 * ar + kb;
+    }
+  }
   const uint8_t *pb[NJ], *psb[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
@@ -299,41 +338,111 @@ __global__ __launch_bounds__(kSkThreads) void mx_few_rows_kernel(MxProdK p) {
     pb[j] = B + (br >> 8) * p.ldb + (br & 255) * 64 + kb * 16;
     psb[j] = Bs + 4 * br + kb;
   }
-  v4f acc[NJ];
+  v4f acc[MI][NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int kt = wave; kt < p.ksteps; kt += kSkThreads / 64) {
-    const uint4 x = *reinterpret_cast<const uint4*>(pa + (int64_t)kt * kMxBlkBytes);
-    const int sa = psa[kt * p.ldas];
-    const v8i fa = v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const uint4 y = *reinterpret_cast<const uint4*>(pb[j] + (int64_t)kt * kMxBlkBytes);
-      const int sb = psb[j][kt * p.ldbs];
-      const v8i fb = v8i{(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
-      acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa, fb, acc[j], 4, 4, 0, sa, 0, sb);
+    for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  uint4 x[Depth][MI], y[Depth][NJ];
+  int sa[Depth][MI], sb[Depth][NJ];
+  auto load = [&](int kt) {
+#pragma unroll
+    for (int d = 0; d < Depth; ++d) {
+      const int64_t k = kt + 4 * d;
+      if (k < p.ksteps) {                          // the same in the whole wave
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          y[d][j] = *reinterpret_cast<const uint4*>(pb[j] + k * kMxBlkBytes);
+          sb[d][j] = psb[j][k * p.ldbs];
+        }
+        if constexpr (!kFused) {
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            x[d][i] = *reinterpret_cast<const uint4*>(pa[i] + k * kMxBlkBytes);
+            sa[d][i] = psa[i][k * p.ldas];
+          }
+        }
+      }
+    }
+  };
+  load(wave);
+  const int row_bytes = (int)sk_row_bytes(p.ksteps);
+  uint8_t* sk_scales = sk_rows + tile_rows * row_bytes;
+  if constexpr (kFused) {
+    bool bad = false;
+    const int sub = threadIdx.x & 15, items = rows * p.ksteps;      // (row, step) pairs, 16 lanes each
+    constexpr int kBatch = 2, kApart = kSkThreads / 16;              // pairs of a thread whose loads go out together
+    for (int it0 = threadIdx.x >> 4; it0 < items; it0 += kBatch * kApart) {
+      Raw8<TIn> v[kBatch];
+      int r[kBatch], kt[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int it = it0 + u * kApart;
+        r[u] = it / p.ksteps;
+        kt[u] = it - r[u] * p.ksteps;
+        const int64_t src = it < items ? mr_source(q, m0 + r[u]) : -1;
+        const int c = kt[u] * 128 + sub * 8;
+        v[u] = mr_load8<TIn, Words>((const TIn*)q.A + (src < 0 ? 0 : src) * q.ld + c, src < 0 ? 0 : q.K - c);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        uint32_t s;
+        const uint32_t w = mr_encode(v[u], s);
+        if (it0 + u * kApart < items) {
+          *reinterpret_cast<uint32_t*>(sk_rows + r[u] * row_bytes + kt[u] * 64 + sub * 4) = w;
+          if (sub == 0) *reinterpret_cast<uint32_t*>(sk_scales + (r[u] * p.ksteps + kt[u]) * 4) = s;
+          bad |= mr_nan_scale(s);
+        }
+      }
+    }
+    if (bad && nt == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_NONFINITE);
+    __syncthreads();
+  }
+  for (int kt = wave; kt < p.ksteps; kt += 4 * Depth) {
+    if (kt != wave) load(kt);
+#pragma unroll
+    for (int d = 0; d < Depth; ++d) {
+      const int k = kt + 4 * d;
+      if (k >= p.ksteps) break;
+      if constexpr (kFused) {
+        x[d][0] = *reinterpret_cast<const uint4*>(sk_rows + lr * row_bytes + k * 64 + kb * 16);
+        sa[d][0] = sk_scales[(lr * p.ksteps + k) * 4 + kb];
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const v8i fa = v8i{(int)x[d][i].x, (int)x[d][i].y, (int)x[d][i].z, (int)x[d][i].w, 0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const v8i fb = v8i{(int)y[d][j].x, (int)y[d][j].y, (int)y[d][j].z, (int)y[d][j].w, 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa, fb, acc[i][j], 4, 4, 0, sa[d][i], 0, sb[d][j]);
+        }
+      }
     }
   }
   if (wave > 0) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave - 1][j][r * 64 + lane] = acc[j][r];
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[wave - 1][i * NJ + j][r * 64 + lane] = acc[i][j][r];
   }
   __syncthreads();
   if (wave > 0) return;
   TOut* out = (TOut*)p.out;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int64_t n = n0 + 16 * j + r15;
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t m = m0 + 4 * kb + r;
-      const float v = ((acc[j][r] + part[0][j][r * 64 + lane]) + part[1][j][r * 64 + lane]) + part[2][j][r * 64 + lane];
-      if (n < p.N && m < m1) store_out(out + m * p.ld_out + n, v);
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t n = n0 + 16 * j + r15;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t m = m0 + 16 * i + 4 * kb + r;
+        const int at = r * 64 + lane, ij = i * NJ + j;
+        const float v = ((acc[i][j][r] + part[0][ij][at]) + part[1][ij][at]) + part[2][ij][at];
+        if (n < p.N && m < m1) store_out(out + m * p.ld_out + n, v);
+      }
     }
-  }
 }
 
 // Many rows: BM x BN tiles, WM x WN waves of (32 MI) x (32 NI) each, operands staged through LDS by
@@ -504,6 +613,15 @@ __device__ __forceinline__ void tile_step(const TileSrc<T>& src, int kt, TileHea
   h = n;
 }
 
+// The first NS steps into the ring.
+template <typename T, int S>
+__device__ __forceinline__ void tile_fill(const TileSrc<T>& src) {
+  if constexpr (S < T::NS) {
+    tile_load<T>(src, ring<T, S>(), S);
+    tile_fill<T, S + 1>(src);
+  }
+}
+
 template <typename T, int S>
 __device__ __forceinline__ void tile_steps(const TileSrc<T>& src, int kt, TileHead<T>& h, v16f (&acc)[T::MI][T::NI]) {
   if constexpr (S < T::NS) {
@@ -640,10 +758,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void mx_tile_kernel(Mx
     for (int j = 0; j < T::NI; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  tile_load<T>(src, ring<T, 0>(), 0);
-  tile_load<T>(src, ring<T, 1>(), 1);
-  tile_load<T>(src, ring<T, 2>(), 2);
-  if constexpr (T::NS > 3) tile_load<T>(src, ring<T, 3>(), 3);
+  tile_fill<T, 0>(src);
   S3R_WAIT_VM(T::Loads * (T::NS - 1));
   __builtin_amdgcn_s_barrier();
   TileHead<T> head;
@@ -660,24 +775,32 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void mx_tile_kernel(Mx
 size_t mx_rows_codes_bytes(int64_t R, int64_t K) { return (size_t)((R + 255) / 256) * (size_t)((K + 127) / 128) * kMxBlkBytes; }
 size_t mx_rows_scales_bytes(int64_t R, int64_t K) { return (size_t)((K + 127) / 128) * (size_t)R * 4; }
 
+namespace {
+bool mr_words(const MxRowsArgs& a) {       // rows in whole 16-byte words
+  const int esize = a.dtype == S3R_BF16 ? 2 : 4;
+  return ((uintptr_t)a.A & 15u) == 0 && ((uintptr_t)a.up & 15u) == 0 && (a.ld * esize) % 16 == 0 &&
+         (a.a_stride * esize) % 16 == 0 && a.K % 8 == 0;
+}
+
+template <typename TIn>
+void run_rows(const MxRowsArgs& a, dim3 grid, int ksteps, hipStream_t st) {
+  const dim3 block(kMrThreads);
+  const bool words = mr_words(a);
+  if (a.up && words) hipLaunchKernelGGL((mx_rows_kernel<TIn, true, true>), grid, block, 0, st, a, ksteps);
+  else if (a.up) hipLaunchKernelGGL((mx_rows_kernel<TIn, true, false>), grid, block, 0, st, a, ksteps);
+  else if (words) hipLaunchKernelGGL((mx_rows_kernel<TIn, false, true>), grid, block, 0, st, a, ksteps);
+  else hipLaunchKernelGGL((mx_rows_kernel<TIn, false, false>), grid, block, 0, st, a, ksteps);
+}
+}  // namespace
+
 hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st) {
   if (a.R == 0 || a.K == 0 || a.G == 0) return hipSuccess;
-  MxRowsArgs b = a;
-  const int esize = a.dtype == S3R_BF16 ? 2 : 4;
-  b.vec = ((uintptr_t)a.A & 15u) == 0 && ((uintptr_t)a.up & 15u) == 0 && (a.ld * esize) % 16 == 0 &&
-          (a.a_stride * esize) % 16 == 0;
   const int ksteps = (int)((a.K + 127) / 128);
   const int64_t kblocks = (ksteps + kMrSteps - 1) / kMrSteps, blocks = kblocks * ((a.R + kMrRows - 1) / kMrRows);
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, (unsigned)a.G);
-  const dim3 block(kMrThreads);
-  if (a.dtype == S3R_BF16) {
-    if (a.up) hipLaunchKernelGGL((mx_rows_kernel<uint16_t, true>), grid, block, 0, st, b, ksteps);
-    else hipLaunchKernelGGL((mx_rows_kernel<uint16_t, false>), grid, block, 0, st, b, ksteps);
-  } else {
-    if (a.up) hipLaunchKernelGGL((mx_rows_kernel<float, true>), grid, block, 0, st, b, ksteps);
-    else hipLaunchKernelGGL((mx_rows_kernel<float, false>), grid, block, 0, st, b, ksteps);
-  }
+  if (a.dtype == S3R_BF16) run_rows<uint16_t>(a, grid, ksteps, st);
+  else run_rows<float>(a, grid, ksteps, st);
   return hipGetLastError();
 }
 
@@ -688,11 +811,19 @@ namespace {
 #ifndef MIDTILE
 #define MIDTILE 2, 2, 4, 2, 3, 4
 #endif
-#ifndef FEW
-#define FEW 32
-#endif
-using BigTile = Tile<BIGTILE>;
-using MidTile = Tile<MIDTILE>;
+using Tile256 = Tile<4, 2, 2, 4, 3, 2>;        // 256 x 256, 8 waves
+using Tile256x128 = Tile<2, 2, 4, 2, 3, 4>;    // 8 waves, two workgroups per CU
+using Tile128 = Tile<2, 2, 2, 2, 3, 3>;        // 4 waves, three workgroups per CU
+using Tile128x64 = Tile<2, 1, 2, 2, 6, 2>;
+using Tile64 = Tile<1, 1, 2, 2, 6, 2>;
+
+// The largest tile that still gives this many workgroups (three quarters of the CUs): larger tiles read
+// the operands less often, fewer workgroups leave CUs idle.  N = 14336, K = 4096, rows and product, us:
+//   rows   128 x 64  128 x 128  256 x 128
+//    128       15.6       19.5       22.7     (224 / 112 / 112 workgroups)
+//    384       28.5       24.4       25.0     (672 / 336 / 224)
+//   1024       55.7       47.3       40.7     (1792 / 896 / 448)
+constexpr int64_t kFillTiles = 192;
 
 template <typename T, typename TOut>
 hipError_t run_tiles(const MxProductArgs& a, MxProdK p, hipStream_t st) {
@@ -705,30 +836,94 @@ hipError_t run_tiles(const MxProductArgs& a, MxProdK p, hipStream_t st) {
 }
 }  // namespace
 
-hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
-  if (a.M == 0 || a.N == 0) return hipSuccess;
+namespace {
+MxProdK product_params(const MxProductArgs& a) {
   MxProdK p{};
   p.A = a.A; p.lda = a.lda; p.As = a.As; p.ldas = a.ldas;
   p.B = a.B; p.ldb = a.ldb; p.Bs = a.Bs; p.ldbs = a.ldbs; p.b_stride = a.b_stride; p.bs_stride = a.bs_stride;
   p.offsets = a.offsets; p.G = a.G; p.M = a.M; p.N = a.N; p.ksteps = (int)((a.K + 127) / 128);
   p.out = a.out; p.ld_out = a.ld_out; p.flags = a.flags;
-  const bool bf16 = a.out_dt == S3R_BF16;
-  // rows per weight, on average (only the device knows the groups' own)
-  const int64_t rows = a.G ? (a.M + a.G - 1) / a.G : a.M;
-  if (rows <= FEW) {
-    // grouped: the tiles of every group, at most one partial tile each
-    const int64_t mt = a.G ? a.M / 16 + std::min(a.G, a.M) : (a.M + 15) / 16;
-    p.tiles_n = (int)((a.N + 31) / 32);
-    if (mt * p.tiles_n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(mt * p.tiles_n));
-    if (bf16) hipLaunchKernelGGL((mx_few_rows_kernel<uint16_t, 2>), grid, dim3(kSkThreads), 0, st, p);
-    else hipLaunchKernelGGL((mx_few_rows_kernel<float, 2>), grid, dim3(kSkThreads), 0, st, p);
-  } else {
-    const int64_t big = ((a.M + BigTile::BM - 1) / BigTile::BM) * ((a.N + BigTile::BN - 1) / BigTile::BN);
-    if (!a.G && big >= 256) return bf16 ? run_tiles<BigTile, uint16_t>(a, p, st) : run_tiles<BigTile, float>(a, p, st);
-    return bf16 ? run_tiles<MidTile, uint16_t>(a, p, st) : run_tiles<MidTile, float>(a, p, st);
-  }
+  return p;
+}
+
+// rows per weight, on average (only the device knows the groups' own)
+int64_t mean_rows(const MxProductArgs& a) { return a.G ? (a.M + a.G - 1) / a.G : a.M; }
+
+template <typename TIn, bool Words, int MI, int NJ, int Depth>
+hipError_t run_few_rows(const MxProductArgs& a, const MxRowsArgs& q, hipStream_t st) {
+  MxProdK p = product_params(a);
+  // grouped: the tiles of every group, at most one partial tile each
+  const int64_t mt = a.G ? a.M / (16 * MI) + std::min(a.G, a.M) : (a.M + 16 * MI - 1) / (16 * MI);
+  p.tiles_n = (int)((a.N + 16 * NJ - 1) / (16 * NJ));
+  if (mt * p.tiles_n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(mt * p.tiles_n)), block(kSkThreads);
+  const int rows = (int)std::min<int64_t>(a.M, 16);
+  const size_t lds = std::is_void<TIn>::value ? 0 : sk_lds_bytes(rows, p.ksteps);
+  if (a.out_dt == S3R_BF16)
+    hipLaunchKernelGGL((mx_few_rows_kernel<uint16_t, TIn, Words, MI, NJ, Depth>), grid, block, lds, st, p, q, rows);
+  else
+    hipLaunchKernelGGL((mx_few_rows_kernel<float, TIn, Words, MI, NJ, Depth>), grid, block, lds, st, p, q, rows);
   return hipGetLastError();
+}
+
+template <typename T>
+int64_t tile_count(const MxProductArgs& a) { return ((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN); }
+
+template <typename T>
+hipError_t run_tiles(const MxProductArgs& a, hipStream_t st) {
+  const MxProdK p = product_params(a);
+  return a.out_dt == S3R_BF16 ? run_tiles<T, uint16_t>(a, p, st) : run_tiles<T, float>(a, p, st);
+}
+
+constexpr int kFewNJ = 2;                       // 16-column tiles of a workgroup
+// Largest number of few-rows workgroups of 16 rows before their repeated reads of the weights cost more
+// than workgroups of 32 rows or LDS tiles lose to latency.  Rows and product, us:
+//   64 rows, N = 1408, K = 2048: 176 of them 6.7, LDS tiles 8.9;  64 rows, N = 4096, K = 4096: 512 10.9, 12.9;
+//   32 rows, N = 14336, K = 4096: 896 15.9, of 32 rows 14.0, LDS tiles 13.5; 48 rows: 1344 19.8, LDS tiles 13.7
+constexpr int64_t kFewBlocks = 512;
+// Rows per weight, on average, up to which a grouped product takes the few-rows kernel.  64 experts,
+// N = 1408, K = 2048: 8 rows 21.0 us against 22.4 in 128 x 128 tiles, 16 rows 26.7 against 29.5, 32 rows
+// 42.7 against 31.5.
+constexpr int64_t kFewGrouped = 16;
+// From here on the taller tile: 8 experts, N = K = 4096, 1024 rows each 102.8 against 103.3 us in 128 x 128
+// tiles, 4096 rows 350 against 363.
+constexpr int64_t kTallGrouped = 1024;
+// Rows that the few-rows kernel rounds itself: 1 row, N = 14336, K = 4096 9.2 us against 11.4 with a launch
+// of their own, 4 rows 11.8 against 12.0, 8 rows 15.7 against 12.1; grouped, at most a row per weight on average.
+constexpr int64_t kRoundRows = 2;
+
+template <typename TIn>
+hipError_t run_round_few(const MxProductArgs& a, const MxRowsArgs& q, hipStream_t st) {
+  return mr_words(q) ? run_few_rows<TIn, true, 1, kFewNJ, 2>(a, q, st) : run_few_rows<TIn, false, 1, kFewNJ, 2>(a, q, st);
+}
+}  // namespace
+
+hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
+  if (a.M == 0 || a.N == 0) return hipSuccess;
+  if (a.G) {
+    const int64_t rows = mean_rows(a);
+    if (rows <= kFewGrouped) return run_few_rows<void, true, 1, kFewNJ, 2>(a, MxRowsArgs{}, st);
+    return rows < kTallGrouped ? run_tiles<Tile128>(a, st) : run_tiles<Tile256x128>(a, st);
+  }
+  const int64_t few = (a.M + 15) / 16 * ((a.N + 16 * kFewNJ - 1) / (16 * kFewNJ));
+  if (a.M <= 16 || (a.M <= 64 && few <= kFewBlocks)) return run_few_rows<void, true, 1, kFewNJ, 4>(a, MxRowsArgs{}, st);
+  if (a.M <= 32) return run_few_rows<void, true, 2, kFewNJ, 4>(a, MxRowsArgs{}, st);
+  if (tile_count<Tile256>(a) >= kFillTiles) return run_tiles<Tile256>(a, st);
+  if (tile_count<Tile256x128>(a) >= kFillTiles) return run_tiles<Tile256x128>(a, st);
+  if (tile_count<Tile128>(a) >= kFillTiles) return run_tiles<Tile128>(a, st);
+  if (tile_count<Tile128x64>(a) >= kFillTiles) return run_tiles<Tile128x64>(a, st);
+  return run_tiles<Tile64>(a, st);
+}
+
+// Rows and product; `rows` writes the codes that `prod` reads, unless the few-rows kernel rounds them itself.
+hipError_t launch_mx_linear(const MxRowsArgs& rows, const MxProductArgs& prod, hipStream_t st) {
+  if (prod.M == 0 || prod.N == 0) return hipSuccess;
+  const int ksteps = (int)((prod.K + 127) / 128);
+  if (!rows.up && prod.M <= std::max(prod.G, kRoundRows) &&
+      sk_lds_bytes((int)std::min<int64_t>(prod.M, 16), ksteps) + 3 * kFewNJ * 1024 <= kSkLdsMax)
+    return rows.dtype == S3R_BF16 ? run_round_few<uint16_t>(prod, rows, st) : run_round_few<float>(prod, rows, st);
+  const hipError_t e = launch_mx_rows(rows, st);
+  return e != hipSuccess ? e : launch_mx_product(prod, st);
 }
 
 }  // namespace s3r

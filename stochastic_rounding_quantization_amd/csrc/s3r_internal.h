@@ -224,7 +224,7 @@ struct MxRowsArgs {
   const int32_t* index; int64_t index_div;
   int64_t G, R, K;
   uint8_t* codes; int64_t ld_c, c_stride; uint8_t* scales; int64_t ld_s, s_stride;
-  uint32_t* flags; int vec;
+  uint32_t* flags;
 };
 struct MxProductArgs {       // out [M x N] = A [M x K] . B [N x K]^T, B + e * stride for the rows of group e
   const uint8_t* A; int64_t lda; const uint8_t* As; int64_t ldas;
@@ -237,6 +237,7 @@ size_t mx_rows_codes_bytes(int64_t R, int64_t K);
 size_t mx_rows_scales_bytes(int64_t R, int64_t K);
 hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st);
 hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st);
+hipError_t launch_mx_linear(const MxRowsArgs& rows, const MxProductArgs& prod, hipStream_t st);
 
 // SwiGLU backward glue (swiglu.hip).
 hipError_t launch_swiglu_backward(int64_t T, int64_t F, const float* dH, int64_t ld_dh, const uint16_t* Ag,

@@ -96,7 +96,8 @@ def test_rows_of_silu_times_up(dtype):
 
 
 SHAPES = [(1, 1, 1), (1, 14, 128), (2, 100, 2048), (5, 33, 300), (16, 256, 640), (17, 130, 96), (40, 300, 1000),
-          (64, 1411, 512), (129, 257, 384), (300, 513, 2024), (513, 128, 130), (260, 1000, 4096)]
+          (64, 1411, 512), (129, 257, 384), (300, 513, 2024), (513, 128, 130), (260, 1000, 4096),
+          (2, 70, 40000), (31, 9000, 96), (400, 3130, 130), (700, 4100, 200), (1500, 4100, 96), (3000, 4100, 129)]
 
 
 @pytest.mark.parametrize("dtype, out", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
@@ -132,7 +133,8 @@ def test_empty_products():
 
 
 GROUPS = [([0, 1], 64, 96), ([5], 40, 128), ([1, 0, 2, 0, 0, 1], 100, 256), ([0, 0, 33, 16, 17], 70, 300),
-          ([300, 0, 1, 129, 255, 256, 7], 150, 640), ([1] * 70, 33, 128), ([40] * 9, 257, 384), ([0, 700, 0], 130, 200)]
+          ([300, 0, 1, 129, 255, 256, 7], 150, 640), ([1] * 70, 33, 128), ([40] * 9, 257, 384), ([0, 700, 0], 130, 200),
+          ([9, 3, 20, 30], 70, 200), ([2600, 0, 700], 300, 130)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -154,11 +156,11 @@ def test_grouped(counts, N, K, out):
     assert int(flags) == 0
 
 
-@pytest.mark.parametrize("R", [8, 4000])
+@pytest.mark.parametrize("R", [4, 8, 400, 8000])
 def test_bad_offsets_compute_nothing(R):
     w = s3r.mx_rows(matrix((4, 64, 128), torch.bfloat16, 1))
     X = matrix((R, 128), torch.bfloat16, 2)
-    for off in ([0, 3, 2, 5, R], [1, 2, 3, 4, R], [0, 1, 2, 3, R - 1], [0, 1, 2, R + 1, R], [0, -1, 2, 3, R],
+    for off in ([0, 3, 2, 4, R], [1, 2, 3, 4, R], [0, 1, 2, 3, R - 1], [0, 1, 2, R + 1, R], [0, -1, 2, 3, R],
                 [0, 1, 1 << 40, 3, R]):
         y = torch.full((R, 64), 7.0, device=DEV)
         flags = torch.zeros(1, dtype=torch.int32, device=DEV)
