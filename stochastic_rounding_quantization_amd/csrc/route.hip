@@ -26,7 +26,7 @@ __device__ __forceinline__ float rt_load(const TIn* p) {
   else return *reinterpret_cast<const float*>(p);
 }
 
-// V consecutive logits from p, of which the first n exist (the others: NaN, "no expert").
+// V consecutive logits from p, of which the first n exist (the others: -inf, as masked).
 template <typename TIn, int V>
 __device__ __forceinline__ void rt_load_row(const TIn* p, int n, bool vec, float (&x)[V]) {
   if (vec && n >= V) {
@@ -50,37 +50,58 @@ __device__ __forceinline__ void rt_load_row(const TIn* p, int n, bool vec, float
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = i < n ? rt_load(p + i) : __builtin_nanf("");
+    for (int i = 0; i < V; ++i) x[i] = i < n ? rt_load(p + i) : -__builtin_inff();
   }
 }
 
-// Reductions over the L lanes of a token.
-template <int L, typename T>
-__device__ __forceinline__ T rt_sum(T v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+// The value of the lane that the reduction's step O pairs this lane with: neighbours, pairs, quads and
+// halves of a 16-lane row by DPP moves, which cost no trip through LDS; rows by a shuffle.
+template <int O>
+__device__ __forceinline__ int rt_partner(int v) {
+  if constexpr (O == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);        // quad_perm 1 0 3 2
+  else if constexpr (O == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);   // quad_perm 2 3 0 1
+  else if constexpr (O == 4) return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);  // row_half_mirror
+  else if constexpr (O == 8) return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);  // row_mirror
+  else return __shfl_xor(v, O, 64);
+}
+template <int O>
+__device__ __forceinline__ uint32_t rt_partner(uint32_t v) { return (uint32_t)rt_partner<O>((int)v); }
+template <int O>
+__device__ __forceinline__ float rt_partner(float v) { return __int_as_float(rt_partner<O>(__float_as_int(v))); }
+template <int O>
+__device__ __forceinline__ double rt_partner(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)rt_partner<O>((int)(uint32_t)u), hi = (uint32_t)rt_partner<O>((int)(u >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Reductions over the aligned L lanes of a token (each step joins equal halves, so every lane ends with
+// the same value).
+template <int L, int O = 1, typename T, typename F>
+__device__ __forceinline__ T rt_reduce(T v, F&& join) {
+  if constexpr (O < L) return rt_reduce<L, 2 * O>(join(v, rt_partner<O>(v)), join);
+  else return v;
 }
 template <int L, typename T>
-__device__ __forceinline__ T rt_max(T v) {      // NaNs lose
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) {
-    const T w = __shfl_xor(v, o, 64);
-    if constexpr (sizeof(T) == 8) v = __builtin_fmax(v, w);
-    else v = __builtin_fmaxf(v, w);
-  }
-  return v;
+__device__ __forceinline__ T rt_sum(T v) {
+  return rt_reduce<L>(v, [](T a, T b) { return a + b; });
+}
+__device__ __forceinline__ float rt_fmax(float a, float b) { return __builtin_fmaxf(a, b); }     // NaNs lose
+__device__ __forceinline__ double rt_fmax(double a, double b) { return __builtin_fmax(a, b); }
+template <int L, typename T>
+__device__ __forceinline__ T rt_max(T v) {
+  return rt_reduce<L>(v, [](T a, T b) { return rt_fmax(a, b); });
 }
 template <int L>
 __device__ __forceinline__ int rt_min(int v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, 64));
-  return v;
+  return rt_reduce<L>(v, [](int a, int b) { return min(a, b); });
 }
 
 template <typename T> __device__ __forceinline__ T rt_neg_inf();
 template <> __device__ __forceinline__ float rt_neg_inf<float>() { return -__builtin_inff(); }
 template <> __device__ __forceinline__ double rt_neg_inf<double>() { return -__builtin_inf(); }
+
+__host__ __device__ inline int64_t rt_hist_ld(int E) { return (E + 3) / 4 * 4; }
 
 struct RouteKernelArgs {
   const void* logits; int64_t ld; const float* bias;
@@ -88,26 +109,27 @@ struct RouteKernelArgs {
   int64_t T;
   int E, K, groups, keep, group_top, sigmoid, renorm;
   float scale;
-  int32_t* hist;             // [nchunk][E] slots of the chunk's tokens at each expert
+  int32_t* hist;             // [nchunk][rt_hist_ld(E)] slots of the chunk's tokens at each expert
   int nchunk; int64_t chunk; // tokens per chunk
   int vec;
+  int group_lanes;           // lanes of an expert group where groups are whole power-of-two runs of lanes, else 0
 };
 
-// The slots [s0, s1) in order, each to row base[e] + (slots of e before it in the range); base is
-// advanced.  Every thread of the block takes part.  A wave ranks its 64 slots by matching expert
+// The slots [s0, s1) in order (e_first: the expert of this thread's first), each to row base[e] + (slots of e
+// before it in the range); base is advanced.  Every thread of the block takes part.  A wave ranks its 64 slots by matching expert
 // indices bit by bit with ballots, and the waves' counts are added in order, so the order is the
 // slots' own and no atomic decides it.
-__device__ void rt_place(const int32_t* ids, int64_t s0, int64_t s1, int E, int32_t* base,
+__device__ __forceinline__ void rt_place(const int32_t* ids, int e_first, int64_t s0, int64_t s1, int E, int32_t* base,
                          uint16_t* wcnt, int32_t* __restrict__ slot_row, int32_t* __restrict__ row_slot) {
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = nt >> 6;
   int bits = 0;
   while ((1 << bits) < E) ++bits;
   for (int64_t t0 = s0; t0 < s1; t0 += nt) {
-    for (int i = tid; i < nw * E; i += nt) wcnt[i] = 0;
+    for (int i = tid; i < (nw * E + 1) / 2; i += nt) reinterpret_cast<uint32_t*>(wcnt)[i] = 0;
     __syncthreads();
     const int64_t s = t0 + tid;
     const bool act = s < s1;
-    const int e = act ? ids[s] : 0;
+    const int e = t0 == s0 ? e_first : act ? ids[s] : 0;
     uint64_t same = __builtin_amdgcn_ballot_w64(act);
     for (int b = 0; b < bits; ++b) {
       const uint64_t m = __builtin_amdgcn_ballot_w64((e >> b) & 1);
@@ -150,122 +172,320 @@ __device__ int rt_scan(int v, int32_t* scratch) {
   return before + s - v;
 }
 
-// LDS of both kernels: base [E] | scratch [16] | hist or partial sums [2048] | wave counts [16][E] (uint16)
+// LDS of both kernels: base [E] | scratch [16] | hist or partial sums [2048] | wave counts [16][E] (uint16),
+// in whose place the choice keeps its lanes' bias: L V <= 1024 floats, at most 512 of them where L follows
+// top_k or groups (<= E) and not E / V, so 32 E + 1024 bytes hold either.
 __host__ __device__ inline size_t rt_lds_bytes(int E) {
-  return (size_t)E * 4 + 64 + 2048 * 4 + align_up((size_t)16 * E * 2, 16);
+  return (size_t)E * 4 + 64 + 2048 * 4 + align_up((size_t)16 * E * 2, 16) + 1024;
+}
+
+// Keys of the row in Key's precision; -inf for masked experts and NaN keys.
+template <typename Key, int L, int V>
+__device__ __forceinline__ void rt_keys(const RouteKernelArgs& a, const float (&x)[V], const float (&bias)[V],
+                                        float shift, Key (&key)[V]) {
+  if constexpr (sizeof(Key) == 8) {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        key[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+        __builtin_amdgcn_sched_barrier(0);     // one after another: interleaved they take twice the registers
+      }
+    } else {
+      double z = 0.0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        key[i] = exp((double)x[i] - (double)shift);
+        z += key[i];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      z = rt_sum<L>(z);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        key[i] = key[i] / z;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  } else {
+    // within 2^-20 + 2^-22 |key| of the fp64 keys: the hardware's exponential and reciprocal, 2^-22 each
+    // of a score that is at most 1, and |x| 2^-23 of the exponent, which |x| e^-|x| < 0.37 bounds
+    constexpr float kLog2e = 1.4426950408889634f;
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -kLog2e));
+    } else {
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        key[i] = __builtin_amdgcn_exp2f((x[i] - shift) * kLog2e);
+        z += key[i];
+      }
+      z = __builtin_amdgcn_rcpf(rt_sum<L>(z));
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = key[i] * z;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] += (Key)bias[i];
+    if (!(x[i] > -__builtin_inff() && key[i] > rt_neg_inf<Key>())) key[i] = rt_neg_inf<Key>();
+  }
+}
+
+// Keys closer than this may be in the other order in exact arithmetic: twice their error, and the low bits
+// that rt_take32 puts an index in.
+__device__ __forceinline__ float rt_margin(float key) { return 0x1p-19f + 0x1p-18f * fabsf(key); }
+
+// The best `keep` groups stay, the keys of the others become -inf.  Groups of whole runs of lanes: two
+// largest keys in the lane, then across the run.  Any groups: one after another over all lanes.
+// Returns whether the last kept and the first dropped group are within the margin.
+template <typename Key, int L, int V>
+__device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int group_lanes, int e0, int per, int sub, int lane,
+                                               Key (&key)[V]) {
+  Key mine = rt_neg_inf<Key>();                           // lane g of the token: the score of group g
+  if (group_lanes) {
+    Key m1 = rt_neg_inf<Key>(), m2 = m1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const Key lo = key[i] > m1 ? m1 : key[i];
+      m2 = lo > m2 ? lo : m2;
+      m1 = key[i] > m1 ? key[i] : m1;
+    }
+    for (int o = 1; o < group_lanes; o <<= 1) {
+      const Key n1 = __shfl_xor(m1, o, 64), n2 = __shfl_xor(m2, o, 64);
+      const Key lo = n1 > m1 ? m1 : n1, hi2 = n2 > m2 ? n2 : m2;
+      m2 = lo > hi2 ? lo : hi2;
+      m1 = n1 > m1 ? n1 : m1;
+    }
+    if (a.group_top == 2) m1 = m1 + m2;
+    mine = __shfl(m1, lane / L * L + (sub < a.groups ? sub : 0) * group_lanes, 64);
+  } else {
+    for (int g = 0; g < a.groups; ++g) {
+      Key m1 = rt_neg_inf<Key>();
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if ((e0 + i) / per == g) m1 = key[i] > m1 ? key[i] : m1;
+      m1 = rt_max<L>(m1);
+      if (a.group_top == 2) {
+        int at = 1 << 30;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if ((e0 + i) / per == g && key[i] == m1) at = e0 + i;
+        at = rt_min<L>(at);
+        Key m2 = rt_neg_inf<Key>();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if ((e0 + i) / per == g && e0 + i != at && key[i] > m2) m2 = key[i];
+        m2 = rt_max<L>(m2);
+        m1 = m1 + m2;
+      }
+      if (sub == g) mine = m1;
+    }
+  }
+  int rank = 0;
+  for (int h = 0; h < a.groups; ++h) {
+    const Key other = __shfl(mine, lane / L * L + h, 64);
+    rank += (other > mine || (other == mine && h < sub)) ? 1 : 0;
+  }
+  const bool in = sub < a.groups;
+  const uint64_t kept = __builtin_amdgcn_ballot_w64(in && rank < a.keep) >> (lane / L * L);
+  bool close = false;
+  if constexpr (sizeof(Key) == 4) {
+    const float least = -rt_max<L>(in && rank < a.keep ? -mine : rt_neg_inf<float>());
+    const float most = rt_max<L>(in && rank >= a.keep ? mine : rt_neg_inf<float>());
+    close = least - most <= 2.f * rt_margin(least);       // -inf - -inf: a tie of nothing, decided by index
+  }
+  if (group_lanes) {
+    const bool stay = (kept >> (sub / group_lanes)) & 1;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!stay) key[i] = rt_neg_inf<Key>();
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!((kept >> ((e0 + i) / per)) & 1)) key[i] = rt_neg_inf<Key>();
+  }
+  return close;
+}
+
+// fp32 keys as whole numbers of the same order, and back.
+__device__ __forceinline__ uint32_t rt_ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float rt_float(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+constexpr uint32_t kNoKey = 0x007FFFFFu;        // rt_ordered(-inf): no eligible expert from here down
+
+// The top_k fp32 keys: every lane sorts its five largest (whole numbers with the place in the low bits, so a
+// maximum brings its index along), and the token's lanes give up their heads, the largest first.  Lane j
+// of the token returns choice j.  Where that cannot be the exact choice, close is set in a lane of the token: a
+// choice without an eligible key, a lane that gave all five, or keys too near each other (kMargin: within
+// rt_margin; kBits: equal but for the low bits; kUnique: bf16 logits, which fit the upper half, never).
+enum { kUnique, kBits, kMargin };
+template <int Kind, int L, int V>
+__device__ __forceinline__ int rt_take32(const RouteKernelArgs& a, int e0, int sub, const float (&key)[V], bool& close) {
+  constexpr int D = 5;
+  uint32_t l[D] = {0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    uint32_t t = rt_ordered(key[i]);
+    t = Kind == kUnique ? (t & 0xFFFF0000u) | (uint32_t)(0xFFFF - (e0 + i)) : (t & ~15u) | (uint32_t)(15 - i);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (d > i) break;
+      const uint32_t hi = max(l[d], t);
+      t = min(l[d], t);
+      l[d] = hi;
+    }
+  }
+  int mine = 0, given = 0;
+  uint32_t last = 0;
+  for (int j = 0; j < a.K + (Kind == kUnique ? 0 : 1); ++j) {
+    const uint32_t m = rt_reduce<L>(l[0], [](uint32_t x, uint32_t y) { return max(x, y); });
+    if constexpr (Kind != kUnique) {
+      if (j > 0) close |= Kind == kBits ? (last ^ m) < 16u : rt_float(last) - rt_float(m) <= rt_margin(rt_float(last));
+      last = m;
+      if (j == a.K) break;
+    }
+    close |= m <= kNoKey;
+    int at;
+    bool win = l[0] == m;
+    if constexpr (Kind == kUnique) {
+      at = 0xFFFF - (int)(m & 0xFFFFu);
+    } else {
+      at = rt_min<L>(win ? e0 + 15 - (int)(m & 15u) : 1 << 30);
+      win = (uint32_t)(at - e0) < (uint32_t)V;
+    }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) l[d] = win ? l[d + 1] : l[d];
+    l[D - 1] = win ? 0u : l[D - 1];
+    given += win ? 1 : 0;
+    if (sub == j) mine = at;
+  }
+  close |= given >= D;
+  return mine;
+}
+
+// The choice of one token by fp64 keys, taken by the whole wave (V experts a lane): one after another the
+// largest key, then the lowest index that holds it; a taken key becomes NaN, which loses every
+// comparison, as do the places past E.  Lane j returns choice j.
+template <typename TIn, int V, bool ByLogit>
+__device__ __forceinline__ int rt_choose64(const RouteKernelArgs& a, const TIn* row, int per) {
+  const int lane = threadIdx.x & 63, e0 = lane * V, n = a.E - e0;
+  float x[V], bias[V], top = -__builtin_inff();
+  rt_load_row<TIn, V>(row + e0, n, false, x);
+  double key[V];
+  if constexpr (ByLogit) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = x[i] == x[i] ? (double)x[i] : -__builtin_inf();
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      bias[i] = a.bias && i < n ? a.bias[e0 + i] : 0.f;
+      top = __builtin_fmaxf(top, x[i]);
+    }
+    top = rt_max<64>(top);
+    rt_keys<double, 64, V>(a, x, bias, top == -__builtin_inff() ? 0.f : top, key);
+  }
+  if (a.groups > 1) rt_keep_groups<double, 64, V>(a, a.group_lanes ? per / V : 0, e0, per, lane, lane, key);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i >= n) key[i] = __builtin_nan("");
+  int mine = 0;
+  for (int j = 0; j < a.K; ++j) {
+    double m = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = __builtin_fmax(m, key[i]);
+    m = rt_max<64>(m);
+    int at = 1 << 30;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) at = key[i] == m ? e0 + i : at;
+    at = rt_min<64>(at);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i == at) key[i] = __builtin_nan("");
+    if (lane == j) mine = at;
+  }
+  return mine;
 }
 
 // L lanes of a wave hold a token's row, V consecutive experts each (L V >= E, L >= top_k, L >= groups).
-// The top_k keys are taken one after another: the largest of the token's lanes, then the lowest index
-// that holds it; a taken key becomes NaN, which loses every comparison, as do the places past E.
-template <typename TIn, int L, int V, bool KEY64>
+template <typename TIn, int L, int V, bool ByLogit>
 __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteKernelArgs a) {
-  using Key = typename std::conditional<KEY64, double, float>::type;
   extern __shared__ __attribute__((aligned(16))) char rt_lds[];
   int32_t* base = reinterpret_cast<int32_t*>(rt_lds);
   int32_t* scratch = base + a.E;
   int32_t* hist = scratch + 16;
+  int32_t* sel = hist + 1024;                              // the choice, for a call of one workgroup
   uint16_t* wcnt = reinterpret_cast<uint16_t*>(hist + 2048);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
   const int sub = lane % L;
+  float* lbias = reinterpret_cast<float*>(wcnt);           // L V values; the waves' counts come after the choice
   for (int e = tid; e < a.E; e += blockDim.x) hist[e] = 0;
+  if (tid == 0) scratch[15] = nw;
+  if constexpr (!ByLogit)
+    for (int e = tid; e < L * V; e += blockDim.x) lbias[e] = a.bias && e < a.E ? a.bias[e] : 0.f;
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
   const int e0 = sub * V;
-  const int per = a.E / a.groups;
+  const int groups_per = a.E / a.groups;
   constexpr int TW = 64 / L;
   const TIn* logits = reinterpret_cast<const TIn*>(a.logits);
-  for (int64_t tb = c0 + wave * TW; tb < c1; tb += nw * TW) {
+  // the waves draw their next tokens from a counter (scratch[15], which nothing else uses before the scan):
+  // one that has an fp64 choice to make, with code not in the instruction cache, leaves the rest to the others
+  for (int64_t tb = c0 + wave * TW; tb < c1;) {
     const int64_t t = min(tb + lane / L, c1 - 1);       // lanes past the chunk repeat its last token, unwritten
     const bool act = tb + lane / L < c1;
+    int per = groups_per;
+    asm volatile("" : "+v"(per));      // else a quotient per place would be kept for the whole loop, and spilled
     float x[V];
     rt_load_row<TIn, V>(logits + t * a.ld + e0, a.E - e0, a.vec != 0, x);
-    bool odd = false;                                     // a NaN or +inf logit: the softmax is NaN
-    float top = -__builtin_inff();
+    bool row_odd = false;                                 // a NaN or +inf logit: the softmax is NaN
+    float shift = 0.f;
+    if (!a.sigmoid) {
+      bool odd = false;
+      float top = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      odd |= (e0 + i < a.E) && !(x[i] < __builtin_inff());
-      top = __builtin_fmaxf(top, x[i]);
-    }
-    top = rt_max<L>(top);
-    const bool row_odd = ((__builtin_amdgcn_ballot_w64(odd) >> (lane / L * L)) & (~0ull >> (64 - L))) != 0;
-    const float shift = top == -__builtin_inff() ? 0.f : top;
-    Key key[V];
-    if constexpr (KEY64) {
-      double z = 0.0;
-      if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = 1.0 / (1.0 + exp(-(double)x[i]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          key[i] = exp((double)x[i] - (double)shift);
-          if (e0 + i < a.E) z += key[i];
-        }
-        z = rt_sum<L>(z);
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = key[i] / z;
+      for (int i = 0; i < V; ++i) {
+        odd |= !(x[i] < __builtin_inff());
+        top = x[i] > top ? x[i] : top;
       }
+      top = rt_max<L>(top);
+      row_odd = ((__builtin_amdgcn_ballot_w64(odd) >> (lane / L * L)) & (~0ull >> (64 - L))) != 0;
+      shift = top == -__builtin_inff() ? 0.f : top;
+    }
+    float z = 0.f;                                        // the softmax's sum, where the weights need it
+    if (!a.sigmoid && !a.renorm) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e0 + i < a.E && a.bias) key[i] += (double)a.bias[e0 + i];
+      for (int i = 0; i < V; ++i) z += expf(x[i] - shift);
+      z = rt_sum<L>(z);
+    }
+    // fp32 keys, and fp64 ones for the tokens in which they may not decide as exact ones
+    float key[V];
+    bool close = false;
+    if constexpr (ByLogit) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = x[i] == x[i] ? x[i] : -__builtin_inff();
     } else {
+      float bias[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = x[i];
+      for (int i = 0; i < V; ++i) bias[i] = lbias[e0 + i];
+      rt_keys<float, L, V>(a, x, bias, shift, key);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i < a.E && !(x[i] > -__builtin_inff() && key[i] > rt_neg_inf<Key>())) key[i] = rt_neg_inf<Key>();
     if (a.groups > 1) {
-      Key mine = rt_neg_inf<Key>();                       // lane g of the token: the score of group g
-      for (int g = 0; g < a.groups; ++g) {
-        Key m1 = (Key)__builtin_nan("");
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if ((e0 + i) / per == g) m1 = key[i] > m1 || m1 != m1 ? key[i] : m1;
-        m1 = rt_max<L>(m1);
-        if (a.group_top == 2) {
-          int at = 1 << 30;
-#pragma unroll
-          for (int i = V - 1; i >= 0; --i)
-            if ((e0 + i) / per == g && key[i] == m1) at = e0 + i;
-          at = rt_min<L>(at);
-          Key m2 = rt_neg_inf<Key>();
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if ((e0 + i) / per == g && e0 + i != at && key[i] > m2) m2 = key[i];
-          m2 = rt_max<L>(m2);
-          m1 = m1 + m2;
-        }
-        if (sub == g) mine = m1;
-      }
-      int rank = 0;
-      for (int h = 0; h < a.groups; ++h) {
-        const Key other = __shfl(mine, lane / L * L + h, 64);
-        rank += (other > mine || (other == mine && h < sub)) ? 1 : 0;
-      }
-      const uint64_t kept = __builtin_amdgcn_ballot_w64(sub < a.groups && rank < a.keep) >> (lane / L * L);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e0 + i < a.E && !((kept >> ((e0 + i) / per)) & 1)) key[i] = rt_neg_inf<Key>();
+      const bool near = rt_keep_groups<float, L, V>(a, a.group_lanes, e0, per, sub, lane, key);
+      close = !ByLogit && near;
     }
-    int mine = 0;                                           // lane j of the token: choice j
-    for (int j = 0; j < a.K; ++j) {
-      Key m = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) {
-        if constexpr (KEY64) m = __builtin_fmax(m, key[i]);
-        else m = __builtin_fmaxf(m, key[i]);
-      }
-      m = rt_max<L>(m);
-      int at = 1 << 30;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i) at = key[i] == m ? e0 + i : at;
-      at = rt_min<L>(at);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e0 + i == at) key[i] = (Key)__builtin_nan("");
-      if (sub == j) mine = at;
+    constexpr int kKind = !ByLogit ? kMargin : sizeof(TIn) == 2 ? kUnique : kBits;
+    int mine = rt_take32<kKind, L, V>(a, e0, sub, key, close);     // lane j of the token: choice j
+    uint64_t left = __builtin_amdgcn_ballot_w64(close);
+    while (left) {
+      const int tok = __builtin_ctzll(left) / L;
+      left &= ~((~0ull >> (64 - L)) << (tok * L));
+      const int theirs = rt_choose64<TIn, (L * V + 63) / 64, ByLogit>(a, logits + min(tb + tok, c1 - 1) * a.ld, per);
+      const int got = __shfl(theirs, sub, 64);
+      if (lane / L == tok) mine = got;
     }
     // weights: lane j < top_k of the token
     const bool live = sub < a.K;
@@ -289,21 +509,21 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteKernelArgs a) {
       const float sum = rt_sum<L>(w);
       w = row_odd ? __builtin_nanf("") : sum == 0.f ? 0.f : w / sum;
     } else {
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) z += e0 + i < a.E ? expf(x[i] - shift) : 0.f;
-      z = rt_sum<L>(z);
       w = row_odd ? __builtin_nanf("") : z == 0.f ? 0.f : expf(xj - shift) / z;
     }
     if (act && live) {
       a.ids[t * a.K + sub] = mine;
+      if (a.nchunk == 1) sel[t * a.K + sub] = mine;
       a.weights[t * a.K + sub] = w * a.scale;
       atomicAdd(&hist[mine], 1);                            // whole numbers: any order gives the same
     }
+    int next = 0;
+    if (lane == 0) next = atomicAdd(&scratch[15], 1);
+    tb = c0 + (int64_t)__builtin_amdgcn_readfirstlane(next) * TW;
   }
   __syncthreads();
   if (a.nchunk > 1) {
-    for (int e = tid; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
+    for (int e = tid; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * rt_hist_ld(a.E) + e] = hist[e];
     return;
   }
   // one chunk: the order too, in this launch
@@ -311,9 +531,8 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteKernelArgs a) {
   const int first = rt_scan(n, scratch);
   if (tid < a.E) { base[tid] = first; a.offsets[tid] = first; }
   if (tid == 0) a.offsets[a.E] = a.T * a.K;
-  __threadfence_block();
   __syncthreads();
-  rt_place(a.ids, 0, a.T * a.K, a.E, base, wcnt, a.slot_row, a.row_slot);
+  rt_place(sel, tid < a.T * a.K ? sel[tid] : 0, 0, a.T * a.K, a.E, base, wcnt, a.slot_row, a.row_slot);
 }
 
 // The order of the slots: block b places chunk b's.  Every block adds up the chunks' counts (at most
@@ -326,24 +545,35 @@ __global__ __launch_bounds__(kRtThreads) void route_place_kernel(RouteKernelArgs
   int32_t* part = scratch + 16;
   uint16_t* wcnt = reinterpret_cast<uint16_t*>(part + 2048);
   const int tid = threadIdx.x, b = blockIdx.x;
-  int epad = 1;
-  while (epad < a.E) epad <<= 1;
-  const int np = kRtThreads / epad, e = tid & (epad - 1), p = tid / epad;
-  int before = 0, total = 0;
-  if (e < a.E) {
-#pragma unroll 8
-    for (int c = p; c < a.nchunk; c += np) {
-      const int h = a.hist[(int64_t)c * a.E + e];
-      total += h;
-      before += c < b ? h : 0;
-    }
-  }
-  part[tid] = total;
-  part[1024 + tid] = before;
+  const int64_t t0 = (int64_t)b * a.chunk, t1 = min(a.T, t0 + a.chunk);
+  const int64_t s0 = t0 * a.K, s1 = t1 * a.K;
+  const int e_first = s0 + tid < s1 ? a.ids[s0 + tid] : 0;     // on its way while the counts are added
+  int32_t *sum = part, *sum_before = part + 1024;
+  for (int e = tid; e < a.E; e += kRtThreads) sum[e] = sum_before[e] = 0;
   __syncthreads();
-  total = before = 0;
-  if (tid < a.E)
-    for (int q = 0; q < np; ++q) { total += part[q * epad + tid]; before += part[1024 + q * epad + tid]; }
+  // four experts a thread, the chunks dealt to the threads that share them; whole numbers, so the
+  // atomics' order changes nothing
+  int quads = 1;
+  while (quads * 4 < a.E) quads <<= 1;
+  const int np = kRtThreads / quads, q = tid & (quads - 1), p = tid / quads;
+  int4 total4 = make_int4(0, 0, 0, 0), before4 = total4;
+  if (q * 4 < a.E) {
+#pragma unroll 16
+    for (int c = p; c < a.nchunk; c += np) {
+      const int4 h = *reinterpret_cast<const int4*>(a.hist + (int64_t)c * rt_hist_ld(a.E) + q * 4);
+      total4.x += h.x; total4.y += h.y; total4.z += h.z; total4.w += h.w;
+      if (c < b) { before4.x += h.x; before4.y += h.y; before4.z += h.z; before4.w += h.w; }
+    }
+    const int t4[4] = {total4.x, total4.y, total4.z, total4.w}, b4[4] = {before4.x, before4.y, before4.z, before4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (q * 4 + i < a.E) {
+        atomicAdd(&sum[q * 4 + i], t4[i]);
+        atomicAdd(&sum_before[q * 4 + i], b4[i]);
+      }
+  }
+  __syncthreads();
+  const int total = tid < a.E ? sum[tid] : 0, before = tid < a.E ? sum_before[tid] : 0;
   const int first = rt_scan(total, scratch);
   if (tid < a.E) {
     base[tid] = first + before;
@@ -351,8 +581,7 @@ __global__ __launch_bounds__(kRtThreads) void route_place_kernel(RouteKernelArgs
   }
   if (b == 0 && tid == 0) a.offsets[a.E] = a.T * a.K;
   __syncthreads();
-  const int64_t t0 = (int64_t)b * a.chunk, t1 = min(a.T, t0 + a.chunk);
-  rt_place(a.ids, t0 * a.K, t1 * a.K, a.E, base, wcnt, a.slot_row, a.row_slot);
+  rt_place(a.ids, e_first, s0, s1, a.E, base, wcnt, a.slot_row, a.row_slot);
 }
 
 // ------------------------------------------------------------ gradient ----
@@ -494,7 +723,7 @@ void rt_dispatch(int L, int E, F&& f) {
 }
 
 // One launch, one workgroup, up to this many slots and two passes over the tokens.
-bool rt_single(int64_t T, int K, int L) { return T * K <= 1024 && T * L <= 2 * kRtThreads; }
+bool rt_single(int64_t T, int E, int K, int L) { return E <= kRtThreads && T * K <= 1024 && T * L <= 2 * kRtThreads; }
 
 bool rt_rows_aligned(const void* p, int64_t ld, int esize) {
   return ((uintptr_t)p & 15u) == 0 && (ld * esize) % 16 == 0;
@@ -503,7 +732,7 @@ bool rt_rows_aligned(const void* p, int64_t ld, int esize) {
 }  // namespace
 
 size_t route_workspace(int64_t T, int E) {
-  return align_up((size_t)std::min<int64_t>(std::max<int64_t>(T, 1), kRtMaxChunks) * E * 4, 256);
+  return align_up((size_t)std::min<int64_t>(std::max<int64_t>(T, 1), kRtMaxChunks) * rt_hist_ld(E) * 4, 256);
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
@@ -515,25 +744,32 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
   const int esize = a.dtype == S3R_BF16 ? 2 : 4;
   k.vec = rt_rows_aligned(a.logits, a.ld, esize) ? 1 : 0;
   const int L = rt_lanes(a.E, a.K, a.groups);
-  const bool key64 = a.bias != nullptr || (a.groups > 1 && a.group_top == 2);
-  if (rt_single(a.T, a.K, L)) {
+  // by the scores only where their values, not their order alone, decide
+  const int per = a.E / a.groups, V = a.E > 8 * L ? 16 : 8, run = per / V;
+  if (a.groups > 1 && per % V == 0 && (run & (run - 1)) == 0) k.group_lanes = run;
+  const bool by_score = a.bias != nullptr || (a.groups > 1 && a.group_top == 2);
+  if (rt_single(a.T, a.E, a.K, L)) {
     k.nchunk = 1;
     k.chunk = std::max<int64_t>(a.T, 1);
   } else {
     k.chunk = (a.T + kRtMaxChunks - 1) / kRtMaxChunks;
     k.nchunk = (int)((a.T + k.chunk - 1) / k.chunk);
   }
+  // threads for the chunk's tokens; one workgroup's own order needs one per slot and expert, too
+  int64_t threads = std::max<int64_t>(k.chunk * L, 64);
+  if (k.nchunk == 1) threads = std::max<int64_t>({threads, k.chunk * a.K, a.E});
+  threads = std::min<int64_t>((threads + 63) / 64 * 64, kRtThreads);
   const size_t lds = rt_lds_bytes(a.E);
   rt_dispatch(L, a.E, [&](auto l, auto v) {
     constexpr int LL = decltype(l)::value, VV = decltype(v)::value;
-    const dim3 grid((unsigned)k.nchunk), block(kRtThreads);
-    if (a.dtype == S3R_BF16) {
-      if (key64) hipLaunchKernelGGL((route_kernel<uint16_t, LL, VV, true>), grid, block, lds, st, k);
-      else hipLaunchKernelGGL((route_kernel<uint16_t, LL, VV, false>), grid, block, lds, st, k);
-    } else {
-      if (key64) hipLaunchKernelGGL((route_kernel<float, LL, VV, true>), grid, block, lds, st, k);
-      else hipLaunchKernelGGL((route_kernel<float, LL, VV, false>), grid, block, lds, st, k);
-    }
+    const dim3 grid((unsigned)k.nchunk), block((unsigned)threads);
+    auto go = [&](auto by_logit) {
+      constexpr bool B = decltype(by_logit)::value;
+      if (a.dtype == S3R_BF16) hipLaunchKernelGGL((route_kernel<uint16_t, LL, VV, B>), grid, block, lds, st, k);
+      else hipLaunchKernelGGL((route_kernel<float, LL, VV, B>), grid, block, lds, st, k);
+    };
+    if (by_score) go(std::false_type{});
+    else go(std::true_type{});
   });
   if (k.nchunk > 1)
     hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)k.nchunk), dim3(kRtThreads), lds, st, k);
