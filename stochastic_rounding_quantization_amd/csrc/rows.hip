@@ -10,7 +10,8 @@
 //   backward   dY[slot_row[t,j]] = w[t,j] dy[t];  dw[t,j] = <dy[t], Y[slot_row[t,j]]>
 // fp32 sums in the order of j (of the columns within a lane, then across lanes),
 // one rounding to the output's type.  All three move whole rows between tokens'
-// order and experts' order and are bound by HBM.
+// order and experts' order and are bound by HBM: a token's side is read or
+// written once, whatever k is, and the rows of one token are in flight together.
 #include "s3r_internal.h"
 
 namespace s3r {
@@ -20,14 +21,17 @@ constexpr int kRowThreads = 256;
 
 // Chunks of W elements: 16 bytes of the row type (8 bf16, 4 f32), or one element for rows that are not
 // 16-byte aligned.
-template <typename T, int W>
+template <typename T, int W, bool NT = false>
 struct Chunk {
+  // NT: the nontemporal hint, where it measured faster.  16384 tokens, 2 rows each, 2048 bf16 columns, us:
+  //   combine:  none 41.3, row loads 37.5, stores 39.4, both 38.3        (202 MB: 5.4 TB/s, a large copy's rate)
+  //   backward: none 75.1, row loads 74.0, row stores 78.8, both 67.0, both and dy 76.0      (336 MB: 5.0 TB/s)
   static __device__ __forceinline__ void load(const T* p, float (&v)[W]) {
     if constexpr (W == 1) {
       if constexpr (sizeof(T) == 2) v[0] = bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
       else v[0] = *p;
     } else if constexpr (sizeof(T) == 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p);
+      const uint4 w = NT ? ld_stream_u4(p) : *reinterpret_cast<const uint4*>(p);
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -35,7 +39,7 @@ struct Chunk {
         v[2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
       }
     } else {
-      const float4 w = *reinterpret_cast<const float4*>(p);
+      const float4 w = NT ? ld_stream_f4(p) : *reinterpret_cast<const float4*>(p);
       v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
     }
   }
@@ -50,9 +54,11 @@ struct Chunk {
         w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(q, bf2));
       }
       if constexpr (W == 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+      else if constexpr (NT) __builtin_nontemporal_store((v4u32{w[0], w[1], w[2], w[3]}), reinterpret_cast<v4u32*>(p));
       else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       if constexpr (W == 1) *p = v[0];
+      else if constexpr (NT) __builtin_nontemporal_store((v4f32{v[0], v[1], v[2], v[3]}), reinterpret_cast<v4f32*>(p));
       else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     }
   }
@@ -87,41 +93,64 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowMoveArgs a, int
     if (r < 0 || r >= a.R) continue;
     const float w = a.weights ? a.weights[t * a.K + j] : 1.f;
     float v[W];
-    Chunk<T, W>::load((const T*)a.in + r * a.ld_in + c, v);
+    Chunk<T, W, true>::load((const T*)a.in + r * a.ld_in + c, v);
 #pragma unroll
     for (int q = 0; q < W; ++q) s[q] = fmaf(w, v[q], s[q]);
   }
   Chunk<T, W>::store((T*)a.out + t * a.ld_out + c, s);
 }
 
-// One wave per token: its dy chunk is read once for every choice; the dot products are lane sums joined
-// across the wave.
+// One wave per token and J of its choices: its dy chunk is read once for them; the dot products are lane
+// sums joined across the wave.
+template <typename T, int W, int J>
+__device__ __forceinline__ void combine_backward_choices(const RowMoveArgs& a, int64_t t, int j0, int lane) {
+  int64_t r[J];
+  float w[J], dot[J];
+  bool ok[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    r[j] = a.slot_row[t * a.K + j0 + j];
+    ok[j] = r[j] >= 0 && r[j] < a.R;
+    w[j] = a.weights[t * a.K + j0 + j];
+    dot[j] = 0.f;
+  }
+  for (int64_t c = (int64_t)lane * W; c < a.D; c += 64 * W) {
+    float g[W], y[J][W];
+    Chunk<T, W>::load((const T*)a.dy + t * a.ld_dy + c, g);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (ok[j]) Chunk<T, W, true>::load((const T*)a.in + r[j] * a.ld_in + c, y[j]);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (!ok[j]) continue;
+      float o[W];
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        dot[j] = fmaf(g[q], y[j][q], dot[j]);
+        o[q] = g[q] * w[j];
+      }
+      Chunk<T, W, true>::store((T*)a.out + r[j] * a.ld_out + c, o);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const float d = wave_sum(dot[j]);
+    if (lane == 0) a.dweights[t * a.K + j0 + j] = d;
+  }
+}
+
 template <typename T, int W>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowMoveArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
+  const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.T) return;
-  for (int j = 0; j < a.K; ++j) {
-    const int64_t r = a.slot_row[t * a.K + j];
-    const bool ok = r >= 0 && r < a.R;
-    const float w = a.weights[t * a.K + j];
-    float dot = 0.f;
-    if (ok) {
-      for (int64_t c = (int64_t)lane * W; c < a.D; c += 64 * W) {
-        float g[W], y[W];
-        Chunk<T, W>::load((const T*)a.dy + t * a.ld_dy + c, g);
-        Chunk<T, W>::load((const T*)a.in + r * a.ld_in + c, y);
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-          dot = fmaf(g[q], y[q], dot);
-          g[q] *= w;
-        }
-        Chunk<T, W>::store((T*)a.out + r * a.ld_out + c, g);
-      }
-    }
-    dot = wave_sum(dot);
-    if (lane == 0) a.dweights[t * a.K + j] = dot;
+  int j = 0;
+  for (; j + 4 <= a.K; j += 4) combine_backward_choices<T, W, 4>(a, t, j, lane);
+  if (j + 2 <= a.K) {
+    combine_backward_choices<T, W, 2>(a, t, j, lane);
+    j += 2;
   }
+  if (j < a.K) combine_backward_choices<T, W, 1>(a, t, j, lane);
 }
 
 bool rows_vec(const void* p, int64_t ld, int64_t D, int esize) {
