@@ -1,0 +1,86 @@
+"""The mixture-of-experts layer (moe.py): its calls together, on an MI355X.
+
+The forward pass against float64 on the values that the 4-bit codes stand for; the gradients, which pass
+two quantizations, by their direction against the unquantized layer's.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx, route
+from stochastic_rounding_quantization_amd import moe, s3r
+from tests._gpu import DEV, host
+
+pytestmark = pytest.mark.gpu
+T, E, K, D, F = 150, 6, 2, 256, 192
+
+
+def normal(g, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g, device=DEV) * std).to(torch.bfloat16)
+
+
+@pytest.fixture(scope="module")
+def step():
+    g = torch.Generator(DEV).manual_seed(1)
+    layer = moe.MoeLayer(normal(g, E, 2 * F, D, std=0.1), normal(g, E, D, F, std=0.1), K)
+    x, logits, dy = normal(g, T, D), normal(g, T, E), normal(g, T, D, std=1e-2)
+    y, saved = layer.forward(x, logits)
+    grads = layer.backward(saved, dy)
+    torch.cuda.synchronize()
+    return layer, x, logits, dy, y, saved, grads
+
+
+def f(t):
+    return host(t.float())
+
+
+def test_forward(step):
+    layer, x, logits, _, y, saved, _ = step
+    ids = route.choose(f(logits), K)
+    np.testing.assert_array_equal(host(saved.routed.ids), ids)
+    offsets, slot_row, row_slot = route.order(ids, E)
+    xq = mx.rows(f(x))["deq"][row_slot // K]
+    a, rows = f(saved.gate_up), f(saved.rows)
+    for e in range(E):
+        r = slice(offsets[e], offsets[e + 1])
+        w = mx.rows(f(layer.gate_up[e]))["deq"]
+        exp = xq[r] @ w.T
+        assert (np.abs(a[r] - exp) <= 2.0 ** -8 * np.abs(exp) + D * 2.0 ** -23 * (np.abs(xq[r]) @ np.abs(w).T)).all()
+        # the down product from the pre-activations that the layer kept: silu in fp64 may round to the other
+        # neighbour of a code's border, one spacing of the block, so this is a bound on all of them together
+        g, u = a[r, :F].astype(np.float64), a[r, F:].astype(np.float64)
+        h = mx.rows((g / (1 + np.exp(-g)) * u).astype(np.float32))["deq"]
+        exp = h @ mx.rows(f(layer.down[e]))["deq"].T
+        assert np.linalg.norm(rows[r] - exp) <= 2.0 ** -7 * np.linalg.norm(exp)
+    w = route.weights(f(logits), ids)
+    exp, _ = route.combine(rows, slot_row, w)
+    assert (np.abs(f(y) - exp) <= 2.0 ** -8 * np.abs(exp) + 2.0 ** -18 * np.abs(exp).max()).all()
+
+
+def test_gradients_point_the_unquantized_way(step):
+    layer, x, logits, dy, _, saved, grads = step
+    xs, ls, wg, wd = (t.float().detach().requires_grad_() for t in (x, logits, layer.gate_up, layer.down))
+    ids = saved.routed.ids.long()
+    p = torch.softmax(ls, 1).gather(1, ids)
+    p = p / p.sum(1, keepdim=True)
+    y = torch.zeros(T, D, device=DEV)
+    for e in range(E):
+        t, j = torch.where(ids == e)
+        a = xs[t] @ wg[e].t()
+        h = torch.nn.functional.silu(a[:, :F]) * a[:, F:]
+        y = y.index_add(0, t, p[t, j, None] * (h @ wd[e].t()))
+    y.backward(dy.float())
+    for got, exp in zip(grads, (xs.grad, ls.grad, wg.grad, wd.grad)):
+        got = got.float()
+        assert got.shape == exp.shape and torch.isfinite(got).all()
+        cos = torch.nn.functional.cosine_similarity(got.flatten(), exp.flatten(), dim=0)
+        assert cos > 0.95, float(cos)
+
+
+def test_empty_batch_and_one_token(step):
+    layer, x, logits = step[:3]
+    y, _ = layer.forward(x[:1], logits[:1])
+    full = step[4]
+    # one token's rows go another way through the product kernels: the order of fp32 sums may differ, then bf16
+    assert (np.abs(f(y) - f(full[:1])) <= 2.0 ** -6 * np.abs(f(full[:1])).max()).all()
+    assert layer.forward(x[:0], logits[:0])[0].shape == (0, D)
