@@ -17,14 +17,14 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------ rows ----
-// A block of 256 threads takes 16 rows x kMrSteps 128-element steps: 16 lanes per
+// A block of 256 threads takes 16 rows x Steps 128-element steps: 16 lanes per
 // row, 8 elements a lane and step (16 bytes of bf16), so a block of 32 elements
 // is four lanes.  Codes leave as 1 KiB and scales as 64 bytes in one run.  With
 // `up` the element is silu(A) * up in fp32, not rounded in between.
 // The arithmetic is what bounded the first version (28 instructions an element:
 // 35 us for 8192 x 4096 bf16, whose bytes need 15); now two elements convert in
 // one instruction, and the maximum of bf16 runs on packed magnitudes.
-constexpr int kMrThreads = 256, kMrRows = 16, kMrSteps = 4;
+constexpr int kMrThreads = 256, kMrRows = 16;
 
 // 8 consecutive elements of a row as they lie in memory: packed bf16, or fp32.
 template <typename TIn> struct Raw8;
@@ -170,10 +170,10 @@ __device__ __forceinline__ int64_t mr_source(const MxRowsArgs& a, int64_t r) {
   return s < a.a_rows ? s : -1;
 }
 
-template <typename TIn, bool UP, bool Words>
+template <typename TIn, bool UP, bool Words, int Steps>
 __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int ksteps) {
   const int sub = threadIdx.x & 15;
-  const int kblocks = (ksteps + kMrSteps - 1) / kMrSteps;
+  const int kblocks = (ksteps + Steps - 1) / Steps;
   const int rb = blockIdx.x / kblocks;
   const int64_t r = (int64_t)rb * kMrRows + (threadIdx.x >> 4);
   const int64_t g = blockIdx.y;
@@ -182,17 +182,17 @@ __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int k
   const int64_t src = mr_source(a, r);
   const TIn* A = (const TIn*)a.A + g * a.a_stride + (src < 0 ? 0 : src) * a.ld;
   const TIn* U = UP ? (const TIn*)a.up + g * a.a_stride + (src < 0 ? 0 : src) * a.ld : nullptr;
-  const int k0 = (blockIdx.x - rb * kblocks) * kMrSteps;
-  Raw8<TIn> v[kMrSteps], u[UP ? kMrSteps : 1];
+  const int k0 = (blockIdx.x - rb * kblocks) * Steps;
+  Raw8<TIn> v[Steps], u[UP ? Steps : 1];
 #pragma unroll
-  for (int q = 0; q < kMrSteps; ++q) {           // every load before the first conversion
+  for (int q = 0; q < Steps; ++q) {           // every load before the first conversion
     const int64_t c = (int64_t)(k0 + q) * 128 + sub * 8;
     const int64_t n = src >= 0 ? a.K - c : 0;
     v[q] = mr_load8<TIn, Words>(A + c, n);
     if constexpr (UP) u[q] = mr_load8<TIn, Words>(U + c, n);
   }
 #pragma unroll
-  for (int q = 0; q < kMrSteps; ++q) {
+  for (int q = 0; q < Steps; ++q) {
     const int kt = k0 + q;
     if (kt >= ksteps) break;
     uint32_t s, w;
@@ -216,44 +216,67 @@ __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int k
 }
 
 // --------------------------------------------------------------- groups ----
-// The m-tile i of `tile` rows in a grouped product: its group e, its first row and the group's end,
-// found by one wave from the offsets themselves (prefix sums of the groups' tile counts, 64 groups a
-// round).  e = -1 past the last tile.  bad: the offsets are not a non-decreasing sequence from 0 to R.
-struct GroupTile { int e; int64_t r0, r1; bool bad; };
+// Row tiles of a grouped product, found by one wave from the offsets themselves (prefix sums of the groups'
+// tile counts, 64 groups a round).  bad: the offsets are not a non-decreasing sequence from 0 to R.
+struct GroupTile { int e; int64_t r0, r1; };
 __device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
   return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
                    (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
 }
-__device__ __forceinline__ GroupTile find_group_tile(const int64_t* __restrict__ offsets, int64_t G, int64_t R, int i,
-                                                     int tile) {
-  const int lane = threadIdx.x & 63;
-  GroupTile h{-1, 0, 0, false};
-  int carry = 0;                              // tiles of the groups before this round's
-  bool bad = false;
-  for (int64_t g0 = 0; g0 < G; g0 += 64) {
-    const int64_t g = g0 + lane;
-    const bool in = g < G;
-    const int64_t o0 = in ? offsets[g] : 0, o1 = in ? offsets[g + 1] : 0;
-    const bool odd = in && (o1 < o0 || o0 < 0 || o1 > R || (g == 0 && o0 != 0) || (g == G - 1 && o1 != R));
-    bad |= odd;
-    const int n = odd ? 0 : ((int)(o1 - o0) + tile - 1) / tile;
-    int s = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int b = __shfl_up(s, o, 64);
-      if (lane >= o) s += b;
-    }
-    const uint64_t m = __builtin_amdgcn_ballot_w64(carry + s > i && carry + s - n <= i);
-    if (m && h.e < 0) {
-      const int w = __builtin_ctzll(m);
-      h.e = (int)g0 + w;
-      h.r1 = read_lane(o1, w);
-      h.r0 = read_lane(o0, w) + (int64_t)(i - (carry + __builtin_amdgcn_readlane(s - n, w))) * tile;
-    }
-    carry += __builtin_amdgcn_readlane(s, 63);
+// Inclusive sums over the wave by DPP: shifts within the 16-lane rows, then the rows' last lanes.
+__device__ __forceinline__ int wave_prefix(int s) {
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x142, 0xA, 0xF, false);     // row_bcast 15 into rows 1 and 3
+  s += __builtin_amdgcn_update_dpp(0, s, 0x143, 0xC, 0xF, false);     // row_bcast 31 into rows 2 and 3
+  return s;
+}
+// One round: groups g0 .. g0 + 63, one a lane; n its tiles, s the inclusive sums of n.
+struct GroupRound { int64_t o0, o1; int n, s; bool bad; };
+__device__ __forceinline__ GroupRound group_round(const int64_t* __restrict__ offsets, int64_t G, int64_t R, int64_t g0,
+                                                  int tile) {
+  const int64_t g = g0 + (threadIdx.x & 63);
+  const bool in = g < G;
+  GroupRound r;
+  r.o0 = in ? offsets[g] : 0;
+  r.o1 = in ? offsets[g + 1] : 0;
+  r.bad = in && (r.o1 < r.o0 || r.o0 < 0 || r.o1 > R || (g == 0 && r.o0 != 0) || (g == G - 1 && r.o1 != R));
+  r.n = r.bad ? 0 : ((int)(r.o1 - r.o0) + tile - 1) / tile;
+  r.s = wave_prefix(r.n);
+  return r;
+}
+// All tiles of all groups; first: round 0, to be kept.
+__device__ __forceinline__ int group_total(const int64_t* offsets, int64_t G, int64_t R, int tile, GroupRound& first,
+                                           bool& bad) {
+  first = group_round(offsets, G, R, 0, tile);
+  int total = __builtin_amdgcn_readlane(first.s, 63);
+  bool b = first.bad;
+  for (int64_t g0 = 64; g0 < G; g0 += 64) {
+    const GroupRound r = group_round(offsets, G, R, g0, tile);
+    total += __builtin_amdgcn_readlane(r.s, 63);
+    b |= r.bad;
   }
-  h.bad = __builtin_amdgcn_ballot_w64(bad) != 0;
-  return h;
+  bad = __builtin_amdgcn_ballot_w64(b) != 0;
+  return total;
+}
+// Tile i, 0 <= i < total, of valid offsets: its group, its first row and the group's end.
+__device__ __forceinline__ GroupTile group_tile(const int64_t* offsets, int64_t G, int64_t R, int tile,
+                                                const GroupRound& first, int i) {
+  GroupRound r = first;
+  int carry = 0;                              // tiles of the groups before this round's
+  for (int64_t g0 = 0;;) {
+    const uint64_t m = __builtin_amdgcn_ballot_w64(carry + r.s > i);
+    if (m || g0 + 64 >= G) {
+      const int w = m ? __builtin_ctzll(m) : 0;
+      const int before = carry + __builtin_amdgcn_readlane(r.s - r.n, w);
+      return GroupTile{(int)g0 + w, read_lane(r.o0, w) + (int64_t)(i - before) * tile, read_lane(r.o1, w)};
+    }
+    carry += __builtin_amdgcn_readlane(r.s, 63);
+    g0 += 64;
+    r = group_round(offsets, G, R, g0, tile);
+  }
 }
 
 // -------------------------------------------------------------- products ----
@@ -303,13 +326,16 @@ __global__ __launch_bounds__(kSkThreads) void mx_few_rows_kernel(MxProdK p, MxRo
   const uint8_t *B = p.B, *Bs = p.Bs;
   const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
   if (p.G) {
-    const GroupTile h = find_group_tile(p.offsets, p.G, p.M, mt, 16 * MI);
-    if (h.bad) {
+    GroupRound first;
+    bool bad;
+    const int total = group_total(p.offsets, p.G, p.M, 16 * MI, first, bad);
+    if (bad) {
       if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_BAD_GROUPS);
       return;
     }
+    if (mt >= total) return;
+    const GroupTile h = group_tile(p.offsets, p.G, p.M, 16 * MI, first, mt);
     const int e = __builtin_amdgcn_readfirstlane(h.e);
-    if (e < 0) return;
     m0 = h.r0;
     m1 = min(h.r1, m0 + 16 * MI);
     B += e * p.b_stride;
@@ -696,9 +722,24 @@ __device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t
 
 template <typename T, typename TOut>
 __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void mx_tile_kernel(MxProdK p, int tiles_m, int vec) {
+  // A contiguous range of tiles per XCD (workgroups go to the 8 XCDs in turn).  Grouped: of the tiles that the
+  // groups have, not of the grid's bound on them, whose surplus would all be the last XCD's.
   int bid = blockIdx.x;
-  const int nblocks = tiles_m * p.tiles_n;
-  if (nblocks % 8 == 0) bid = (bid % 8) * (nblocks / 8) + bid / 8;   // a contiguous range of tiles per XCD
+  GroupRound first;
+  if (p.G) {
+    bool bad;
+    tiles_m = group_total(p.offsets, p.G, p.M, T::BM, first, bad);
+    if (bad) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_BAD_GROUPS);
+      return;
+    }
+    const int nblocks = tiles_m * p.tiles_n, per = (nblocks + 7) / 8;
+    bid = (blockIdx.x % 8) * per + blockIdx.x / 8;
+    if ((int)blockIdx.x / 8 >= per || bid >= nblocks) return;
+  } else {
+    const int nblocks = tiles_m * p.tiles_n;
+    if (nblocks % 8 == 0) bid = (bid % 8) * (nblocks / 8) + bid / 8;
+  }
   const int group = 8 * p.tiles_n;
   const int first_m = (bid / group) * 8;
   const int gsz = min(tiles_m - first_m, 8);
@@ -707,17 +748,11 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void mx_tile_kernel(Mx
   const int64_t n0 = (int64_t)tn * T::BN;
   const uint8_t *B = p.B, *Bs = p.Bs;
   if (p.G) {
-    const GroupTile h = find_group_tile(p.offsets, p.G, p.M, tm, T::BM);
-    if (h.bad) {
-      if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_BAD_GROUPS);
-      return;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(h.e);
-    if (e < 0) return;
+    const GroupTile h = group_tile(p.offsets, p.G, p.M, T::BM, first, tm);
     m0 = h.r0;
     m1 = h.r1;
-    B += e * p.b_stride;
-    Bs += e * p.bs_stride;
+    B += h.e * p.b_stride;
+    Bs += h.e * p.bs_stride;
   }
   TileSrc<T> src;
   src.nk = p.ksteps;
@@ -782,26 +817,30 @@ bool mr_words(const MxRowsArgs& a) {       // rows in whole 16-byte words
          (a.a_stride * esize) % 16 == 0 && a.K % 8 == 0;
 }
 
-template <typename TIn>
-void run_rows(const MxRowsArgs& a, dim3 grid, int ksteps, hipStream_t st) {
-  const dim3 block(kMrThreads);
+template <typename TIn, int Steps>
+hipError_t run_rows(const MxRowsArgs& a, hipStream_t st) {
+  const int ksteps = (int)((a.K + 127) / 128);
+  const int64_t blocks = (ksteps + Steps - 1) / Steps * ((a.R + kMrRows - 1) / kMrRows);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)a.G), block(kMrThreads);
   const bool words = mr_words(a);
-  if (a.up && words) hipLaunchKernelGGL((mx_rows_kernel<TIn, true, true>), grid, block, 0, st, a, ksteps);
-  else if (a.up) hipLaunchKernelGGL((mx_rows_kernel<TIn, true, false>), grid, block, 0, st, a, ksteps);
-  else if (words) hipLaunchKernelGGL((mx_rows_kernel<TIn, false, true>), grid, block, 0, st, a, ksteps);
-  else hipLaunchKernelGGL((mx_rows_kernel<TIn, false, false>), grid, block, 0, st, a, ksteps);
+  if (a.up && words) hipLaunchKernelGGL((mx_rows_kernel<TIn, true, true, Steps>), grid, block, 0, st, a, ksteps);
+  else if (a.up) hipLaunchKernelGGL((mx_rows_kernel<TIn, true, false, Steps>), grid, block, 0, st, a, ksteps);
+  else if (words) hipLaunchKernelGGL((mx_rows_kernel<TIn, false, true, Steps>), grid, block, 0, st, a, ksteps);
+  else hipLaunchKernelGGL((mx_rows_kernel<TIn, false, false, Steps>), grid, block, 0, st, a, ksteps);
+  return hipGetLastError();
 }
+
+// Steps of a workgroup: 4 keep more bytes in flight, 1 fills the GPU and has less code to fetch where there
+// are few rows.
+constexpr int64_t kMrFill = 2048;
 }  // namespace
 
 hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st) {
   if (a.R == 0 || a.K == 0 || a.G == 0) return hipSuccess;
-  const int ksteps = (int)((a.K + 127) / 128);
-  const int64_t kblocks = (ksteps + kMrSteps - 1) / kMrSteps, blocks = kblocks * ((a.R + kMrRows - 1) / kMrRows);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks, (unsigned)a.G);
-  if (a.dtype == S3R_BF16) run_rows<uint16_t>(a, grid, ksteps, st);
-  else run_rows<float>(a, grid, ksteps, st);
-  return hipGetLastError();
+  const int64_t one = (a.K + 127) / 128 * ((a.R + kMrRows - 1) / kMrRows) * a.G;       // workgroups of one step
+  if (a.dtype == S3R_BF16) return one < kMrFill ? run_rows<uint16_t, 1>(a, st) : run_rows<uint16_t, 4>(a, st);
+  return one < kMrFill ? run_rows<float, 1>(a, st) : run_rows<float, 4>(a, st);
 }
 
 namespace {
@@ -814,6 +853,10 @@ namespace {
 using Tile256 = Tile<4, 2, 2, 4, 3, 2>;        // 256 x 256, 8 waves
 using Tile256x128 = Tile<2, 2, 4, 2, 3, 4>;    // 8 waves, two workgroups per CU
 using Tile128 = Tile<2, 2, 2, 2, 3, 3>;        // 4 waves, three workgroups per CU
+#ifndef GT
+#define GT 2, 2, 2, 2, 3, 3
+#endif
+using GTile = Tile<GT>;
 using Tile128x64 = Tile<2, 1, 2, 2, 6, 2>;
 using Tile64 = Tile<1, 1, 2, 2, 6, 2>;
 
@@ -829,9 +872,10 @@ template <typename T, typename TOut>
 hipError_t run_tiles(const MxProductArgs& a, MxProdK p, hipStream_t st) {
   const int64_t mt = a.G ? a.M / T::BM + std::min(a.G, a.M) : (a.M + T::BM - 1) / T::BM;
   p.tiles_n = (int)((a.N + T::BN - 1) / T::BN);
-  if (mt * p.tiles_n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (mt * p.tiles_n > 0x7FFFFFF0) return hipErrorInvalidConfiguration;
   const int vec = ((uintptr_t)a.out & 15u) == 0 && (a.ld_out * (int64_t)sizeof(TOut)) % 16 == 0;
-  hipLaunchKernelGGL((mx_tile_kernel<T, TOut>), dim3((unsigned)(mt * p.tiles_n)), dim3(T::Threads), 0, st, p, (int)mt, vec);
+  const int64_t blocks = a.G ? (mt * p.tiles_n + 7) / 8 * 8 : mt * p.tiles_n;
+  hipLaunchKernelGGL((mx_tile_kernel<T, TOut>), dim3((unsigned)blocks), dim3(T::Threads), 0, st, p, (int)mt, vec);
   return hipGetLastError();
 }
 }  // namespace
@@ -903,7 +947,7 @@ hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
   if (a.G) {
     const int64_t rows = mean_rows(a);
     if (rows <= kFewGrouped) return run_few_rows<void, true, 1, kFewNJ, 2>(a, MxRowsArgs{}, st);
-    return rows < kTallGrouped ? run_tiles<Tile128>(a, st) : run_tiles<Tile256x128>(a, st);
+    return rows < kTallGrouped ? run_tiles<GTile>(a, st) : run_tiles<Tile256x128>(a, st);
   }
   const int64_t few = (a.M + 15) / 16 * ((a.N + 16 * kFewNJ - 1) / (16 * kFewNJ));
   if (a.M <= 16 || (a.M <= 64 && few <= kFewBlocks)) return run_few_rows<void, true, 1, kFewNJ, 4>(a, MxRowsArgs{}, st);
