@@ -11,6 +11,7 @@ the entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -663,7 +664,7 @@ def s3r_mx_linear_workspace(rows: int, K: int) -> int:
 
 def mx_linear_buffer(rows: int, K: int, device):
     """A workspace for s3r_mx_linear on that many rows."""
-    return _workspace(s3r_mx_linear_workspace(rows, K), device)
+    return _scratch(s3r_mx_linear_workspace(rows, K), device)
 
 
 def s3r_mx_linear(A, w: MxRows, out, *, up=None, offsets=None, index=None, index_div=1, ws=None, flags=None,
@@ -900,6 +901,20 @@ def mx_backward_dw(q: MxQuantized, Xt, Xt_scales, xs=None, stream=None):
 
 
 # ------------------------------------------- routing and expert-row helpers ----
+# With ``stream`` (a raw handle) these allocate on that stream, so that neither their outputs nor a workspace that
+# is freed on return can be handed to work of another stream too early; the inputs have to be ready there.
+
+def _on(stream):
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream))
+
+
+def _scratch(nbytes: int, device):
+    import torch
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
 
 @dataclass
 class Routed:
@@ -920,7 +935,7 @@ def routed_buffers(desc: RouteDesc, device) -> Routed:
     i32 = dict(dtype=torch.int32, device=device)
     return Routed(torch.empty(T, k, **i32), torch.empty(T, k, dtype=torch.float32, device=device),
                   torch.empty(E + 1, dtype=torch.int64, device=device), torch.empty(T, k, **i32),
-                  torch.empty(T * k, **i32), desc, _workspace(s3r_route_workspace(desc), device))
+                  torch.empty(T * k, **i32), desc, _scratch(s3r_route_workspace(desc), device))
 
 
 def route(logits, top_k, *, score=SOFTMAX, bias=None, groups=1, keep=1, group_top=1, renorm=True, scale=1.0,
@@ -928,7 +943,8 @@ def route(logits, top_k, *, score=SOFTMAX, bias=None, groups=1, keep=1, group_to
     """Choose top_k experts for every row of the logits [T x E]."""
     d = route_desc(*logits.shape, top_k, score=score, groups=groups, keep=keep, group_top=group_top, renorm=renorm,
                    scale=scale)
-    r = routed_buffers(d, logits.device)
+    with _on(stream):
+        r = routed_buffers(d, logits.device)
     s3r_route(d, logits, bias, r.ids, r.weights, r.offsets, r.slot_row, r.row_slot, r.ws, stream)
     return r
 
@@ -936,7 +952,8 @@ def route(logits, top_k, *, score=SOFTMAX, bias=None, groups=1, keep=1, group_to
 def route_backward(r: Routed, logits, dweights, stream=None):
     """The logits' gradient from the weights'."""
     import torch
-    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    with _on(stream):
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     s3r_route_backward(r.desc, logits, r.ids, dweights, dlogits, stream)
     return dlogits
 
@@ -944,7 +961,8 @@ def route_backward(r: Routed, logits, dweights, stream=None):
 def dispatch(X, r: Routed, stream=None):
     """The tokens' rows in the experts' order: [T * k x D]."""
     import torch
-    rows = torch.empty(r.row_slot.numel(), X.shape[1], dtype=X.dtype, device=X.device)
+    with _on(stream):
+        rows = torch.empty(r.row_slot.numel(), X.shape[1], dtype=X.dtype, device=X.device)
     s3r_dispatch(X, r.slot_row, rows, stream)
     return rows
 
@@ -952,7 +970,8 @@ def dispatch(X, r: Routed, stream=None):
 def combine(rows, r: Routed, weighted=True, stream=None):
     """The experts' rows summed back into the tokens, weighted (or not: dispatch's gradient)."""
     import torch
-    y = torch.empty(r.ids.shape[0], rows.shape[1], dtype=rows.dtype, device=rows.device)
+    with _on(stream):
+        y = torch.empty(r.ids.shape[0], rows.shape[1], dtype=rows.dtype, device=rows.device)
     s3r_combine(rows, r.slot_row, r.weights if weighted else None, y, stream)
     return y
 
@@ -960,7 +979,9 @@ def combine(rows, r: Routed, weighted=True, stream=None):
 def combine_backward(dy, rows, r: Routed, stream=None):
     """(drows, dweights) of combine(rows, r)."""
     import torch
-    drows, dw = torch.empty_strided(rows.shape, rows.stride(), dtype=rows.dtype, device=rows.device), torch.empty_like(r.weights)
+    with _on(stream):
+        drows = torch.empty_strided(rows.shape, rows.stride(), dtype=rows.dtype, device=rows.device)
+        dw = torch.empty_like(r.weights)
     s3r_combine_backward(dy, rows, r.slot_row, r.weights, drows, dw, stream)
     return drows, dw
 
@@ -968,14 +989,16 @@ def combine_backward(dy, rows, r: Routed, stream=None):
 def mx_rows(A, *, up=None, index=None, index_div=1, flags=None, stream=None) -> MxRows:
     """RTNE MXFP4 of the rows of A ([rows x K], or [groups x rows x K]: weights [N x K] of every expert)."""
     G = 1 if A.dim() == 2 else A.shape[0]
-    out = mx_rows_buffer(A.shape[-2] if index is None else index.numel(), A.shape[-1], A.device, G)
+    with _on(stream):
+        out = mx_rows_buffer(A.shape[-2] if index is None else index.numel(), A.shape[-1], A.device, G)
     s3r_mx_rows(A, out, up, index, index_div, flags, stream)
     return out
 
 
 def mx_product(a: MxRows, w: MxRows, *, offsets=None, out_dtype=None, flags=None, stream=None):
     import torch
-    out = torch.empty(a.rows, w.rows, dtype=out_dtype or torch.float32, device=a.codes.device)
+    with _on(stream):
+        out = torch.empty(a.rows, w.rows, dtype=out_dtype or torch.float32, device=a.codes.device)
     s3r_mx_product(a, w, out, offsets, flags, stream)
     return out
 
@@ -984,7 +1007,8 @@ def mx_linear(A, w: MxRows, *, up=None, offsets=None, index=None, index_div=1, o
     """A's rows in MXFP4 times the weights w (mx_rows): [rows x w.rows], of A's dtype unless out_dtype is given."""
     import torch
     rows = A.shape[0] if index is None else index.numel()
-    out = torch.empty(rows, w.rows, dtype=out_dtype or A.dtype, device=A.device)
-    s3r_mx_linear(A, w, out, up=up, offsets=offsets, index=index, index_div=index_div,
-                  ws=mx_linear_buffer(rows, w.K, A.device), flags=flags, stream=stream)
+    with _on(stream):
+        out = torch.empty(rows, w.rows, dtype=out_dtype or A.dtype, device=A.device)
+        ws = mx_linear_buffer(rows, w.K, A.device)
+    s3r_mx_linear(A, w, out, up=up, offsets=offsets, index=index, index_div=index_div, ws=ws, flags=flags, stream=stream)
     return out

@@ -126,10 +126,41 @@ def test_linear_writes_its_rows_and_columns_only():
 def test_empty_products():
     w = s3r.mx_rows(matrix((20, 64), torch.bfloat16, 9))
     assert s3r.mx_linear(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), w).shape == (0, 20)
-    y = torch.full((3, 20), 7.0, device=DEV)                               # K = 0: an empty sum
     z = s3r.mx_rows_buffer(20, 0, DEV)
-    s3r.s3r_mx_product(s3r.mx_rows_buffer(3, 0, DEV), z, y)
-    assert (y == 0).all()
+    for rows in (3, 24, 100):                                              # K = 0: an empty sum
+        y = torch.full((rows, 20), 7.0, device=DEV)
+        s3r.s3r_mx_product(s3r.mx_rows_buffer(rows, 0, DEV), z, y)
+        assert (y == 0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5, 40, 200])
+def test_non_finite_rows_and_indices_outside(rows):
+    """A non-finite element makes its row NaN, an index outside the source makes its row zero, whichever kernel runs."""
+    A, w = matrix((rows, 300), torch.bfloat16, 3), s3r.mx_rows(matrix((70, 300), torch.bfloat16, 4))
+    idx = torch.arange(rows, dtype=torch.int32, device=DEV)
+    want = s3r.mx_linear(A, w)
+    A[rows // 2, 299] = float("inf")
+    idx[0] = rows if rows > 1 else -1
+    flags = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = s3r.mx_linear(A, w, flags=flags)
+    bad = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    bad[rows // 2] = True
+    assert int(flags) == s3r.FLAG_NONFINITE and got[bad].isnan().all() and torch.equal(got[~bad], want[~bad])
+    got = s3r.mx_linear(A, w, index=idx)
+    assert (got[0] == 0).all() and torch.equal(got[1:][~bad[1:]], want[1:][~bad[1:]])
+
+
+def test_helpers_on_a_stream():
+    A, w = matrix((300, 256), torch.bfloat16, 5), s3r.mx_rows(matrix((200, 256), torch.bfloat16, 6))
+    want = s3r.mx_linear(A, w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(10):                             # the workspaces of these overlap work of the current stream
+        got.append(s3r.mx_linear(A, w, stream=side.cuda_stream))
+        torch.zeros(1 << 20, device=DEV)
+    side.synchronize()
+    assert all(torch.equal(g, want) for g in got)
 
 
 GROUPS = [([0, 1], 64, 96), ([5], 40, 128), ([1, 0, 2, 0, 0, 1], 100, 256), ([0, 0, 33, 16, 17], 70, 300),
