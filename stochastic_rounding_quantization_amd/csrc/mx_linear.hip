@@ -5,6 +5,15 @@
 //
 // The contraction K is padded to whole steps of 128 elements with zero codes, so
 // K, like the rows and the columns, can have any size.
+//
+// What bounds them (MI355X; a large copy moves 5.4 TB/s, the FP4 cores have 10.1 PFLOP/s):
+//   rows       HBM: 8192 x 4096 bf16 16 us, 5.2 TB/s; 32768 rows of 2048 gathered 26 us
+//   few rows   the weights' bytes: 1 x 14336 x 4096 8.3 us, 3.8 TB/s with the launch
+//   tiles      power: 8192 x 14336 x 4096 243 us, 4.0 PFLOP/s (zero operands: 185 us; a tile's epilogue,
+//              235 MB of results in all, is a fifth of it); 64 experts, 32768 x 1408 x 2048 93 us, of which
+//              the weights', rows' and results' 225 MB need 42
+// Rounding the tokens once and gathering their codes in the product's loads instead of gathering in the rounding
+// made the experts' product 126 us (64-byte pieces of 128-byte lines), so the rows are gathered first.
 #include <type_traits>
 
 #include "mx_math.h"
@@ -612,7 +621,8 @@ __device__ __forceinline__ void tile_head(const uint8_t* st, TileHead<T>& h) {
 // Step kt on stage S = kt % NS.  The first half's products cover the reads of the second half's
 // fragments; the barrier in the middle then makes step kt + 1 visible and retires stage S, which takes
 // step kt + NS; the second half's products cover the reads of step kt + 1's head.  So the matrix cores
-// wait for no LDS read, and a load has NS - 1 steps and a half to arrive.
+// wait for no LDS read, and a load has NS - 1 steps and a half to arrive.  (A barrier at the step's start, before
+// its reads: 254 us instead of 243 for 8192 x 14336 x 4096.)
 template <typename T, int S>
 __device__ __forceinline__ void tile_step(const TileSrc<T>& src, int kt, TileHead<T>& h, v16f (&acc)[T::MI][T::NI]) {
   TileFrag<T> f1;
@@ -659,7 +669,8 @@ __device__ __forceinline__ void tile_steps(const TileSrc<T>& src, int kt, TileHe
 }
 
 // The wave's results, 32 rows at a time through its own part of the (now free) ring, so that whole
-// 16-byte words of consecutive columns are stored.
+// 16-byte words of consecutive columns are stored, past the last-level cache (fp32 results of
+// 8192 x 14336 x 4096: 264 us, with plain stores 297).
 template <typename T, typename TOut>
 __device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t m1, int64_t n0, bool vec,
                                            const v16f (&acc)[T::MI][T::NI]) {
@@ -796,6 +807,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void mx_tile_kernel(Mx
   tile_fill<T, 0>(src);
   S3R_WAIT_VM(T::Loads * (T::NS - 1));
   __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
   TileHead<T> head;
   tile_head<T>(ring<T, 0>(), head);
   for (int kt = 0; kt < p.ksteps; kt += T::NS) tile_steps<T, 0>(src, kt, head, acc);
@@ -832,7 +844,7 @@ hipError_t run_rows(const MxRowsArgs& a, hipStream_t st) {
 }
 
 // Steps of a workgroup: 4 keep more bytes in flight, 1 fills the GPU and has less code to fetch where there
-// are few rows.
+// are few rows (333 x 2024 fp32, rows and product: 11.7 us instead of 13.6).
 constexpr int64_t kMrFill = 2048;
 }  // namespace
 
@@ -844,19 +856,9 @@ hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st) {
 }
 
 namespace {
-#ifndef BIGTILE
-#define BIGTILE 4, 2, 2, 4, 3, 2
-#endif
-#ifndef MIDTILE
-#define MIDTILE 2, 2, 4, 2, 3, 4
-#endif
 using Tile256 = Tile<4, 2, 2, 4, 3, 2>;        // 256 x 256, 8 waves
 using Tile256x128 = Tile<2, 2, 4, 2, 3, 4>;    // 8 waves, two workgroups per CU
 using Tile128 = Tile<2, 2, 2, 2, 3, 3>;        // 4 waves, three workgroups per CU
-#ifndef GT
-#define GT 2, 2, 2, 2, 3, 3
-#endif
-using GTile = Tile<GT>;
 using Tile128x64 = Tile<2, 1, 2, 2, 6, 2>;
 using Tile64 = Tile<1, 1, 2, 2, 6, 2>;
 
@@ -947,7 +949,7 @@ hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
   if (a.G) {
     const int64_t rows = mean_rows(a);
     if (rows <= kFewGrouped) return run_few_rows<void, true, 1, kFewNJ, 2>(a, MxRowsArgs{}, st);
-    return rows < kTallGrouped ? run_tiles<GTile>(a, st) : run_tiles<Tile256x128>(a, st);
+    return rows < kTallGrouped ? run_tiles<Tile128>(a, st) : run_tiles<Tile256x128>(a, st);
   }
   const int64_t few = (a.M + 15) / 16 * ((a.N + 16 * kFewNJ - 1) / (16 * kFewNJ));
   if (a.M <= 16 || (a.M <= 64 && few <= kFewBlocks)) return run_few_rows<void, true, 1, kFewNJ, 4>(a, MxRowsArgs{}, st);

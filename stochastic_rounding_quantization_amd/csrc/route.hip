@@ -9,7 +9,14 @@
 //
 // A decision between two keys has to be the one of exact arithmetic as far as
 // 64 bits tell it: without a bias and without sums of keys the logits themselves
-// are compared (the scores are monotone in them), otherwise fp64 keys.
+// are compared (the scores are monotone in them), otherwise fp64 keys.  All keys
+// in fp64 cost 179 us for 65536 tokens x 256 experts (8 groups, top 8); fp32 keys
+// with an error bound, and fp64 for the tokens whose decisions lie within it
+// (0.4 % there), cost 43.
+//
+// 16384 x 64 bf16, top 2: choice 4.6 us, order 6.7, for 2.6 MB: two launches' latency.
+// 65536 x 256 fp32, grouped top 8: choice 43 us (850 vector instructions per four
+// tokens take 31, fp64 choices the rest), order 12; the 75 MB alone would take 14.
 #include <type_traits>
 
 #include "s3r_internal.h"
@@ -307,9 +314,9 @@ __device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int gro
   return close;
 }
 
-// fp32 keys as whole numbers of the same order, and back.
+// fp32 keys as whole numbers of the same order, and back; the two zeros are one number.
 __device__ __forceinline__ uint32_t rt_ordered(float f) {
-  const uint32_t u = __float_as_uint(f);
+  const uint32_t u = __float_as_uint(f + 0.f);
   return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float rt_float(uint32_t u) {

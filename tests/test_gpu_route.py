@@ -64,6 +64,14 @@ def test_ties_go_to_the_lower_index(groups, keep, bias):
     check(torch.zeros(70, 64, device=DEV), 5, bias=b, groups=groups, keep=keep)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_both_zeros_are_one_key(dtype):
+    x = torch.where(torch.rand(300, 64, device=DEV, generator=torch.Generator(DEV).manual_seed(4)) < 0.5, -0.0, 0.0)
+    x[:, ::5] = -1.0
+    for kw in ({}, dict(score=1), dict(groups=4, keep=2), dict(bias=torch.zeros(64, device=DEV))):
+        check(x.to(dtype), 6, **kw)
+
+
 def test_keys_that_only_64_bits_tell_apart():
     # sigmoid(x) + bias of neighbours differ by 2^-30: equal in fp32
     x = torch.zeros(200, 40, device=DEV)
