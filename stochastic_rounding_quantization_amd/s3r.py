@@ -14,7 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libs3r.so")
@@ -174,9 +174,10 @@ def _ptr(t):
 def _ld(t, default=0):
     if t is None:
         return default
-    if t.dim() != 2 or t.stride(1) != 1:
+    s = t.stride()
+    if len(s) != 2 or s[1] != 1:
         raise ValueError("expected a row-major 2-D tensor (unit column stride)")
-    return t.stride(0)
+    return s[0]
 
 
 def _stream(stream):
@@ -194,9 +195,10 @@ def _check(fn, rc):
 
 def _gdtype(t):
     import torch
-    if t.dtype == torch.float32:
+    dt = t.dtype
+    if dt is torch.float32:
         return S3R_F32
-    if t.dtype == torch.bfloat16:
+    if dt is torch.bfloat16:
         return S3R_BF16
     raise ValueError(f"unsupported gradient dtype {t.dtype}")
 
@@ -466,24 +468,24 @@ def s3r_mx_backward_dw(desc: QDesc, Qt, Qt_scales, Xt, Xt_scales, xs, ec_row_t, 
     _check("s3r_mx_backward_dw", rc)
 
 
-def _contig(what, *ts):
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"expected a contiguous {what}")
-
-
 def _typed(t, dtype, what):
-    if t is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
 
 
 def _shaped(t, shape, what):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def s3r_route_workspace(desc: RouteDesc) -> int:
     return lib().s3r_route_workspace(ctypes.byref(desc))
+
+
+def _flat(what, t, dtype, n):
+    """Refuse t unless it is n contiguous elements of dtype."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous elements of {dtype}, got {t.dtype} {tuple(t.shape)}")
 
 
 def s3r_route(desc: RouteDesc, logits, bias, ids, weights, offsets, slot_row, row_slot, ws, stream=None, *,
@@ -492,55 +494,65 @@ def s3r_route(desc: RouteDesc, logits, bias, ids, weights, offsets, slot_row, ro
     [E + 1], slot_row int32 [T x k], row_slot int32 [T * k]."""
     import torch
     T, E, k = desc.tokens, desc.experts, desc.top_k
+    n, i32, f32 = T * k, torch.int32, torch.float32
     _shaped(logits, (T, E), "logits")
-    for t, dt, n, what in ((bias, torch.float32, E, "bias"), (ids, torch.int32, T * k, "ids"),
-                           (weights, torch.float32, T * k, "weights"), (offsets, torch.int64, E + 1, "offsets"),
-                           (slot_row, torch.int32, T * k, "slot_row"), (row_slot, torch.int32, T * k, "row_slot")):
-        if t is not None and (t.dtype != dt or t.numel() != n or not t.is_contiguous()):
-            raise ValueError(f"{what}: expected {n} contiguous elements of {dt}")
-    rc = lib().s3r_route(ctypes.byref(desc), _ptr(logits), _gdtype(logits), _ld(logits, E), _ptr(bias), _ptr(ids),
-                         _ptr(weights), _ptr(offsets), _ptr(slot_row), _ptr(row_slot), _ptr(ws), _nbytes(ws),
-                         _stream(stream))
+    if bias is not None:
+        _flat("bias", bias, f32, E)
+    _flat("ids", ids, i32, n)
+    _flat("weights", weights, f32, n)
+    _flat("offsets", offsets, torch.int64, E + 1)
+    _flat("slot_row", slot_row, i32, n)
+    _flat("row_slot", row_slot, i32, n)
+    rc = lib().s3r_route(desc, logits.data_ptr(), _gdtype(logits), _ld(logits), _ptr(bias), ids.data_ptr(),
+                         weights.data_ptr(), offsets.data_ptr(), slot_row.data_ptr(), row_slot.data_ptr(), _ptr(ws),
+                         _nbytes(ws), _stream(stream))
     if rc_only:
         return rc
-    _check("s3r_route", rc)
+    if rc:
+        _check("s3r_route", rc)
 
 
 def s3r_route_backward(desc: RouteDesc, logits, ids, dweights, dlogits, stream=None, *, rc_only=False):
     """dlogits [T x E], of the logits' dtype, from dweights f32 [T x k] at the choice ids int32 [T x k]."""
     import torch
-    T, E, k = desc.tokens, desc.experts, desc.top_k
-    _shaped(logits, (T, E), "logits")
-    _shaped(dlogits, (T, E), "dlogits")
+    T, E = shape = desc.tokens, desc.experts
+    n = T * desc.top_k
+    _shaped(logits, shape, "logits")
+    _shaped(dlogits, shape, "dlogits")
     _typed(dlogits, logits.dtype, "dlogits")
-    for t, dt, what in ((ids, torch.int32, "ids"), (dweights, torch.float32, "dweights")):
-        if t.dtype != dt or t.numel() != T * k or not t.is_contiguous():
-            raise ValueError(f"{what}: expected {T * k} contiguous elements of {dt}")
-    rc = lib().s3r_route_backward(ctypes.byref(desc), _ptr(logits), _gdtype(logits), _ld(logits, E), _ptr(ids),
-                                  _ptr(dweights), _ptr(dlogits), _ld(dlogits, E), _stream(stream))
+    _flat("ids", ids, torch.int32, n)
+    _flat("dweights", dweights, torch.float32, n)
+    rc = lib().s3r_route_backward(desc, logits.data_ptr(), _gdtype(logits), _ld(logits), ids.data_ptr(),
+                                  dweights.data_ptr(), dlogits.data_ptr(), _ld(dlogits), _stream(stream))
     if rc_only:
         return rc
-    _check("s3r_route_backward", rc)
+    if rc:
+        _check("s3r_route_backward", rc)
 
 
 def _slots(slot_row, tokens):
+    """(T, k) of a slot table that fits the token rows."""
     import torch
-    if slot_row.dtype != torch.int32 or slot_row.dim() != 2 or slot_row.shape[0] != tokens.shape[0] or \
+    shape = slot_row.shape
+    if slot_row.dtype is not torch.int32 or len(shape) != 2 or shape[0] != tokens.shape[0] or \
             not slot_row.is_contiguous():
         raise ValueError("slot_row: expected a contiguous int32 [T x k]")
-    return slot_row.shape
+    return shape
 
 
 def s3r_dispatch(X, slot_row, rows, stream=None, *, rc_only=False):
     """rows[slot_row[t, j]] = X[t]; rows [R x D] of X's dtype."""
     T, k = _slots(slot_row, X)
     _typed(rows, X.dtype, "rows")
-    _shaped(rows, (rows.shape[0], X.shape[1]), "rows")
-    rc = lib().s3r_dispatch(T, k, rows.shape[0], X.shape[1], _gdtype(X), _ptr(X), _ld(X), _ptr(slot_row), _ptr(rows),
-                            _ld(rows), _stream(stream))
+    R, D = rows.shape
+    if X.shape[1] != D:
+        raise ValueError("X and rows differ in width")
+    rc = lib().s3r_dispatch(T, k, R, D, _gdtype(X), X.data_ptr(), _ld(X), slot_row.data_ptr(), rows.data_ptr(), _ld(rows),
+                            _stream(stream))
     if rc_only:
         return rc
-    _check("s3r_dispatch", rc)
+    if rc:
+        _check("s3r_dispatch", rc)
 
 
 def s3r_combine(rows, slot_row, weights, y, stream=None, *, rc_only=False):
@@ -548,36 +560,43 @@ def s3r_combine(rows, slot_row, weights, y, stream=None, *, rc_only=False):
     import torch
     T, k = _slots(slot_row, y)
     _typed(y, rows.dtype, "y")
-    _shaped(y, (T, rows.shape[1]), "y")
-    _typed(weights, torch.float32, "weights")
-    _shaped(weights, (T, k), "weights")
-    _contig("weights", weights)
-    rc = lib().s3r_combine(T, k, rows.shape[0], rows.shape[1], _gdtype(rows), _ptr(rows), _ld(rows), _ptr(slot_row),
-                           _ptr(weights), _ptr(y), _ld(y), _stream(stream))
+    R, D = rows.shape
+    if y.shape[1] != D:
+        raise ValueError("rows and y differ in width")
+    if weights is not None:
+        _shaped(weights, (T, k), "weights")
+        _flat("weights", weights, torch.float32, T * k)
+    rc = lib().s3r_combine(T, k, R, D, _gdtype(rows), rows.data_ptr(), _ld(rows), slot_row.data_ptr(), _ptr(weights),
+                           y.data_ptr(), _ld(y), _stream(stream))
     if rc_only:
         return rc
-    _check("s3r_combine", rc)
+    if rc:
+        _check("s3r_combine", rc)
 
 
 def s3r_combine_backward(dy, rows, slot_row, weights, drows, dweights, stream=None, *, rc_only=False):
     """drows[slot_row[t, j]] = weights[t, j] dy[t]; dweights[t, j] = <dy[t], rows[slot_row[t, j]]>."""
     import torch
-    T, k = _slots(slot_row, dy)
-    D = dy.shape[1]
-    for t, what in ((rows, "rows"), (drows, "drows")):
-        _typed(t, dy.dtype, what)
-        _shaped(t, (rows.shape[0], D), what)
-    if _ld(drows) != _ld(rows):
+    T, k = shape = _slots(slot_row, dy)
+    (R, D), dt, f32 = rows.shape, dy.dtype, torch.float32
+    _typed(rows, dt, "rows")
+    _typed(drows, dt, "drows")
+    _shaped(drows, (R, D), "drows")
+    if dy.shape[1] != D:
+        raise ValueError("dy and rows differ in width")
+    ld = _ld(rows)
+    if _ld(drows) != ld:
         raise ValueError("rows and drows must share their layout")
-    for t, what in ((weights, "weights"), (dweights, "dweights")):
-        _typed(t, torch.float32, what)
-        _shaped(t, (T, k), what)
-        _contig(what, t)
-    rc = lib().s3r_combine_backward(T, k, rows.shape[0], D, _gdtype(dy), _ptr(dy), _ld(dy), _ptr(rows), _ptr(slot_row),
-                                    _ptr(weights), _ptr(drows), _ld(rows), _ptr(dweights), _stream(stream))
+    _shaped(weights, shape, "weights")
+    _shaped(dweights, shape, "dweights")
+    _flat("weights", weights, f32, T * k)
+    _flat("dweights", dweights, f32, T * k)
+    rc = lib().s3r_combine_backward(T, k, R, D, _gdtype(dy), dy.data_ptr(), _ld(dy), rows.data_ptr(), slot_row.data_ptr(),
+                                    weights.data_ptr(), drows.data_ptr(), ld, dweights.data_ptr(), _stream(stream))
     if rc_only:
         return rc
-    _check("s3r_combine_backward", rc)
+    if rc:
+        _check("s3r_combine_backward", rc)
 
 
 @dataclass
@@ -589,6 +608,7 @@ class MxRows:
     rows: int
     K: int
     groups: int = 1
+    _descs: dict = field(default_factory=dict, repr=False)      # product descriptors by (rows, output dtype, grouped)
 
 
 def mx_rows_buffer(rows: int, K: int, device, groups: int = 1) -> MxRows:
@@ -600,9 +620,9 @@ def mx_rows_buffer(rows: int, K: int, device, groups: int = 1) -> MxRows:
 
 
 def _index(index, rows):
-    import torch
-    if index is not None and (index.dtype != torch.int32 or index.numel() != rows or not index.is_contiguous()):
-        raise ValueError(f"index: expected {rows} contiguous int32")
+    if index is not None:
+        import torch
+        _flat("index", index, torch.int32, rows)
 
 
 def _like(A, up):
@@ -631,17 +651,25 @@ def s3r_mx_rows(A, out: MxRows, up=None, index=None, index_div=1, flags=None, st
 
 def _mx_pdesc(rows, w: MxRows, out, offsets):
     import torch
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"unsupported output dtype {out.dtype}")
+    dt = out.dtype
     _shaped(out, (rows, w.rows), "out")
     if offsets is None:
         if w.groups != 1:
             raise ValueError("several weights need the rows' offsets")
-    elif offsets.dtype != torch.int64 or offsets.numel() != w.groups + 1 or not offsets.is_contiguous():
-        raise ValueError(f"offsets: expected {w.groups + 1} contiguous int64")
-    steps, blocks = (w.K + 127) // 128, (w.rows + 255) // 256
-    return MxPDesc(rows, w.rows, w.K, 0 if offsets is None else w.groups, 16384 * steps, 4 * w.rows,
-                   blocks * 16384 * steps, steps * 4 * w.rows, S3R_BF16 if out.dtype == torch.bfloat16 else S3R_F32, 0)
+    else:
+        _flat("offsets", offsets, torch.int64, w.groups + 1)
+    key = rows, dt, offsets is None
+    d = w._descs.get(key)
+    if d is None:
+        if dt not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"unsupported output dtype {dt}")
+        steps, blocks = (w.K + 127) // 128, (w.rows + 255) // 256
+        if len(w._descs) >= 64:         # a program with ever new row counts
+            w._descs.clear()
+        d = w._descs[key] = MxPDesc(rows, w.rows, w.K, 0 if offsets is None else w.groups, 16384 * steps, 4 * w.rows,
+                                    blocks * 16384 * steps, steps * 4 * w.rows,
+                                    S3R_BF16 if dt is torch.bfloat16 else S3R_F32, 0)
+    return d
 
 
 def s3r_mx_product(a: MxRows, w: MxRows, out, offsets=None, flags=None, stream=None, *, rc_only=False):
@@ -650,7 +678,7 @@ def s3r_mx_product(a: MxRows, w: MxRows, out, offsets=None, flags=None, stream=N
     if a.groups != 1 or a.K != w.K:
         raise ValueError("a and w do not fit")
     d = _mx_pdesc(a.rows, w, out, offsets)
-    rc = lib().s3r_mx_product(ctypes.byref(d), _ptr(a.codes), 16384 * ((a.K + 127) // 128), _ptr(a.scales), 4 * a.rows,
+    rc = lib().s3r_mx_product(d, _ptr(a.codes), 16384 * ((a.K + 127) // 128), _ptr(a.scales), 4 * a.rows,
                               _ptr(offsets), _ptr(w.codes), _ptr(w.scales), _ptr(out), _ld(out), _ptr(flags),
                               _stream(stream))
     if rc_only:
@@ -671,17 +699,19 @@ def s3r_mx_linear(A, w: MxRows, out, *, up=None, offsets=None, index=None, index
                   stream=None, rc_only=False):
     """out = mx(A) w^T in one call (A as in s3r_mx_rows, the product as in s3r_mx_product)."""
     rows = out.shape[0]
-    if A.dim() != 2 or A.shape[1] != w.K or (index is None and A.shape[0] != rows):
+    a_rows, K = A.shape
+    if K != w.K or (index is None and a_rows != rows):
         raise ValueError("A, w and out do not fit")
     _index(index, rows)
     _like(A, up)
     d = _mx_pdesc(rows, w, out, offsets)
-    rc = lib().s3r_mx_linear(ctypes.byref(d), _ptr(A), _ptr(up), _gdtype(A), _ld(A), A.shape[0], _ptr(index), index_div,
-                             _ptr(offsets), _ptr(w.codes), _ptr(w.scales), _ptr(out), _ld(out), _ptr(flags), _ptr(ws),
+    rc = lib().s3r_mx_linear(d, A.data_ptr(), _ptr(up), _gdtype(A), _ld(A), a_rows, _ptr(index), index_div, _ptr(offsets),
+                             w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), _ld(out), _ptr(flags), _ptr(ws),
                              _nbytes(ws), _stream(stream))
     if rc_only:
         return rc
-    _check("s3r_mx_linear", rc)
+    if rc:
+        _check("s3r_mx_linear", rc)
 
 
 def swiglu_backward(dH, A_gate, A_up, stream=None):
