@@ -8,8 +8,8 @@
 // rest, ties to the lower index.  Weights w_j = c s_j, or c s_j / sum_i s_i.
 //
 // A decision between two keys has to be the one of exact arithmetic as far as
-// 64 bits tell it: without a bias and without sums of keys the logits themselves
-// are compared (the scores are monotone in them), otherwise fp64 keys.  All keys
+// 64 bits tell it: without a bias the logits themselves are compared (the scores
+// are monotone in them), otherwise, and for the sums of two, fp64 scores.  All keys
 // in fp64 cost 179 us for 65536 tokens x 256 experts (8 groups, top 8); fp32 keys
 // with an error bound, and fp64 for the tokens whose decisions lie within it
 // (0.4 % there), cost 43.
@@ -324,31 +324,38 @@ __device__ __forceinline__ float rt_float(uint32_t u) {
 }
 constexpr uint32_t kNoKey = 0x007FFFFFu;        // rt_ordered(-inf): no eligible expert from here down
 
-// The top_k fp32 keys: every lane sorts its five largest (whole numbers with the place in the low bits, so a
-// maximum brings its index along), and the token's lanes give up their heads, the largest first.  Lane j
-// of the token returns choice j.  Where that cannot be the exact choice, close is set in a lane of the token: a
-// choice without an eligible key, a lane that gave all five, or keys too near each other (kMargin: within
-// rt_margin; kBits: equal but for the low bits; kUnique: bf16 logits, which fit the upper half, never).
+// The top_k fp32 keys: every lane sorts its four largest (whole numbers with the place in the low bits, so a
+// maximum brings its index along), and the token's lanes give up their heads, the largest first; when a lane
+// has given all four, every lane of the wave sorts again what lies below its last.  Lane j of the token returns
+// choice j.  Where that cannot be the exact choice, close is set: a choice without an eligible key, or keys too near
+// each other (kMargin: within rt_margin; kBits: equal but for the low bits; kUnique: bf16 logits, which fit the
+// upper half, never).
 enum { kUnique, kBits, kMargin };
 template <int Kind, int L, int V>
 __device__ __forceinline__ int rt_take32(const RouteKernelArgs& a, int e0, int sub, const float (&key)[V], bool& close) {
-  constexpr int D = 5;
-  uint32_t l[D] = {0u, 0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    uint32_t t = rt_ordered(key[i]);
-    t = Kind == kUnique ? (t & 0xFFFF0000u) | (uint32_t)(0xFFFF - (e0 + i)) : (t & ~15u) | (uint32_t)(15 - i);
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (d > i) break;
-      const uint32_t hi = max(l[d], t);
-      t = min(l[d], t);
-      l[d] = hi;
-    }
-  }
-  int mine = 0, given = 0;
-  uint32_t last = 0;
+  constexpr int D = V < 4 ? V : 4;
+  uint32_t l[D];
+  uint32_t below = 0xFFFFFFFFu, last = 0;
+  int mine = 0, have = 0;
   for (int j = 0; j < a.K + (Kind == kUnique ? 0 : 1); ++j) {
+    if (j == 0 || (V > D && __builtin_amdgcn_ballot_w64(have == 0) != 0)) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) l[d] = 0u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        uint32_t t = rt_ordered(key[i]);
+        t = Kind == kUnique ? (t & 0xFFFF0000u) | (uint32_t)(0xFFFF - (e0 + i)) : (t & ~15u) | (uint32_t)(15 - i);
+        t = t < below ? t : 0u;
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          if (d > i) break;
+          const uint32_t hi = max(l[d], t);
+          t = min(l[d], t);
+          l[d] = hi;
+        }
+      }
+      have = D;
+    }
     const uint32_t m = rt_reduce<L>(l[0], [](uint32_t x, uint32_t y) { return max(x, y); });
     if constexpr (Kind != kUnique) {
       if (j > 0) close |= Kind == kBits ? (last ^ m) < 16u : rt_float(last) - rt_float(m) <= rt_margin(rt_float(last));
@@ -364,13 +371,13 @@ __device__ __forceinline__ int rt_take32(const RouteKernelArgs& a, int e0, int s
       at = rt_min<L>(win ? e0 + 15 - (int)(m & 15u) : 1 << 30);
       win = (uint32_t)(at - e0) < (uint32_t)V;
     }
+    below = win ? m : below;
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) l[d] = win ? l[d + 1] : l[d];
     l[D - 1] = win ? 0u : l[D - 1];
-    given += win ? 1 : 0;
+    have -= win ? 1 : 0;
     if (sub == j) mine = at;
   }
-  close |= given >= D;
   return mine;
 }
 
@@ -383,19 +390,24 @@ __device__ __forceinline__ int rt_choose64(const RouteKernelArgs& a, const TIn* 
   float x[V], bias[V], top = -__builtin_inff();
   rt_load_row<TIn, V>(row + e0, n, false, x);
   double key[V];
-  if constexpr (ByLogit) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = x[i] == x[i] ? (double)x[i] : -__builtin_inf();
-  } else {
+  const bool sums = a.groups > 1 && a.group_top == 2;      // the groups' order needs the scores
+  if (!ByLogit || sums) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       bias[i] = a.bias && i < n ? a.bias[e0 + i] : 0.f;
-      top = __builtin_fmaxf(top, x[i]);
+      top = x[i] > top ? x[i] : top;
     }
     top = rt_max<64>(top);
     rt_keys<double, 64, V>(a, x, bias, top == -__builtin_inff() ? 0.f : top, key);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = x[i] == x[i] ? (double)x[i] : -__builtin_inf();
   }
   if (a.groups > 1) rt_keep_groups<double, 64, V>(a, a.group_lanes ? per / V : 0, e0, per, lane, lane, key);
+  if (ByLogit && sums) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = key[i] > -__builtin_inf() ? (double)x[i] : -__builtin_inf();
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i)
     if (i >= n) key[i] = __builtin_nan("");
@@ -471,18 +483,23 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteKernelArgs a) {
     // fp32 keys, and fp64 ones for the tokens in which they may not decide as exact ones
     float key[V];
     bool close = false;
-    if constexpr (ByLogit) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = x[i] == x[i] ? x[i] : -__builtin_inff();
-    } else {
+    const bool sums = a.groups > 1 && a.group_top == 2;   // the groups' order needs the scores
+    if (!ByLogit || sums) {
       float bias[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) bias[i] = lbias[e0 + i];
+      for (int i = 0; i < V; ++i) bias[i] = ByLogit ? 0.f : lbias[e0 + i];
       rt_keys<float, L, V>(a, x, bias, shift, key);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = x[i] == x[i] ? x[i] : -__builtin_inff();
     }
     if (a.groups > 1) {
       const bool near = rt_keep_groups<float, L, V>(a, a.group_lanes, e0, per, sub, lane, key);
-      close = !ByLogit && near;
+      close = (!ByLogit || sums) && near;
+    }
+    if (ByLogit && sums) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = key[i] > -__builtin_inff() ? x[i] : -__builtin_inff();
     }
     constexpr int kKind = !ByLogit ? kMargin : sizeof(TIn) == 2 ? kUnique : kBits;
     int mine = rt_take32<kKind, L, V>(a, e0, sub, key, close);     // lane j of the token: choice j
@@ -767,10 +784,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
   const int esize = a.dtype == S3R_BF16 ? 2 : 4;
   k.vec = rt_rows_aligned(a.logits, a.ld, esize) ? 1 : 0;
   const int L = rt_lanes(a.E, a.K, a.groups);
-  // by the scores only where their values, not their order alone, decide
   const int per = a.E / a.groups, V = a.E > 8 * L ? 16 : 8, run = per / V;
   if (a.groups > 1 && per % V == 0 && (run & (run - 1)) == 0) k.group_lanes = run;
-  const bool by_score = a.bias != nullptr || (a.groups > 1 && a.group_top == 2);
+  const bool by_score = a.bias != nullptr;      // else the logits' order is the scores'
   if (rt_single(a.T, a.E, a.K, L)) {
     k.nchunk = 1;
     k.chunk = std::max<int64_t>(a.T, 1);
