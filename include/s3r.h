@@ -541,8 +541,8 @@ int s3r_mx_backward_dw(const s3r_qdesc* desc, const uint8_t* Qt, int64_t ld_qt,
  *            key (group_top 1) or the sum of its two largest (2); the `keep`
  *            best runs stay, the others' keys become -inf;
  *   choice   the top_k largest keys in descending order.  Every tie, of keys or
- *            of runs, goes to the lower index.  Keys are compared as fp64 values
- *            (without a bias and without sums: by the logits, the same order).
+ *            of runs, goes to the lower index.  Keys and sums are compared as
+ *            fp64 values (keys without a bias by the logits, the same order).
  *            A logit of -inf (a masked expert) or NaN, and a NaN key, rank as -inf:
  *            such experts are taken only when no others are left;
  *   weights  scale * s_j, or with renorm scale * s_j / sum of the chosen s
