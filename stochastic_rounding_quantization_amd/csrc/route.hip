@@ -14,7 +14,7 @@
 // with an error bound, and fp64 for the tokens whose decisions lie within it
 // (0.4 % there), cost 43.
 //
-// 16384 x 64 bf16, top 2: choice 4.7 us, order 6.9, for 2.6 MB: two launches' latency.
+// 16384 x 64 bf16, top 2: choice 4.7 us, order 6.5, for 2.6 MB: two launches' latency.
 // 65536 x 256 fp32, grouped top 8: choice 43 us (850 vector instructions per four
 // tokens take 31, fp64 choices the rest), order 12; the 75 MB alone would take 14.
 #include <type_traits>
@@ -27,7 +27,7 @@ namespace {
 constexpr int kRtThreads = 1024;
 constexpr int kRtMaxChunks = 256;    // token chunks of one call: the place kernel reads every chunk's counts
 // A chunk fills four waves at least.  Geometric mean of 36 routers of 100 .. 20000 tokens, us: 13.3 with chunks of
-// T / 256 tokens, two waves 12.5, four 12.4, eight 12.9.
+// T / 256 tokens, two waves 12.5, four 12.4, eight 12.9 (all with 1024 threads for the order).
 constexpr int kRtChunkLanes = 256;
 
 template <typename TIn>
@@ -576,13 +576,13 @@ __global__ __launch_bounds__(kRtThreads) void route_place_kernel(RouteKernelArgs
   const int64_t s0 = t0 * a.K, s1 = t1 * a.K;
   const int e_first = s0 + tid < s1 ? a.ids[s0 + tid] : 0;     // on its way while the counts are added
   int32_t *sum = part, *sum_before = part + 1024;
-  for (int e = tid; e < a.E; e += kRtThreads) sum[e] = sum_before[e] = 0;
+  for (int e = tid; e < a.E; e += (int)blockDim.x) sum[e] = sum_before[e] = 0;
   __syncthreads();
   // four experts a thread, the chunks dealt to the threads that share them; whole numbers, so the
   // atomics' order changes nothing
   int quads = 1;
   while (quads * 4 < a.E) quads <<= 1;
-  const int np = kRtThreads / quads, q = tid & (quads - 1), p = tid / quads;
+  const int np = (int)blockDim.x / quads, q = tid & (quads - 1), p = tid / quads;
   int4 total4 = make_int4(0, 0, 0, 0), before4 = total4;
   if (q * 4 < a.E) {
 #pragma unroll 16
@@ -814,8 +814,14 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
     if (by_score) go(std::false_type{});
     else go(std::true_type{});
   });
-  if (k.nchunk > 1)
-    hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)k.nchunk), dim3(kRtThreads), lds, st, k);
+  if (k.nchunk > 1) {
+    // A thread per slot of a chunk and per expert, to the next of three sizes: fewer waves meet at each barrier.
+    // Geometric mean of 36 routers of 100 .. 20000 tokens, us: 12.4 with 1024 threads for all, 11.1 so; the order
+    // of 16384 x 64 top 2 6.9 and 6.5.
+    const int64_t want = std::max<int64_t>(k.chunk * a.K, a.E);
+    const unsigned place = want <= 256 ? 256 : want <= 512 ? 512 : kRtThreads;
+    hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)k.nchunk), dim3(place), lds, st, k);
+  }
   return hipGetLastError();
 }
 
