@@ -833,7 +833,7 @@ template <typename TIn, int Steps>
 hipError_t run_rows(const MxRowsArgs& a, hipStream_t st) {
   const int ksteps = (int)((a.K + 127) / 128);
   const int64_t blocks = (ksteps + Steps - 1) / Steps * ((a.R + kMrRows - 1) / kMrRows);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (blocks * kMrThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, (unsigned)a.G), block(kMrThreads);
   const bool words = mr_words(a);
   if (a.up && words) hipLaunchKernelGGL((mx_rows_kernel<TIn, true, true, Steps>), grid, block, 0, st, a, ksteps);
@@ -874,7 +874,7 @@ template <typename T, typename TOut>
 hipError_t run_tiles(const MxProductArgs& a, MxProdK p, hipStream_t st) {
   const int64_t mt = a.G ? a.M / T::BM + std::min(a.G, a.M) : (a.M + T::BM - 1) / T::BM;
   p.tiles_n = (int)((a.N + T::BN - 1) / T::BN);
-  if (mt * p.tiles_n > 0x7FFFFFF0) return hipErrorInvalidConfiguration;
+  if ((mt * p.tiles_n + 7) * T::Threads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   const int vec = ((uintptr_t)a.out & 15u) == 0 && (a.ld_out * (int64_t)sizeof(TOut)) % 16 == 0;
   const int64_t blocks = a.G ? (mt * p.tiles_n + 7) / 8 * 8 : mt * p.tiles_n;
   hipLaunchKernelGGL((mx_tile_kernel<T, TOut>), dim3((unsigned)blocks), dim3(T::Threads), 0, st, p, (int)mt, vec);
@@ -901,7 +901,7 @@ hipError_t run_few_rows(const MxProductArgs& a, const MxRowsArgs& q, hipStream_t
   // grouped: the tiles of every group, at most one partial tile each
   const int64_t mt = a.G ? a.M / (16 * MI) + std::min(a.G, a.M) : (a.M + 16 * MI - 1) / (16 * MI);
   p.tiles_n = (int)((a.N + 16 * NJ - 1) / (16 * NJ));
-  if (mt * p.tiles_n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (mt * p.tiles_n * kSkThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(mt * p.tiles_n)), block(kSkThreads);
   const int rows = (int)std::min<int64_t>(a.M, 16);
   const size_t lds = std::is_void<TIn>::value ? 0 : sk_lds_bytes(rows, p.ksteps);

@@ -361,7 +361,8 @@ __device__ __forceinline__ int rt_take32(const RouteKernelArgs& a, int e0, int s
     }
     const uint32_t m = rt_reduce<L>(l[0], [](uint32_t x, uint32_t y) { return max(x, y); });
     if constexpr (Kind != kUnique) {
-      if (j > 0) close |= Kind == kBits ? (last ^ m) < 16u : rt_float(last) - rt_float(m) <= rt_margin(rt_float(last));
+      // kMargin: also where the difference is NaN (two infinite keys, whose low bits make them one)
+      if (j > 0) close |= Kind == kBits ? (last ^ m) < 16u : !(rt_float(last) - rt_float(m) > rt_margin(rt_float(last)));
       last = m;
       if (j == a.K) break;
     }
@@ -661,7 +662,7 @@ __global__ __launch_bounds__(kRbThreads) void route_backward_kernel(RouteBwdKern
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int sub = lane % L;
   constexpr int TW = 64 / L, W = 16 / (int)sizeof(TIn), NQ = V / W;
-  const int64_t tb = ((int64_t)blockIdx.x * (kRbThreads / 64) + wave) * TW + lane / L;
+  const int64_t tb = (wide_block() * (kRbThreads / 64) + wave) * TW + lane / L;
   const bool act = tb < a.T;
   const int64_t t = act ? tb : a.T - 1;
   const TIn* row = reinterpret_cast<const TIn*>(a.logits) + t * a.ld;
@@ -837,7 +838,7 @@ hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
   rt_dispatch(L, a.E, [&](auto l, auto v) {
     constexpr int LL = decltype(l)::value, VV = decltype(v)::value;
     const int64_t per = (kRbThreads / 64) * (64 / LL);
-    const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kRbThreads);
+    const dim3 grid = wide_grid((a.T + per - 1) / per), block(kRbThreads);
     if (a.dtype == S3R_BF16) hipLaunchKernelGGL((route_backward_kernel<uint16_t, LL, VV>), grid, block, 0, st, k);
     else hipLaunchKernelGGL((route_backward_kernel<float, LL, VV>), grid, block, 0, st, k);
   });

@@ -67,7 +67,7 @@ struct Chunk {
 // One thread per (token, chunk).
 template <typename T, int W>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowMoveArgs a, int chunks) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const int64_t i = wide_block() * kRowThreads + threadIdx.x;
   const int64_t t = i / chunks;
   if (t >= a.T) return;
   const int64_t c = (i - t * chunks) * W;
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowMoveArgs a, in
 
 template <typename T, int W>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowMoveArgs a, int chunks) {
-  const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+  const int64_t i = wide_block() * kRowThreads + threadIdx.x;
   const int64_t t = i / chunks;
   if (t >= a.T) return;
   const int64_t c = (i - t * chunks) * W;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void combine_backward_choices(const RowMoveArgs& a, i
 template <typename T, int W>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowMoveArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = wide_block() * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.T) return;
   int j = 0;
   for (; j + 4 <= a.K; j += 4) combine_backward_choices<T, W, 4>(a, t, j, lane);
@@ -163,8 +163,8 @@ void run_rows(const RowMoveArgs& a, int what, hipStream_t st) {
   const bool vec = rows_vec(a.in, a.ld_in, a.D, sizeof(T)) && rows_vec(a.out, a.ld_out, a.D, sizeof(T)) &&
                    (what != 2 || rows_vec(a.dy, a.ld_dy, a.D, sizeof(T)));
   const int chunks = (int)(vec ? a.D / W : a.D);
-  const dim3 grid((unsigned)((a.T * chunks + kRowThreads - 1) / kRowThreads)), block(kRowThreads);
-  const dim3 bgrid((unsigned)((a.T + kRowThreads / 64 - 1) / (kRowThreads / 64)));
+  const dim3 grid = wide_grid((a.T * chunks + kRowThreads - 1) / kRowThreads), block(kRowThreads);
+  const dim3 bgrid = wide_grid((a.T + kRowThreads / 64 - 1) / (kRowThreads / 64));
   if (what == 0) {
     if (vec) hipLaunchKernelGGL((dispatch_kernel<T, W>), grid, block, 0, st, a, chunks);
     else hipLaunchKernelGGL((dispatch_kernel<T, 1>), grid, block, 0, st, a, chunks);

@@ -251,6 +251,15 @@ hipError_t launch_swiglu_backward_amax(int64_t T, int64_t F, const float* dH, in
                                        const float* sx, const float* swg, const float* swu, uint32_t* amax_bits,
                                        char* ws, hipStream_t st);
 
+// Launches of any number of workgroups: a dimension of a grid has fewer than 2^32 work-items, so those past 2^22
+// workgroups go on in the next row of a 2-D grid.
+constexpr int kWideShift = 22;
+inline dim3 wide_grid(int64_t blocks) {
+  constexpr int64_t row = (int64_t)1 << kWideShift;
+  return blocks <= row ? dim3((unsigned)blocks) : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+__device__ __forceinline__ int64_t wide_block() { return ((int64_t)blockIdx.y << kWideShift) + blockIdx.x; }
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // The gate and up projections' quantizers with the SwiGLU glue computed in them (quantize.hip): G_gate

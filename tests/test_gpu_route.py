@@ -56,6 +56,16 @@ def test_route_groups_and_bias(E, k, groups, keep, top, bias, score):
     check(logits(300, E, torch.float32, E + k), k, score=score, bias=b, groups=groups, keep=keep, group_top=top)
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("groups, keep, top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+def test_route_infinite_bias(groups, keep, top, score):
+    """Experts that a bias of inf puts first tie, to the lower index; -inf puts them last."""
+    b = torch.zeros(64, device=DEV)
+    b[[3, 8, 20]] = float("inf")
+    b[[0, 9, 40]] = float("-inf")
+    check(logits(300, 64, torch.float32, 3), 5, score=score, bias=b, groups=groups, keep=keep, group_top=top)
+
+
 @pytest.mark.parametrize("groups, keep", [(1, 1), (4, 2)])
 @pytest.mark.parametrize("bias", [False, True])
 def test_ties_go_to_the_lower_index(groups, keep, bias):
@@ -242,6 +252,46 @@ def test_slots_without_a_row():
     s3r.s3r_combine_backward(x, rows, sr, w, d, dw)
     assert torch.equal(d[:2], 2 * x[:2]) and (d[2:] == 0).all()
     assert host(dw)[[0, 1, 2, 2], [1, 0, 0, 1]].tolist() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("T, D", [(2 ** 21 + 5, 2049), (2 ** 26 + 7, 8)])
+def test_rows_past_32_bits(T, D):
+    """More than 2^32 elements in odd rows; more tokens than a grid's dimension has waves."""
+    x = ((torch.arange(T, device=DEV, dtype=torch.int32) % 127)[:, None].to(torch.bfloat16)
+         + (torch.arange(D, device=DEV, dtype=torch.int32) % 63).to(torch.bfloat16))          # exact, below 2^8
+    sr = torch.arange(T - 1, -1, -1, device=DEV, dtype=torch.int32)[:, None].contiguous()
+    rows = torch.empty_like(x)
+    s3r.s3r_dispatch(x, sr, rows)
+    last = [0, 1, T // 2, T - 2, T - 1]
+    part = torch.arange(0, T, 4099, device=DEV)
+    for at in (part, torch.tensor(last, device=DEV)):
+        assert torch.equal(rows[T - 1 - at], x[at])
+    w = torch.full((T, 1), 2.0, device=DEV)
+    y = torch.empty_like(x)
+    s3r.s3r_combine(rows, sr, w, y)
+    for at in (part, torch.tensor(last, device=DEV)):
+        assert torch.equal(y[at], 2 * x[at])
+    drows, dw = y, torch.empty_like(w)
+    s3r.s3r_combine_backward(x, rows, sr, w, drows, dw)
+    for at in (part, torch.tensor(last, device=DEV)):
+        assert torch.equal(drows[T - 1 - at], 2 * x[at])
+        exp = (x[at].double() ** 2).sum(1)                 # terms of one sign, D roundings of at most U each
+        assert ((dw[at, 0].double() - exp).abs() <= (D + 8) * U * exp).all()
+
+
+def test_route_backward_past_32_bits():
+    T, E = 2 ** 29 + 9, 8                                   # 8 lanes a token: more than 2^32 of them
+    x = (torch.arange(T, device=DEV, dtype=torch.int32) % 61)[:, None].to(torch.bfloat16) / 16 * torch.arange(
+        E, device=DEV).to(torch.bfloat16)
+    ids = torch.full((T, 1), 3, dtype=torch.int32, device=DEV)
+    dw = torch.ones(T, 1, device=DEV)
+    dx = torch.empty_like(x)
+    s3r.s3r_route_backward(s3r.route_desc(T, E, 1, renorm=False), x, ids, dw, dx)
+    at = torch.cat([torch.arange(0, T, 1048573, device=DEV), torch.arange(T - 70, T, device=DEV)])
+    xs, chosen = host(x[at].double()), np.full((len(at), 1), 3)
+    exp = ref.backward(xs, chosen, np.ones((len(at), 1)), renorm=False)
+    # the softmax's exponentials and sums, |x| U and 16 roundings, on the scale of the gradient 1; half a bf16 step
+    assert (np.abs(host(dx[at].double()) - exp) <= U * (64 + 2 * np.abs(xs).max()) + half(torch.bfloat16) * np.abs(exp)).all()
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
