@@ -582,7 +582,9 @@ int s3r_route(const s3r_route_desc* desc, const void* logits, int32_t dtype, int
  *   renorm:   dl_j = p_j (g_j - sum_i p_i g_i), times 1 - s_j for the sigmoid;
  *   sigmoid:  dl_j = g_j s_j (1 - s_j);
  *   softmax:  dl_e = s_e (g_e - sum_i g_i s_i) for every expert (g_e 0 where not chosen);
- * and 0 elsewhere.  groups, keep and group_top are not used. */
+ * and 0 elsewhere.  With renorm or the sigmoid only the chosen logits are read (a NaN elsewhere
+ * in the row, which makes its softmax weights NaN, has no part).  groups, keep and
+ * group_top are not used. */
 int s3r_route_backward(const s3r_route_desc* desc, const void* logits, int32_t dtype, int64_t ld, const int32_t* ids,
                        const float* dweights, void* dlogits, int64_t ld_d, hipStream_t stream);
 
@@ -590,7 +592,8 @@ int s3r_route_backward(const s3r_route_desc* desc, const void* logits, int32_t d
  * Rows of D elements, all F32 or all BF16 (dtype), any alignment (16-byte-aligned
  * bases, leading dims and widths take the vector path).  slot_row [T x k] int32
  * as s3r_route writes it; an index outside 0 .. R-1 is no row: it is skipped, and
- * its weight's gradient is 0.  k >= 1.
+ * its weight's gradient is 0.  Rows that no slot names are left as they are; no two
+ * slots may name one row.  k >= 1.
  *   s3r_dispatch:          rows[slot_row[t,j]] = X[t].  Its gradient is
  *                          s3r_combine without weights.
  *   s3r_combine:           y[t] = sum_j w[t,j] Y[slot_row[t,j]] (fp32, j ascending;
@@ -644,7 +647,9 @@ typedef struct s3r_mx_pdesc {
 /* s3r_mx_product: out [M x N] = dq(A) dq(B)^T, fp32 accumulation in the matrix cores,
  * rounded once; B [N x K] as s3r_mx_rows wrote it.  With groups, the rows of A and out
  * are sorted by group and offsets is as in the grouped calls above (invalid offsets
- * raise S3R_FLAG_BAD_GROUPS and nothing is computed). */
+ * raise S3R_FLAG_BAD_GROUPS and nothing is computed).  The order of a sum's terms is
+ * fixed by the call's sizes: the same call gives the same bits, a row among other rows
+ * may differ in the last ones. */
 int s3r_mx_product(const s3r_mx_pdesc* desc, const uint8_t* A, int64_t ld_a, const uint8_t* A_scales, int64_t ld_as,
                    const int64_t* offsets, const uint8_t* B, const uint8_t* B_scales,
                    void* out, int64_t ld_out, uint32_t* flags, hipStream_t stream);
