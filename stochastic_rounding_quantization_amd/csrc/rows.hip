@@ -19,8 +19,13 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// Chunks of W elements: 16 bytes of the row type (8 bf16, 4 f32), or one element for rows that are not
-// 16-byte aligned.
+typedef uint32_t v4u32_a2 __attribute__((ext_vector_type(4), aligned(2)));     // 16 bytes at a bf16's alignment
+typedef uint32_t v4u32_a4 __attribute__((ext_vector_type(4), aligned(4)));     // at an f32's
+
+// Chunks of W elements: 16 bytes of the row type (8 bf16, 4 f32), or one element for rows shorter than that.  Rows
+// that are not 16-byte aligned (odd widths, slices) take the same accesses at their elements' alignment.  16384 tokens,
+// 2 rows each, 2047 bf16 columns, us, element by element and so: dispatch 113 and 37, combine 155 and 42,
+// backward 131 and 70 (2048 columns: 34, 37, 63).
 template <typename T, int W, bool NT = false>
 struct Chunk {
   // NT: the nontemporal hint, where it measured faster.  16384 tokens, 2 rows each, 2048 bf16 columns, us:
@@ -31,16 +36,34 @@ struct Chunk {
       if constexpr (sizeof(T) == 2) v[0] = bf16_to_f32(*reinterpret_cast<const uint16_t*>(p));
       else v[0] = *p;
     } else if constexpr (sizeof(T) == 2) {
-      const uint4 w = NT ? ld_stream_u4(p) : *reinterpret_cast<const uint4*>(p);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      const v4u32 w = word(p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(ww[i] << 16);
-        v[2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     } else {
-      const float4 w = NT ? ld_stream_f4(p) : *reinterpret_cast<const float4*>(p);
-      v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+      const v4u32 w = word(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    }
+  }
+  static __device__ __forceinline__ v4u32 word(const T* p) {
+    if constexpr (sizeof(T) == 2) {
+      const v4u32_a2* q = reinterpret_cast<const v4u32_a2*>(p);
+      return NT ? __builtin_nontemporal_load(q) : *q;
+    } else {
+      const v4u32_a4* q = reinterpret_cast<const v4u32_a4*>(p);
+      return NT ? __builtin_nontemporal_load(q) : *q;
+    }
+  }
+  static __device__ __forceinline__ void put(T* p, v4u32 w) {
+    if constexpr (sizeof(T) == 2) {
+      v4u32_a2* q = reinterpret_cast<v4u32_a2*>(p);
+      if constexpr (NT) __builtin_nontemporal_store(w, q); else *q = w;
+    } else {
+      v4u32_a4* q = reinterpret_cast<v4u32_a4*>(p);
+      if constexpr (NT) __builtin_nontemporal_store(w, q); else *q = w;
     }
   }
   static __device__ __forceinline__ void store(T* p, const float (&v)[W]) {
@@ -54,23 +77,21 @@ struct Chunk {
         w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(q, bf2));
       }
       if constexpr (W == 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
-      else if constexpr (NT) __builtin_nontemporal_store((v4u32{w[0], w[1], w[2], w[3]}), reinterpret_cast<v4u32*>(p));
-      else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      else put(p, v4u32{w[0], w[1], w[2], w[3]});
     } else {
       if constexpr (W == 1) *p = v[0];
-      else if constexpr (NT) __builtin_nontemporal_store((v4f32{v[0], v[1], v[2], v[3]}), reinterpret_cast<v4f32*>(p));
-      else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      else put(p, v4u32{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
     }
   }
 };
 
-// One thread per (token, chunk).
+// One thread per (token, chunk); the last chunk of a row ends with the row, over the one before it.
 template <typename T, int W>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowMoveArgs a, int chunks) {
   const int64_t i = wide_block() * kRowThreads + threadIdx.x;
   const int64_t t = i / chunks;
   if (t >= a.T) return;
-  const int64_t c = (i - t * chunks) * W;
+  const int64_t c = min((i - t * chunks) * W, a.D - W);
   float v[W];
   Chunk<T, W>::load((const T*)a.in + t * a.ld_in + c, v);
   for (int j = 0; j < a.K; ++j) {
@@ -84,7 +105,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowMoveArgs a, int
   const int64_t i = wide_block() * kRowThreads + threadIdx.x;
   const int64_t t = i / chunks;
   if (t >= a.T) return;
-  const int64_t c = (i - t * chunks) * W;
+  const int64_t c = min((i - t * chunks) * W, a.D - W);
   float s[W];
 #pragma unroll
   for (int q = 0; q < W; ++q) s[q] = 0.f;
@@ -114,7 +135,8 @@ __device__ __forceinline__ void combine_backward_choices(const RowMoveArgs& a, i
     w[j] = a.weights[t * a.K + j0 + j];
     dot[j] = 0.f;
   }
-  for (int64_t c = (int64_t)lane * W; c < a.D; c += 64 * W) {
+  for (int64_t at = (int64_t)lane * W; at < a.D; at += 64 * W) {
+    const int64_t c = min(at, a.D - W);          // the last chunk ends with the row
     float g[W], y[J][W];
     Chunk<T, W>::load((const T*)a.dy + t * a.ld_dy + c, g);
 #pragma unroll
@@ -126,7 +148,7 @@ __device__ __forceinline__ void combine_backward_choices(const RowMoveArgs& a, i
       float o[W];
 #pragma unroll
       for (int q = 0; q < W; ++q) {
-        dot[j] = fmaf(g[q], y[j][q], dot[j]);
+        if (W == 1 || c + q >= at) dot[j] = fmaf(g[q], y[j][q], dot[j]);
         o[q] = g[q] * w[j];
       }
       Chunk<T, W, true>::store((T*)a.out + r[j] * a.ld_out + c, o);
@@ -153,16 +175,11 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowMoveAr
   if (j < a.K) combine_backward_choices<T, W, 1>(a, t, j, lane);
 }
 
-bool rows_vec(const void* p, int64_t ld, int64_t D, int esize) {
-  return ((uintptr_t)p & 15u) == 0 && (ld * esize) % 16 == 0 && (D * esize) % 16 == 0;
-}
-
 template <typename T>
 void run_rows(const RowMoveArgs& a, int what, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(T);
-  const bool vec = rows_vec(a.in, a.ld_in, a.D, sizeof(T)) && rows_vec(a.out, a.ld_out, a.D, sizeof(T)) &&
-                   (what != 2 || rows_vec(a.dy, a.ld_dy, a.D, sizeof(T)));
-  const int chunks = (int)(vec ? a.D / W : a.D);
+  const bool vec = a.D >= W;
+  const int chunks = (int)(vec ? (a.D + W - 1) / W : a.D);
   const dim3 grid = wide_grid((a.T * chunks + kRowThreads - 1) / kRowThreads), block(kRowThreads);
   const dim3 bgrid = wide_grid((a.T + kRowThreads / 64 - 1) / (kRowThreads / 64));
   if (what == 0) {

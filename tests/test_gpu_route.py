@@ -254,6 +254,42 @@ def test_slots_without_a_row():
     assert host(dw)[[0, 1, 2, 2], [1, 0, 0, 1]].tolist() == [0, 0, 0, 0]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset", [0, 1, 8])
+def test_rows_of_every_width(dtype, offset):
+    """Row ends at every place of a 16-byte word; nothing around the rows is read into them or written."""
+    T, k = 7, 3
+    sr = slots(T, k, T * k, 1)
+    w = torch.rand(T, k, device=DEV)
+
+    def inside(n, D, fill=None):
+        wide = torch.full((n + 2, D + 21), 9.0 if fill is None else float("nan"), dtype=dtype, device=DEV)
+        rows = wide[1:n + 1, offset:offset + D]
+        if fill is not None:
+            rows.copy_(fill)
+        return wide, rows
+
+    for D in [*range(1, 26), 511, 513, 515, 1029]:
+        _, x = inside(T, D, torch.randn(T, D, device=DEV))
+        _, rows = inside(T * k, D, torch.randn(T * k, D, device=DEV))
+        wide, out = inside(T * k, D)
+        s3r.s3r_dispatch(x, sr, out)
+        assert all(torch.equal(out[sr[:, j].long()], x) for j in range(k))
+        assert (wide == 9).sum() >= wide.numel() - out.numel()
+        wide, y = inside(T, D)
+        s3r.s3r_combine(rows, sr, w, y)
+        exp, mag = ref.combine(host(rows.double()), host(sr), host(w))
+        assert (np.abs(host(y.double()) - exp) <= (k + 1) * U * mag + half(dtype) * np.abs(exp) * (1 + 1e-6)).all()
+        assert (wide == 9).sum() >= wide.numel() - y.numel()
+        wide, d = inside(T * k, D)
+        dw = torch.empty_like(w)
+        s3r.s3r_combine_backward(x, rows, sr, w, d, dw)
+        exp, edw, mag = ref.combine_backward(host(x.double()), host(rows.double()), host(sr), host(w))
+        assert (np.abs(host(d.double()) - exp) <= (U + half(dtype) * (1 + 1e-6)) * np.abs(exp)).all()
+        assert (np.abs(host(dw) - edw) <= (D + 8) * U * mag).all()
+        assert (wide == 9).sum() >= wide.numel() - d.numel()
+
+
 @pytest.mark.parametrize("T, D", [(2 ** 21 + 5, 2049), (2 ** 26 + 7, 8)])
 def test_rows_past_32_bits(T, D):
     """More than 2^32 elements in odd rows; more tokens than a grid's dimension has waves."""
