@@ -70,6 +70,20 @@ def test_rows_borders_and_non_finite():
     assert np.isnan(y[[1, 2, 4]]).all() and np.isfinite(y[[0, 3]]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset", [0, 1, 8])
+def test_rows_of_every_width(dtype, offset):
+    """Row ends at every place of a 16-byte word, with NaN around the rows; two rows also as the product rounds them."""
+    for K in [*range(1, 26), *range(120, 138), 255, 257]:
+        wide = torch.full((22, K + 21), float("nan"), dtype=dtype, device=DEV)
+        A = wide[1:21, offset:offset + K]
+        A.copy_(matrix((20, K), dtype, K))
+        check_rows(s3r.mx_rows(A), mx.rows(f32(A)))
+        W = matrix((40, K), dtype, 7)
+        y = s3r.mx_linear(A[:2], s3r.mx_rows(W), out_dtype=torch.float32)
+        check_product(y, mx.rows(f32(A[:2]))["deq"], mx.rows(f32(W))["deq"])
+
+
 def test_rows_strides_index_and_groups():
     wide = matrix((50, 400), torch.bfloat16, 3)
     for A in (wide[:, 1:301], wide[:, 8:308], wide[::3, :96]):
