@@ -36,26 +36,53 @@ __device__ __forceinline__ float rt_load(const TIn* p) {
   else return *reinterpret_cast<const float*>(p);
 }
 
-// V consecutive logits from p, of which the first n exist (the others: -inf, as masked).
+// 16 bytes at an element's alignment: rows of any width and any slice of a tensor take them.
+typedef uint32_t rt_u4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t rt_u4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t rt_u2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t rt_u2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t rt_u1_a2 __attribute__((aligned(2)));
+
+// V consecutive logits of a row from p, which has n left from there (the others: -inf, as masked).  kEnds: the row has
+// a 16-byte word at least, so its end is read as its last word and moved to its place (65536 x 255 bf16, top 2: 47 us
+// element by element, 30 so); kWhole: no lane sees the row's end; kElements: shorter rows, and where time does not
+// count.
+enum { kElements, kEnds, kWhole };
 template <typename TIn, int V>
-__device__ __forceinline__ void rt_load_row(const TIn* p, int n, bool vec, float (&x)[V]) {
-  if (vec && n >= V) {
-    if constexpr (sizeof(TIn) == 2) {
+__device__ __forceinline__ void rt_load_row(const TIn* p, int n, int words, float (&x)[V]) {
+  constexpr int W = 16 / (int)sizeof(TIn);
+  if (words != kElements) {
 #pragma unroll
-      for (int q = 0; q < V / 8; ++q) {
-        const uint4 w = reinterpret_cast<const uint4*>(p)[q];
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    for (int q = 0; q < V / W; ++q) {
+      const int left = n - q * W;
+      float* y = x + q * W;
+      v4u32 w = {0u, 0u, 0u, 0u};
+      if (left > 0) {
+        const TIn* at = p + q * W + (left < W ? left - W : 0);
+        if constexpr (sizeof(TIn) == 2) w = *reinterpret_cast<const rt_u4_a2*>(at);
+        else w = *reinterpret_cast<const rt_u4_a4*>(at);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[8 * q + 2 * i] = __uint_as_float(ww[i] << 16);
-          x[8 * q + 2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(TIn) == 2) {
+          y[2 * i] = __uint_as_float(w[i] << 16);
+          y[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+          y[i] = __uint_as_float(w[i]);
         }
       }
-    } else {
+    }
+    if (words == kWhole) return;
 #pragma unroll
-      for (int q = 0; q < V / 4; ++q) {
-        const float4 w = reinterpret_cast<const float4*>(p)[q];
-        x[4 * q] = w.x; x[4 * q + 1] = w.y; x[4 * q + 2] = w.z; x[4 * q + 3] = w.w;
+    for (int q = 0; q < V / W; ++q) {
+      const int left = n - q * W;
+      float* y = x + q * W;
+      if (left < W) {
+        const int by = left > 0 ? W - left : W;
+#pragma unroll
+        for (int o = W; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < W; ++i) y[i] = by & o ? (i + o < W ? y[i + o] : -__builtin_inff()) : y[i];
       }
     }
   } else {
@@ -121,7 +148,7 @@ struct RouteKernelArgs {
   float scale;
   int32_t* hist;             // [nchunk][rt_hist_ld(E)] slots of the chunk's tokens at each expert
   int nchunk; int64_t chunk; // tokens per chunk
-  int vec;
+  int words;                 // of rt_load_row
   int group_lanes;           // lanes of an expert group where groups are whole power-of-two runs of lanes, else 0
 };
 
@@ -392,7 +419,7 @@ template <typename TIn, int V, bool ByLogit>
 __device__ __forceinline__ int rt_choose64(const RouteKernelArgs& a, const TIn* row, int per) {
   const int lane = threadIdx.x & 63, e0 = lane * V, n = a.E - e0;
   float x[V], bias[V], top = -__builtin_inff();
-  rt_load_row<TIn, V>(row + e0, n, false, x);
+  rt_load_row<TIn, V>(row + e0, n, kElements, x);
   double key[V];
   const bool sums = a.groups > 1 && a.group_top == 2;      // the groups' order needs the scores
   if (!ByLogit || sums) {
@@ -433,8 +460,10 @@ __device__ __forceinline__ int rt_choose64(const RouteKernelArgs& a, const TIn* 
   return mine;
 }
 
-// L lanes of a wave hold a token's row, V consecutive experts each (L V >= E, L >= top_k, L >= groups).
-template <typename TIn, int L, int V, bool ByLogit>
+// L lanes of a wave hold a token's row, V consecutive experts each (L V >= E, L >= top_k, L >= groups).  Whole:
+// L V = E; a kernel of its own, since the code for a row's end costs the others registers (65536 x 256 fp32, top 2:
+// 30 us, 33 with it).
+template <typename TIn, int L, int V, bool ByLogit, bool Whole>
 __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteKernelArgs a) {
   extern __shared__ __attribute__((aligned(16))) char rt_lds[];
   int32_t* base = reinterpret_cast<int32_t*>(rt_lds);
@@ -463,7 +492,7 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteKernelArgs a) {
     int per = groups_per;
     asm volatile("" : "+v"(per));      // else a quotient per place would be kept for the whole loop, and spilled
     float x[V];
-    rt_load_row<TIn, V>(logits + t * a.ld + e0, a.E - e0, a.vec != 0, x);
+    rt_load_row<TIn, V>(logits + t * a.ld + e0, Whole ? V : a.E - e0, Whole ? kWhole : a.words, x);
     bool row_odd = false;                                 // a NaN or +inf logit: the softmax is NaN
     float shift = 0.f;
     if (!a.sigmoid) {
@@ -623,12 +652,12 @@ __global__ __launch_bounds__(kRtThreads) void route_place_kernel(RouteKernelArgs
 constexpr int kRbThreads = 256;
 struct RouteBwdKernelArgs {
   const void* logits; int64_t ld; const int32_t* ids; const float* dweights; void* dlogits; int64_t ld_d;
-  int64_t T; int E, K, sigmoid, renorm; float scale; int vec, vec_out;
+  int64_t T; int E, K, sigmoid, renorm; float scale; int words;
 };
 
 // Word of W elements at p, of which n exist.
 template <typename TIn, int W>
-__device__ __forceinline__ void rt_store_word(TIn* p, int n, bool vec, const float* v) {
+__device__ __forceinline__ void rt_store_word(TIn* p, int n, const float* v) {
   if constexpr (sizeof(TIn) == 2) {
     typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
     typedef float f2 __attribute__((ext_vector_type(2)));
@@ -638,20 +667,33 @@ __device__ __forceinline__ void rt_store_word(TIn* p, int n, bool vec, const flo
       const f2 q = {v[2 * i], v[2 * i + 1]};
       w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(q, bf2));
     }
-    if (vec && n >= W) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < n) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    if (n >= W) {
+      *reinterpret_cast<rt_u4_a2*>(p) = v4u32{w[0], w[1], w[2], w[3]};
+    } else {                           // the row's end: 4, 2 and 1 elements
+      uint32_t a = w[0], b = w[1];
+      if (n & 4) {
+        *reinterpret_cast<rt_u2_a2*>(p) = rt_u2_a2{a, b};
+        a = w[2]; b = w[3];
+        p += 4;
+      }
+      if (n & 2) {
+        *reinterpret_cast<rt_u1_a2*>(p) = a;
+        a = b;
+        p += 2;
+      }
+      if (n & 1) *p = (uint16_t)a;
     }
   } else {
-    if (vec && n >= W) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    if (n >= W) {
+      *reinterpret_cast<rt_u4_a4*>(p) = v4u32{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
     } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < n) p[i] = v[i];
+      float a = v[0];
+      if (n & 2) {
+        *reinterpret_cast<rt_u2_a4*>(p) = rt_u2_a4{__float_as_uint(a), __float_as_uint(v[1])};
+        a = v[2];
+        p += 2;
+      }
+      if (n & 1) *p = a;
     }
   }
 }
@@ -679,7 +721,7 @@ __global__ __launch_bounds__(kRbThreads) void route_backward_kernel(RouteBwdKern
     for (int q = 0; q < NQ; ++q) {
       const int e = (q * L + sub) * W;
       float word[W];
-      rt_load_row<TIn, W>(row + e, a.E - e, a.vec != 0, word);      // -inf past E
+      rt_load_row<TIn, W>(row + e, a.E - e, a.words, word);      // -inf past E
 #pragma unroll
       for (int i = 0; i < W; ++i) x[q * W + i] = word[i];
     }
@@ -737,7 +779,7 @@ __global__ __launch_bounds__(kRbThreads) void route_backward_kernel(RouteBwdKern
       const float s = mine[e + i];
       o[i] = full ? x[q * W + i] * inv * (s - dot) : s;
     }
-    if (act && e < a.E) rt_store_word<TIn, W>(out + e, a.E - e, a.vec_out != 0, o);
+    if (act && e < a.E) rt_store_word<TIn, W>(out + e, a.E - e, o);
   }
 }
 
@@ -769,10 +811,6 @@ void rt_dispatch(int L, int E, F&& f) {
 // One launch, one workgroup, up to this many slots and two passes over the tokens.
 bool rt_single(int64_t T, int E, int K, int L) { return E <= kRtThreads && T * K <= 1024 && T * L <= 2 * kRtThreads; }
 
-bool rt_rows_aligned(const void* p, int64_t ld, int esize) {
-  return ((uintptr_t)p & 15u) == 0 && (ld * esize) % 16 == 0;
-}
-
 }  // namespace
 
 size_t route_workspace(int64_t T, int E) {
@@ -786,9 +824,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
   k.T = a.T; k.E = a.E; k.K = a.K; k.groups = a.groups; k.keep = a.keep; k.group_top = a.group_top;
   k.sigmoid = a.sigmoid; k.renorm = a.renorm; k.scale = a.scale; k.hist = (int32_t*)a.ws;
   const int esize = a.dtype == S3R_BF16 ? 2 : 4;
-  k.vec = rt_rows_aligned(a.logits, a.ld, esize) ? 1 : 0;
   if (a.keep == a.groups) k.groups = k.keep = 1;       // every group stays
   const int L = rt_lanes(a.E, a.K, k.groups);
+  k.words = a.E * esize < 16 ? kElements : a.E % (8 * L) ? kEnds : kWhole;      // 8 or 16 experts a lane
   const int per = a.E / k.groups, V = a.E > 8 * L ? 16 : 8, run = per / V;
   if (k.groups > 1 && per % V == 0 && (run & (run - 1)) == 0) k.group_lanes = run;
   const bool by_score = a.bias != nullptr;      // else the logits' order is the scores'
@@ -807,13 +845,17 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
   rt_dispatch(L, a.E, [&](auto l, auto v) {
     constexpr int LL = decltype(l)::value, VV = decltype(v)::value;
     const dim3 grid((unsigned)k.nchunk), block((unsigned)threads);
-    auto go = [&](auto by_logit) {
-      constexpr bool B = decltype(by_logit)::value;
-      if (a.dtype == S3R_BF16) hipLaunchKernelGGL((route_kernel<uint16_t, LL, VV, B>), grid, block, lds, st, k);
-      else hipLaunchKernelGGL((route_kernel<float, LL, VV, B>), grid, block, lds, st, k);
+    auto go = [&](auto by_logit, auto whole) {
+      constexpr bool B = decltype(by_logit)::value, F = decltype(whole)::value;
+      if (a.dtype == S3R_BF16) hipLaunchKernelGGL((route_kernel<uint16_t, LL, VV, B, F>), grid, block, lds, st, k);
+      else hipLaunchKernelGGL((route_kernel<float, LL, VV, B, F>), grid, block, lds, st, k);
     };
-    if (by_score) go(std::false_type{});
-    else go(std::true_type{});
+    auto pick = [&](auto by_logit) {
+      if (k.words == kWhole) go(by_logit, std::true_type{});
+      else go(by_logit, std::false_type{});
+    };
+    if (by_score) pick(std::false_type{});
+    else pick(std::true_type{});
   });
   if (k.nchunk > 1) {
     // A thread per slot of a chunk and per expert, to the next of three sizes: fewer waves meet at each barrier.
@@ -832,9 +874,8 @@ hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
   k.logits = a.logits; k.ld = a.ld; k.ids = a.ids; k.dweights = a.dweights; k.dlogits = a.dlogits; k.ld_d = a.ld_d;
   k.T = a.T; k.E = a.E; k.K = a.K; k.sigmoid = a.sigmoid; k.renorm = a.renorm; k.scale = a.scale;
   const int esize = a.dtype == S3R_BF16 ? 2 : 4;
-  k.vec = rt_rows_aligned(a.logits, a.ld, esize) ? 1 : 0;
-  k.vec_out = rt_rows_aligned(a.dlogits, a.ld_d, esize) ? 1 : 0;
   const int L = rt_lanes(a.E, a.K, 1);
+  k.words = a.E * esize < 16 ? kElements : a.E % (8 * L) ? kEnds : kWhole;      // 8 or 16 experts a lane
   rt_dispatch(L, a.E, [&](auto l, auto v) {
     constexpr int LL = decltype(l)::value, VV = decltype(v)::value;
     const int64_t per = (kRbThreads / 64) * (64 / LL);

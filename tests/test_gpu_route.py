@@ -66,6 +66,33 @@ def test_route_infinite_bias(groups, keep, top, score):
     check(logits(300, 64, torch.float32, 3), 5, score=score, bias=b, groups=groups, keep=keep, group_top=top)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset", [0, 1, 8])
+def test_route_of_every_width(dtype, offset):
+    """Row ends at every place of a 16-byte word, with +inf around the rows; nothing else of the gradient is written."""
+    T = 9
+    for E in [*range(1, 34), 127, 129, 131, 252, 255, 257, 1019]:
+        k = min(E, 3)
+        wide = torch.full((T + 2, E + 21), float("inf"), dtype=dtype, device=DEV)
+        x = wide[1:T + 1, offset:offset + E]
+        x.copy_(logits(T, E, dtype, E))
+        bias = torch.randn(E, device=DEV) * 0.1
+        check(x, k, renorm=False)
+        r = check(x, k, score=E % 2, bias=bias)
+        dw = torch.randn(T, k, device=DEV)
+        for score, renorm in ((0, False), (1, False)):
+            out = torch.full((T + 2, E + 21), 9.0, dtype=dtype, device=DEV)
+            dx = out[1:T + 1, offset:offset + E]
+            s3r.s3r_route_backward(s3r.route_desc(T, E, k, score=score, renorm=renorm), x, r.ids, dw, dx)
+            xs = host(x.double())
+            exp = ref.backward(xs, host(r.ids), host(dw), score=score, renorm=renorm)
+            # of a gradient of at most |dw|: exponentials and sums, |x| U and 80 roundings; half a bf16 step
+            tol = U * (80 + 4 * np.abs(xs).max()) * np.abs(host(dw)).max() * 4
+            step = half(dtype) * (1 + 1e-3) if dtype == torch.bfloat16 else 0.0
+            assert (np.abs(host(dx.double()) - exp) <= tol + step * np.abs(exp)).all()
+            assert (out == 9).sum() >= out.numel() - dx.numel()
+
+
 @pytest.mark.parametrize("groups, keep", [(1, 1), (4, 2)])
 @pytest.mark.parametrize("bias", [False, True])
 def test_ties_go_to_the_lower_index(groups, keep, bias):
