@@ -589,8 +589,8 @@ int s3r_route_backward(const s3r_route_desc* desc, const void* logits, int32_t d
                        const float* dweights, void* dlogits, int64_t ld_d, hipStream_t stream);
 
 /* ---- tokens to the experts' rows and back ---------------------------------
- * Rows of D elements, all F32 or all BF16 (dtype), any alignment (16-byte-aligned
- * bases, leading dims and widths take the vector path).  slot_row [T x k] int32
+ * Rows of D elements, all F32 or all BF16 (dtype), any alignment (rows of 16
+ * bytes or more take 16-byte accesses).  slot_row [T x k] int32
  * as s3r_route writes it; an index outside 0 .. R-1 is no row: it is skipped, and
  * its weight's gradient is 0.  Rows that no slot names are left as they are; no two
  * slots may name one row.  k >= 1.
