@@ -137,6 +137,24 @@ def test_linear_writes_its_rows_and_columns_only():
             assert (big[0] == 5).all() and (big[1 + rows:] == 5).all() and (big[:, :3] == 5).all() and (big[:, 93:] == 5).all()
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M, K", [(5, 200), (300, 129), (1500, 96)])
+def test_linear_into_any_alignment(M, K, out):
+    """Results of every width mod 16 bytes, from any element on, have an aligned result's bits; nothing else is written."""
+    A = s3r.mx_rows(matrix((M, K), torch.bfloat16, M))
+    W = matrix((2064, K), torch.bfloat16, K)
+    for N in (1, 7, 65, 130, 1411, *range(2056, 2065)):
+        w = s3r.mx_rows(W[:N])
+        exp = s3r.mx_product(A, w, out_dtype=out)
+        for offset in (0, 1, 2, 3, 8):
+            wide = torch.full((M + 2, N + 17), 9.0, dtype=out, device=DEV)
+            y = wide[1:M + 1, offset:offset + N]
+            s3r.s3r_mx_product(A, w, y)
+            assert torch.equal(y, exp)
+            y.fill_(9)
+            assert (wide == 9).all()
+
+
 def test_empty_products():
     w = s3r.mx_rows(matrix((20, 64), torch.bfloat16, 9))
     assert s3r.mx_linear(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), w).shape == (0, 20)
