@@ -29,14 +29,69 @@ class Saved:
     rows: object           # bf16 [R x D]: the experts' outputs
 
 
+class _Codes:
+    """A weight's codes, kept between the calls that need them and made again when the weight has changed.
+
+    ``of`` sees a change that torch counts (an operation in place) and another tensor; ``renew`` is for the others.
+    The same tensor's codes keep their buffers.  While a graph is recorded, ``of`` makes a changed weight's codes as a
+    part of the graph and keeps nothing.
+    """
+
+    def __init__(self, make):
+        self.make = make                # make(W, codes or None): the codes of W, in the buffers given
+        self.codes = self.weight = self.version = None
+
+    def of(self, W):
+        import torch
+        if self.weight is not W or self.version != _version(W):
+            if torch.cuda.is_current_stream_capturing():
+                return self.make(W, None)
+            self.renew(W)
+        return self.codes
+
+    def renew(self, W):
+        import torch
+        if self.weight is not W and torch.cuda.is_current_stream_capturing():
+            return                      # no buffers yet that outlive the graph
+        self.codes = self.make(W, self.codes if self.weight is W else None)
+        self.weight, self.version = W, _version(W)
+
+
+def _version(W):
+    return None if W.is_inference() else W._version
+
+
 class MoeLayer:
-    """gate_up: bf16 [E x 2F x D] (an expert's gate rows, then its up rows), down: bf16 [E x D x F]."""
+    """gate_up: bf16 [E x 2F x D] (an expert's gate rows, then its up rows), down: bf16 [E x D x F].
+
+    The layer keeps codes of the weights: MXFP4 from the start, INT8 from the first backward pass.  It follows weights
+    that torch's operations change in place, as an optimizer's step does, or that other tensors replace.  After changes
+    that torch does not count (through ``.data``, by a kernel that was given the address, by the replay of a graph, to
+    inference tensors), and before the replay of a graph that holds the layer's own calls, call ``weights_changed``.
+    """
 
     def __init__(self, gate_up, down, top_k, **router):
         self.gate_up, self.down, self.top_k, self.router = gate_up, down, top_k, router
         self.ff = down.shape[2]
-        self.mx_gate_up, self.mx_down = s3r.mx_rows(gate_up), s3r.mx_rows(down)
-        self._int8 = None
+        self._mx = _Codes(_mx_weights), _Codes(_mx_weights)
+        self._int8 = _Codes(_int8_gate_up), _Codes(_int8_weights)
+        for codes, W in zip(self._mx, (gate_up, down)):
+            codes.renew(W)
+
+    @property
+    def mx_gate_up(self):
+        return self._mx[0].of(self.gate_up)
+
+    @property
+    def mx_down(self):
+        return self._mx[1].of(self.down)
+
+    def weights_changed(self):
+        """Make the codes that the layer keeps again, in their buffers, from the weights as they are."""
+        for pair in (self._mx, self._int8):
+            for codes, W in zip(pair, (self.gate_up, self.down)):
+                if codes.weight is not None:
+                    codes.renew(W)
 
     def forward(self, x, logits, bias=None):
         """(y, Saved) of tokens x [T x D] bf16 with router logits [T x E]."""
@@ -51,26 +106,46 @@ class MoeLayer:
         """(dx f32, dlogits, dgate_up f32, ddown f32) from dy [T x D] bf16."""
         import torch
         r, F = saved.routed, self.ff
-        if self._int8 is None:           # the weights' INT8 codes, scales and column sums, once per weight update
-            self._int8 = [_int8_weights(w) for w in (self.gate_up[:, :F], self.gate_up[:, F:], self.down)]
+        gate_w, up_w = self._int8[0].of(self.gate_up)
+        down_w = self._int8[1].of(self.down)
         gate, up = saved.gate_up[:, :F].contiguous(), saved.gate_up[:, F:].contiguous()
         drows, dweights = s3r.combine_backward(dy, saved.rows, r)
         dlogits = s3r.route_backward(r, saved.logits, dweights)
         g = gate.float()
         hidden = (g * torch.sigmoid(g) * up.float()).to(torch.bfloat16)
-        dh, ddown = _linear_backward(drows, _int8_rows(hidden, r.offsets), self._int8[2], r.offsets, seed, 4 * layer_id)
+        dh, ddown = _linear_backward(drows, _int8_rows(hidden, r.offsets), down_w, r.offsets, seed, 4 * layer_id)
         dgate, dup = s3r.swiglu_backward(dh, gate, up)
         xq = _int8_rows(s3r.dispatch(saved.x, r), r.offsets)
-        dxr, dwg = _linear_backward(dgate, xq, self._int8[0], r.offsets, seed, 4 * layer_id + 1)
-        dxr, dwu = _linear_backward(dup, xq, self._int8[1], r.offsets, seed, 4 * layer_id + 2, into=dxr)
+        dxr, dwg = _linear_backward(dgate, xq, gate_w, r.offsets, seed, 4 * layer_id + 1)
+        dxr, dwu = _linear_backward(dup, xq, up_w, r.offsets, seed, 4 * layer_id + 2, into=dxr)
         return s3r.combine(dxr, r, weighted=False), dlogits, torch.cat([dwg, dwu], dim=1), ddown
 
 
-def _int8_weights(W):
+def _mx_weights(W, codes):
+    """MXFP4 rows of W [E x N x K]."""
+    if codes is None:
+        return s3r.mx_rows(W)
+    s3r.s3r_mx_rows(W, codes)
+    return codes
+
+
+def _int8_weights(W, codes):
     """(codes [E x N x K], s_w [E x N], r_W [E x K]) of W [E x N x K]."""
-    E, N, K = W.shape
-    q = s3r.forward_operand(W.reshape(E * N, K), rows_per_example=N)
-    return q.Q.unflatten(0, (E, N)), q.delta.reshape(E, N), q.code_colsum
+    import torch
+    (E, N, K), dev = W.shape, W.device
+    d = s3r.qdesc(E * N, K, N, s3r.RTNE, s3r.EC_NONE, s3r.PER_TOKEN)
+    Q, s_w, r_W = codes or (s3r.q_buffer(E * N, K, dev).unflatten(0, (E, N)),
+                            torch.empty(E, N, dtype=torch.float32, device=dev),
+                            torch.empty(E, K, dtype=torch.int32, device=dev))
+    ws = torch.empty(s3r.s3r_quantize_workspace(d), dtype=torch.uint8, device=dev)
+    s3r.s3r_quantize(d, W.reshape(E * N, K), None, None, Q.flatten(0, 1), s_w, r_W, ws=ws)
+    return Q, s_w, r_W
+
+
+def _int8_gate_up(W, codes):
+    """Those of the gate rows and those of the up rows."""
+    F = W.shape[1] // 2
+    return [_int8_weights(w, c) for w, c in zip((W[:, :F], W[:, F:]), codes or (None, None))]
 
 
 def _int8_rows(X, offsets):

@@ -84,3 +84,69 @@ def test_empty_batch_and_one_token(step):
     # one token's rows go another way through the product kernels: the order of fp32 sums may differ, then bf16
     assert (np.abs(f(y) - f(full[:1])) <= 2.0 ** -6 * np.abs(f(full[:1])).max()).all()
     assert layer.forward(x[:0], logits[:0])[0].shape == (0, D)
+
+
+# ------------------------------------------------------- changed weights ----
+
+def fresh(layer):
+    return moe.MoeLayer(layer.gate_up.clone(), layer.down.clone(), layer.top_k, **layer.router)
+
+
+def same_step(layer, x, logits, dy, other=None):
+    """A training step of the layer has the bits of one of a layer made anew from its weights."""
+    other = other or fresh(layer)
+    y, saved = layer.forward(x, logits)
+    got = y, *layer.backward(saved, dy)
+    y, saved = other.forward(x, logits)
+    return all(torch.equal(a, b) for a, b in zip(got, (y, *other.backward(saved, dy))))
+
+
+def test_weights_changed_in_place(step):
+    """As an optimizer does between two steps, and once between construction and the first backward pass."""
+    g = torch.Generator(DEV).manual_seed(6)
+    x, logits, dy = step[1:4]
+    layer = moe.MoeLayer(normal(g, E, 2 * F, D, std=0.1), normal(g, E, D, F, std=0.1), K)
+    layer.gate_up.mul_(1.5)
+    assert same_step(layer, x, logits, dy)
+    layer.down.add_(normal(g, E, D, F, std=0.1))
+    assert same_step(layer, x, logits, dy)
+    layer.gate_up.sub_(normal(g, E, 2 * F, D, std=0.1))
+    layer.down.mul_(-1)
+    assert same_step(layer, x, logits, dy)
+    layer.down = normal(g, E, D, F, std=0.1)             # another tensor
+    assert same_step(layer, x, logits, dy)
+
+
+def test_weights_changed_unseen(step):
+    """Through .data, which torch does not count: the codes follow the call that says so."""
+    g = torch.Generator(DEV).manual_seed(7)
+    x, logits, dy = step[1:4]
+    layer = moe.MoeLayer(normal(g, E, 2 * F, D, std=0.1), normal(g, E, D, F, std=0.1), K)
+    assert same_step(layer, x, logits, dy)
+    layer.gate_up.data.mul_(0.5)
+    layer.down.data.mul_(-1)
+    layer.weights_changed()
+    assert same_step(layer, x, logits, dy)
+
+
+def test_codes_in_a_graph(step):
+    """A graph takes the kept codes, which weights_changed renews in place, or makes its own of a weight changed since."""
+    g = torch.Generator(DEV).manual_seed(9)
+    x, logits = step[1:3]
+    for changed in (False, True):
+        layer = moe.MoeLayer(normal(g, E, 2 * F, D, std=0.1), normal(g, E, D, F, std=0.1), K)
+        layer.forward(x, logits)
+        if changed:
+            layer.gate_up.mul_(1.5)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y, _ = layer.forward(x, logits)
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, fresh(layer).forward(x, logits)[0])
+            assert torch.equal(y, layer.forward(x, logits)[0])
+            layer.gate_up.mul_(1.5)
+            layer.down.sub_(0.01)
+            layer.weights_changed()
