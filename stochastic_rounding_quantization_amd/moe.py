@@ -33,13 +33,13 @@ class _Codes:
     """A weight's codes, kept between the calls that need them and made again when the weight has changed.
 
     ``of`` sees a change that torch counts (an operation in place) and another tensor; ``renew`` is for the others.
-    The same tensor's codes keep their buffers.  While a graph is recorded, ``of`` makes a changed weight's codes as a
-    part of the graph and keeps nothing.
+    The same tensor's codes keep their buffers.  A call on another stream than the one that made the codes waits for
+    them.  While a graph is recorded, ``of`` makes a changed weight's codes as a part of the graph and keeps nothing.
     """
 
     def __init__(self, make):
         self.make = make                # make(W, codes or None): the codes of W, in the buffers given
-        self.codes = self.weight = self.version = None
+        self.codes = self.weight = self.version = self.stream = self.ready = None
 
     def of(self, W):
         import torch
@@ -47,14 +47,20 @@ class _Codes:
             if torch.cuda.is_current_stream_capturing():
                 return self.make(W, None)
             self.renew(W)
+        elif self.stream != s3r._stream(None) and not torch.cuda.is_current_stream_capturing():
+            self.ready.wait()           # (torch.cuda.graph synchronises the device before it records)
         return self.codes
 
     def renew(self, W):
         import torch
-        if self.weight is not W and torch.cuda.is_current_stream_capturing():
+        recording = torch.cuda.is_current_stream_capturing()
+        if recording and self.weight is not W:
             return                      # no buffers yet that outlive the graph
         self.codes = self.make(W, self.codes if self.weight is W else None)
         self.weight, self.version = W, _version(W)
+        if not recording:
+            self.stream, self.ready = s3r._stream(None), self.ready or torch.cuda.Event()
+            self.ready.record()
 
 
 def _version(W):

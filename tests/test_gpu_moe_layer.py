@@ -129,6 +129,30 @@ def test_weights_changed_unseen(step):
     assert same_step(layer, x, logits, dy)
 
 
+def test_codes_for_another_stream(step):
+    """A stream that did not make the codes waits for them: the second pass follows the first with no word between them."""
+    g = torch.Generator(DEV).manual_seed(8)
+    x, logits, dy = step[1:4]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        layer = moe.MoeLayer(normal(g, E, 2 * F, D, std=0.1), normal(g, E, D, F, std=0.1), K)
+        other = fresh(layer)
+        y, saved = other.forward(x, logits)
+        want = y, *other.backward(saved, dy)
+        for renewed in (False, True):
+            if renewed:
+                layer.gate_up.mul_(1.0)                  # the same values, made again
+            torch.cuda.synchronize()
+            torch.randn(1 << 24, device=DEV).sort()       # the codes of this stream's pass come after this
+            y, saved = layer.forward(x, logits)
+            layer.backward(saved, dy)
+            with torch.cuda.stream(side):
+                y, saved = layer.forward(x, logits)
+                got = y, *layer.backward(saved, dy)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_codes_in_a_graph(step):
     """A graph takes the kept codes, which weights_changed renews in place, or makes its own of a weight changed since."""
     g = torch.Generator(DEV).manual_seed(9)
