@@ -112,6 +112,10 @@ class MoeLayer:
         """(dx f32, dlogits, dgate_up f32, ddown f32) from dy [T x D] bf16."""
         import torch
         r, F = saved.routed, self.ff
+        if dy.shape[0] == 0:             # the grouped calls take no empty lists of steps
+            zeros = dict(dtype=torch.float32, device=dy.device)
+            return (torch.zeros(dy.shape, **zeros), torch.empty_like(saved.logits),
+                    torch.zeros(self.gate_up.shape, **zeros), torch.zeros(self.down.shape, **zeros))
         gate_w, up_w = self._int8[0].of(self.gate_up)
         down_w = self._int8[1].of(self.down)
         gate, up = saved.gate_up[:, :F].contiguous(), saved.gate_up[:, F:].contiguous()

@@ -86,6 +86,15 @@ def test_empty_batch_and_one_token(step):
     assert layer.forward(x[:0], logits[:0])[0].shape == (0, D)
 
 
+def test_gradients_without_tokens(step):
+    layer, x, logits, dy = step[:4]
+    y, saved = layer.forward(x[:0], logits[:0])
+    dx, dlogits, dgu, dd = layer.backward(saved, dy[:0])
+    assert dx.shape == (0, D) and dlogits.shape == (0, E) and dx.dtype == dgu.dtype == dd.dtype == torch.float32
+    assert dgu.shape == layer.gate_up.shape and dd.shape == layer.down.shape and (dgu == 0).all() and (dd == 0).all()
+    assert dlogits.dtype == logits.dtype
+
+
 # ------------------------------------------------------- changed weights ----
 
 def fresh(layer):
