@@ -32,15 +32,21 @@ def choose(x, top_k, *, score=SOFTMAX, bias=None, groups=1, keep=1, group_top=1)
     """ids int32 [T x top_k]."""
     x = np.asarray(x, np.float64)
     T, E = x.shape
-    by_logit = bias is None and (groups == 1 or group_top == 1)
-    key = x.copy() if by_logit else scores(x, score) + (0.0 if bias is None else np.asarray(bias, np.float64))
-    key = np.where(np.isneginf(x) | np.isnan(x) | np.isnan(key), -np.inf, key)
+    masked = np.isneginf(x) | np.isnan(x)
+    key = scores(x, score) + (0.0 if bias is None else np.asarray(bias, np.float64))
+    key = np.where(masked | np.isnan(key), -np.inf, key)
+    # without a bias the logits stand for the scores, wherever these are not added up: their order, also where fp64
+    # scores meet
+    by_logit = np.where(masked, -np.inf, x)
+    group_key = by_logit if bias is None and group_top == 1 else key
+    if bias is None:
+        key = by_logit if groups == 1 or group_top == 1 else np.where(np.isneginf(key), -np.inf, x)
     per = E // groups
     ids = np.empty((T, top_k), np.int32)
     for t in range(T):
-        k = key[t]
+        k, g_key = key[t], group_key[t]
         if groups > 1:
-            of = [sum(sorted(k[g * per:(g + 1) * per], reverse=True)[:group_top]) for g in range(groups)]
+            of = [sum(sorted(g_key[g * per:(g + 1) * per], reverse=True)[:group_top]) for g in range(groups)]
             best = set(_descending(of)[:keep])
             k = np.array([k[e] if e // per in best else -np.inf for e in range(E)])
         ids[t] = _descending(k)[:top_k]

@@ -212,6 +212,16 @@ def test_route_backward_masked_and_foreign_ids(score, renorm):
     assert (np.abs(got - exp) <= 2 * U * (64 + 2 * 160) * np.abs(host(g)).max()).all()
 
 
+# ------------------------------------------------- groups by sums of two ----
+
+def test_groups_of_two_choose_by_logits_where_scores_meet():
+    x = torch.tensor([[40.0, 50.0, 0.0, 0.0], [40.0, 50.0, 60.0, 39.0]], device=DEV)
+    r = check(x, 1, score=1, groups=2, keep=1, group_top=2)
+    assert host(r.ids).tolist() == [[1], [1]]
+    x = torch.tensor([[-800.0, -790.0, 0.0, -1000.0]], device=DEV)
+    assert host(check(x, 4, groups=2, keep=2, group_top=2).ids).tolist() == [[2, 1, 0, 3]]
+
+
 # ------------------------------------------------------------------ rows ----
 
 def slots(T, k, R, seed):

@@ -83,3 +83,13 @@ def test_mx_rows_pads_with_zeros():
     assert q["codes"].shape == (3, 128) and (q["codes"][:, 77:] == 0).all() and (q["scale"][:, 3:] == 0).all()
     step = np.repeat(np.ldexp(1.0, q["scale"].astype(int) - 127), 32, axis=1)[:, :77]
     assert (np.abs(q["deq"] - M) <= step).all()           # half the widest spacing, 2
+
+
+def test_two_largest_groups_choose_by_logits_where_scores_meet():
+    """Without a bias the scores order the groups and the logits the experts in them: equal scores are no tie."""
+    x = np.array([[40.0, 50.0, 0.0, 0.0]])                # both sigmoids are 1 in fp64
+    assert route.choose(x, 1, score=route.SIGMOID, groups=2, keep=1, group_top=2).tolist() == [[1]]
+    x = np.array([[-800.0, -790.0, 0.0, -1000.0]])        # all softmax scores but one are 0
+    assert route.choose(x, 4, groups=2, keep=2, group_top=2).tolist() == [[2, 1, 0, 3]]
+    x = np.array([[-800.0, np.nan, 0.0, -np.inf]])        # a NaN logit makes the row's scores NaN: all rank as -inf
+    assert route.choose(x, 3, groups=2, keep=2, group_top=2).tolist() == [[0, 1, 2]]
