@@ -46,7 +46,8 @@ def choose(x, top_k, *, score=SOFTMAX, bias=None, groups=1, keep=1, group_top=1)
     for t in range(T):
         k, g_key = key[t], group_key[t]
         if groups > 1:
-            of = [sum(sorted(g_key[g * per:(g + 1) * per], reverse=True)[:group_top]) for g in range(groups)]
+            with np.errstate(invalid="ignore"):          # inf - inf: NaN
+                of = [sum(sorted(g_key[g * per:(g + 1) * per], reverse=True)[:group_top]) for g in range(groups)]
             best = set(_descending(of)[:keep])
             k = np.array([k[e] if e // per in best else -np.inf for e in range(E)])
         ids[t] = _descending(k)[:top_k]

@@ -272,6 +272,14 @@ __device__ __forceinline__ void rt_keys(const RouteKernelArgs& a, const float (&
 // that rt_take32 puts an index in.
 __device__ __forceinline__ float rt_margin(float key) { return 0x1p-19f + 0x1p-18f * fabsf(key); }
 
+// A group's score from its two largest keys; inf - inf is none, and ranks last (a NaN would beat nothing and lose to
+// nothing: one group more than `keep` would stay).
+template <typename Key>
+__device__ __forceinline__ Key rt_pair(Key m1, Key m2) {
+  const Key sum = m1 + m2;
+  return sum == sum ? sum : rt_neg_inf<Key>();
+}
+
 // The best `keep` groups stay, the keys of the others become -inf.  Groups of whole runs of lanes: two
 // largest keys in the lane, then across the run.  Any groups: one after another over all lanes.
 // Returns whether the last kept and the first dropped group are within the margin.
@@ -293,7 +301,7 @@ __device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int gro
       m2 = lo > hi2 ? lo : hi2;
       m1 = n1 > m1 ? n1 : m1;
     }
-    if (a.group_top == 2) m1 = m1 + m2;
+    if (a.group_top == 2) m1 = rt_pair(m1, m2);
     mine = __shfl(m1, lane / L * L + (sub < a.groups ? sub : 0) * group_lanes, 64);
   } else {
     for (int g = 0; g < a.groups; ++g) {
@@ -313,7 +321,7 @@ __device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int gro
         for (int i = 0; i < V; ++i)
           if ((e0 + i) / per == g && e0 + i != at && key[i] > m2) m2 = key[i];
         m2 = rt_max<L>(m2);
-        m1 = m1 + m2;
+        m1 = rt_pair(m1, m2);
       }
       if (sub == g) mine = m1;
     }

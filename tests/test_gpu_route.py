@@ -214,6 +214,29 @@ def test_route_backward_masked_and_foreign_ids(score, renorm):
 
 # ------------------------------------------------- groups by sums of two ----
 
+SUMS = [(8, 4), (32, 4), (36, 3), (256, 8)]      # experts and groups: of two, of a lane, of neither, of several lanes
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E, groups", SUMS)
+def test_group_sums_of_infinities(E, groups, score):
+    """inf - inf is no sum: the group ranks last, and no group more than `keep` stays."""
+    per = E // groups
+    x = logits(300, E, torch.float32, E)
+    b = torch.zeros(E, device=DEV)
+    b[:per] = float("-inf")
+    b[0] = float("inf")
+    for keep in (1, 2):
+        check(x, 2, score=score, bias=b, groups=groups, keep=keep, group_top=2)
+    b[:] = 0
+    b[per] = float("inf")                                 # beside masked logits
+    x[:150, per + 1:2 * per] = float("-inf")
+    x[:20, 2 * per:] = float("-inf")
+    x[:10] = float("-inf")
+    for keep in (1, 2):
+        check(x, 2, score=score, bias=b, groups=groups, keep=keep, group_top=2)
+
+
 def test_groups_of_two_choose_by_logits_where_scores_meet():
     x = torch.tensor([[40.0, 50.0, 0.0, 0.0], [40.0, 50.0, 60.0, 39.0]], device=DEV)
     r = check(x, 1, score=1, groups=2, keep=1, group_top=2)

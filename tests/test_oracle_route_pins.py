@@ -93,3 +93,10 @@ def test_two_largest_groups_choose_by_logits_where_scores_meet():
     assert route.choose(x, 4, groups=2, keep=2, group_top=2).tolist() == [[2, 1, 0, 3]]
     x = np.array([[-800.0, np.nan, 0.0, -np.inf]])        # a NaN logit makes the row's scores NaN: all rank as -inf
     assert route.choose(x, 3, groups=2, keep=2, group_top=2).tolist() == [[0, 1, 2]]
+
+
+def test_group_sum_of_both_infinities_ranks_last():
+    b = np.array([np.inf, -np.inf, 0, 0, 1, 1])
+    x = np.zeros((1, 6))
+    assert route.choose(x, 2, bias=b, groups=3, keep=1, group_top=2).tolist() == [[4, 5]]
+    assert route.choose(x, 4, bias=b, groups=3, keep=2, group_top=2).tolist() == [[4, 5, 2, 3]]
