@@ -243,8 +243,11 @@ __device__ __forceinline__ void rt_keys(const RouteKernelArgs& a, const float (&
       }
     }
   } else {
-    // within 2^-20 + 2^-22 |key| of the fp64 keys: the hardware's exponential and reciprocal, 2^-22 each
-    // of a score that is at most 1, and |x| 2^-23 of the exponent, which |x| e^-|x| < 0.37 bounds
+    // The difference of two keys is within 2^-19 of the fp64 keys' (and the rounding of the bias's addition).  In
+    // units of 2^-24: a sigmoid has 4 each of the hardware's exponential and reciprocal, 1 of the sum, and 2 |x| of the
+    // exponent, which |x| e^-|x| < 0.37 bounds, 20 of two.  A softmax's sum has 21 (15 additions in a lane, 6 across the
+    // lanes), its reciprocal 4, and these err in both scores alike: 25 of their difference, which is at most 1, and near
+    // 1 only where the other terms, whose 4 of the exponential and 2.25 |x| of the exponent enter, are small.
     constexpr float kLog2e = 1.4426950408889634f;
     if (a.sigmoid) {
 #pragma unroll
@@ -268,8 +271,8 @@ __device__ __forceinline__ void rt_keys(const RouteKernelArgs& a, const float (&
   }
 }
 
-// Keys closer than this may be in the other order in exact arithmetic: twice their error, and the low bits
-// that rt_take32 puts an index in.
+// Keys closer than this may be in the other order in exact arithmetic: their errors, the rounding of the bias's
+// addition, and the four low bits of both that rt_take32 puts an index in (30 x 2^-23 |key|).
 __device__ __forceinline__ float rt_margin(float key) { return 0x1p-19f + 0x1p-18f * fabsf(key); }
 
 // A group's score from its two largest keys; inf - inf is none, and ranks last (a NaN would beat nothing and lose to
@@ -282,11 +285,13 @@ __device__ __forceinline__ Key rt_pair(Key m1, Key m2) {
 
 // The best `keep` groups stay, the keys of the others become -inf.  Groups of whole runs of lanes: two
 // largest keys in the lane, then across the run.  Any groups: one after another over all lanes.
-// Returns whether the last kept and the first dropped group are within the margin.
+// Returns whether a kept and a dropped group are within the margin of both.  A sum's margin is that of its keys'
+// magnitudes: 256 - 256 is as far off as the 256s are.  Keys of +-inf are exact.
 template <typename Key, int L, int V>
 __device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int group_lanes, int e0, int per, int sub, int lane,
                                                Key (&key)[V]) {
-  Key mine = rt_neg_inf<Key>();                           // lane g of the token: the score of group g
+  const bool two = a.group_top == 2;
+  Key mine = rt_neg_inf<Key>(), mine2 = mine;             // lane g of the token: the two largest keys of group g
   if (group_lanes) {
     Key m1 = rt_neg_inf<Key>(), m2 = m1;
 #pragma unroll
@@ -301,8 +306,9 @@ __device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int gro
       m2 = lo > hi2 ? lo : hi2;
       m1 = n1 > m1 ? n1 : m1;
     }
-    if (a.group_top == 2) m1 = rt_pair(m1, m2);
-    mine = __shfl(m1, lane / L * L + (sub < a.groups ? sub : 0) * group_lanes, 64);
+    const int from = lane / L * L + (sub < a.groups ? sub : 0) * group_lanes;
+    mine = __shfl(m1, from, 64);
+    if (two) mine2 = __shfl(m2, from, 64);
   } else {
     for (int g = 0; g < a.groups; ++g) {
       Key m1 = rt_neg_inf<Key>();
@@ -310,22 +316,27 @@ __device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int gro
       for (int i = 0; i < V; ++i)
         if ((e0 + i) / per == g) m1 = key[i] > m1 ? key[i] : m1;
       m1 = rt_max<L>(m1);
-      if (a.group_top == 2) {
+      Key m2 = rt_neg_inf<Key>();
+      if (two) {
         int at = 1 << 30;
 #pragma unroll
         for (int i = V - 1; i >= 0; --i)
           if ((e0 + i) / per == g && key[i] == m1) at = e0 + i;
         at = rt_min<L>(at);
-        Key m2 = rt_neg_inf<Key>();
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if ((e0 + i) / per == g && e0 + i != at && key[i] > m2) m2 = key[i];
         m2 = rt_max<L>(m2);
-        m1 = rt_pair(m1, m2);
       }
-      if (sub == g) mine = m1;
+      if (sub == g) { mine = m1; mine2 = m2; }
     }
   }
+  float margin = 0.f;
+  if constexpr (sizeof(Key) == 4) {
+    const float inf = __builtin_inff(), m1 = fabsf(mine), m2 = two ? fabsf(mine2) : 0.f;
+    margin = rt_margin(m1 < inf && m2 < inf ? m1 + m2 : 0.f);      // inf: a sum that may overflow
+  }
+  if (two) mine = rt_pair(mine, mine2);
   int rank = 0;
   for (int h = 0; h < a.groups; ++h) {
     const Key other = __shfl(mine, lane / L * L + h, 64);
@@ -335,9 +346,10 @@ __device__ __forceinline__ bool rt_keep_groups(const RouteKernelArgs& a, int gro
   const uint64_t kept = __builtin_amdgcn_ballot_w64(in && rank < a.keep) >> (lane / L * L);
   bool close = false;
   if constexpr (sizeof(Key) == 4) {
-    const float least = -rt_max<L>(in && rank < a.keep ? -mine : rt_neg_inf<float>());
-    const float most = rt_max<L>(in && rank >= a.keep ? mine : rt_neg_inf<float>());
-    close = least - most <= 2.f * rt_margin(least);       // -inf - -inf: a tie of nothing, decided by index
+    const float inf = __builtin_inff();
+    const float least = -rt_max<L>(in && rank < a.keep ? margin < inf ? margin - mine : inf : -inf);
+    const float most = rt_max<L>(in && rank >= a.keep ? margin < inf ? mine + margin : inf : -inf);
+    close = most > -inf && !(least > most);               // -inf and -inf: a tie of nothing, decided by index
   }
   if (group_lanes) {
     const bool stay = (kept >> (sub / group_lanes)) & 1;

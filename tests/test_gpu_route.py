@@ -219,6 +219,38 @@ SUMS = [(8, 4), (32, 4), (36, 3), (256, 8)]      # experts and groups: of two, o
 
 @pytest.mark.parametrize("score", [0, 1])
 @pytest.mark.parametrize("E, groups", SUMS)
+@pytest.mark.parametrize("size", [256.0, 2.0 ** 20])
+def test_group_sums_that_cancel(E, groups, size, score):
+    """A group's two largest keys of opposite signs: their sum is far more exact in fp64 than the keys are in fp32."""
+    per = E // groups
+    b = torch.full((E,), -size, device=DEV)
+    b[::per] = size
+    x = logits(4000, E, torch.float32, E)
+    check(x, 2, score=score, bias=b, groups=groups, keep=groups // 2, group_top=2)
+    check(x, 1, score=score, bias=b, groups=groups, keep=1, group_top=2)          # one key of that size
+
+
+@pytest.mark.parametrize("E, groups", SUMS)
+def test_group_sums_that_only_64_bits_tell_apart(E, groups):
+    """Sums of two that differ by 2^-30 around 1, and sums that overflow fp32."""
+    per = E // groups
+    x = torch.zeros(100, E, device=DEV)
+    b = torch.full((E,), -0.25, device=DEV)
+    for g in range(groups):
+        b[g * per] = ((g * 5 + 3) % groups) * 2.0 ** -30
+        b[g * per + 1] = -(2.0 ** -31)
+    check(x, 2, score=1, bias=b, groups=groups, keep=1, group_top=2)
+    check(x, 3, score=1, bias=b, groups=groups, keep=2, group_top=2)
+    for sign in (1.0, -1.0):
+        b = torch.full((E,), -3.4e38, device=DEV)
+        for g in range(groups):
+            b[g * per:g * per + 2] = sign * (2e38 + 1e37 * ((g * 5 + 3) % groups))
+            b[g * per + 1] -= 1e36
+        check(x, 1, score=1, bias=b, groups=groups, keep=1, group_top=2)
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E, groups", SUMS)
 def test_group_sums_of_infinities(E, groups, score):
     """inf - inf is no sum: the group ranks last, and no group more than `keep` stays."""
     per = E // groups
@@ -243,6 +275,19 @@ def test_groups_of_two_choose_by_logits_where_scores_meet():
     assert host(r.ids).tolist() == [[1], [1]]
     x = torch.tensor([[-800.0, -790.0, 0.0, -1000.0]], device=DEV)
     assert host(check(x, 4, groups=2, keep=2, group_top=2).ids).tolist() == [[2, 1, 0, 3]]
+
+
+@pytest.mark.parametrize("T, E", [(60, 1024), (60, 256), (200, 40)])
+def test_softmax_keys_within_the_error_of_their_sum(T, E):
+    """The bias evens out the scores to 2^-24 of one another, the largest score about a half."""
+    g = np.random.default_rng(E)
+    one = g.normal(size=E) * 2
+    one[E // 3] = np.log(np.exp(np.delete(one, E // 3)).sum())
+    x = torch.from_numpy(np.tile(one, (T, 1)) + g.normal(size=(T, 1))).to(DEV, torch.float32)
+    s = ref.scores(host(x.double()), 0)
+    bias = torch.from_numpy((0.6 - s[0]).astype(np.float32)).to(DEV)
+    check(x, 6, bias=bias)
+    check(x, 6, bias=bias - 0.6)
 
 
 # ------------------------------------------------------------------ rows ----
