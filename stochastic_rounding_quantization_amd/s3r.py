@@ -608,7 +608,7 @@ class MxRows:
     rows: int
     K: int
     groups: int = 1
-    _descs: dict = field(default_factory=dict, repr=False)      # product descriptors by (rows, output dtype, grouped)
+    _descs: dict = field(default_factory=dict, repr=False)      # product descriptors by their sizes
 
 
 def mx_rows_buffer(rows: int, K: int, device, groups: int = 1) -> MxRows:
@@ -617,6 +617,15 @@ def mx_rows_buffer(rows: int, K: int, device, groups: int = 1) -> MxRows:
     u8 = dict(dtype=torch.uint8, device=device)
     return MxRows(torch.empty(groups, (rows + 255) // 256, 16384 * steps, **u8),
                   torch.empty(groups, steps, 4 * rows, **u8), rows, K, groups)
+
+
+def _mx_fit(m: MxRows):
+    """Refuse codes and scales that are smaller than m says (negative sizes are the library's to refuse)."""
+    rows, codes, scales = m.rows, m.codes, m.scales
+    n = m.groups * ((m.K + 127) // 128)
+    if codes.nbytes < n * 16384 * ((rows + 255) // 256) or scales.nbytes < 4 * n * rows or \
+            not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("MXFP4 codes or scales are not contiguous, or smaller than their rows")
 
 
 def _index(index, rows):
@@ -638,6 +647,7 @@ def s3r_mx_rows(A, out: MxRows, up=None, index=None, index_div=1, flags=None, st
     G, a_rows, K = (1, *A.shape) if A.dim() == 2 else A.shape
     if (out.groups, out.K) != (G, K) or (index is None and out.rows != a_rows):
         raise ValueError("out does not fit A")
+    _mx_fit(out)
     _index(index, out.rows)
     _like(A, up)
     steps, blocks = (K + 127) // 128, (out.rows + 255) // 256
@@ -658,7 +668,7 @@ def _mx_pdesc(rows, w: MxRows, out, offsets):
             raise ValueError("several weights need the rows' offsets")
     else:
         _flat("offsets", offsets, torch.int64, w.groups + 1)
-    key = rows, dt, offsets is None
+    key = rows, dt, offsets is None, w.rows, w.K, w.groups
     d = w._descs.get(key)
     if d is None:
         if dt not in (torch.float32, torch.bfloat16):
@@ -677,6 +687,8 @@ def s3r_mx_product(a: MxRows, w: MxRows, out, offsets=None, flags=None, stream=N
     group e takes w's matrix e."""
     if a.groups != 1 or a.K != w.K:
         raise ValueError("a and w do not fit")
+    _mx_fit(a)
+    _mx_fit(w)
     d = _mx_pdesc(a.rows, w, out, offsets)
     rc = lib().s3r_mx_product(d, _ptr(a.codes), 16384 * ((a.K + 127) // 128), _ptr(a.scales), 4 * a.rows,
                               _ptr(offsets), _ptr(w.codes), _ptr(w.scales), _ptr(out), _ld(out), _ptr(flags),
@@ -702,6 +714,7 @@ def s3r_mx_linear(A, w: MxRows, out, *, up=None, offsets=None, index=None, index
     a_rows, K = A.shape
     if K != w.K or (index is None and a_rows != rows):
         raise ValueError("A, w and out do not fit")
+    _mx_fit(w)
     _index(index, rows)
     _like(A, up)
     d = _mx_pdesc(rows, w, out, offsets)

@@ -157,3 +157,46 @@ def test_binding_checks_tensors():
         s3r.s3r_mx_linear(f, w, torch.zeros(4, 5), offsets=torch.zeros(3, dtype=torch.int64))
     with pytest.raises(ValueError):
         s3r.s3r_route(s3r.route_desc(4, 8, 2), f, None, i, torch.zeros(4, 2), torch.zeros(8, dtype=torch.int64), i, i.reshape(-1), None)
+
+
+def test_binding_refuses_short_codes_and_scales(L):
+    """An MxRows built by hand, a buffer of fewer rows, steps or matrices than it says: before anything is read."""
+    import torch
+    A, y = torch.zeros(300, 200), torch.zeros(300, 300)
+    off = torch.zeros(3, dtype=torch.int64)
+    ws = torch.empty(s3r.s3r_mx_linear_workspace(300, 200) + 256, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+
+    def calls(m):
+        """With m as the result, and as each operand."""
+        good = s3r.mx_rows_buffer(300, 200, "cpu")
+        both = torch.zeros(2, 300, 200)
+        if m.groups == 2:
+            return [lambda: s3r.s3r_mx_rows(both, m, stream=0),
+                    lambda: s3r.s3r_mx_product(good, m, y, offsets=off, stream=0),
+                    lambda: s3r.s3r_mx_linear(A, m, y, offsets=off, ws=ws, stream=0)]
+        return [lambda: s3r.s3r_mx_rows(A, m, stream=0), lambda: s3r.s3r_mx_product(m, good, y, stream=0),
+                lambda: s3r.s3r_mx_product(good, m, y, stream=0), lambda: s3r.s3r_mx_linear(A, m, y, ws=ws, stream=0)]
+
+    for groups in (1, 2):
+        full = s3r.mx_rows_buffer(300, 200, "cpu", groups)
+        c, s = full.codes, full.scales
+        for codes, scales in ((c[:, :1].contiguous(), s), (c[..., :16384].contiguous(), s), (c[:-1], s), (c.flatten()[1:], s),
+                              (c, s[:, :1].contiguous()), (c, s[..., :-4].contiguous()), (c, s[:-1]), (c, s.flatten()[1:]),
+                              (torch.empty(*c.shape, 2, dtype=torch.uint8)[..., 0], s)):
+            for call in calls(s3r.MxRows(codes, scales, 300, 200, groups)):
+                with pytest.raises(ValueError):
+                    call()
+        for call in calls(s3r.MxRows(torch.cat([c, c]), torch.cat([s, s]), 300, 200, groups)):
+            with pytest.raises(s3r.S3RError) as e:       # larger than they need be, they pass, as far as to the missing GPU
+                call()
+            assert e.value.code in PAST
+
+
+def test_product_descriptors_follow_the_rows_they_are_for():
+    import torch
+    w = s3r.mx_rows_buffer(300, 200, "cpu")
+    first = s3r._mx_pdesc(4, w, torch.zeros(4, 300), None)
+    w.rows = 200
+    second = s3r._mx_pdesc(4, w, torch.zeros(4, 200), None)
+    assert (first.cols, second.cols, second.ld_bs) == (300, 200, 800)
