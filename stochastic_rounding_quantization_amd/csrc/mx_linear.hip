@@ -746,7 +746,7 @@ __device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         buf[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * T::EpiLd + j * 32 + (lane & 31)] = acc[i][j][r];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     for (int q = 0; q < 32; q += 64 / LR) {
       const int64_t m = m0 + (wm * T::MI + i) * 32 + q + lr;
@@ -777,7 +777,7 @@ __device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t
           if (n + x < p.N) store_out(o + x, v[x]);
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 }

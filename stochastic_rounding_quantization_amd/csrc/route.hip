@@ -784,10 +784,10 @@ __global__ __launch_bounds__(kRbThreads) void route_backward_kernel(RouteBwdKern
   for (int q = 0; q < NQ; ++q)
 #pragma unroll
     for (int i = 0; i < W; ++i) mine[(q * L + sub) * W + i] = 0.f;
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");      // the wave's LDS operations keep their order
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");      // the wave's LDS operations keep their order
   __builtin_amdgcn_wave_barrier();
   if (ok) mine[id] = val;
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   TIn* out = reinterpret_cast<TIn*>(a.dlogits) + t * a.ld_d;
 #pragma unroll
