@@ -86,6 +86,73 @@ def test_empty_batch_and_one_token(step):
     assert layer.forward(x[:0], logits[:0])[0].shape == (0, D)
 
 
+# ---------------------------------------------------- gradients, by size ----
+
+def gradients(layer, x, logits, saved, dy, scale):
+    """The layer's gradients in float64 at the values that its forward pass kept: dx, dlogits, dgate_up, ddown."""
+    x, logits, dy, a, rows = (t.double().cpu() for t in (x, logits, dy, saved.gate_up, saved.rows))
+    wg, wd = layer.gate_up.double().cpu(), layer.down.double().cpu()
+    r = saved.routed
+    o, slot = r.offsets.tolist(), r.row_slot.long().cpu()
+    tok = slot // layer.top_k
+    w = torch.from_numpy(route.weights(logits.numpy(), host(r.ids), scale=scale)).reshape(-1)
+    drows = w[slot, None] * dy[tok]
+    dw = (dy[tok] * rows).sum(1)
+    dweights = torch.empty_like(w)
+    dweights[slot] = dw
+    dlogits = route.backward(logits.numpy(), host(r.ids), dweights.reshape(r.ids.shape).numpy(), scale=scale)
+    dx, dgu, dd = torch.zeros_like(x), torch.zeros_like(wg), torch.zeros_like(wd)
+    for e in range(wg.shape[0]):
+        s = slice(o[e], o[e + 1])
+        g, u = a[s, :layer.ff], a[s, layer.ff:]
+        sg = torch.sigmoid(g)
+        dh = drows[s] @ wd[e]
+        dd[e] = drows[s].t() @ (g * sg * u)
+        da = torch.cat([dh * u * sg * (1 + g * (1 - sg)), dh * g * sg], 1)
+        dgu[e] = da.t() @ x[tok[s]]
+        dx.index_add_(0, tok[s], da @ wg[e])
+    return dx, torch.from_numpy(dlogits), dgu, dd
+
+
+def close(got, exp, bound):
+    """Relative error of the whole tensor and its length."""
+    got = got.double().cpu()
+    assert torch.isfinite(got).all()
+    assert (got - exp).norm() <= bound * exp.norm(), float((got - exp).norm() / exp.norm())
+    assert abs(got.norm() / exp.norm() - 1) <= bound
+
+
+# What is left is the INT8 rounding.  An expert's gradients are rounded to 127 steps of their largest magnitude, about
+# 10 times their root mean square (products of two normal factors): stochastic rounding errs by 0.41 of a step, 10 / 127 *
+# 0.41 = 3 %; the INT8 rows and weights (4 / 127 * 0.29 = 1 %) and bf16 (0.2 %) add little, and a second product doubles
+# the square of it: under 5 % for dx, dgate and dup.  Twice that is the bound; a factor or a term that is missing is more.
+BOUND = 0.1
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+def test_gradients_by_expert(scale):
+    g = torch.Generator(DEV).manual_seed(5)
+    n, none = 300, 3
+    layer = moe.MoeLayer(normal(g, E, 2 * F, D, std=0.1), normal(g, E, D, F, std=0.1), K, scale=scale)
+    x, logits, dy = normal(g, n, D), normal(g, n, E), normal(g, n, D, std=1e-2)
+    logits[:, none] = float("-inf")                      # an expert without a row
+    y, saved = layer.forward(x, logits)
+    dx, dlogits, dgu, dd = layer.backward(saved, dy)
+    ex, el, egu, ed = gradients(layer, x, logits, saved, dy, scale)
+    close(dx, ex, BOUND)
+    # the router's gradient passes no rounding but fp32's and a bf16 result's: D additions of both weights' products, 2^-8
+    mag = (dy.double().abs()[:, None].cpu() * saved.rows.double().abs().cpu()[saved.routed.slot_row.long().cpu()]).sum(2).amax(1)
+    assert ((dlogits.double().cpu() - el).abs() <= 2 ** -8 * el.abs() + scale * (D + 80) * 2 ** -24 * mag[:, None]).all()
+    for e in range(E):
+        if e == none:
+            assert (dgu[e] == 0).all() and (dd[e] == 0).all()
+        else:
+            close(dgu[e, :F], egu[e, :F], BOUND)
+            close(dgu[e, F:], egu[e, F:], BOUND)
+            close(dd[e], ed[e], BOUND)
+
+
+
 def test_gradients_without_tokens(step):
     layer, x, logits, dy = step[:4]
     y, saved = layer.forward(x[:0], logits[:0])

@@ -258,3 +258,28 @@ def test_stream_and_graph_replays():
         step()
         torch.cuda.synchronize()
         assert torch.equal(got[0], y) and torch.equal(got[1], y1)
+
+
+def test_bf16_rows_borders_and_non_finite():
+    """As test_rows_borders_and_non_finite in bf16, which has its own maximum and conversion: from its smallest subnormal."""
+    vals = np.array([0, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, 6, 0.5, 1, 1.5, 2, 3, 4, 5.96875, 2.484375, 2.515625, 0.2490234375,
+                     0.2509765625], np.float32)                              # exact in bf16 but for the smallest exponents
+    row = np.concatenate([vals, -vals])[:32]
+    rows = np.stack([row * 2.0 ** e for e in (-133, -132, -131, -130, -129, -128, -127, -126, -125, -3, 0, 5, 100, 125)])
+    most = float(torch.finfo(torch.bfloat16).max)
+    rows = np.concatenate([rows, np.zeros((1, 32)), -np.zeros((1, 32)), np.full((1, 32), most), np.full((1, 32), -most)])
+    rows = np.concatenate([rows, np.eye(4, 32) * 2.0 ** -133, np.eye(4, 32) * -(2.0 ** -126)])
+    A = torch.from_numpy(rows.astype(np.float32)).to(DEV).bfloat16()
+    check_rows(s3r.mx_rows(A), mx.rows(f32(A)))
+    w = s3r.mx_rows(matrix((40, 32), torch.bfloat16, 3))
+    for i in range(0, len(rows), 2):                     # rounded by the product itself
+        assert torch.equal(s3r.mx_linear(A[i:i + 2], w, out_dtype=torch.float32),
+                           s3r.mx_product(s3r.mx_rows(A[i:i + 2]), w))
+    bad = torch.from_numpy(np.random.default_rng(1).normal(size=(5, 200)).astype(np.float32)).to(DEV).bfloat16()
+    bad[1, 40], bad[2, 199], bad[4, 0] = float("nan"), float("inf"), float("-inf")
+    flags = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = s3r.mx_rows(bad, flags=flags)
+    check_rows(q, mx.rows(f32(bad)))
+    assert int(flags) == s3r.FLAG_NONFINITE
+    y = host(s3r.mx_product(q, s3r.mx_rows(matrix((40, 200), torch.bfloat16, 2))))
+    assert np.isnan(y[[1, 2, 4]]).all() and np.isfinite(y[[0, 3]]).all()
