@@ -88,6 +88,13 @@ def backward(x, ids, dweights, *, score=SOFTMAX, renorm=True, scale=1.0):
     x = np.asarray(x, np.float64)
     T, E = x.shape
     out = np.zeros((T, E))
+    with np.errstate(over="ignore", invalid="ignore"):   # a NaN or +inf among the chosen leaves NaN
+        _backward_rows(out, x, ids, dweights, score, renorm, scale)
+    return out
+
+
+def _backward_rows(out, x, ids, dweights, score, renorm, scale):
+    T, E = x.shape
     for t in range(T):
         at = [j for j, e in enumerate(ids[t]) if 0 <= e < E]
         e = ids[t][at].astype(np.int64)
@@ -96,8 +103,8 @@ def backward(x, ids, dweights, *, score=SOFTMAX, renorm=True, scale=1.0):
             # p_j of the chosen, from their log scores; dp/dlog s = p (g - <p, g>)
             log_s = -np.logaddexp(0.0, -x[t, e]) if score == SIGMOID else x[t, e]
             top = log_s.max() if len(e) else -np.inf
-            p = np.exp(log_s - top) if np.isfinite(top) else np.zeros(len(e))
-            p = p / p.sum() if p.sum() > 0 else p
+            p = np.exp(log_s - top) if top != -np.inf else np.zeros(len(e))
+            p = p / p.sum() if p.sum() != 0 else p
             d = p * (g - (p * g).sum())
             out[t, e] = d * np.exp(-np.logaddexp(0.0, x[t, e])) if score == SIGMOID else d
         else:
@@ -108,7 +115,6 @@ def backward(x, ids, dweights, *, score=SOFTMAX, renorm=True, scale=1.0):
                 spread = np.zeros(E)
                 spread[e] = g
                 out[t] = s * (spread - (g * s[e]).sum())
-    return out
 
 
 def combine(rows, slot_row, w=None):

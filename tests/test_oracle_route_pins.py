@@ -100,3 +100,16 @@ def test_group_sum_of_both_infinities_ranks_last():
     x = np.zeros((1, 6))
     assert route.choose(x, 2, bias=b, groups=3, keep=1, group_top=2).tolist() == [[4, 5]]
     assert route.choose(x, 4, bias=b, groups=3, keep=2, group_top=2).tolist() == [[4, 5, 2, 3]]
+
+
+@pytest.mark.parametrize("score, odd", [(route.SOFTMAX, np.nan), (route.SOFTMAX, np.inf), (route.SIGMOID, np.nan)])
+def test_gradient_of_a_chosen_nan(score, odd):
+    x = np.array([[1.0, odd, 0.5, 2.0], [1.0, 3.0, 0.5, 2.0]])
+    d = route.backward(x, np.array([[1, 3], [1, 3]], np.int32), np.ones((2, 2)), score=score)
+    assert np.isnan(d[0, [1, 3]]).all() and (d[0, [0, 2]] == 0).all() and np.isfinite(d[1]).all()
+
+
+def test_gradient_of_a_saturated_sigmoid_is_finite():
+    d = route.backward(np.array([[np.inf, 0.0, -np.inf]]), np.array([[0, 1, 2]], np.int32), np.array([[1.0, 2.0, 3.0]]),
+                       score=route.SIGMOID)
+    np.testing.assert_allclose(d, [[0.0, (1 / 3) * (2 - 4 / 3) / 2, 0.0]])
