@@ -583,8 +583,8 @@ int s3r_route(const s3r_route_desc* desc, const void* logits, int32_t dtype, int
  *   sigmoid:  dl_j = g_j s_j (1 - s_j);
  *   softmax:  dl_e = s_e (g_e - sum_i g_i s_i) for every expert (g_e 0 where not chosen);
  * and 0 elsewhere.  With renorm or the sigmoid only the chosen logits are read (a NaN elsewhere
- * in the row, which makes its softmax weights NaN, has no part).  groups, keep and
- * group_top are not used. */
+ * in the row, which makes its softmax weights NaN, has no part; a chosen NaN leaves NaNs at
+ * the row's choices).  groups, keep and group_top are not used. */
 int s3r_route_backward(const s3r_route_desc* desc, const void* logits, int32_t dtype, int64_t ld, const int32_t* ids,
                        const float* dweights, void* dlogits, int64_t ld_d, hipStream_t stream);
 

@@ -763,7 +763,7 @@ __global__ __launch_bounds__(kRbThreads) void route_backward_kernel(RouteBwdKern
     if (a.renorm) {
       const float ls = ok ? fminf(xj, 0.f) - log1pf(expf(-fabsf(xj))) : -__builtin_inff();
       const float m = rt_max<L>(ls);
-      const float p0 = m == -__builtin_inff() ? 0.f : expf(ls - m);
+      const float p0 = expf(ls - (m == -__builtin_inff() ? 0.f : m));       // (m passes over NaNs, the exponential keeps them)
       const float sum = rt_sum<L>(p0);
       const float p = sum == 0.f ? 0.f : p0 / sum;
       val = p * up * (g - rt_sum<L>(p * g));
@@ -772,7 +772,7 @@ __global__ __launch_bounds__(kRbThreads) void route_backward_kernel(RouteBwdKern
     }
   } else {
     const float m = rt_max<L>(xj);
-    const float p0 = m == -__builtin_inff() ? 0.f : expf(xj - m);
+    const float p0 = expf(xj - (m == -__builtin_inff() ? 0.f : m));
     const float sum = rt_sum<L>(p0);
     const float p = sum == 0.f ? 0.f : p0 / sum;
     val = p * (g - rt_sum<L>(p * g));

@@ -212,6 +212,30 @@ def test_route_backward_masked_and_foreign_ids(score, renorm):
     assert (np.abs(got - exp) <= 2 * U * (64 + 2 * 160) * np.abs(host(g)).max()).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_backward_of_nan_and_infinity(score, renorm, dtype):
+    """NaN where the weights of a chosen logit are, and nowhere else."""
+    x = logits(40, 20, dtype, 14)
+    x[1, 3] = float("nan")
+    x[2, 5] = float("inf")
+    x[3, :9] = float("-inf")
+    x[4, 2], x[4, 7] = float("inf"), float("-inf")
+    x[5] = float("nan")
+    ids = torch.tensor([[3, 5, 2, 7, 0]] * 40, dtype=torch.int32, device=DEV)
+    g = torch.randn(40, 5, device=DEV, generator=torch.Generator(DEV).manual_seed(4))
+    d = torch.empty_like(x)
+    s3r.s3r_route_backward(s3r.route_desc(40, 20, 5, score=score, renorm=renorm), x, ids, g, d)
+    got = host(d.double())
+    with np.errstate(all="ignore"):
+        exp = ref.backward(host(x.double()), host(ids), host(g), score=score, renorm=renorm)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(exp))
+    fine = np.isfinite(exp)
+    tol = 2 * U * (64 + 2 * 20) * np.abs(host(g)).max() + (half(dtype) if dtype == torch.bfloat16 else 0) * (1 + 1e-3) * np.abs(exp)
+    assert (np.abs(got - exp)[fine] <= tol[fine]).all()
+
+
 # ------------------------------------------------- groups by sums of two ----
 
 SUMS = [(8, 4), (32, 4), (36, 3), (256, 8)]      # experts and groups: of two, of a lane, of neither, of several lanes
