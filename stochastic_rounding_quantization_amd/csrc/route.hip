@@ -572,10 +572,12 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteKernelArgs a) {
       w = live ? 1.f / (1.f + expf(-xj)) : 0.f;
       if (a.renorm) {
         float sum = rt_sum<L>(w);
-        if (sum < 1e-30f) {      // scores near or below the smallest normal: from their logarithms
+        // a score near or below the smallest normal (e^-80 is 2e-35): all of the token from their logarithms, since
+        // its weight among other small scores need not be small
+        if (((__builtin_amdgcn_ballot_w64(live && xj < -80.f) >> (lane / L * L)) & (~0ull >> (64 - L))) != 0) {
           const float ls = live ? fminf(xj, 0.f) - log1pf(expf(-fabsf(xj))) : -__builtin_inff();
           const float m = rt_max<L>(ls);
-          w = m == -__builtin_inff() ? 0.f : expf(ls - m);
+          w = expf(ls - (m == -__builtin_inff() ? 0.f : m));
           sum = rt_sum<L>(w);
         }
         w = sum == 0.f ? 0.f : w / sum;

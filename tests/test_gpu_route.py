@@ -152,6 +152,21 @@ def test_tiny_sigmoid_scores_renormalise():
     np.testing.assert_allclose(host(r.weights).sum(axis=1), 1.0, rtol=8 * U)
 
 
+def test_sigmoid_scores_of_all_sizes_renormalise():
+    """Chosen scores that underflow fp32 beside ones that nearly do, and beside ordinary, masked and NaN ones."""
+    check(logits(300, 12, torch.float32, 8) * 25, 12, score=1)
+    x = torch.tensor([[-89.0, -51.5, -300, -300], [-59.0, -91, -300, -300], [-87.0, -88, -89, -90], [-104.0, -105, -120, -90],
+                      [-300.0, -301, -302, -310], [5.0, -100, -200, 3]], device=DEV)
+    for k in (2, 4):
+        check(x, k, score=1)
+    ninf = float("-inf")
+    x = torch.tensor([[ninf, -95.0, ninf, -93], [ninf] * 4, [-95.0, ninf, float("nan"), ninf]], device=DEV)
+    r = s3r.route(x, 4, score=1)
+    w = host(r.weights)
+    assert host(r.ids)[0].tolist() == [3, 1, 0, 2] and (w[1] == 0).all() and np.isnan(w[2]).all()
+    np.testing.assert_allclose(w[0], [1 / (1 + np.exp(-2)), 1 / (1 + np.exp(2)), 0, 0], rtol=U * 400)
+
+
 def test_no_tokens():
     r = s3r.route(torch.empty(0, 8, device=DEV), 2)
     assert host(r.offsets).tolist() == [0] * 9
