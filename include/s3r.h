@@ -539,7 +539,8 @@ int s3r_mx_backward_dw(const s3r_qdesc* desc, const uint8_t* Qt, int64_t ld_qt,
  *            has no gradient);
  *   groups   the experts in `groups` equal runs; a run's score is its largest
  *            key (group_top 1) or the sum of its two largest (2; inf - inf counts
- *            as -inf); the `keep` best runs stay, the others' keys become -inf;
+ *            as -inf); the `keep` best runs stay, the others' keys become -inf
+ *            (keep == groups: no runs);
  *   choice   the top_k largest keys in descending order.  Every tie, of keys or
  *            of runs, goes to the lower index.  Keys and sums are compared as
  *            fp64 values (keys without a bias by the logits, the same order).

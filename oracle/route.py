@@ -32,6 +32,8 @@ def choose(x, top_k, *, score=SOFTMAX, bias=None, groups=1, keep=1, group_top=1)
     """ids int32 [T x top_k]."""
     x = np.asarray(x, np.float64)
     T, E = x.shape
+    if keep == groups:
+        groups = 1
     masked = np.isneginf(x) | np.isnan(x)
     key = scores(x, score) + (0.0 if bias is None else np.asarray(bias, np.float64))
     key = np.where(masked | np.isnan(key), -np.inf, key)

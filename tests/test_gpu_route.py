@@ -329,6 +329,15 @@ def test_softmax_keys_within_the_error_of_their_sum(T, E):
     check(x, 6, bias=bias - 0.6)
 
 
+@pytest.mark.parametrize("top", [1, 2])
+def test_all_groups_kept_are_no_groups(top):
+    x = logits(50, 24, torch.float32, 15)
+    x[::3, 5], x[1::3, 20] = float("nan"), float("inf")
+    r, one = s3r.route(x, 4, groups=4, keep=4, group_top=top), s3r.route(x, 4)
+    assert torch.equal(r.ids, one.ids) and torch.equal(r.row_slot, one.row_slot)
+    np.testing.assert_array_equal(host(r.ids), ref.choose(host(x), 4, groups=4, keep=4, group_top=top))
+
+
 # ------------------------------------------------------------------ rows ----
 
 def slots(T, k, R, seed):

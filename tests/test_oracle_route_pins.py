@@ -89,10 +89,10 @@ def test_two_largest_groups_choose_by_logits_where_scores_meet():
     """Without a bias the scores order the groups and the logits the experts in them: equal scores are no tie."""
     x = np.array([[40.0, 50.0, 0.0, 0.0]])                # both sigmoids are 1 in fp64
     assert route.choose(x, 1, score=route.SIGMOID, groups=2, keep=1, group_top=2).tolist() == [[1]]
-    x = np.array([[-800.0, -790.0, 0.0, -1000.0]])        # all softmax scores but one are 0
-    assert route.choose(x, 4, groups=2, keep=2, group_top=2).tolist() == [[2, 1, 0, 3]]
-    x = np.array([[-800.0, np.nan, 0.0, -np.inf]])        # a NaN logit makes the row's scores NaN: all rank as -inf
-    assert route.choose(x, 3, groups=2, keep=2, group_top=2).tolist() == [[0, 1, 2]]
+    x = np.array([[-800.0, -790.0, 0.0, -1000.0, -900.0, -900.0]])    # all softmax scores but one are 0
+    assert route.choose(x, 4, groups=3, keep=2, group_top=2).tolist() == [[2, 1, 0, 3]]
+    x = np.array([[-800.0, np.nan, 0.0, -np.inf, 1.0, 2.0]])      # a NaN logit makes the row's scores NaN: all rank as -inf
+    assert route.choose(x, 3, groups=3, keep=2, group_top=2).tolist() == [[0, 1, 2]]
 
 
 def test_group_sum_of_both_infinities_ranks_last():
@@ -113,3 +113,10 @@ def test_gradient_of_a_saturated_sigmoid_is_finite():
     d = route.backward(np.array([[np.inf, 0.0, -np.inf]]), np.array([[0, 1, 2]], np.int32), np.array([[1.0, 2.0, 3.0]]),
                        score=route.SIGMOID)
     np.testing.assert_allclose(d, [[0.0, (1 / 3) * (2 - 4 / 3) / 2, 0.0]])
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_all_groups_kept_are_no_groups(group_top):
+    """Also where the scores are NaN: without a bias the logits decide."""
+    x = np.array([[1.0, np.nan, 0.5, 2.0], [1.0, np.inf, 0.5, 2.0], [0.0, 3.0, 0.5, 2.0]])
+    assert route.choose(x, 3, groups=2, keep=2, group_top=group_top).tolist() == [[3, 0, 2], [1, 3, 0], [1, 3, 2]]
