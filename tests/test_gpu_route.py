@@ -314,6 +314,8 @@ def test_groups_of_two_choose_by_logits_where_scores_meet():
     assert host(r.ids).tolist() == [[1], [1]]
     x = torch.tensor([[-800.0, -790.0, 0.0, -1000.0]], device=DEV)
     assert host(check(x, 4, groups=2, keep=2, group_top=2).ids).tolist() == [[2, 1, 0, 3]]
+    x = torch.tensor([[-800.0, -790.0, 0.0, -1000.0, -900.0, -900.0]], device=DEV)
+    assert host(check(x, 4, groups=3, keep=2, group_top=2).ids).tolist() == [[2, 1, 0, 3]]
 
 
 @pytest.mark.parametrize("T, E", [(60, 1024), (60, 256), (200, 40)])
