@@ -761,7 +761,7 @@ static int check_mx_source(int64_t rows, int64_t K, const void* A, const void* u
   if ((rc = check_rows(up, dtype, ld, K, false))) return rc;
   if (a_rows < 0 || a_rows > 0x7FFFFFFF || index_div < 1 || index_div > 0x7FFFFFFF || !al4(index))
     return S3R_ERR_INVALID_ARG;
-  if (!index && a_rows != rows) return S3R_ERR_INVALID_ARG;
+  if (!index && rows > 0 && a_rows != rows) return S3R_ERR_INVALID_ARG;       // an empty index may be NULL
   return S3R_OK;
 }
 

@@ -200,3 +200,11 @@ def test_product_descriptors_follow_the_rows_they_are_for():
     w.rows = 200
     second = s3r._mx_pdesc(4, w, torch.zeros(4, 200), None)
     assert (first.cols, second.cols, second.ld_bs) == (300, 200, 800)
+
+
+def test_no_rows_of_a_source_that_has_some(L):
+    """An empty index has no address."""
+    assert L.s3r_mx_rows(1, 0, K, P, None, 1, 200, 60000, 5, None, 1, None, LD, 2 * LD, None, 0, 0, None, None) in PAST
+    d = ctypes.byref(pdesc(rows=0, groups=2))
+    assert L.s3r_mx_linear(d, P, None, 1, 200, 5, None, 2, P, P, P, None, ROWS, None, P, 1 << 20, None) in PAST
+    assert L.s3r_mx_rows(1, 1, K, P, None, 1, 200, 60000, 5, None, 1, P, LD, 2 * LD, P, 4, 0, None, None) == INVALID

@@ -283,3 +283,11 @@ def test_bf16_rows_borders_and_non_finite():
     assert int(flags) == s3r.FLAG_NONFINITE
     y = host(s3r.mx_product(q, s3r.mx_rows(matrix((40, 200), torch.bfloat16, 2))))
     assert np.isnan(y[[1, 2, 4]]).all() and np.isfinite(y[[0, 3]]).all()
+
+
+def test_no_rows_gathered():
+    X, w = matrix((9, 64), torch.bfloat16, 1), s3r.mx_rows(matrix((3, 20, 64), torch.bfloat16, 2))
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    assert s3r.mx_rows(X, index=none, index_div=2).rows == 0
+    y = s3r.mx_linear(X, w, offsets=torch.zeros(4, dtype=torch.int64, device=DEV), index=none, index_div=2)
+    assert y.shape == (0, 20)
