@@ -317,6 +317,13 @@ __device__ __forceinline__ int group_total(const int64_t* offsets, int64_t G, in
   bad = __builtin_amdgcn_ballot_w64(b) != 0;
   return total;
 }
+// The offsets of a product without results.
+__global__ __launch_bounds__(64) void mx_offsets_kernel(const int64_t* offsets, int64_t G, int64_t R, uint32_t* flags) {
+  GroupRound first;
+  bool bad;
+  group_total(offsets, G, R, 1, first, bad);
+  if (bad && threadIdx.x == 0) atomicOr(flags, S3R_FLAG_BAD_GROUPS);
+}
 // Tile i, 0 <= i < total, of valid offsets: its group, its first row and the group's end.
 __device__ __forceinline__ GroupTile group_tile(const int64_t* offsets, int64_t G, int64_t R, int tile,
                                                 const GroupRound& first, int i) {
@@ -989,6 +996,12 @@ constexpr int64_t kTallGrouped = 1024;
 // of their own, 4 rows 11.8 against 12.0, 8 rows 15.7 against 12.1; grouped, at most a row per weight on average.
 constexpr int64_t kRoundRows = 2;
 
+hipError_t run_empty(const MxProductArgs& a, hipStream_t st) {
+  if (!a.G || !a.flags) return hipSuccess;
+  hipLaunchKernelGGL(mx_offsets_kernel, dim3(1), dim3(64), 0, st, a.offsets, a.G, a.M, a.flags);
+  return hipGetLastError();
+}
+
 template <typename TIn>
 hipError_t run_round_few(const MxProductArgs& a, const MxRowsArgs& q, hipStream_t st) {
   return mr_words(q) ? run_few_rows<TIn, true, 1, kFewNJ, 2>(a, q, st) : run_few_rows<TIn, false, 1, kFewNJ, 2>(a, q, st);
@@ -996,7 +1009,7 @@ hipError_t run_round_few(const MxProductArgs& a, const MxRowsArgs& q, hipStream_
 }  // namespace
 
 hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
-  if (a.M == 0 || a.N == 0) return hipSuccess;
+  if (a.M == 0 || a.N == 0) return run_empty(a, st);
   if (a.G) {
     const int64_t rows = mean_rows(a);
     if (rows <= kFewGrouped) return run_few_rows<void, true, 1, kFewNJ, 2>(a, MxRowsArgs{}, st);
@@ -1014,7 +1027,7 @@ hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
 
 // Rows and product; `rows` writes the codes that `prod` reads, unless the few-rows kernel rounds them itself.
 hipError_t launch_mx_linear(const MxRowsArgs& rows, const MxProductArgs& prod, hipStream_t st) {
-  if (prod.M == 0 || prod.N == 0) return hipSuccess;
+  if (prod.M == 0 || prod.N == 0) return run_empty(prod, st);
   const int ksteps = (int)((prod.K + 127) / 128);
   if (!rows.up && prod.M <= std::max(prod.G, kRoundRows) &&
       sk_lds_bytes((int)std::min<int64_t>(prod.M, 16), ksteps) + 3 * kFewNJ * 1024 <= kSkLdsMax)

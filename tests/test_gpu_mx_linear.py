@@ -291,3 +291,23 @@ def test_no_rows_gathered():
     assert s3r.mx_rows(X, index=none, index_div=2).rows == 0
     y = s3r.mx_linear(X, w, offsets=torch.zeros(4, dtype=torch.int64, device=DEV), index=none, index_div=2)
     assert y.shape == (0, 20)
+
+
+@pytest.mark.parametrize("R, N", [(0, 20), (5, 0), (0, 0)])
+def test_offsets_of_an_empty_product(R, N):
+    """They are looked at as those of any product."""
+    bf16 = dict(dtype=torch.bfloat16, device=DEV)
+    w, a = s3r.mx_rows(torch.ones(70, N, 64, **bf16)), torch.ones(R, 64, **bf16)
+    y, ws = torch.empty(R, N, device=DEV), s3r.mx_linear_buffer(R, 64, DEV)
+    good = torch.full((71,), R, dtype=torch.int64, device=DEV)
+    good[:30] = 0
+    for at, value in ((None, 0), (0, 1), (70, R + 1), (65, R + 1), (3, -1)):
+        off = good.clone()
+        if at is not None:
+            off[at] = value
+        for flags in (None, torch.zeros(2, dtype=torch.int32, device=DEV)):
+            f = None if flags is None else flags[:1]
+            s3r.s3r_mx_product(s3r.mx_rows(a), w, y, offsets=off, flags=f)
+            s3r.s3r_mx_linear(a, w, y, offsets=off, ws=ws, flags=None if flags is None else flags[1:])
+            if flags is not None:
+                assert host(flags).tolist() == ([0, 0] if at is None else [s3r.FLAG_BAD_GROUPS] * 2)
