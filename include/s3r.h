@@ -615,8 +615,10 @@ int s3r_combine_backward(int64_t T, int64_t k, int64_t R, int64_t D, int32_t dty
  * layout), blocked along the row.  K is padded to steps of 128 elements with zero
  * codes: ld >= 16384 * ceil(K / 128), scales [ceil(K/128)][rows][4]; the scale of a
  * padding block is byte 0.  Codes buffers hold ceil(rows / 256) * ld bytes, below
- * 2^32.  The backward of a product is s3r_mx_backward_dx / _dw, over the experts
- * s3r_grouped_backward_dx / _dw.
+ * 2^32.  The backward of a dense product is s3r_mx_backward_dx / _dw (MXFP4 gradients,
+ * rows and channels in multiples of 128, their own operand layouts), or as over the
+ * experts, where there is no MXFP4 backward, s3r_backward_dx / _dw and
+ * s3r_grouped_backward_dx / _dw (INT8, any size).
  */
 
 /* s3r_mx_rows: `groups` matrices of rows x K elements (a_stride elements, c_stride

@@ -9,9 +9,9 @@
 // What bounds them (MI355X; a large copy moves 5.4 TB/s, the FP4 cores have 10.1 PFLOP/s):
 //   rows       HBM: 8192 x 4096 fp32 28 us, 5.5 TB/s, bf16 14.5 - 16; 32768 rows of 2048 gathered 26 us
 //   few rows   the weights' bytes: 1 x 14336 x 4096 8.3 us, 3.8 TB/s with the launch
-//   tiles      power: 8192 x 14336 x 4096 243 us, 4.0 PFLOP/s (zero operands: 185 us; a tile's epilogue,
-//              235 MB of results in all, is a fifth of it); 64 experts, 32768 x 1408 x 2048 93 us, of which
-//              the weights', rows' and results' 225 MB need 42
+//   tiles      power: 8192 x 14336 x 4096 250 - 270 us, 3.6 - 3.85 PFLOP/s (zero operands: 185 - 205 us; a tile's
+//              epilogue, 235 MB of results in all, is a fifth of it); 64 experts, 32768 x 1408 x 2048 82 - 97 us, of
+//              which the weights', rows' and results' 225 MB need 42
 // Rounding the tokens once and gathering their codes in the product's loads instead of gathering in the rounding
 // made the experts' product 126 us (64-byte pieces of 128-byte lines), so the rows are gathered first.
 #include <type_traits>
@@ -678,7 +678,7 @@ __device__ __forceinline__ void tile_head(const uint8_t* st, TileHead<T>& h) {
 // fragments; the barrier in the middle then makes step kt + 1 visible and retires stage S, which takes
 // step kt + NS; the second half's products cover the reads of step kt + 1's head.  So the matrix cores
 // wait for no LDS read, and a load has NS - 1 steps and a half to arrive.  (A barrier at the step's start, before
-// its reads: 254 us instead of 243 for 8192 x 14336 x 4096.)
+// its reads: 4.5 % more for 8192 x 14336 x 4096.)
 template <typename T, int S>
 __device__ __forceinline__ void tile_step(const TileSrc<T>& src, int kt, TileHead<T>& h, v16f (&acc)[T::MI][T::NI]) {
   TileFrag<T> f1;
@@ -726,8 +726,8 @@ __device__ __forceinline__ void tile_steps(const TileSrc<T>& src, int kt, TileHe
 
 // The wave's results, 32 rows at a time through its own part of the (now free) ring, so that whole
 // 16-byte words of consecutive columns are stored, past the last-level cache (fp32 results of
-// 8192 x 14336 x 4096: 264 us, with plain stores 297).  At the elements' alignment, for any width and slice: 8192 x 14335
-// x 4096 in bf16 276 us, element by element 393 (14336 columns: 242 - 251).
+// 8192 x 14336 x 4096: 264 - 272 us, with plain stores 297).  At the elements' alignment, for any width and slice: 8192 x
+// 14335 x 4096 in bf16 276 - 281 us, element by element 393 (14336 columns: 250 - 270).
 template <typename T, typename TOut>
 __device__ __forceinline__ void tile_store(const MxProdK& p, int64_t m0, int64_t m1, int64_t n0,
                                            const v16f (&acc)[T::MI][T::NI]) {

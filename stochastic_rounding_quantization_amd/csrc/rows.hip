@@ -10,8 +10,11 @@
 //   backward   dY[slot_row[t,j]] = w[t,j] dy[t];  dw[t,j] = <dy[t], Y[slot_row[t,j]]>
 // fp32 sums in the order of j (of the columns within a lane, then across lanes),
 // one rounding to the output's type.  All three move whole rows between tokens'
-// order and experts' order and are bound by HBM: a token's side is read or
-// written once, whatever k is, and the rows of one token are in flight together.
+// order and experts' order, and with many tokens are bound by HBM: a token's side
+// is read or written once, whatever k is.  A thread of combine loads its rows one
+// after another (the other waves of the CU cover that: two choices run at a
+// large copy's rate); the backward has the rows of up to four choices in flight.
+// With few tokens latency bounds them: 16 tokens x 8 x 4096, combine 6.0 us.
 #include "s3r_internal.h"
 
 namespace s3r {

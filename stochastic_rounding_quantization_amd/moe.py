@@ -9,7 +9,8 @@ forward   route the logits; the tokens' rows in the experts' order times the exp
           stacked product, 4-bit weights and rows); silu(gate) * up rounded straight into the down product's
           rows; the experts' outputs summed into the tokens with the router's weights.
 backward  the sum's gradients; the router's; each projection as the grouped INT8 path takes it (G rounded with
-          S3R-EC, dX and dW from one set of codes); the rows' gradients summed back into the tokens.
+          S3R-EC, dX and dW from one set of codes, up to its 131072 rows); the rows' gradients summed back into the
+          tokens.  silu(gate) * up and the joining of the gate and up gradients are torch operations.
 """
 from __future__ import annotations
 
