@@ -1002,7 +1002,8 @@ def route_backward(r: Routed, logits, dweights, stream=None):
 
 
 def dispatch(X, r: Routed, stream=None):
-    """The tokens' rows in the experts' order: [T * k x D]."""
+    """The tokens' rows in the experts' order: [T * k x D].  Where r's slot_row was changed to leave rows out, they are
+    not written (use s3r_dispatch on a cleared buffer)."""
     import torch
     with _on(stream):
         rows = torch.empty(r.row_slot.numel(), X.shape[1], dtype=X.dtype, device=X.device)
@@ -1020,10 +1021,13 @@ def combine(rows, r: Routed, weighted=True, stream=None):
 
 
 def combine_backward(dy, rows, r: Routed, stream=None):
-    """(drows, dweights) of combine(rows, r)."""
+    """(drows, dweights) of combine(rows, r).  Rows past r's slots have the gradient 0; where r's slot_row was changed
+    to leave rows out, theirs is not written (use s3r_combine_backward on a cleared buffer)."""
     import torch
     with _on(stream):
         drows = torch.empty_strided(rows.shape, rows.stride(), dtype=rows.dtype, device=rows.device)
+        if rows.shape[0] > r.slot_row.numel():
+            drows[r.slot_row.numel():].zero_()
         dw = torch.empty_like(r.weights)
     s3r_combine_backward(dy, rows, r.slot_row, r.weights, drows, dw, stream)
     return drows, dw

@@ -409,6 +409,22 @@ def test_slots_without_a_row():
     assert host(dw)[[0, 1, 2, 2], [1, 0, 0, 1]].tolist() == [0, 0, 0, 0]
 
 
+@pytest.mark.parametrize("extra", [0, 5])
+def test_gradient_of_rows_past_the_slots(extra):
+    """More rows than slots: the helper's gradient of the others is 0, whatever its memory held."""
+    T, k, D = 12, 2, 40
+    r = s3r.route(logits(T, 8, torch.float32, 1), k)
+    rows = torch.randn(T * k + extra, D, device=DEV)
+    dy = torch.randn(T, D, device=DEV)
+    for _ in range(3):
+        torch.full_like(rows, float("nan"))              # left in the memory that is taken next
+        drows, dw = s3r.combine_backward(dy, rows, r)
+        exp, edw, mag = ref.combine_backward(host(dy), host(rows), host(r.slot_row), host(r.weights))
+        assert (host(drows)[T * k:] == 0).all() and np.isfinite(exp[:T * k]).all()
+        assert (np.abs(host(drows) - exp)[:T * k] <= U * np.abs(exp[:T * k])).all()
+        assert (np.abs(host(dw) - edw) <= (D + 8) * U * mag).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("offset", [0, 1, 8])
 def test_rows_of_every_width(dtype, offset):
