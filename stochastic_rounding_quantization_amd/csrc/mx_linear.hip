@@ -16,8 +16,10 @@
 // made the experts' product 126 us (64-byte pieces of 128-byte lines), so the rows are gathered first.
 #include <type_traits>
 
+#include "group_tiles.h"
 #include "mx_math.h"
-#include "swiglu_math.h"
+#include "rows8.h"
+#include "tile_ring.h"
 
 namespace s3r {
 namespace {
@@ -34,117 +36,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // 35 us for 8192 x 4096 bf16, whose bytes need 15); now two elements convert in
 // one instruction, and the maximum of bf16 runs on packed magnitudes.
 constexpr int kMrThreads = 256, kMrRows = 16;
-
-// 8 consecutive elements of a row as they lie in memory: packed bf16, or fp32.
-template <typename TIn> struct Raw8;
-template <> struct Raw8<uint16_t> { uint32_t w[4]; };
-template <> struct Raw8<float> { float w[8]; };
-
-// The 8 elements at p, of which the row of K has n left (none: zeros).  Words: 16-byte aligned rows with K a
-// multiple of 8, so that n is 8 or more, or 0 or less (a path for fewer in an unrolled loop is code that has to
-// be fetched, whether it runs or not: a kernel of few instructions per byte was twice as slow with it).  Else
-// 16-byte loads at the elements' alignment, for a row's end the row's last 8, which mr_tail moves to their
-// place once every load is on its way; element by element where K < 8.  8192 x 4095 bf16: 36 us with elements
-// alone, 16 so (8192 x 4096: 14.5); fp32 61 and 28.
-typedef uint32_t mr_u4_a2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t mr_u4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-template <typename TIn, bool Words>
-__device__ __forceinline__ Raw8<TIn> mr_load8(const TIn* p, int64_t n, int64_t K) {
-  Raw8<TIn> r;
-  if constexpr (sizeof(TIn) == 2) {
-    if constexpr (Words) {
-      const uint4 w = n > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
-      r.w[0] = w.x; r.w[1] = w.y; r.w[2] = w.z; r.w[3] = w.w;
-    } else if (K >= 8) {
-      v4u32 w = {0u, 0u, 0u, 0u};
-      if (n > 0) w = *reinterpret_cast<const mr_u4_a2*>(p + (n < 8 ? n - 8 : 0));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.w[i] = w[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-    }
-  } else {
-    if (Words || K >= 8) {
-      v4u32 a = {0u, 0u, 0u, 0u}, b = a;
-      if (n > 0) {                     // one branch for both words: with one each, 8192 x 4096 took 60 us instead of 28
-        if constexpr (Words) {
-          a = reinterpret_cast<const v4u32*>(p)[0];
-          b = reinterpret_cast<const v4u32*>(p)[1];
-        } else {
-          const mr_u4_a4* q = reinterpret_cast<const mr_u4_a4*>(p + (n < 8 ? n - 8 : 0));
-          a = q[0];
-          b = q[1];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { r.w[i] = __uint_as_float(a[i]); r.w[4 + i] = __uint_as_float(b[i]); }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r.w[i] = i < n ? p[i] : 0.f;
-    }
-  }
-  return r;
-}
-
-// The row's last 8 elements to its last n, 0 < n < 8, and zeros after them.
-template <bool Words>
-__device__ __forceinline__ void mr_tail(Raw8<uint16_t>& r, int64_t n, int64_t K) {
-  if constexpr (!Words)
-    if (n > 0 && n < 8 && K >= 8) {
-      const int by = 16 * (8 - (int)n);
-      uint64_t lo = (uint64_t)r.w[1] << 32 | r.w[0], hi = (uint64_t)r.w[3] << 32 | r.w[2];
-      lo = by < 64 ? lo >> by | hi << (64 - by) : hi >> (by - 64);
-      hi = by < 64 ? hi >> by : 0;
-      r.w[0] = (uint32_t)lo; r.w[1] = (uint32_t)(lo >> 32);
-      r.w[2] = (uint32_t)hi; r.w[3] = (uint32_t)(hi >> 32);
-    }
-}
-template <bool Words>
-__device__ __forceinline__ void mr_tail(Raw8<float>& r, int64_t n, int64_t K) {
-  if constexpr (!Words)
-    if (n > 0 && n < 8 && K >= 8) {
-      const int by = 8 - (int)n;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.w[i] = by & o ? (i + o < 8 ? r.w[i + o] : 0.f) : r.w[i];
-    }
-}
-
-__device__ __forceinline__ Raw8<float> mr_float8(const Raw8<float>& r) { return r; }
-__device__ __forceinline__ Raw8<float> mr_float8(const Raw8<uint16_t>& r) {
-  Raw8<float> f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f.w[2 * i] = __uint_as_float(r.w[i] << 16);
-    f.w[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
-  }
-  return f;
-}
-
-// silu(a) * u in fp32 with the glue's exponential and reciprocal.
-__device__ __forceinline__ float mr_swiglu(float a, float u) {
-  const float d = 1.f + glue_exp32(-a);
-  const float s = glue_slow_recip(d) ? __fdiv_rn(1.f, d) : glue_recip(d);
-  return (a * s) * u;
-}
-
-// Largest magnitude of the 8 elements, as fp32 bits.
-__device__ __forceinline__ uint32_t mr_amax(const Raw8<float>& r) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(r.w[i]) & 0x7FFFFFFFu);
-  return m;
-}
-__device__ __forceinline__ uint32_t mr_amax(const Raw8<uint16_t>& r) {
-  typedef unsigned short u2 __attribute__((ext_vector_type(2)));
-  u2 m = __builtin_bit_cast(u2, r.w[0] & 0x7FFF7FFFu);
-#pragma unroll
-  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u2, r.w[i] & 0x7FFF7FFFu));
-  return (uint32_t)(m.x > m.y ? m.x : m.y) << 16;
-}
 
 // Codes of 8 elements in a block of scale 2^(sb - 127), 1 <= sb <= 254: the hardware's conversion divides
 // by the scale and rounds to nearest, ties to even.  Its sign survives a magnitude of 0; the format here
@@ -172,12 +63,6 @@ __device__ __forceinline__ uint32_t mr_codes(const Raw8<uint16_t>& r, int sb) {
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf2, r.w[3]), scale, 3);
   return mr_one_zero(w);
 }
-
-template <int Ctrl>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, 0xF, 0xF, true);
-}
-constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppRor4 = 0x124, kDppRor8 = 0x128;
 
 // Codes of 8 elements of a block with the scale byte sb, any of them: 0 is below the conversion's scales
 // (2^-127 is no normal fp32 number), so there elements and scale are taken times 2^64, which is exact.
@@ -211,16 +96,6 @@ __device__ __forceinline__ uint32_t mr_encode(const TRaw& v, uint32_t& scales) {
 
 __device__ __forceinline__ bool mr_nan_scale(uint32_t s) {
   return (s & 0xFFu) == 0xFFu || (s & 0xFF00u) == 0xFF00u || (s & 0xFF0000u) == 0xFF0000u || (s >> 24) == 0xFFu;
-}
-
-// The source row of row r, or -1: none (past the end, or an index outside the source).
-__device__ __forceinline__ int64_t mr_source(const MxRowsArgs& a, int64_t r) {
-  if (r >= a.R) return -1;
-  if (!a.index) return r;
-  const int i = a.index[r];
-  if (i < 0) return -1;
-  const int s = (int)((uint32_t)i / (uint32_t)a.index_div);
-  return s < a.a_rows ? s : -1;
 }
 
 template <typename TIn, bool UP, bool Words, int Steps>
@@ -272,51 +147,6 @@ __global__ __launch_bounds__(kMrThreads) void mx_rows_kernel(MxRowsArgs a, int k
 }
 
 // --------------------------------------------------------------- groups ----
-// Row tiles of a grouped product, found by one wave from the offsets themselves (prefix sums of the groups'
-// tile counts, 64 groups a round).  bad: the offsets are not a non-decreasing sequence from 0 to R.
-struct GroupTile { int e; int64_t r0, r1; };
-__device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
-  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
-                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
-}
-// Inclusive sums over the wave by DPP: shifts within the 16-lane rows, then the rows' last lanes.
-__device__ __forceinline__ int wave_prefix(int s) {
-  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
-  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, true);
-  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, true);
-  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, true);
-  s += __builtin_amdgcn_update_dpp(0, s, 0x142, 0xA, 0xF, false);     // row_bcast 15 into rows 1 and 3
-  s += __builtin_amdgcn_update_dpp(0, s, 0x143, 0xC, 0xF, false);     // row_bcast 31 into rows 2 and 3
-  return s;
-}
-// One round: groups g0 .. g0 + 63, one a lane; n its tiles, s the inclusive sums of n.
-struct GroupRound { int64_t o0, o1; int n, s; bool bad; };
-__device__ __forceinline__ GroupRound group_round(const int64_t* __restrict__ offsets, int64_t G, int64_t R, int64_t g0,
-                                                  int tile) {
-  const int64_t g = g0 + (threadIdx.x & 63);
-  const bool in = g < G;
-  GroupRound r;
-  r.o0 = in ? offsets[g] : 0;
-  r.o1 = in ? offsets[g + 1] : 0;
-  r.bad = in && (r.o1 < r.o0 || r.o0 < 0 || r.o1 > R || (g == 0 && r.o0 != 0) || (g == G - 1 && r.o1 != R));
-  r.n = r.bad ? 0 : ((int)(r.o1 - r.o0) + tile - 1) / tile;
-  r.s = wave_prefix(r.n);
-  return r;
-}
-// All tiles of all groups; first: round 0, to be kept.
-__device__ __forceinline__ int group_total(const int64_t* offsets, int64_t G, int64_t R, int tile, GroupRound& first,
-                                           bool& bad) {
-  first = group_round(offsets, G, R, 0, tile);
-  int total = __builtin_amdgcn_readlane(first.s, 63);
-  bool b = first.bad;
-  for (int64_t g0 = 64; g0 < G; g0 += 64) {
-    const GroupRound r = group_round(offsets, G, R, g0, tile);
-    total += __builtin_amdgcn_readlane(r.s, 63);
-    b |= r.bad;
-  }
-  bad = __builtin_amdgcn_ballot_w64(b) != 0;
-  return total;
-}
 // The offsets of a product without results.
 __global__ __launch_bounds__(64) void mx_offsets_kernel(const int64_t* offsets, int64_t G, int64_t R, uint32_t* flags) {
   GroupRound first;
@@ -324,24 +154,6 @@ __global__ __launch_bounds__(64) void mx_offsets_kernel(const int64_t* offsets, 
   group_total(offsets, G, R, 1, first, bad);
   if (bad && threadIdx.x == 0) atomicOr(flags, S3R_FLAG_BAD_GROUPS);
 }
-// Tile i, 0 <= i < total, of valid offsets: its group, its first row and the group's end.
-__device__ __forceinline__ GroupTile group_tile(const int64_t* offsets, int64_t G, int64_t R, int tile,
-                                                const GroupRound& first, int i) {
-  GroupRound r = first;
-  int carry = 0;                              // tiles of the groups before this round's
-  for (int64_t g0 = 0;;) {
-    const uint64_t m = __builtin_amdgcn_ballot_w64(carry + r.s > i);
-    if (m || g0 + 64 >= G) {
-      const int w = m ? __builtin_ctzll(m) : 0;
-      const int before = carry + __builtin_amdgcn_readlane(r.s - r.n, w);
-      return GroupTile{(int)g0 + w, read_lane(r.o0, w) + (int64_t)(i - before) * tile, read_lane(r.o1, w)};
-    }
-    carry += __builtin_amdgcn_readlane(r.s, 63);
-    g0 += 64;
-    r = group_round(offsets, G, R, g0, tile);
-  }
-}
-
 // -------------------------------------------------------------- products ----
 struct MxProdK {
   const uint8_t* A; int64_t lda; const uint8_t* As; int64_t ldas;
@@ -543,13 +355,6 @@ __global__ __launch_bounds__(kSkThreads) void mx_few_rows_kernel(MxProdK p, MxRo
 // v_mfma_scale_f32_32x32x64_f8f6f4: lane l holds row or column l % 32, K elements 32 (l / 32) .. + 31;
 // result register r is row (r / 4) 8 + (l / 32) 4 + r % 4, column l % 32.
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void lds_void;
-constexpr int kRsrcWord3 = 0x00020000;   // raw buffer, 32-bit dword format
-
-#define S3R_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (((n) >> 4) << 14) | 0x70 | 0xF00)
-#define S3R_WAIT_LGKM0() __builtin_amdgcn_s_waitcnt(0xC07F)
-constexpr int kSgMfma = 0x008, kSgDsRead = 0x100, kSgVmem = 0x010;
-
 template <int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
 struct Tile {
   static constexpr int WavesPerSimd = WavesPerSimd_;
@@ -566,22 +371,9 @@ struct Tile {
   static_assert(BM % (16 * Waves) == 0 && BN % (16 * Waves) == 0, "whole pieces per wave");
 };
 
-// One LDS object per stage: the compiler then sees that a stage's reads and the DMA into another touch
-// different memory, and does not drain the loads in flight before the reads.
-template <typename T, int S>
-__device__ __forceinline__ uint8_t* ring() {
-  __shared__ __attribute__((aligned(1024))) uint8_t stage[T::StageBytes];
-  return stage;
-}
-
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 0);
-}
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, voff, soff, 0, 0);
 }
-
-__device__ __forceinline__ int chunk_pos(int r, int q) { return q ^ ((r >> 2) & 3); }
 
 template <typename T>
 struct TileSrc {
@@ -996,20 +788,20 @@ constexpr int64_t kTallGrouped = 1024;
 // of their own, 4 rows 11.8 against 12.0, 8 rows 15.7 against 12.1; grouped, at most a row per weight on average.
 constexpr int64_t kRoundRows = 2;
 
-hipError_t run_empty(const MxProductArgs& a, hipStream_t st) {
-  if (!a.G || !a.flags) return hipSuccess;
-  hipLaunchKernelGGL(mx_offsets_kernel, dim3(1), dim3(64), 0, st, a.offsets, a.G, a.M, a.flags);
-  return hipGetLastError();
-}
-
 template <typename TIn>
 hipError_t run_round_few(const MxProductArgs& a, const MxRowsArgs& q, hipStream_t st) {
   return mr_words(q) ? run_few_rows<TIn, true, 1, kFewNJ, 2>(a, q, st) : run_few_rows<TIn, false, 1, kFewNJ, 2>(a, q, st);
 }
 }  // namespace
 
+hipError_t launch_check_offsets(const int64_t* offsets, int64_t G, int64_t R, uint32_t* flags, hipStream_t st) {
+  if (!G || !flags) return hipSuccess;
+  hipLaunchKernelGGL(mx_offsets_kernel, dim3(1), dim3(64), 0, st, offsets, G, R, flags);
+  return hipGetLastError();
+}
+
 hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
-  if (a.M == 0 || a.N == 0) return run_empty(a, st);
+  if (a.M == 0 || a.N == 0) return launch_check_offsets(a.offsets, a.G, a.M, a.flags, st);
   if (a.G) {
     const int64_t rows = mean_rows(a);
     if (rows <= kFewGrouped) return run_few_rows<void, true, 1, kFewNJ, 2>(a, MxRowsArgs{}, st);
@@ -1027,7 +819,7 @@ hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st) {
 
 // Rows and product; `rows` writes the codes that `prod` reads, unless the few-rows kernel rounds them itself.
 hipError_t launch_mx_linear(const MxRowsArgs& rows, const MxProductArgs& prod, hipStream_t st) {
-  if (prod.M == 0 || prod.N == 0) return run_empty(prod, st);
+  if (prod.M == 0 || prod.N == 0) return launch_check_offsets(prod.offsets, prod.G, prod.M, prod.flags, st);
   const int ksteps = (int)((prod.K + 127) / 128);
   if (!rows.up && prod.M <= std::max(prod.G, kRoundRows) &&
       sk_lds_bytes((int)std::min<int64_t>(prod.M, 16), ksteps) + 3 * kFewNJ * 1024 <= kSkLdsMax)

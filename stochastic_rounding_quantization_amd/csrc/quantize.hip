@@ -19,6 +19,7 @@
 // X = floor(fl(G'*inv*2^24)), q = (clamp(X) + r*2^24) >> 24.  Scaling by 2^24
 // is exact except where G'*inv is subnormal, and there both forms give the
 // same code.  The build disables FP contraction.
+#include "int8_step.h"
 #include "s3r_internal.h"
 #include "swiglu_math.h"
 
@@ -94,25 +95,6 @@ __device__ __forceinline__ void store8(int8_t* __restrict__ row, int64_t j0, int
     for (int i = 0; i < 8; ++i)
       if (j0 + i < D) row[j0 + i] = (int8_t)q[i];
   }
-}
-
-// |v| as ordered bits: for non-negative floats uint order == float order, and
-// NaN (> 0x7F800000) wins every max, so a NaN anywhere reaches the step.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-// Step from amax bits: Delta = fl(a/127), inv = fl(127/a) (a == 0: 1 and 0).
-struct Step { float delta, inv, inv24; uint32_t flag; };
-__device__ __forceinline__ Step make_step(uint32_t abits) {
-  const float a = __uint_as_float(abits);
-  Step s;
-  s.flag = 0;
-  if (abits == 0) { s.delta = 1.f; s.inv = 0.f; s.inv24 = 0.f; return s; }
-  s.delta = __fdiv_rn(a, 127.f);
-  s.inv = __fdiv_rn(127.f, a);
-  s.inv24 = s.inv * 16777216.f;
-  if (!(abits < 0x7F800000u)) s.flag |= S3R_FLAG_NONFINITE;
-  else if (!(__float_as_uint(s.inv24) < 0x7F800000u)) s.flag |= S3R_FLAG_TINY_STEP;
-  return s;
 }
 
 // ---------------------------------------------------------------- pass 1 ----

@@ -238,6 +238,8 @@ size_t mx_rows_scales_bytes(int64_t R, int64_t K);
 hipError_t launch_mx_rows(const MxRowsArgs& a, hipStream_t st);
 hipError_t launch_mx_product(const MxProductArgs& a, hipStream_t st);
 hipError_t launch_mx_linear(const MxRowsArgs& rows, const MxProductArgs& prod, hipStream_t st);
+// A grouped product without results still looks at its offsets.
+hipError_t launch_check_offsets(const int64_t* offsets, int64_t G, int64_t R, uint32_t* flags, hipStream_t st);
 
 // SwiGLU backward glue (swiglu.hip).
 hipError_t launch_swiglu_backward(int64_t T, int64_t F, const float* dH, int64_t ld_dh, const uint16_t* Ag,
