@@ -159,8 +159,8 @@ def prepare(case, seed):
         else:
             rows = case["tokens"] * case["top_k"] if op == "experts" else case["rows"]
             s["out"] = torch.empty(rows, case["n"], dtype=DTYPES[case["out"]], device="cuda")
-            s["w"] = s3r.i8_rows(s["W"])                            # codes and steps, laid out once
-            s["ws"] = s3r.i8_linear_buffer(rows, case["k"], "cuda")
+            s["w"] = s3r.int_rows(s["W"])                            # codes and steps, laid out once
+            s["ws"] = s3r.int_linear_buffer(rows, case["k"], "cuda")
     elif op != "orth":
         q, s["sw"] = _codes(s["W"].float())
         s["w"] = q.transpose(1, 2).contiguous()                     # the codes as numbers [E, K, N]
@@ -184,12 +184,12 @@ def _run_own(s):
     if op == "orth":
         s3r.s3r_orthogonalize(s["G"], s["out"], steps=c["steps"], coeffs=COEFFS, eps=EPS, ws=s["ws"])
     elif op == "experts":
-        s3r.s3r_i8_linear(s["x"], s["w"], s["out"], offsets=s["offsets"], index=s["row_slot"], index_div=c["top_k"],
+        s3r.s3r_int_linear(s["x"], s["w"], s["out"], offsets=s["offsets"], index=s["row_slot"], index_div=c["top_k"],
                           ws=s["ws"])
     elif op == "glu":
-        s3r.s3r_i8_linear(s["gate"], s["w"], s["out"], up=s["up"], ws=s["ws"])
+        s3r.s3r_int_linear(s["gate"], s["w"], s["out"], up=s["up"], ws=s["ws"])
     else:
-        s3r.s3r_i8_linear(s["x"], s["w"], s["out"], bias=s["bias"], ws=s["ws"])
+        s3r.s3r_int_linear(s["x"], s["w"], s["out"], bias=s["bias"], ws=s["ws"])
     return s["out"]
 
 
