@@ -666,6 +666,66 @@ int s3r_mx_linear(const s3r_mx_pdesc* desc, const void* A, const void* up, int32
                   const uint8_t* B_scales, void* out, int64_t ld_out, uint32_t* flags,
                   void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- INT8 rows and forward products -----------------------------------------
+ * The forward product whose backward the calls above are: y = X W^T on the codes that
+ * the backward takes, X with one step per token (s_x), W with one per output channel
+ * (s_w); S3R page, "Quantized Backpropagation with Stochastic Rounding" (the forward
+ * quantizer).  Codes are row-major as the backward's operands: 16-byte-aligned bases,
+ * leading dims that are multiples of 16, at least K and below 2^23.  K <= 131072, rows
+ * and columns below 2^31.
+ */
+
+/* s3r_int_rows: `groups` matrices of rows x K elements (a_stride elements, c_stride bytes
+ * apart; steps in runs of rows) to codes and steps, as s3r_quantize with RTNE and
+ * PER_TOKEN gives them, in one pass and without a workspace.
+ *   A, up, dtype, ld, a_rows, index, index_div: as s3r_mx_rows (up: the elements are
+ *            silu(A) * up in fp32; index: row r is row index[r] / index_div of A, a row of
+ *            zeros where that is outside 0 .. a_rows - 1);
+ *   codes    [rows x K] int8 in [-127, 127], ld_c; the columns from K to the next
+ *            multiple of 16 are written too (zeros);
+ *   delta    [groups x rows] f32: fl(amax / 127), 1 for a row of zeros;
+ *   flags    S3R_FLAG_NONFINITE, S3R_FLAG_TINY_STEP: as s3r_quantize, the row's codes are 0. */
+int s3r_int_rows(int64_t groups, int64_t rows, int64_t K, const void* A, const void* up, int32_t dtype, int64_t ld,
+                int64_t a_stride, int64_t a_rows, const int32_t* index, int64_t index_div,
+                int8_t* codes, int64_t ld_c, int64_t c_stride, float* delta, uint32_t* flags, hipStream_t stream);
+
+/* s3r_int_colsum: sums [groups x K] int32 of the codes Q [rows x K] (ld) over each group of
+ * rows: with offsets as in the grouped calls (xs of s3r_grouped_backward_dw; invalid ones
+ * raise S3R_FLAG_BAD_GROUPS and nothing is computed), with NULL over equal runs of rows
+ * (rows % groups == 0: xs_b over the examples, r_W with one group).  A group's sum is to
+ * fit 32 bits: at most 2^24 rows. */
+int s3r_int_colsum(int64_t groups, const int64_t* offsets, int64_t rows, int64_t K, const int8_t* Q, int64_t ld,
+                  int32_t* sums, uint32_t* flags, hipStream_t stream);
+
+/* Shape and weights' layout of a product. */
+typedef struct s3r_int_pdesc {
+  int64_t rows, cols, depth;        /* M (or R), N, K */
+  int64_t groups;                   /* 0: one weight; else 1 .. 4096, offsets required */
+  int64_t ld_b, b_stride;           /* bytes: a row of B's codes, from one group's B to the next (a multiple of 16) */
+  int32_t out_dtype;                /* S3R_F32 or S3R_BF16 */
+  uint32_t reserved;                /* must be 0 */
+} s3r_int_pdesc;
+
+/* s3r_int_product: out [M x N] = fl(fl(s_a[m] s_b[n]) fl(sum_k A[m,k] B[n,k])) + bias[n],
+ * the sum in int32, the result rounded once more for S3R_BF16.  A [M x K] and B [N x K]
+ * codes (columns past K may hold anything), s_a [M], s_b [N], bias [N] f32 or NULL.
+ * With groups, the rows of A and out are sorted by group, offsets is as in the grouped
+ * calls (invalid offsets raise S3R_FLAG_BAD_GROUPS and nothing is computed) and group e has
+ * B + e * b_stride, s_b and bias [groups x N].  The results do not depend on what other rows
+ * the call has. */
+int s3r_int_product(const s3r_int_pdesc* desc, const int8_t* A, int64_t ld_a, const float* s_a, const int64_t* offsets,
+                   const int8_t* B, const float* s_b, const float* bias, void* out, int64_t ld_out, uint32_t* flags,
+                   hipStream_t stream);
+
+/* s3r_int_linear: s3r_int_rows on A (one group; up and index as there) and s3r_int_product of
+ * the result, which lives in the workspace.
+ *   ws: s3r_int_linear_workspace(rows, K) bytes, 256-byte aligned. */
+size_t s3r_int_linear_workspace(int64_t rows, int64_t K);
+int s3r_int_linear(const s3r_int_pdesc* desc, const void* A, const void* up, int32_t dtype, int64_t ld, int64_t a_rows,
+                  const int32_t* index, int64_t index_div, const int64_t* offsets, const int8_t* B, const float* s_b,
+                  const float* bias, void* out, int64_t ld_out, uint32_t* flags,
+                  void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- measurement aid --------------------------------------------------
  * s3r_time_next_gemm: record `start` immediately before and `stop` immediately
  * after the GEMM kernel launched by the next s3r_backward_dx / s3r_backward_dw

@@ -851,6 +851,111 @@ int s3r_mx_linear(const s3r_mx_pdesc* d, const void* A, const void* up, int32_t 
   return finish(launch_mx_linear(r, product_args(d, c, r.ld_c, s, r.ld_s, offsets, B, Bs, out, ld_out, flags), stream));
 }
 
+// ---- INT8 rows and forward products
+constexpr int64_t kMaxI8Ld = (int64_t)1 << 23;     // 256 rows of a tile stay below 2^31 bytes
+static bool i8_size_ok(int64_t rows, int64_t K) { return rows >= 0 && rows <= 0x7FFFFFFF && K >= 0 && K <= kMaxK; }
+static int64_t whole16(int64_t K) { return (K + 15) / 16 * 16; }
+// Codes of rows x K.
+static int check_i8_codes(const int8_t* p, int64_t ld, int64_t rows, int64_t K) {
+  if (rows == 0 || K == 0) return S3R_OK;
+  return p && al16(p) && ld % 16 == 0 && ld >= K && ld < kMaxI8Ld ? S3R_OK : S3R_ERR_INVALID_ARG;
+}
+static bool f32_list(const float* p, bool needed) { return al4(p) && (p || !needed); }
+
+int s3r_int_rows(int64_t groups, int64_t rows, int64_t K, const void* A, const void* up, int32_t dtype, int64_t ld,
+                int64_t a_stride, int64_t a_rows, const int32_t* index, int64_t index_div, int8_t* codes, int64_t ld_c,
+                int64_t c_stride, float* delta, uint32_t* flags, hipStream_t stream) {
+  if (groups < 1 || groups > kMaxGroups || !i8_size_ok(rows, K)) return S3R_ERR_INVALID_ARG;
+  if (index && groups != 1) return S3R_ERR_UNSUPPORTED;
+  int rc = check_mx_source(rows, K, A, up, dtype, ld, a_rows, index, index_div);
+  if (rc) return rc;
+  if ((rc = check_i8_codes(codes, ld_c, rows, K))) return rc;
+  if (!f32_list(delta, rows > 0)) return S3R_ERR_INVALID_ARG;
+  if (groups > 1 && rows > 0 && K > 0 &&
+      (a_stride < (rows - 1) * ld + K || c_stride % 16 || c_stride < (rows - 1) * ld_c + whole16(K)))
+    return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  I8RowsArgs a{};
+  a.A = A; a.up = up; a.dtype = dtype; a.ld = ld; a.a_stride = a_stride; a.a_rows = a_rows; a.index = index;
+  a.index_div = index_div; a.G = groups; a.R = rows; a.K = K; a.K_out = whole16(K); a.codes = codes; a.ld_c = ld_c;
+  a.c_stride = c_stride; a.delta = delta; a.d_stride = rows; a.flags = flags;
+  return finish(launch_i8_rows(a, stream));
+}
+
+int s3r_int_colsum(int64_t groups, const int64_t* offsets, int64_t rows, int64_t K, const int8_t* Q, int64_t ld,
+                  int32_t* sums, uint32_t* flags, hipStream_t stream) {
+  if (groups < 1 || !i8_size_ok(rows, K)) return S3R_ERR_INVALID_ARG;
+  if (offsets ? groups > kMaxGroups || ((uintptr_t)offsets & 7u) : groups > 0x7FFFFFFF || rows % groups != 0)
+    return S3R_ERR_INVALID_ARG;
+  int rc = check_i8_codes(Q, ld, rows, K);
+  if (rc) return rc;
+  if ((K > 0 && !sums) || !al4(sums)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  return finish(launch_i8_colsum(offsets, groups, rows, K, Q, ld, sums, flags, stream));
+}
+
+static int check_i8_pdesc(const s3r_int_pdesc* d, const int64_t* offsets, const int8_t* B, const float* s_b,
+                          const float* bias, const void* out, int64_t ld_out) {
+  if (!d || d->reserved != 0 || !i8_size_ok(d->rows, d->depth) || d->cols < 0 || d->cols > 0x7FFFFFFF)
+    return S3R_ERR_INVALID_ARG;
+  if (d->groups < 0 || d->groups > kMaxGroups) return S3R_ERR_INVALID_ARG;
+  if ((d->groups > 0) != (offsets != nullptr) || ((uintptr_t)offsets & 7u)) return S3R_ERR_INVALID_ARG;
+  if (d->out_dtype != S3R_F32 && d->out_dtype != S3R_BF16) return S3R_ERR_UNSUPPORTED;
+  const bool any = d->rows > 0 && d->cols > 0;
+  int rc = check_rows(out, d->out_dtype, ld_out, d->cols, any);
+  if (rc) return rc;
+  if ((rc = check_i8_codes(B, d->ld_b, d->cols, d->depth))) return rc;
+  if (!f32_list(s_b, any) || !f32_list(bias, false)) return S3R_ERR_INVALID_ARG;
+  if (d->groups > 1 && d->cols > 0 && d->depth > 0 &&
+      (d->b_stride % 16 || d->b_stride < (d->cols - 1) * d->ld_b + whole16(d->depth)))
+    return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
+static I8ProductArgs i8_product_args(const s3r_int_pdesc* d, const int8_t* A, int64_t ld_a, const float* s_a,
+                                     const int64_t* offsets, const int8_t* B, const float* s_b, const float* bias,
+                                     void* out, int64_t ld_out, uint32_t* flags) {
+  I8ProductArgs a{};
+  a.A = A; a.lda = ld_a; a.sa = s_a; a.B = B; a.ldb = d->ld_b; a.b_stride = d->b_stride; a.sb = s_b; a.bias = bias;
+  a.offsets = offsets; a.G = d->groups; a.M = d->rows; a.N = d->cols; a.K = d->depth;
+  a.out = out; a.out_dt = d->out_dtype; a.ld_out = ld_out; a.flags = flags;
+  return a;
+}
+
+int s3r_int_product(const s3r_int_pdesc* d, const int8_t* A, int64_t ld_a, const float* s_a, const int64_t* offsets,
+                   const int8_t* B, const float* s_b, const float* bias, void* out, int64_t ld_out, uint32_t* flags,
+                   hipStream_t stream) {
+  int rc = check_i8_pdesc(d, offsets, B, s_b, bias, out, ld_out);
+  if (rc) return rc;
+  if ((rc = check_i8_codes(A, ld_a, d->rows, d->depth))) return rc;
+  if (!f32_list(s_a, d->rows > 0)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  return finish(launch_i8_product(i8_product_args(d, A, ld_a, s_a, offsets, B, s_b, bias, out, ld_out, flags), stream));
+}
+
+size_t s3r_int_linear_workspace(int64_t rows, int64_t K) {
+  if (!i8_size_ok(rows, K)) return 0;
+  return std::max<size_t>(256, align_up((size_t)rows * whole16(K), 256) + align_up((size_t)rows * 4, 256));
+}
+
+int s3r_int_linear(const s3r_int_pdesc* d, const void* A, const void* up, int32_t dtype, int64_t ld, int64_t a_rows,
+                  const int32_t* index, int64_t index_div, const int64_t* offsets, const int8_t* B, const float* s_b,
+                  const float* bias, void* out, int64_t ld_out, uint32_t* flags, void* ws, size_t ws_bytes,
+                  hipStream_t stream) {
+  int rc = check_i8_pdesc(d, offsets, B, s_b, bias, out, ld_out);
+  if (rc) return rc;
+  if ((rc = check_mx_source(d->rows, d->depth, A, up, dtype, ld, a_rows, index, index_div))) return rc;
+  if (ws_bytes < s3r_int_linear_workspace(d->rows, d->depth)) return S3R_ERR_WORKSPACE;
+  if (!ws || ((uintptr_t)ws & 255u)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  I8RowsArgs r{};
+  r.A = A; r.up = up; r.dtype = dtype; r.ld = ld; r.a_rows = a_rows; r.index = index; r.index_div = index_div;
+  r.G = 1; r.R = d->rows; r.K = d->depth; r.K_out = r.ld_c = whole16(d->depth); r.codes = (int8_t*)ws;
+  r.delta = (float*)((char*)ws + align_up((size_t)d->rows * r.ld_c, 256)); r.flags = flags;
+  return finish(launch_i8_linear(r, i8_product_args(d, r.codes, r.ld_c, r.delta, offsets, B, s_b, bias, out, ld_out, flags),
+                                 stream));
+}
+
 int s3r_time_next_gemm(hipEvent_t start, hipEvent_t stop) {
   GemmTiming& t = gemm_timing();
   t.start = start;

@@ -1,0 +1,938 @@
+// Forward products on INT8 operands: rows rounded to INT8 with one step a row (RTNE, as the backward's forward
+// operands), and y = diag(s_a) A B^T diag(s_b) + bias, dense or over expert-sorted rows with one B per group, on
+// the INT8 matrix cores.  Codes are row-major, K (the contraction) along the row: the layout that the backward's
+// products take, so one set of codes serves both.  Sums are integers, so every variant gives the same bits.
+#include <type_traits>
+
+#include "group_tiles.h"
+#include "int8_step.h"
+#include "rows8.h"
+#include "tile_ring.h"
+
+namespace s3r {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+
+// ------------------------------------------------------------------ rows ----
+// Threads threads take a row of up to 8 * Threads * Pieces elements, which stay in registers between the maximum and
+// the codes; longer rows (Long) are read again for the codes.  Codes are written up to the next multiple of 16
+// columns (zeros past K).  With `up` the element is silu(A) * up in fp32, not rounded in between.
+constexpr int kIrBlock = 256;
+
+template <typename TIn, bool UP, bool Words>
+struct I8Source {
+  const TIn *A, *U;
+  int64_t K;
+  bool some;
+  __device__ __forceinline__ I8Source(const I8RowsArgs& a, int64_t g, int64_t src) {
+    some = src >= 0;
+    const int64_t at = g * a.a_stride + (some ? src : 0) * a.ld;
+    A = (const TIn*)a.A + at;
+    U = UP ? (const TIn*)a.up + at : nullptr;
+    K = a.K;
+  }
+  __device__ __forceinline__ int64_t left(int64_t c) const { return some ? K - c : 0; }
+};
+
+// The codes of 8 elements, two words.
+__device__ __forceinline__ uint2 i8_codes(const Raw8<float>& v, const Step& s) {
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)       // 1.5 * 2^23: the sum holds the integer nearest to x, ties to even, in its low byte
+    y[i] = __float_as_uint(fminf(fmaxf(v.w[i] * s.inv, -127.f), 127.f) + 12582912.f);
+  uint2 w;
+  w.x = __builtin_amdgcn_perm(y[1], y[0], 0x0C0C0400u) | __builtin_amdgcn_perm(y[3], y[2], 0x04000C0Cu);
+  w.y = __builtin_amdgcn_perm(y[5], y[4], 0x0C0C0400u) | __builtin_amdgcn_perm(y[7], y[6], 0x04000C0Cu);
+  return s.flag ? make_uint2(0u, 0u) : w;
+}
+
+template <typename TRaw>
+__device__ __forceinline__ Raw8<float> i8_swiglu(const TRaw& v, const TRaw& u) {
+  const Raw8<float> x = mr_float8(v), y = mr_float8(u);
+  Raw8<float> h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h.w[i] = mr_swiglu(x.w[i], y.w[i]);        // 0 * 0 past the end
+  return h;
+}
+
+// Elements c, c + stride, ... (Pieces of them, 8 each) of a row.
+template <typename TIn, bool UP, bool Words, int Pieces>
+struct I8Pieces {
+  std::conditional_t<UP, Raw8<float>, Raw8<TIn>> v[Pieces];
+  __device__ __forceinline__ void load(const I8Source<TIn, UP, Words>& s, int64_t c, int stride) {
+    Raw8<TIn> a[Pieces], u[UP ? Pieces : 1];
+#pragma unroll
+    for (int q = 0; q < Pieces; ++q) {           // every load before the first conversion
+      const int64_t at = c + (int64_t)q * stride;
+      a[q] = mr_load8<TIn, Words>(s.A + at, s.left(at), s.K);
+      if constexpr (UP) u[q] = mr_load8<TIn, Words>(s.U + at, s.left(at), s.K);
+    }
+#pragma unroll
+    for (int q = 0; q < Pieces; ++q) {
+      const int64_t n = s.left(c + (int64_t)q * stride);
+      mr_tail<Words>(a[q], n, s.K);
+      if constexpr (UP) {
+        mr_tail<Words>(u[q], n, s.K);
+        v[q] = i8_swiglu(a[q], u[q]);
+      } else {
+        v[q] = a[q];
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < Pieces; ++q) m = max(m, mr_amax(v[q]));
+    return m;
+  }
+  template <typename TStore>
+  __device__ __forceinline__ void codes(const Step& s, int64_t c, int stride, TStore store) const {
+#pragma unroll
+    for (int q = 0; q < Pieces; ++q) store(c + (int64_t)q * stride, i8_codes(mr_float8(v[q]), s));
+  }
+};
+
+template <typename TIn, bool UP, bool Words, int Threads, int Pieces, bool Long>
+__global__ __launch_bounds__(kIrBlock) void i8_rows_kernel(I8RowsArgs a) {
+  constexpr int kRows = kIrBlock / Threads, kWaves = Threads / 64;
+  __shared__ uint32_t red[kIrBlock / 64];
+  const int sub = threadIdx.x % Threads, mine = threadIdx.x / Threads;
+  const int64_t r = wide_block() * kRows + mine;
+  const int64_t g = blockIdx.z;
+  if (kRows == 1 ? r >= a.R : wide_block() * kRows >= a.R) return;       // the same for the whole workgroup
+  const I8Source<TIn, UP, Words> s(a, g, mr_source(a, r));
+  constexpr int kStride = Threads * 8;
+  constexpr int64_t kSpan = (int64_t)kStride * Pieces;
+  I8Pieces<TIn, UP, Words, Pieces> p;
+  p.load(s, sub * 8, kStride);
+  uint32_t m = p.amax();
+  if constexpr (Long)
+    for (int64_t c = kSpan; c < a.K; c += kSpan) {
+      I8Pieces<TIn, UP, Words, Pieces> more;
+      more.load(s, c + sub * 8, kStride);
+      m = max(m, more.amax());
+    }
+  m = wave_max_u32(m);
+  if constexpr (kWaves > 1) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = max(m, red[w]);
+  }
+  if (r >= a.R) return;
+  const Step st = make_step(m);
+  if (sub == 0) {
+    a.delta[g * a.d_stride + r] = st.delta;
+    if (st.flag && a.flags) atomicOr(a.flags, st.flag);
+  }
+  int8_t* out = a.codes + g * a.c_stride + r * a.ld_c;
+  auto store = [&](int64_t c, uint2 w) {
+    if (c < a.K_out) *reinterpret_cast<uint2*>(out + c) = w;
+  };
+  p.codes(st, sub * 8, kStride, store);
+  if constexpr (Long)
+    for (int64_t c = kSpan; c < a.K_out; c += kSpan) {
+      I8Pieces<TIn, UP, Words, Pieces> more;
+      more.load(s, c + sub * 8, kStride);
+      more.codes(st, c + sub * 8, kStride, store);
+    }
+}
+
+// -------------------------------------------------------------- products ----
+struct I8ProdK {
+  const int8_t* A; int64_t lda; const float* sa;
+  const int8_t* B; int64_t ldb; const float* sb; const float* bias;
+  int64_t b_stride;
+  const int64_t* offsets; int64_t G;          // G = 0: dense
+  int64_t M, N, K; int tiles_n;
+  void* out; int64_t ld_out;
+  uint32_t* flags;
+};
+
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(uint16_t* p, float v) {
+  *reinterpret_cast<__bf16*>(p) = (__bf16)v;
+}
+// One result: the sum in fp32, times the product of the steps, one rounding each.
+__device__ __forceinline__ float i8_result(int acc, float sa, float sb, float bias) {
+  return (sa * sb) * (float)acc + bias;
+}
+
+// A buffer of `rows` rows of K codes (whole 16-byte words of the last one); reads past it give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* p, int64_t rows, int64_t ld, int64_t K) {
+  const int64_t bytes = rows <= 0 ? 0 : (rows - 1) * ld + (K + 15) / 16 * 16;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)(uint32_t)bytes, kRsrcWord3);
+}
+// Which of the 16 bytes at column c of a row lie before K, as masks of 4 words.
+__device__ __forceinline__ v4i tail_mask(int64_t c, int64_t K) {
+  v4i m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = K - c - 4 * i;
+    m[i] = n >= 4 ? -1 : n <= 0 ? 0 : (int)((1u << (8 * (int)n)) - 1u);
+  }
+  return m;
+}
+
+// The rows [m0, m1) of tile mt and its weight, or nothing to do.
+struct I8Tile { int64_t m0, m1; int e; bool some; };
+__device__ __forceinline__ I8Tile i8_tile(const I8ProdK& p, int mt, int tile) {
+  if (!p.G) return I8Tile{(int64_t)mt * tile, min(p.M, (int64_t)(mt + 1) * tile), 0, true};
+  GroupRound first;
+  bool bad;
+  const int total = group_total(p.offsets, p.G, p.M, tile, first, bad);
+  if (bad) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_BAD_GROUPS);
+    return I8Tile{0, 0, 0, false};
+  }
+  if (mt >= total) return I8Tile{0, 0, 0, false};
+  const GroupTile h = group_tile(p.offsets, p.G, p.M, tile, first, mt);
+  return I8Tile{h.r0, min(h.r1, h.r0 + tile), __builtin_amdgcn_readfirstlane(h.e), true};
+}
+
+// Up to four rows: byte dot products.  A wave takes kDotR weight rows, 1 KiB of each at a time (whole lines, 16 bytes a
+// lane), against the rows' codes in LDS; `split` of the workgroup's eight waves share weight rows and deal the 1 KiB
+// pieces of K among them.  The matrix cores would want a weight row in 4 lanes and 16 lines a quarter-wave.
+// With TIn the rows come unrounded: every workgroup rounds them while its first weights are on the way, so there is no
+// second launch and no codes go through memory.  TIn void: rows already in codes.
+constexpr int kDotThreads = 512, kDotWaves = kDotThreads / 64, kDotR = 4, kDotPiece = 1024;
+constexpr size_t kDotLdsMax = 60000;              // of the 64 KiB that a workgroup has without asking
+
+template <typename TOut, typename TIn, bool UP, bool Words, int MT>
+__global__ __launch_bounds__(kDotThreads) void i8_dot_kernel(I8ProdK p, I8RowsArgs q, int split) {
+  constexpr bool kFused = !std::is_void<TIn>::value;
+  __shared__ uint32_t red[kDotWaves];
+  __shared__ int part[kDotWaves][kDotR * MT];
+  extern __shared__ __attribute__((aligned(16))) int8_t rows[];         // MT rows of kpad codes
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
+  const I8Tile t = i8_tile(p, mt, MT);
+  if (!t.some) return;
+  const int rows_n = (int)(t.m1 - t.m0);
+  const int slice = wave % split, group = wave / split;
+  const int64_t n0 = ((int64_t)nt * (kDotWaves / split) + group) * kDotR;
+  const int pieces = (int)((p.K + kDotPiece - 1) / kDotPiece), kpad = pieces * kDotPiece;
+  const __amdgpu_buffer_rsrc_t rb =
+      rows_rsrc(p.B + t.e * p.b_stride + (n0 < p.N ? n0 : 0) * p.ldb, min(p.N - n0, (int64_t)kDotR), p.ldb, p.K);
+  v4i cur[kDotR], nxt[kDotR];
+  auto load = [&](v4i (&w)[kDotR], int pc) {
+    if (pc < pieces) {                             // the same in the whole wave
+#pragma unroll
+      for (int r = 0; r < kDotR; ++r)
+        w[r] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, (uint32_t)(pc * kDotPiece + lane * 16),
+                                                                             (uint32_t)r * (uint32_t)p.ldb, 0));
+    }
+  };
+  load(cur, slice);
+  load(nxt, slice + split);
+  float sa[MT];
+  if constexpr (kFused) {
+    constexpr int kPer = kDotThreads / MT, kStride = kPer * 8, kPieces = 4;
+    const int mine = threadIdx.x / kPer, c0 = (threadIdx.x % kPer) * 8;
+    const I8Source<TIn, UP, Words> s(q, 0, mine < rows_n ? mr_source(q, t.m0 + mine) : -1);
+    I8Pieces<TIn, UP, Words, kPieces> v;
+    v.load(s, c0, kStride);
+    uint32_t m = v.amax();
+    for (int64_t c = kPieces * kStride; c < p.K; c += kPieces * kStride) {
+      I8Pieces<TIn, UP, Words, kPieces> more;
+      more.load(s, c + c0, kStride);
+      m = max(m, more.amax());
+    }
+    m = wave_max_u32(m);
+    if (lane == 0) red[wave] = m;
+    __syncthreads();
+    uint32_t flag = 0;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int w = 0; w < kDotWaves / MT; ++w) a = max(a, red[i * (kDotWaves / MT) + w]);
+      const Step st = make_step(a);
+      sa[i] = st.delta;
+      flag |= st.flag;
+      if (i == mine) m = a;
+    }
+    if (flag && nt == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, flag);
+    const Step st = make_step(m);
+    auto store = [&](int64_t c, uint2 w) {
+      if (c < kpad) *reinterpret_cast<uint2*>(rows + mine * kpad + c) = w;
+    };
+    v.codes(st, c0, kStride, store);
+    for (int64_t c = kPieces * kStride; c < kpad; c += kPieces * kStride) {
+      I8Pieces<TIn, UP, Words, kPieces> more;
+      more.load(s, c + c0, kStride);
+      more.codes(st, c + c0, kStride, store);
+    }
+  } else {
+    for (int at = threadIdx.x * 16; at < MT * kpad; at += kDotThreads * 16) {
+      const int i = at / kpad, c = at - i * kpad;
+      v4i w = {0, 0, 0, 0};
+      if (i < rows_n && c < p.K)
+        w = *reinterpret_cast<const v4i*>(p.A + (t.m0 + i) * p.lda + c) & tail_mask(c, p.K);
+      *reinterpret_cast<v4i*>(rows + at) = w;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sa[i] = i < rows_n ? p.sa[t.m0 + i] : 0.f;
+  }
+  __syncthreads();
+  int acc[kDotR][MT];
+#pragma unroll
+  for (int r = 0; r < kDotR; ++r)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[r][i] = 0;
+  for (int pc = slice; pc < pieces; pc += split) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const v4i x = *reinterpret_cast<const v4i*>(rows + i * kpad + pc * kDotPiece + lane * 16);
+#pragma unroll
+      for (int r = 0; r < kDotR; ++r)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) acc[r][i] = __builtin_amdgcn_sdot4(cur[r][w], x[w], acc[r][i], false);
+    }
+#pragma unroll
+    for (int r = 0; r < kDotR; ++r) cur[r] = nxt[r];
+    load(nxt, pc + 2 * split);
+  }
+  // lane r * MT + i gets the sum of (weight row r, row i)
+  int sum = 0;
+#pragma unroll
+  for (int r = 0; r < kDotR; ++r)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int all = __builtin_amdgcn_readlane(wave_prefix(acc[r][i]), 63);
+      sum = lane == r * MT + i ? all : sum;
+    }
+  if (split > 1) {
+    if (lane < kDotR * MT) part[wave][lane] = sum;
+    __syncthreads();
+    if (slice > 0) return;
+    if (lane < kDotR * MT)
+      for (int w = 1; w < split; ++w) sum += part[wave + w][lane];
+  }
+  const int i = lane % MT;
+  const int64_t n = n0 + lane / MT;
+  if (lane >= kDotR * MT || i >= rows_n || n >= p.N) return;
+  float step = sa[0];
+#pragma unroll
+  for (int x = 1; x < MT; ++x) step = i == x ? sa[x] : step;
+  const int64_t col = t.e * p.N + n;
+  store_out((TOut*)p.out + (t.m0 + i) * p.ld_out + n, i8_result(sum, step, p.sb[col], p.bias ? p.bias[col] : 0.f));
+}
+
+// Few rows: 16 MI rows x 16 NJ columns per workgroup, whose eight waves deal K's units of 128 bytes among them and
+// join their sums in LDS.  Fragments go straight from memory to the matrix cores (v_mfma_i32_16x16x64_i8: lane l holds
+// row or column l % 16, bytes 16 (l / 16) .. + 15 of 64; the result's register r is row 4 (l / 16) + r, column l % 16);
+// the weights' bytes are the bound, so a wave issues the loads of `Depth` units before its first product.
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;
+
+template <typename TOut, int MI, int NJ, int Depth>
+__global__ __launch_bounds__(kFewThreads) void i8_few_rows_kernel(I8ProdK p) {
+  __shared__ int part[kFewWaves - 1][MI * NJ][256];
+  // The wave's index in a scalar register: the loop over its units has to branch, since the matrix instructions run
+  // whatever the execution mask says.
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
+  const I8Tile t = i8_tile(p, mt, 16 * MI);
+  if (!t.some) return;
+  const int64_t n0 = (int64_t)nt * (16 * NJ);
+  const int r15 = lane & 15, kb = lane >> 4;
+  const int units = (int)((p.K + 127) / 128);
+  const __amdgpu_buffer_rsrc_t ra = rows_rsrc(p.A + t.m0 * p.lda, t.m1 - t.m0, p.lda, p.K);
+  const __amdgpu_buffer_rsrc_t rb = rows_rsrc(p.B + t.e * p.b_stride + n0 * p.ldb, min(p.N - n0, (int64_t)(16 * NJ)), p.ldb, p.K);
+  uint32_t va[MI], vb[NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) va[i] = (uint32_t)((16 * i + r15) * p.lda + kb * 16);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) vb[j] = (uint32_t)((16 * j + r15) * p.ldb + kb * 16);
+  v4i acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  v4i x[Depth][2][MI], y[Depth][2][NJ];
+  auto load = [&](int u0) {
+#pragma unroll
+    for (int d = 0; d < Depth; ++d) {
+      const int u = u0 + d * kFewWaves;
+      if (u < units) {                             // the same in the whole wave
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            y[d][h][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb[j] + h * 64, (uint32_t)u * 128u, 0));
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+            x[d][h][i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, va[i] + h * 64, (uint32_t)u * 128u, 0));
+        }
+      }
+    }
+  };
+  for (int u0 = wave; u0 < units; u0 += kFewWaves * Depth) {
+    load(u0);
+#pragma unroll
+    for (int d = 0; d < Depth; ++d) {
+      const int u = u0 + d * kFewWaves;
+      if (u >= units) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if ((u + 1) * 128 > p.K) {                 // the last unit of a K that fills none: the rows' codes past K count as 0
+          const v4i m = tail_mask(u * 128 + h * 64 + kb * 16, p.K);
+#pragma unroll
+          for (int i = 0; i < MI; ++i) x[d][h][i] &= m;
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[d][h][i], y[d][h][j], acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[wave - 1][i * NJ + j][r * 64 + lane] = acc[i][j][r];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  TOut* out = (TOut*)p.out;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int64_t n = n0 + 16 * j + r15;
+    if (n >= p.N) continue;
+    const float sb = p.sb[t.e * p.N + n], bias = p.bias ? p.bias[t.e * p.N + n] : 0.f;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t m = t.m0 + 16 * i + 4 * kb + r;
+        if (m >= t.m1) continue;
+        int v = acc[i][j][r];
+#pragma unroll
+        for (int w = 0; w < kFewWaves - 1; ++w) v += part[w][i * NJ + j][r * 64 + lane];
+        store_out(out + m * p.ld_out + n, i8_result(v, p.sa[m], sb, bias));
+      }
+  }
+}
+
+// Many rows: BM x BN tiles, WM x WN waves of (32 MI) x (32 NI) each, operands staged through LDS by buffer-load DMA in
+// a ring of NS steps of 128 bytes of K.  A stage holds 128 bytes of each of the tile's rows (8 lanes of a load read a
+// whole line), the eight 16-byte chunks of a row at permuted places (chunk q of row r at q ^ ((r >> 1) & 7), so a
+// quarter-wave's reads hit 16 bank groups).  v_mfma_i32_32x32x32_i8: lane l holds row or column l % 32, bytes
+// 16 (l / 32) .. + 15 of 32; result register r is row (r / 4) 8 + (l / 32) 4 + r % 4, column l % 32.
+template <int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
+struct I8Geo {
+  static constexpr int WavesPerSimd = WavesPerSimd_;
+  static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr int Waves = WM * WN, Threads = 64 * Waves;
+  static constexpr int BM = 32 * MI * WM, BN = 32 * NI * WN;
+  static constexpr int PA = BM / 8 / Waves, PB = BN / 8 / Waves;          // 1 KiB pieces per wave
+  static constexpr int Loads = PA + PB;
+  static constexpr int OffB = BM * 128;
+  static constexpr int StageBytes = OffB + BN * 128;
+  static constexpr int EpiLd = 32 * NI + 4;                               // words per row of the epilogue's staging
+  static_assert(BM % (8 * Waves) == 0 && BN % (8 * Waves) == 0, "whole pieces per wave");
+};
+
+template <typename T>
+struct I8TileSrc {
+  __amdgpu_buffer_rsrc_t a, b, z;
+  uint32_t va[T::PA], vb[T::PB];              // this lane's byte offsets in step 0
+  int nk;
+};
+
+__device__ __forceinline__ int chunk_pos8(int r, int q) { return q ^ ((r >> 1) & 7); }
+
+// Step kt into stage st; past the last step every load reads zeros, so the wait counts stay the same.
+template <typename T>
+__device__ __forceinline__ void i8_load(const I8TileSrc<T>& s, uint8_t* st, int kt) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool live = kt < s.nk;
+  const __amdgpu_buffer_rsrc_t ra = live ? s.a : s.z, rb = live ? s.b : s.z;
+  const uint32_t koff = (uint32_t)kt * 128u;
+#pragma unroll
+  for (int q = 0; q < T::PA; ++q) dma16(ra, st + (wave * T::PA + q) * 1024, s.va[q], koff);
+#pragma unroll
+  for (int q = 0; q < T::PB; ++q) dma16(rb, st + T::OffB + (wave * T::PB + q) * 1024, s.vb[q], koff);
+}
+
+template <typename T>
+struct I8Frag { v4i a[T::MI], b[T::NI]; };
+
+// The fragments of quarter h of a stage.
+template <typename T>
+__device__ __forceinline__ void i8_frag(const uint8_t* st, int h, I8Frag<T>& f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  const int r31 = lane & 31, c = h * 2 + (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i) {
+    const int r = (wm * T::MI + i) * 32 + r31;
+    f.a[i] = *reinterpret_cast<const v4i*>(st + r * 128 + (chunk_pos8(r, c) << 4));
+  }
+#pragma unroll
+  for (int j = 0; j < T::NI; ++j) {
+    const int r = (wn * T::NI + j) * 32 + r31;
+    f.b[j] = *reinterpret_cast<const v4i*>(st + T::OffB + r * 128 + (chunk_pos8(r, c) << 4));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void i8_mfma(const I8Frag<T>& f, v16i (&acc)[T::MI][T::NI]) {
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+}
+
+// Quarter h of step kt with the fragments of its first quarter in f: its products cover the reads of quarter h + 1.
+template <typename T, int S, int H>
+__device__ __forceinline__ void i8_quarter(I8Frag<T>& f, v16i (&acc)[T::MI][T::NI]) {
+  I8Frag<T> n;
+  i8_frag<T>(ring<T, S>(), H + 1, n);
+  i8_mfma<T>(f, acc);
+#pragma unroll
+  for (int x = 0; x < T::MI * T::NI; ++x) {
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, (T::MI + T::NI + T::MI * T::NI - 1) / (T::MI * T::NI), 0);
+    __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  f = n;
+}
+
+// Step kt on stage S = kt % NS, the fragments of its first quarter in f.  Before the last quarter's products every read
+// of the stage has arrived; the barrier there makes step kt + 1 visible and retires stage S, which takes step kt + NS.
+template <typename T, int S>
+__device__ __forceinline__ void i8_step(const I8TileSrc<T>& src, int kt, I8Frag<T>& f, v16i (&acc)[T::MI][T::NI]) {
+  i8_quarter<T, S, 0>(f, acc);
+  i8_quarter<T, S, 1>(f, acc);
+  i8_quarter<T, S, 2>(f, acc);
+  S3R_WAIT_VM(T::Loads * (T::NS - 2));
+  S3R_WAIT_LGKM0();
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  I8Frag<T> n;
+  i8_load<T>(src, ring<T, S>(), kt + T::NS);
+  i8_frag<T>(ring<T, (S + 1) % T::NS>(), 0, n);
+  i8_mfma<T>(f, acc);
+#pragma unroll
+  for (int x = 0; x < T::MI * T::NI; ++x) {
+    __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, (T::MI + T::NI + T::MI * T::NI - 1) / (T::MI * T::NI), 0);
+    __builtin_amdgcn_sched_group_barrier(kSgVmem, (T::Loads + T::MI * T::NI - 1) / (T::MI * T::NI), 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  f = n;
+}
+
+// The first NS steps into the ring.
+template <typename T, int S>
+__device__ __forceinline__ void i8_fill(const I8TileSrc<T>& src) {
+  if constexpr (S < T::NS) {
+    i8_load<T>(src, ring<T, S>(), S);
+    i8_fill<T, S + 1>(src);
+  }
+}
+
+template <typename T, int S>
+__device__ __forceinline__ void i8_steps(const I8TileSrc<T>& src, int kt, int full, I8Frag<T>& f, v16i (&acc)[T::MI][T::NI]) {
+  if constexpr (S < T::NS) {
+    if (kt + S < full) {
+      i8_step<T, S>(src, kt + S, f, acc);
+      i8_steps<T, S + 1>(src, kt, full, f, acc);
+    }
+  }
+}
+
+// The last step where K fills none: the rows' codes past K count as 0 (what lies there may be anything).
+template <typename T, int S>
+__device__ __forceinline__ void i8_last(int stage, int kt, int64_t K, I8Frag<T>& f, v16i (&acc)[T::MI][T::NI]) {
+  if constexpr (S < T::NS) {
+    if (stage == S) {
+      const int c = (threadIdx.x & 63) >> 5;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if (h > 0) i8_frag<T>(ring<T, S>(), h, f);
+        const v4i m = tail_mask((int64_t)kt * 128 + (h * 2 + c) * 16, K);
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i) f.a[i] &= m;
+        i8_mfma<T>(f, acc);
+      }
+    } else {
+      i8_last<T, S + 1>(stage, kt, K, f, acc);
+    }
+  }
+}
+
+// The wave's results, 32 rows at a time through its own part of the (now free) ring, so that whole 16-byte words of
+// consecutive columns are stored, past the last-level cache, at the elements' alignment.
+typedef uint32_t i8_u4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t i8_u4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+template <typename T, typename TOut>
+__device__ __forceinline__ void i8_store(const I8ProdK& p, const I8Tile& t, int64_t n0, const v16i (&acc)[T::MI][T::NI]) {
+  constexpr int kBuf = 32 * T::EpiLd * 4;
+  constexpr int kPer = T::StageBytes / kBuf;                  // waves' buffers in one stage
+  static_assert(kPer > 0 && kPer * T::NS >= T::Waves, "the epilogue's staging fits the ring");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  uint8_t* stage = ring<T, 0>();
+  if (wave / kPer == 1) stage = ring<T, 1 % T::NS>();
+  if (wave / kPer == 2) stage = ring<T, 2 % T::NS>();
+  int* buf = reinterpret_cast<int*>(stage + (wave % kPer) * kBuf);
+  constexpr int W = 16 / (int)sizeof(TOut);                   // elements of a store
+  constexpr int LR = 32 * T::NI / W;                          // lanes of a row
+  const int lr = lane / LR, lc = (lane % LR) * W;
+  const int64_t n = n0 + wn * (32 * T::NI) + lc;
+  TOut* out = (TOut*)p.out;
+  float sb[W], bias[W];
+#pragma unroll
+  for (int x = 0; x < W; ++x) {
+    const bool in = n + x < p.N;
+    sb[x] = in ? p.sb[t.e * p.N + n + x] : 0.f;
+    bias[x] = in && p.bias ? p.bias[t.e * p.N + n + x] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i) {
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        buf[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * T::EpiLd + j * 32 + (lane & 31)] = acc[i][j][r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (int q = 0; q < 32; q += 64 / LR) {
+      const int64_t m = t.m0 + (wm * T::MI + i) * 32 + q + lr;
+      if (m >= t.m1) continue;
+      const float sa = p.sa[m];
+      float v[W];
+#pragma unroll
+      for (int x = 0; x < W; x += 4) {
+        const v4i c = *reinterpret_cast<const v4i*>(buf + (q + lr) * T::EpiLd + lc + x);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[x + y] = i8_result(c[y], sa, sb[x + y], bias[x + y]);
+      }
+      TOut* o = out + m * p.ld_out + n;
+      if (n + W <= p.N) {
+        if constexpr (sizeof(TOut) == 2) {
+          typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+          typedef float f2 __attribute__((ext_vector_type(2)));
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[2 * x], v[2 * x + 1]}), bf2));
+          __builtin_nontemporal_store((v4u32{w[0], w[1], w[2], w[3]}), reinterpret_cast<i8_u4_a2*>(o));
+        } else {
+          __builtin_nontemporal_store((v4u32{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}),
+                                      reinterpret_cast<i8_u4_a4*>(o));
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < W; ++x)
+          if (n + x < p.N) store_out(o + x, v[x]);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <typename T, typename TOut>
+__global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void i8_tile_kernel(I8ProdK p, int tiles_m) {
+  // A contiguous range of tiles per XCD (workgroups go to the 8 XCDs in turn).  Grouped: of the tiles that the
+  // groups have, not of the grid's bound on them, whose surplus would all be the last XCD's.
+  int bid = blockIdx.x;
+  GroupRound first;
+  if (p.G) {
+    bool bad;
+    tiles_m = group_total(p.offsets, p.G, p.M, T::BM, first, bad);
+    if (bad) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, S3R_FLAG_BAD_GROUPS);
+      return;
+    }
+    const int nblocks = tiles_m * p.tiles_n, per = (nblocks + 7) / 8;
+    bid = (blockIdx.x % 8) * per + blockIdx.x / 8;
+    if ((int)blockIdx.x / 8 >= per || bid >= nblocks) return;
+  } else {
+    const int nblocks = tiles_m * p.tiles_n;
+    if (nblocks % 8 == 0) bid = (bid % 8) * (nblocks / 8) + bid / 8;
+  }
+  const int group = 8 * p.tiles_n;
+  const int first_m = (bid / group) * 8;
+  const int gsz = min(tiles_m - first_m, 8);
+  const int tm = first_m + (bid % group) % gsz, tn = (bid % group) / gsz;
+  I8Tile t{(int64_t)tm * T::BM, p.M, 0, true};
+  const int64_t n0 = (int64_t)tn * T::BN;
+  if (p.G) {
+    const GroupTile h = group_tile(p.offsets, p.G, p.M, T::BM, first, tm);
+    t = I8Tile{h.r0, h.r1, h.e, true};
+  }
+  // the tile's rows of both operands; rows past the group's end reach only results that are not stored
+  I8TileSrc<T> src;
+  src.nk = (int)((p.K + 127) / 128);
+  src.a = rows_rsrc(p.A + t.m0 * p.lda, min(p.M - t.m0, (int64_t)T::BM), p.lda, p.K);
+  src.b = rows_rsrc(p.B + t.e * p.b_stride + n0 * p.ldb, min(p.N - n0, (int64_t)T::BN), p.ldb, p.K);
+  src.z = __builtin_amdgcn_make_buffer_rsrc((void*)p.A, (short)0, 0, kRsrcWord3);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int q = 0; q < T::PA; ++q) {
+    const int r = (wave * T::PA + q) * 8 + (lane >> 3);
+    src.va[q] = (uint32_t)(r * p.lda + chunk_pos8(r, lane & 7) * 16);
+  }
+#pragma unroll
+  for (int q = 0; q < T::PB; ++q) {
+    const int r = (wave * T::PB + q) * 8 + (lane >> 3);
+    src.vb[q] = (uint32_t)(r * p.ldb + chunk_pos8(r, lane & 7) * 16);
+  }
+  v16i acc[T::MI][T::NI];
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+  i8_fill<T, 0>(src);
+  S3R_WAIT_VM(T::Loads * (T::NS - 1));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  I8Frag<T> f;
+  i8_frag<T>(ring<T, 0>(), 0, f);
+  const int full = (int)(p.K / 128);
+  for (int kt = 0; kt < full; kt += T::NS) i8_steps<T, 0>(src, kt, full, f, acc);
+  if (full < src.nk) i8_last<T, 0>(full % T::NS, full, p.K, f, acc);
+  S3R_WAIT_VM(0);
+  S3R_WAIT_LGKM0();
+  __builtin_amdgcn_s_barrier();
+  i8_store<T, TOut>(p, t, n0, acc);
+}
+
+// ----------------------------------------------------------- column sums ----
+// A workgroup adds 64 rows of 1024 columns, four columns a thread; integer sums, so the order of its additions into
+// memory does not change them.
+constexpr int kCsRows = 64;
+__global__ __launch_bounds__(256) void i8_colsum_clear_kernel(const int64_t* offsets, int64_t G, int64_t R, int64_t K,
+                                                              int32_t* sums, uint32_t* flags) {
+  if (offsets) {
+    GroupRound first;
+    bool bad;
+    group_total(offsets, G, R, 1, first, bad);
+    if (bad) {
+      if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && flags) atomicOr(flags, S3R_FLAG_BAD_GROUPS);
+      return;
+    }
+  }
+  const int64_t i = wide_block() * 256 + threadIdx.x;
+  if (i < G * K) sums[i] = 0;
+}
+
+__global__ __launch_bounds__(256) void i8_colsum_kernel(const int64_t* offsets, int64_t G, int64_t R, int64_t K,
+                                                        const int8_t* Q, int64_t ld, int32_t* sums) {
+  const int64_t kblocks = (K + 1023) / 1024;
+  const int64_t block = wide_block(), rb = block / kblocks, c = (block - rb * kblocks) * 1024 + threadIdx.x * 4;
+  const int64_t r0 = rb * kCsRows, r1 = min(r0 + kCsRows, R);
+  if (r0 >= R) return;
+  int64_t e = 0;
+  if (offsets) {
+    GroupRound first;
+    bool bad;
+    group_total(offsets, G, R, 1, first, bad);
+    if (bad) return;
+    e = group_tile(offsets, G, R, 1, first, (int)r0).e;
+  } else {
+    e = r0 / (R / G);
+  }
+  const __amdgpu_buffer_rsrc_t rq = rows_rsrc(Q + r0 * ld, r1 - r0, ld, K);
+  for (int64_t r = r0; r < r1; ++e) {
+    const int64_t end = min(r1, offsets ? offsets[e + 1] : (e + 1) * (R / G));
+    if (end <= r) continue;
+    int s[4] = {0, 0, 0, 0};
+#pragma unroll 8
+    for (; r < end; ++r) {
+      const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(rq, (uint32_t)((r - r0) * ld + c), 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += (int)(w << (24 - 8 * i)) >> 24;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < K) atomicAdd(sums + e * K + c + i, s[i]);
+  }
+}
+
+bool i8_words(const I8RowsArgs& a) {       // rows in whole 16-byte words
+  const int esize = a.dtype == S3R_BF16 ? 2 : 4;
+  return ((uintptr_t)a.A & 15u) == 0 && ((uintptr_t)a.up & 15u) == 0 && (a.ld * esize) % 16 == 0 &&
+         (a.a_stride * esize) % 16 == 0 && a.K % 8 == 0;
+}
+
+template <typename TIn, bool UP, bool Words, int Threads, int Pieces, bool Long>
+hipError_t run_i8_rows(const I8RowsArgs& a, hipStream_t st) {
+  dim3 grid = wide_grid((a.R + kIrBlock / Threads - 1) / (kIrBlock / Threads));
+  grid.z = (unsigned)a.G;
+  hipLaunchKernelGGL((i8_rows_kernel<TIn, UP, Words, Threads, Pieces, Long>), grid, dim3(kIrBlock), 0, st, a);
+  return hipGetLastError();
+}
+
+template <typename TIn, bool UP, bool Words>
+hipError_t run_i8_rows(const I8RowsArgs& a, hipStream_t st) {
+  if (a.K <= 512) return run_i8_rows<TIn, UP, Words, 64, 1, false>(a, st);
+  if (a.K <= 2048) return run_i8_rows<TIn, UP, Words, 64, 4, false>(a, st);
+  if (a.K <= 4096) return run_i8_rows<TIn, UP, Words, 256, 2, false>(a, st);
+  if (a.K <= 8192) return run_i8_rows<TIn, UP, Words, 256, 4, false>(a, st);
+  if (a.K <= 16384) return run_i8_rows<TIn, UP, Words, 256, 8, false>(a, st);
+  return run_i8_rows<TIn, UP, Words, 256, 4, true>(a, st);
+}
+
+template <typename TIn>
+hipError_t run_i8_rows(const I8RowsArgs& a, hipStream_t st) {
+  const bool words = i8_words(a);
+  if (a.up) return words ? run_i8_rows<TIn, true, true>(a, st) : run_i8_rows<TIn, true, false>(a, st);
+  return words ? run_i8_rows<TIn, false, true>(a, st) : run_i8_rows<TIn, false, false>(a, st);
+}
+}  // namespace
+
+hipError_t launch_i8_rows(const I8RowsArgs& a, hipStream_t st) {
+  if (a.R == 0 || a.G == 0) return hipSuccess;
+  return a.dtype == S3R_BF16 ? run_i8_rows<uint16_t>(a, st) : run_i8_rows<float>(a, st);
+}
+
+hipError_t launch_i8_colsum(const int64_t* offsets, int64_t G, int64_t R, int64_t K, const int8_t* Q, int64_t ld,
+                            int32_t* sums, uint32_t* flags, hipStream_t st) {
+  if (G * K == 0) return launch_check_offsets(offsets, offsets ? G : 0, R, flags, st);
+  hipLaunchKernelGGL(i8_colsum_clear_kernel, wide_grid((G * K + 255) / 256), dim3(256), 0, st, offsets, G, R, K, sums, flags);
+  if (R > 0)
+    hipLaunchKernelGGL(i8_colsum_kernel, wide_grid((R + kCsRows - 1) / kCsRows * ((K + 1023) / 1024)), dim3(256), 0, st,
+                       offsets, G, R, K, Q, ld, sums);
+  return hipGetLastError();
+}
+
+namespace {
+using I8Tile256 = I8Geo<4, 2, 2, 4, 2, 2>;        // 256 x 256, 8 waves
+using I8Tile256x128 = I8Geo<2, 2, 4, 2, 3, 2>;    // 8 waves
+using I8Tile128 = I8Geo<2, 2, 2, 2, 2, 2>;        // 4 waves, two workgroups per CU
+using I8Tile128x64 = I8Geo<2, 1, 2, 2, 3, 2>;
+using I8Tile64 = I8Geo<1, 1, 2, 2, 3, 2>;
+
+// The largest tile that still gives this many workgroups (three quarters of the CUs).
+constexpr int64_t kFillTiles = 192;
+
+I8ProdK product_params(const I8ProductArgs& a) {
+  I8ProdK p{};
+  p.A = a.A; p.lda = a.lda; p.sa = a.sa; p.B = a.B; p.ldb = a.ldb; p.sb = a.sb; p.bias = a.bias; p.b_stride = a.b_stride;
+  p.offsets = a.offsets; p.G = a.G; p.M = a.M; p.N = a.N; p.K = a.K;
+  p.out = a.out; p.ld_out = a.ld_out; p.flags = a.flags;
+  return p;
+}
+
+// rows per weight, on average (only the device knows the groups' own)
+int64_t mean_rows(const I8ProductArgs& a) { return a.G ? (a.M + a.G - 1) / a.G : a.M; }
+// Row tiles of a product; grouped: of every group, at most one partial tile each.
+int64_t row_tiles(const I8ProductArgs& a, int tile) {
+  return a.G ? a.M / tile + std::min(a.G, a.M) : (a.M + tile - 1) / tile;
+}
+constexpr int64_t kMostItems = (int64_t)1 << 32;
+
+template <typename T, typename TOut>
+hipError_t run_i8_tiles(const I8ProductArgs& a, I8ProdK p, hipStream_t st) {
+  const int64_t mt = row_tiles(a, T::BM);
+  p.tiles_n = (int)((a.N + T::BN - 1) / T::BN);
+  if ((mt * p.tiles_n + 7) * T::Threads >= kMostItems) return hipErrorInvalidConfiguration;
+  const int64_t blocks = a.G ? (mt * p.tiles_n + 7) / 8 * 8 : mt * p.tiles_n;
+  hipLaunchKernelGGL((i8_tile_kernel<T, TOut>), dim3((unsigned)blocks), dim3(T::Threads), 0, st, p, (int)mt);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t run_i8_tiles(const I8ProductArgs& a, hipStream_t st) {
+  const I8ProdK p = product_params(a);
+  return a.out_dt == S3R_BF16 ? run_i8_tiles<T, uint16_t>(a, p, st) : run_i8_tiles<T, float>(a, p, st);
+}
+
+template <int MI, int NJ, int Depth>
+hipError_t run_i8_few(const I8ProductArgs& a, hipStream_t st) {
+  I8ProdK p = product_params(a);
+  const int64_t mt = row_tiles(a, 16 * MI);
+  p.tiles_n = (int)((a.N + 16 * NJ - 1) / (16 * NJ));
+  if (mt * p.tiles_n * kFewThreads >= kMostItems) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(mt * p.tiles_n)), block(kFewThreads);
+  if (a.out_dt == S3R_BF16) hipLaunchKernelGGL((i8_few_rows_kernel<uint16_t, MI, NJ, Depth>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((i8_few_rows_kernel<float, MI, NJ, Depth>), grid, block, 0, st, p);
+  return hipGetLastError();
+}
+
+size_t dot_lds(int rows, int64_t K) { return (size_t)rows * (size_t)((K + kDotPiece - 1) / kDotPiece) * kDotPiece; }
+
+template <typename TIn, bool UP, bool Words, int MT>
+hipError_t run_i8_dot(const I8ProductArgs& a, const I8RowsArgs& q, hipStream_t st) {
+  I8ProdK p = product_params(a);
+  const int64_t mt = row_tiles(a, MT), groups = (a.N + kDotR - 1) / kDotR;
+  // waves that share weight rows: enough for two workgroups a CU, where K has pieces for them
+  int split = 1;
+  while (split < kDotWaves && mt * ((groups * split + kDotWaves - 1) / kDotWaves) < 512 && split * kDotPiece < a.K) split *= 2;
+  p.tiles_n = (int)((groups * split + kDotWaves - 1) / kDotWaves);
+  if (mt * p.tiles_n * kDotThreads >= kMostItems) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(mt * p.tiles_n)), block(kDotThreads);
+  const size_t lds = dot_lds(MT, a.K);
+  if (a.out_dt == S3R_BF16)
+    hipLaunchKernelGGL((i8_dot_kernel<uint16_t, TIn, UP, Words, MT>), grid, block, lds, st, p, q, split);
+  else
+    hipLaunchKernelGGL((i8_dot_kernel<float, TIn, UP, Words, MT>), grid, block, lds, st, p, q, split);
+  return hipGetLastError();
+}
+// Rows of a workgroup: 1, 2 or 4.
+int dot_rows(const I8ProductArgs& a) { return a.M <= 2 ? (int)a.M : 4; }
+template <typename TIn, bool UP, bool Words>
+hipError_t run_i8_dot(const I8ProductArgs& a, const I8RowsArgs& q, hipStream_t st) {
+  const int rows = dot_rows(a);
+  if (rows == 1) return run_i8_dot<TIn, UP, Words, 1>(a, q, st);
+  return rows == 2 ? run_i8_dot<TIn, UP, Words, 2>(a, q, st) : run_i8_dot<TIn, UP, Words, 4>(a, q, st);
+}
+template <typename TIn>
+hipError_t run_i8_dot(const I8ProductArgs& a, const I8RowsArgs& q, hipStream_t st) {
+  const bool words = i8_words(q);
+  if (q.up) return words ? run_i8_dot<TIn, true, true>(a, q, st) : run_i8_dot<TIn, true, false>(a, q, st);
+  return words ? run_i8_dot<TIn, false, true>(a, q, st) : run_i8_dot<TIn, false, false>(a, q, st);
+}
+
+// Rows (per weight, on average) that the byte dot products take.
+constexpr int64_t kDotRows = 4, kDotGrouped = 1;
+bool takes_dots(const I8ProductArgs& a) {
+  return mean_rows(a) <= (a.G ? kDotGrouped : kDotRows) && dot_lds(dot_rows(a), a.K) <= kDotLdsMax;
+}
+// Rows per weight, on average, up to which a grouped product takes the few-rows kernel.
+constexpr int64_t kFewGrouped = 16;
+
+template <typename T>
+int64_t tile_count(const I8ProductArgs& a) { return ((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN); }
+}  // namespace
+
+hipError_t launch_i8_product(const I8ProductArgs& a, hipStream_t st) {
+  if (a.M == 0 || a.N == 0) return launch_check_offsets(a.offsets, a.G, a.M, a.flags, st);
+  if (takes_dots(a)) return run_i8_dot<void, false, true>(a, I8RowsArgs{}, st);
+  if (a.G) {
+    const int64_t rows = mean_rows(a);
+    if (rows <= kFewGrouped) return run_i8_few<1, 2, 2>(a, st);
+    return rows < 1024 ? run_i8_tiles<I8Tile128>(a, st) : run_i8_tiles<I8Tile256x128>(a, st);
+  }
+  if (a.M <= 16) return run_i8_few<1, 1, 4>(a, st);
+  if (a.M <= 32) return run_i8_few<2, 1, 4>(a, st);
+  if (a.M <= 64) return run_i8_few<4, 1, 2>(a, st);
+  if (tile_count<I8Tile256>(a) >= kFillTiles) return run_i8_tiles<I8Tile256>(a, st);
+  if (tile_count<I8Tile256x128>(a) >= kFillTiles) return run_i8_tiles<I8Tile256x128>(a, st);
+  if (tile_count<I8Tile128>(a) >= kFillTiles) return run_i8_tiles<I8Tile128>(a, st);
+  if (tile_count<I8Tile128x64>(a) >= kFillTiles) return run_i8_tiles<I8Tile128x64>(a, st);
+  return run_i8_tiles<I8Tile64>(a, st);
+}
+
+// Rows and product; `rows` writes the codes that `prod` reads, unless the product rounds them itself.
+hipError_t launch_i8_linear(const I8RowsArgs& rows, const I8ProductArgs& prod, hipStream_t st) {
+  if (prod.M == 0 || prod.N == 0) return launch_check_offsets(prod.offsets, prod.G, prod.M, prod.flags, st);
+  if (takes_dots(prod)) return rows.dtype == S3R_BF16 ? run_i8_dot<uint16_t>(prod, rows, st) : run_i8_dot<float>(prod, rows, st);
+  const hipError_t e = launch_i8_rows(rows, st);
+  return e != hipSuccess ? e : launch_i8_product(prod, st);
+}
+
+}  // namespace s3r

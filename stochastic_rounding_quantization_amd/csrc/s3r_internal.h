@@ -241,6 +241,27 @@ hipError_t launch_mx_linear(const MxRowsArgs& rows, const MxProductArgs& prod, h
 // A grouped product without results still looks at its offsets.
 hipError_t launch_check_offsets(const int64_t* offsets, int64_t G, int64_t R, uint32_t* flags, hipStream_t st);
 
+// INT8 rows and forward products (int_linear.hip).
+struct I8RowsArgs {
+  const void* A; const void* up; int dtype; int64_t ld, a_stride, a_rows;
+  const int32_t* index; int64_t index_div;
+  int64_t G, R, K, K_out;      // K_out: K in whole 16-byte words, the columns that are written
+  int8_t* codes; int64_t ld_c, c_stride; float* delta; int64_t d_stride;
+  uint32_t* flags;
+};
+struct I8ProductArgs {       // out [M x N] = diag(sa) A [M x K] . B [N x K]^T diag(sb) + bias, those of group e for its rows
+  const int8_t* A; int64_t lda; const float* sa;
+  const int8_t* B; int64_t ldb, b_stride; const float* sb; const float* bias;
+  const int64_t* offsets; int64_t G;
+  int64_t M, N, K;
+  void* out; int out_dt; int64_t ld_out; uint32_t* flags;
+};
+hipError_t launch_i8_rows(const I8RowsArgs& a, hipStream_t st);
+hipError_t launch_i8_product(const I8ProductArgs& a, hipStream_t st);
+hipError_t launch_i8_linear(const I8RowsArgs& rows, const I8ProductArgs& prod, hipStream_t st);
+hipError_t launch_i8_colsum(const int64_t* offsets, int64_t G, int64_t R, int64_t K, const int8_t* Q, int64_t ld,
+                            int32_t* sums, uint32_t* flags, hipStream_t st);
+
 // SwiGLU backward glue (swiglu.hip).
 hipError_t launch_swiglu_backward(int64_t T, int64_t F, const float* dH, int64_t ld_dh, const uint16_t* Ag,
                                   const uint16_t* Au, int64_t ld_a, uint16_t* Gg, uint16_t* Gu, int64_t ld_g,

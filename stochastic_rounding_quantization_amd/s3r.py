@@ -36,7 +36,8 @@ EXPORTED = ["s3r_quantize_workspace", "s3r_quantize", "s3r_quantize_with_amax", 
             "s3r_grouped_backward_dx", "s3r_grouped_backward_dw", "s3r_mx_workspace", "s3r_mx_operand_workspace",
             "s3r_mx_operand", "s3r_mx_quantize", "s3r_mx_backward_dx", "s3r_mx_backward_dw", "s3r_route_workspace", "s3r_route",
             "s3r_route_backward", "s3r_dispatch", "s3r_combine", "s3r_combine_backward", "s3r_mx_rows",
-            "s3r_mx_product", "s3r_mx_linear_workspace", "s3r_mx_linear", "s3r_time_next_gemm",
+            "s3r_mx_product", "s3r_mx_linear_workspace", "s3r_mx_linear", "s3r_int_rows", "s3r_int_colsum", "s3r_int_product",
+            "s3r_int_linear_workspace", "s3r_int_linear", "s3r_time_next_gemm",
             "s3r_status_string", "s3r_version"]
 
 
@@ -70,6 +71,12 @@ class MxPDesc(ctypes.Structure):
                 ("groups", ctypes.c_int64), ("ld_b", ctypes.c_int64), ("ld_bs", ctypes.c_int64),
                 ("b_stride", ctypes.c_int64), ("bs_stride", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_uint32)]
+
+
+class IntPDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("depth", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("ld_b", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_uint32)]
 
 
 def qdesc(rows, cols, rows_per_example=None, mode=S3R, ec=EC_NONE, scale=PER_TENSOR, layer_id=0, seed=0,
@@ -152,6 +159,15 @@ def lib() -> ctypes.CDLL:
     L.s3r_mx_linear_workspace.argtypes = [I64, I64]
     L.s3r_mx_linear_workspace.restype = SZ
     L.s3r_mx_linear.argtypes = [MP, P, P, I32, I64, I64, P, I64, P, P, P, P, I64, P, P, SZ, P]
+    IP = ctypes.POINTER(IntPDesc)
+    L.s3r_int_rows.argtypes = [I64, I64, I64, P, P, I32, I64, I64, I64, P, I64, P, I64, I64, P, P, P]
+    L.s3r_int_colsum.argtypes = [I64, P, I64, I64, P, I64, P, P, P]
+    L.s3r_int_product.argtypes = [IP, P, I64, P, P, P, P, P, P, I64, P, P]
+    L.s3r_int_linear_workspace.argtypes = [I64, I64]
+    L.s3r_int_linear_workspace.restype = SZ
+    L.s3r_int_linear.argtypes = [IP, P, P, I32, I64, I64, P, I64, P, P, P, P, P, I64, P, P, SZ, P]
+    for f in ("s3r_int_rows", "s3r_int_colsum", "s3r_int_product", "s3r_int_linear"):
+        getattr(L, f).restype = ctypes.c_int
     for f in ("s3r_route", "s3r_route_backward", "s3r_dispatch", "s3r_combine", "s3r_combine_backward",
               "s3r_mx_rows", "s3r_mx_product", "s3r_mx_linear"):
         getattr(L, f).restype = ctypes.c_int
@@ -727,6 +743,169 @@ def s3r_mx_linear(A, w: MxRows, out, *, up=None, offsets=None, index=None, index
         _check("s3r_mx_linear", rc)
 
 
+def _here(*tensors):
+    """Refuse tensors of another device than the current one (the library works on that), or of the host."""
+    import torch
+    first = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != first:
+            raise ValueError("tensors on different devices")
+    if torch.cuda.is_available() if first < 0 else first != torch._C._cuda_getDevice():
+        raise ValueError("tensors are not on the current device")
+
+
+def _whole(t):
+    """t, without elements contiguous (torch gives such tensors any strides)."""
+    return t if t is None or t.numel() else t.new_empty(t.shape)
+
+
+@dataclass
+class IntRows:
+    """INT8 matrices of rows x K codes, a step a row: codes int8 [groups x rows x K in whole 16s], delta f32
+    [groups x rows].  ``Q`` is the codes as the backward's products take them."""
+    codes: object
+    delta: object
+    rows: int
+    K: int
+    groups: int = 1
+    _descs: dict = field(default_factory=dict, repr=False)      # product descriptors by their sizes
+
+    @property
+    def Q(self):
+        q = self.codes[..., :self.K]
+        return q[0] if self.groups == 1 else q
+
+
+def int_rows_buffer(rows: int, K: int, device, groups: int = 1) -> IntRows:
+    import torch
+    return IntRows(torch.empty(groups, rows, _pad16(K), dtype=torch.int8, device=device),
+                  torch.empty(groups, rows, dtype=torch.float32, device=device), rows, K, groups)
+
+
+def _int_fit(m: IntRows):
+    """Refuse codes and steps that are not what m says."""
+    import torch
+    c, d = m.codes, m.delta
+    _typed(c, torch.int8, "codes")
+    _typed(d, torch.float32, "delta")
+    if c.shape != (m.groups, m.rows, _pad16(m.K)) or d.shape != (m.groups, m.rows) or not c.is_contiguous() or \
+            not d.is_contiguous():
+        raise ValueError("INT8 codes or steps are not contiguous, or not of their rows' sizes")
+
+
+def s3r_int_rows(A, out: IntRows, up=None, index=None, index_div=1, flags=None, stream=None, *, rc_only=False):
+    """A [rows x K], or [groups x rows x K], f32/bf16 (silu(A) * up with up) -> out; with index, row r of out is
+    row index[r] // index_div of the 2-D A."""
+    A, up = _whole(A), _whole(up)
+    if A.dim() not in (2, 3) or A.stride(-1) != 1:
+        raise ValueError("expected row-major matrices (unit column stride)")
+    G, a_rows, K = (1, *A.shape) if A.dim() == 2 else A.shape
+    if (out.groups, out.K) != (G, K) or (index is None and out.rows != a_rows):
+        raise ValueError("out does not fit A")
+    _int_fit(out)
+    _index(index, out.rows)
+    _like(A, up)
+    _here(A, out.codes, out.delta, up, index, flags)
+    ld = _pad16(K)
+    rc = lib().s3r_int_rows(G, out.rows, K, _ptr(A), _ptr(up), _gdtype(A), A.stride(-2), A.stride(0) if A.dim() == 3 else 0,
+                           a_rows, _ptr(index), index_div, _ptr(out.codes), ld, out.rows * ld, _ptr(out.delta), _ptr(flags),
+                           _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_int_rows", rc)
+
+
+def s3r_int_colsum(Q, sums, offsets=None, flags=None, stream=None, *, rc_only=False):
+    """sums int32 [groups x K] of the codes Q [rows x K] over each group's rows (offsets int64 [groups + 1]), or over
+    equal runs of rows."""
+    import torch
+    _typed(Q, torch.int8, "Q")
+    rows, K = Q.shape
+    groups = sums.shape[0]
+    _typed(sums, torch.int32, "sums")
+    _shaped(sums, (groups, K), "sums")
+    if not sums.is_contiguous():
+        raise ValueError("sums: expected a contiguous tensor")
+    if offsets is not None:
+        _flat("offsets", offsets, torch.int64, groups + 1)
+    _here(Q, sums, offsets, flags)
+    rc = lib().s3r_int_colsum(groups, _ptr(offsets), rows, K, _ptr(Q), _ld(Q), _ptr(sums), _ptr(flags), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_int_colsum", rc)
+
+
+def _int_pdesc(rows, w: IntRows, out, offsets, bias):
+    import torch
+    dt = out.dtype
+    _shaped(out, (rows, w.rows), "out")
+    if offsets is None:
+        if w.groups != 1:
+            raise ValueError("several weights need the rows' offsets")
+    else:
+        _flat("offsets", offsets, torch.int64, w.groups + 1)
+    if bias is not None:
+        _flat("bias", bias, torch.float32, w.groups * w.rows)
+    key = rows, dt, offsets is None, w.rows, w.K, w.groups
+    d = w._descs.get(key)
+    if d is None:
+        if dt not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"unsupported output dtype {dt}")
+        if len(w._descs) >= 64:         # a program with ever new row counts
+            w._descs.clear()
+        ld = _pad16(w.K)
+        d = w._descs[key] = IntPDesc(rows, w.rows, w.K, 0 if offsets is None else w.groups, ld, w.rows * ld,
+                                    S3R_BF16 if dt is torch.bfloat16 else S3R_F32, 0)
+    return d
+
+
+def s3r_int_product(a: IntRows, w: IntRows, out, offsets=None, bias=None, flags=None, stream=None, *, rc_only=False):
+    """out [rows x w.rows] (f32/bf16) = a w^T + bias; with offsets int64 [groups + 1], a's rows are sorted by group and
+    group e takes w's matrix e and bias[e] (f32 [w.rows], or [groups x w.rows])."""
+    if a.groups != 1 or a.K != w.K:
+        raise ValueError("a and w do not fit")
+    _int_fit(a)
+    _int_fit(w)
+    _here(a.codes, a.delta, w.codes, w.delta, out, offsets, bias, flags)
+    d = _int_pdesc(a.rows, w, out, offsets, bias)
+    rc = lib().s3r_int_product(d, _ptr(a.codes), _pad16(a.K), _ptr(a.delta), _ptr(offsets), _ptr(w.codes), _ptr(w.delta),
+                              _ptr(bias), _ptr(out), _ld(out), _ptr(flags), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_int_product", rc)
+
+
+def s3r_int_linear_workspace(rows: int, K: int) -> int:
+    return lib().s3r_int_linear_workspace(rows, K)
+
+
+def int_linear_buffer(rows: int, K: int, device):
+    """A workspace for s3r_int_linear on that many rows."""
+    return _scratch(s3r_int_linear_workspace(rows, K), device)
+
+
+def s3r_int_linear(A, w: IntRows, out, *, up=None, offsets=None, index=None, index_div=1, bias=None, ws=None, flags=None,
+                  stream=None, rc_only=False):
+    """out = int8(A) w^T + bias in one call (A as in s3r_int_rows, the product as in s3r_int_product)."""
+    rows = out.shape[0]
+    A, up = _whole(A), _whole(up)
+    a_rows, K = A.shape
+    if K != w.K or (index is None and a_rows != rows):
+        raise ValueError("A, w and out do not fit")
+    _int_fit(w)
+    _index(index, rows)
+    _like(A, up)
+    _here(A, w.codes, w.delta, out, up, offsets, index, bias, ws, flags)
+    d = _int_pdesc(rows, w, out, offsets, bias)
+    rc = lib().s3r_int_linear(d, A.data_ptr(), _ptr(up), _gdtype(A), _ld(A), a_rows, _ptr(index), index_div, _ptr(offsets),
+                             w.codes.data_ptr(), w.delta.data_ptr(), _ptr(bias), out.data_ptr(), _ld(out), _ptr(flags),
+                             _ptr(ws), _nbytes(ws), _stream(stream))
+    if rc_only:
+        return rc
+    if rc:
+        _check("s3r_int_linear", rc)
+
+
 def swiglu_backward(dH, A_gate, A_up, stream=None):
     """Allocate G_gate, G_up (bf16, like A_gate) and run s3r_swiglu_backward."""
     import torch
@@ -1058,4 +1237,46 @@ def mx_linear(A, w: MxRows, *, up=None, offsets=None, index=None, index_div=1, o
         out = torch.empty(rows, w.rows, dtype=out_dtype or A.dtype, device=A.device)
         ws = mx_linear_buffer(rows, w.K, A.device)
     s3r_mx_linear(A, w, out, up=up, offsets=offsets, index=index, index_div=index_div, ws=ws, flags=flags, stream=stream)
+    return out
+
+
+# ------------------------------------------------- INT8 forward helpers ----
+# ``stream`` as in the helpers above.
+
+def int_rows(A, *, up=None, index=None, index_div=1, flags=None, stream=None) -> IntRows:
+    """INT8 rows of A ([rows x K], or [groups x rows x K]: weights [N x K] of every expert), a step each (RTNE)."""
+    G = 1 if A.dim() == 2 else A.shape[0]
+    with _on(stream):
+        out = int_rows_buffer(A.shape[-2] if index is None else index.numel(), A.shape[-1], A.device, G)
+    s3r_int_rows(A, out, up, index, index_div, flags, stream)
+    return out
+
+
+def int_colsum(Q, groups=1, *, offsets=None, flags=None, stream=None):
+    """Column sums of the codes Q [rows x K] over equal runs of rows, or over the groups of offsets: int32 [groups x K]."""
+    import torch
+    with _on(stream):
+        sums = torch.empty(groups if offsets is None else offsets.numel() - 1, Q.shape[1], dtype=torch.int32, device=Q.device)
+    s3r_int_colsum(Q, sums, offsets, flags, stream)
+    return sums
+
+
+def int_product(a: IntRows, w: IntRows, *, offsets=None, bias=None, out_dtype=None, flags=None, stream=None):
+    import torch
+    with _on(stream):
+        out = torch.empty(a.rows, w.rows, dtype=out_dtype or torch.float32, device=a.codes.device)
+    s3r_int_product(a, w, out, offsets, bias, flags, stream)
+    return out
+
+
+def int_linear(A, w: IntRows, *, up=None, offsets=None, index=None, index_div=1, bias=None, out_dtype=None, flags=None,
+              stream=None):
+    """A's rows in INT8 times the weights w (int_rows): [rows x w.rows], of A's dtype unless out_dtype is given."""
+    import torch
+    rows = A.shape[0] if index is None else index.numel()
+    with _on(stream):
+        out = torch.empty(rows, w.rows, dtype=out_dtype or A.dtype, device=A.device)
+        ws = int_linear_buffer(rows, w.K, A.device)
+    s3r_int_linear(A, w, out, up=up, offsets=offsets, index=index, index_div=index_div, bias=bias, ws=ws, flags=flags,
+                  stream=stream)
     return out
