@@ -726,6 +726,39 @@ int s3r_int_linear(const s3r_int_pdesc* desc, const void* A, const void* up, int
                   const float* bias, void* out, int64_t ld_out, uint32_t* flags,
                   void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- orthogonalised updates ---------------------------------------------------
+ * What an optimizer that orthogonalises its updates does with a weight's gradient (or its
+ * momentum) between the dW of the calls above and the step: Newton-Schulz steps that drive
+ * every singular value to about 1.  Not of the S3R page, which leaves the optimizer open.
+ *   X <- G / (|G|_F + eps)      (|G|_F in fp64)
+ *   `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X    (X^T X from the other side
+ *                   where G has more rows than columns: the same values)
+ *   out <- keep out + scale X   (keep 0: out is not read; fp32, rounded once for S3R_BF16)
+ * The products keep values of 22 bits (two fp16 planes) and sum in fp32; results agree with
+ * fp64 to about 1e-5 of their size or better; X itself is kept to 2^-37, so matrices far
+ * smaller than eps lose digits, and below 2^-37 eps give zeros.  Every singular value of every X, A and b A +
+ * c A A + a I has to stay below 16 (the usual coefficients stay below 4); past that, results
+ * are infinite or NaN.  A matrix with a non-finite element gives NaN throughout; one of
+ * zeros gives zeros.
+ *   groups  matrices of rows x cols (0 .. 65535; rows and cols below 2^20), g_stride and
+ *           out_stride elements apart;
+ *   G, out  F32 or BF16 each, any alignment; out may be G itself (the same layout and
+ *           type), and is not to overlap it otherwise;
+ *   steps   1 .. 64; a, b, c, eps, scale, keep finite, eps >= 0;
+ *   ws      s3r_orthogonalize_workspace(desc) bytes, 256-byte aligned (about 16 bytes for
+ *           every element of G and more for the smaller side's square).
+ */
+typedef struct s3r_orth_desc {
+  int64_t groups, rows, cols;
+  int32_t g_dtype, out_dtype;       /* S3R_F32 or S3R_BF16 */
+  int32_t steps;
+  float a, b, c, eps, scale, keep;
+  uint32_t reserved;                /* must be 0 */
+} s3r_orth_desc;
+size_t s3r_orthogonalize_workspace(const s3r_orth_desc* desc);
+int s3r_orthogonalize(const s3r_orth_desc* desc, const void* G, int64_t ld, int64_t g_stride, void* out, int64_t ld_out,
+                      int64_t out_stride, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- measurement aid --------------------------------------------------
  * s3r_time_next_gemm: record `start` immediately before and `stop` immediately
  * after the GEMM kernel launched by the next s3r_backward_dx / s3r_backward_dw

@@ -956,6 +956,48 @@ int s3r_int_linear(const s3r_int_pdesc* d, const void* A, const void* up, int32_
                                  stream));
 }
 
+// ---- orthogonalised updates
+static int check_orth(const s3r_orth_desc* d) {
+  if (!d || d->reserved != 0 || d->groups < 0 || d->groups > 65535 || d->rows < 0 || d->rows >= 1 << 20 || d->cols < 0 ||
+      d->cols >= 1 << 20 || d->steps < 1 || d->steps > 64)
+    return S3R_ERR_INVALID_ARG;
+  for (float v : {d->a, d->b, d->c, d->eps, d->scale, d->keep})
+    if (!std::isfinite(v)) return S3R_ERR_INVALID_ARG;
+  if (d->eps < 0.f) return S3R_ERR_INVALID_ARG;
+  for (int32_t t : {d->g_dtype, d->out_dtype})
+    if (t != S3R_F32 && t != S3R_BF16) return S3R_ERR_UNSUPPORTED;
+  return S3R_OK;
+}
+static OrthArgs orth_args(const s3r_orth_desc* d) {
+  OrthArgs a{};
+  a.g_dtype = d->g_dtype; a.out_dt = d->out_dtype; a.E = d->groups; a.N = d->rows; a.K = d->cols;
+  a.steps = d->steps; a.a = d->a; a.b = d->b; a.c = d->c; a.eps = d->eps; a.scale = d->scale; a.keep = d->keep;
+  return a;
+}
+
+size_t s3r_orthogonalize_workspace(const s3r_orth_desc* d) {
+  return check_orth(d) == S3R_OK ? std::max<size_t>(256, orth_workspace(orth_args(d))) : 0;
+}
+
+int s3r_orthogonalize(const s3r_orth_desc* d, const void* G, int64_t ld, int64_t g_stride, void* out, int64_t ld_out,
+                      int64_t out_stride, void* ws, size_t ws_bytes, hipStream_t stream) {
+  int rc = check_orth(d);
+  if (rc) return rc;
+  const bool any = d->groups > 0 && d->rows > 0 && d->cols > 0;
+  if ((rc = check_rows(G, d->g_dtype, ld, d->cols, any))) return rc;
+  if ((rc = check_rows(out, d->out_dtype, ld_out, d->cols, any))) return rc;
+  if (any && d->groups > 1 && (g_stride < (d->rows - 1) * ld + d->cols || out_stride < (d->rows - 1) * ld_out + d->cols))
+    return S3R_ERR_INVALID_ARG;
+  if (any && G == out && (d->g_dtype != d->out_dtype || ld != ld_out || (d->groups > 1 && g_stride != out_stride)))
+    return S3R_ERR_INVALID_ARG;
+  if (ws_bytes < s3r_orthogonalize_workspace(d)) return S3R_ERR_WORKSPACE;
+  if (!ws || ((uintptr_t)ws & 255u)) return S3R_ERR_INVALID_ARG;
+  if ((rc = check_arch())) return rc;
+  OrthArgs a = orth_args(d);
+  a.G = G; a.ld = ld; a.g_stride = g_stride; a.out = out; a.ld_out = ld_out; a.out_stride = out_stride; a.ws = ws;
+  return finish(launch_orthogonalize(a, stream));
+}
+
 int s3r_time_next_gemm(hipEvent_t start, hipEvent_t stop) {
   GemmTiming& t = gemm_timing();
   t.start = start;

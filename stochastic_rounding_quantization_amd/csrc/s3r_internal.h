@@ -262,6 +262,17 @@ hipError_t launch_i8_linear(const I8RowsArgs& rows, const I8ProductArgs& prod, h
 hipError_t launch_i8_colsum(const int64_t* offsets, int64_t G, int64_t R, int64_t K, const int8_t* Q, int64_t ld,
                             int32_t* sums, uint32_t* flags, hipStream_t st);
 
+// Orthogonalised updates (orth.hip): E matrices N x K, out = keep out + scale (Newton-Schulz steps of G).
+struct OrthArgs {
+  const void* G; int g_dtype; int64_t ld, g_stride;
+  void* out; int out_dt; int64_t ld_out, out_stride;
+  int64_t E, N, K;
+  int steps; float a, b, c, eps, scale, keep;
+  void* ws;
+};
+size_t orth_workspace(const OrthArgs& a);
+hipError_t launch_orthogonalize(const OrthArgs& a, hipStream_t st);
+
 // SwiGLU backward glue (swiglu.hip).
 hipError_t launch_swiglu_backward(int64_t T, int64_t F, const float* dH, int64_t ld_dh, const uint16_t* Ag,
                                   const uint16_t* Au, int64_t ld_a, uint16_t* Gg, uint16_t* Gu, int64_t ld_g,

@@ -37,7 +37,8 @@ EXPORTED = ["s3r_quantize_workspace", "s3r_quantize", "s3r_quantize_with_amax", 
             "s3r_mx_operand", "s3r_mx_quantize", "s3r_mx_backward_dx", "s3r_mx_backward_dw", "s3r_route_workspace", "s3r_route",
             "s3r_route_backward", "s3r_dispatch", "s3r_combine", "s3r_combine_backward", "s3r_mx_rows",
             "s3r_mx_product", "s3r_mx_linear_workspace", "s3r_mx_linear", "s3r_int_rows", "s3r_int_colsum", "s3r_int_product",
-            "s3r_int_linear_workspace", "s3r_int_linear", "s3r_time_next_gemm",
+            "s3r_int_linear_workspace", "s3r_int_linear", "s3r_orthogonalize_workspace", "s3r_orthogonalize",
+            "s3r_time_next_gemm",
             "s3r_status_string", "s3r_version"]
 
 
@@ -77,6 +78,13 @@ class IntPDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("depth", ctypes.c_int64),
                 ("groups", ctypes.c_int64), ("ld_b", ctypes.c_int64), ("b_stride", ctypes.c_int64),
                 ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_uint32)]
+
+
+class OrthDesc(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("g_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("keep", ctypes.c_float), ("reserved", ctypes.c_uint32)]
 
 
 def qdesc(rows, cols, rows_per_example=None, mode=S3R, ec=EC_NONE, scale=PER_TENSOR, layer_id=0, seed=0,
@@ -166,7 +174,11 @@ def lib() -> ctypes.CDLL:
     L.s3r_int_linear_workspace.argtypes = [I64, I64]
     L.s3r_int_linear_workspace.restype = SZ
     L.s3r_int_linear.argtypes = [IP, P, P, I32, I64, I64, P, I64, P, P, P, P, P, I64, P, P, SZ, P]
-    for f in ("s3r_int_rows", "s3r_int_colsum", "s3r_int_product", "s3r_int_linear"):
+    OP = ctypes.POINTER(OrthDesc)
+    L.s3r_orthogonalize_workspace.argtypes = [OP]
+    L.s3r_orthogonalize_workspace.restype = SZ
+    L.s3r_orthogonalize.argtypes = [OP, P, I64, I64, P, I64, I64, P, SZ, P]
+    for f in ("s3r_int_rows", "s3r_int_colsum", "s3r_int_product", "s3r_int_linear", "s3r_orthogonalize"):
         getattr(L, f).restype = ctypes.c_int
     for f in ("s3r_route", "s3r_route_backward", "s3r_dispatch", "s3r_combine", "s3r_combine_backward",
               "s3r_mx_rows", "s3r_mx_product", "s3r_mx_linear"):
@@ -906,6 +918,45 @@ def s3r_int_linear(A, w: IntRows, out, *, up=None, offsets=None, index=None, ind
         _check("s3r_int_linear", rc)
 
 
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def orth_desc(shape, g_dtype=S3R_F32, out_dtype=S3R_F32, *, steps=5, coeffs=NS_COEFFS, eps=1e-7, scale=1.0,
+              keep=0.0) -> OrthDesc:
+    """Of matrices [rows x cols] or [groups x rows x cols]."""
+    groups, rows, cols = (1, *shape) if len(shape) == 2 else shape
+    return OrthDesc(groups, rows, cols, g_dtype, out_dtype, steps, *coeffs, eps, scale, keep, 0)
+
+
+def s3r_orthogonalize_workspace(desc: OrthDesc) -> int:
+    return lib().s3r_orthogonalize_workspace(desc)
+
+
+def orthogonalize_buffer(G):
+    """A workspace for s3r_orthogonalize on matrices of G's shape."""
+    return _scratch(s3r_orthogonalize_workspace(orth_desc(G.shape)), G.device)
+
+
+def s3r_orthogonalize(G, out, *, steps=5, coeffs=NS_COEFFS, eps=1e-7, scale=1.0, keep=0.0, ws=None, stream=None,
+                      rc_only=False):
+    """out = keep out + scale X, X the Newton-Schulz steps' result of G [rows x cols] or [groups x rows x cols] (f32/bf16,
+    out too); out may be G."""
+    G, out = _whole(G), _whole(out)
+    if G.dim() not in (2, 3):
+        raise ValueError("expected a matrix, or several")
+    _shaped(out, G.shape, "out")
+    if G.stride(-1) != 1 or out.stride(-1) != 1:
+        raise ValueError("expected row-major matrices (unit column stride)")
+    _here(G, out, ws)
+    d = orth_desc(G.shape, _gdtype(G), _gdtype(out), steps=steps, coeffs=coeffs, eps=eps, scale=scale, keep=keep)
+    many = G.dim() == 3
+    rc = lib().s3r_orthogonalize(d, _ptr(G), G.stride(-2), G.stride(0) if many else 0, _ptr(out), out.stride(-2),
+                                 out.stride(0) if many else 0, _ptr(ws), _nbytes(ws), _stream(stream))
+    if rc_only:
+        return rc
+    _check("s3r_orthogonalize", rc)
+
+
 def swiglu_backward(dH, A_gate, A_up, stream=None):
     """Allocate G_gate, G_up (bf16, like A_gate) and run s3r_swiglu_backward."""
     import torch
@@ -1279,4 +1330,14 @@ def int_linear(A, w: IntRows, *, up=None, offsets=None, index=None, index_div=1,
         ws = int_linear_buffer(rows, w.K, A.device)
     s3r_int_linear(A, w, out, up=up, offsets=offsets, index=index, index_div=index_div, bias=bias, ws=ws, flags=flags,
                   stream=stream)
+    return out
+
+
+def orthogonalize(G, *, steps=5, coeffs=NS_COEFFS, eps=1e-7, scale=1.0, out_dtype=None, stream=None):
+    """G's singular values driven to about 1 by Newton-Schulz steps, times scale; of G's dtype unless out_dtype is given."""
+    import torch
+    with _on(stream):
+        out = torch.empty(G.shape, dtype=out_dtype or G.dtype, device=G.device)
+        ws = orthogonalize_buffer(G)
+    s3r_orthogonalize(G, out, steps=steps, coeffs=coeffs, eps=eps, scale=scale, ws=ws, stream=stream)
     return out

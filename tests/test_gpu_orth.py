@@ -1,0 +1,183 @@
+"""Orthogonalised updates on an MI355X against oracle/orth.py in float64.
+
+How far a result may be off, before any was seen: a value is kept to 2^-24 of itself in two planes of 11 bits, a product
+leaves out 2^-24 of its terms and adds in fp32, a few 2^-24 of the running magnitudes more.  So the oracle runs again with
+every stored value off by a normal error of 2^-22 of the magnitudes that went into it, and a result may be 4 times as far
+(in the Frobenius norm) from the exact one, plus half a step of its type and what the planes' smallest step, 2^-37 of X's
+largest possible singular value, comes to in the steps (which matters where eps leaves X tiny).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import orth
+from stochastic_rounding_quantization_amd import s3r
+from tests._gpu import DEV, host
+
+pytestmark = pytest.mark.gpu
+BOTH = [torch.float32, torch.bfloat16]
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def gradient(shape, dtype, seed, size=1e-4):
+    """A few strong directions and noise."""
+    r = np.random.default_rng(seed)
+    *batch, N, K = shape
+    k = min(4, N, K)
+    x = r.normal(size=(*batch, N, k)) @ r.normal(size=(*batch, k, K)) + r.normal(size=shape)
+    return torch.from_numpy(x * size).to(DEV, dtype)
+
+
+def check(got, G, out=torch.float32, **kw):
+    g = host(G.double())
+    exp = orth.newton_schulz(g, **kw)
+    far = orth.newton_schulz(g, noise=2.0 ** -22, **kw)
+    floor = 2.0 ** -37 * max(1.0, abs(kw.get("coeffs", orth.COEFFS)[0])) ** kw.get("steps", 5) * np.sqrt(exp.size)
+    most = 4 * np.linalg.norm(far - exp) + HALF[out] * np.linalg.norm(exp) + floor
+    off = np.linalg.norm(host(got.double()) - exp)
+    print(f"{tuple(G.shape)}: {off / max(np.linalg.norm(exp), 1e-300):.2e} of {most / max(np.linalg.norm(exp), 1e-300):.2e}")
+    assert off <= most
+
+
+SHAPES = [(1, 1), (1, 7), (7, 1), (16, 16), (31, 33), (33, 65), (64, 64), (65, 64), (100, 300), (300, 100), (3, 1000),
+          (256, 512), (701, 1283), (1283, 701), (40, 5000), (200, 8192)]
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_shapes(shape, dtype):
+    G = gradient(shape, dtype, shape[0])
+    check(s3r.orthogonalize(G, out_dtype=torch.float32), G)
+    check(s3r.orthogonalize(G, out_dtype=torch.bfloat16), G, torch.bfloat16)
+
+
+@pytest.mark.parametrize("steps, coeffs, eps", [(1, orth.COEFFS, 1e-7), (2, (1.5, -0.5, 0.0), 1e-3), (9, (1.875, -1.25, 0.375), 0.0),
+                                                (6, orth.COEFFS, 1.0), (3, (0.0, 1.0, 0.0), 1e-7)])
+def test_steps_and_coefficients(steps, coeffs, eps):
+    for shape in ((50, 120), (130, 70)):
+        G = gradient(shape, torch.float32, steps)
+        check(s3r.orthogonalize(G, steps=steps, coeffs=coeffs, eps=eps), G, steps=steps, coeffs=coeffs, eps=eps)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-12, 1e12, 1e36])
+def test_sizes_of_values(size):
+    """No square leaves its range, and what eps leaves of a tiny matrix is right."""
+    G = gradient((70, 90), torch.float32, 3, size)
+    check(s3r.orthogonalize(G, eps=0.0), G, eps=0.0)
+    check(s3r.orthogonalize(G), G)
+
+
+def test_several_matrices_strides_scale_and_keep():
+    G = gradient((5, 70, 133), torch.float32, 1)
+    each = torch.stack([s3r.orthogonalize(g) for g in G])
+    for dtype in BOTH:
+        wide = torch.full((5, 80, 140), 7.0, device=DEV).to(dtype)
+        src = torch.full((5, 72, 150), float("nan"), device=DEV)
+        src[:, 1:71, 3:136] = G
+        out = wide[:, 5:75, 1:134]
+        ws = s3r.orthogonalize_buffer(G)
+        s3r.s3r_orthogonalize(src[:, 1:71, 3:136], out, ws=ws)
+        assert torch.equal(out, each.to(dtype))
+        s3r.s3r_orthogonalize(src[:, 1:71, 3:136], out, scale=-0.5, keep=0.25, ws=ws)
+        exp = 0.25 * each.to(dtype).double() - 0.5 * each.double()
+        # the results' own rounding, and those of the product and the sum in fp32
+        assert ((out.double() - exp).abs() <= HALF[dtype] * exp.abs() + 3 * 2.0 ** -24 * each.double().abs()).all()
+        assert (wide[:, :5] == 7).all() and (wide[:, 75:] == 7).all() and (wide[..., 0] == 7).all() and (wide[..., 134:] == 7).all()
+        H = G.to(dtype, copy=True)                    # (of the same type it would be G, which this changes)
+        exp = s3r.orthogonalize(H)
+        s3r.s3r_orthogonalize(H, H, ws=ws)
+        assert torch.equal(H, exp)                    # in place
+    nan = torch.full((5, 70, 133), float("nan"), device=DEV)
+    s3r.s3r_orthogonalize(G, nan, ws=ws)              # keep 0 reads nothing
+    assert torch.equal(nan, each)
+    tall = G.transpose(1, 2).contiguous()
+    for e, y in enumerate(s3r.orthogonalize(tall)):
+        check(y, tall[e])
+
+
+def test_zeros_and_non_finite():
+    G = gradient((4, 40, 50), torch.float32, 2)
+    G[1] = 0
+    G[2, 3, 4] = float("nan")
+    G[3, 39, 49] = float("-inf")
+    for eps in (0.0, 1e-7):
+        y = s3r.orthogonalize(G, eps=eps)
+        check(y[0], G[0], eps=eps)
+        assert not y[1].any() and y[2:].isnan().all()
+    low = gradient((40, 1), torch.float32, 4) @ gradient((1, 50), torch.float32, 5)       # rank one
+    check(s3r.orthogonalize(low), low)
+    for shape in ((0, 5), (5, 0), (0, 3, 4), (2, 0, 4)):
+        assert s3r.orthogonalize(torch.empty(shape, device=DEV)).shape == shape
+
+
+def exact64(G, steps=5):
+    """The steps in float64 on the GPU, which torch's products do quickly enough for the large tiles."""
+    a, b, c = (float(np.float32(v)) for v in orth.COEFFS)
+    X = G.double()
+    tall = X.shape[0] > X.shape[1]
+    X = X.t().contiguous() if tall else X
+    X = X / (X.norm() + float(np.float32(1e-7)))
+    for _ in range(steps):
+        A = X @ X.t()
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return X.t() if tall else X
+
+
+@pytest.mark.parametrize("shape", [(2048, 2048), (1500, 4000), (4000, 1500), (4096, 4096), (3900, 6000), (6200, 4097), (64, 60000)])
+def test_large(shape):
+    """Tiles of 128 and 256, shared among workgroups and not; errors as of the small ones."""
+    g = torch.Generator(DEV).manual_seed(1)
+    G = torch.randn(*shape, generator=g, device=DEV) * 1e-3
+    G += torch.randn(shape[0], 1, generator=g, device=DEV) @ torch.randn(1, shape[1], generator=g, device=DEV) * 1e-2
+    exp = exact64(G)
+    y = s3r.orthogonalize(G)
+    off = float((y.double() - exp).norm() / exp.norm())
+    print(f"{shape}: {off:.2e}")
+    # measured by the small matrices' rule: 2^-22 of the magnitudes at every step; the longest sums here add
+    # 60000 terms, whose fp32 roundings may be 2^-25 sqrt(3 * 60000 / 16) = 2^-18 of them
+    assert off <= 1e-5
+    assert torch.equal(y, s3r.orthogonalize(G))
+
+
+def test_many_matrices_in_tiles_of_128():
+    G = gradient((20, 300, 700), torch.bfloat16, 9)
+    y = s3r.orthogonalize(G, out_dtype=torch.float32)
+    for e in (0, 7, 19):
+        check(y[e], G[e])
+
+
+def test_singular_values_near_one():
+    g = torch.Generator(DEV).manual_seed(2)
+    for shape in ((200, 300), (300, 200)):
+        s = torch.linalg.svdvals(s3r.orthogonalize(torch.randn(*shape, generator=g, device=DEV)).double().cpu())
+        assert 0.6 < float(s.min()) and float(s.max()) < 1.3
+
+
+def test_streams_and_graph_replays():
+    G = gradient((3, 200, 300), torch.float32, 1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y0 = s3r.orthogonalize(G, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(y0, s3r.orthogonalize(G))
+    out, ws = torch.empty_like(G), s3r.orthogonalize_buffer(G)
+    long, long_out = gradient((64, 8192), torch.float32, 2), torch.empty(64, 8192, device=DEV)
+    ws2 = s3r.orthogonalize_buffer(long)
+
+    def step():
+        s3r.s3r_orthogonalize(G, out, ws=ws)
+        s3r.s3r_orthogonalize(long, long_out, ws=ws2)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(3):
+        G.copy_(gradient((3, 200, 300), torch.float32, 10 + seed))
+        long.copy_(gradient((64, 8192), torch.float32, 20 + seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), long_out.clone()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], out) and torch.equal(got[1], long_out)
