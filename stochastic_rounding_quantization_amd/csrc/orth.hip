@@ -6,14 +6,17 @@
 // products carry about 22 bits: a value is kept as two fp16 planes, v 2^12 = h + l with h and l the nearest fp16, and
 // a product is h h' + h l' + l h' in fp32 (three matrix instructions; l l' is below 2^-22).  The factor 2^12 keeps l of
 // entries down to 2^-15 normal; entries up to 16 fit, and the singular values of X, A and B stay below 4.
+// Where the result is bf16, the last kLoose steps take h alone (a third of the work): what they lose, a few 2^-12 of the
+// matrix, is multiplied by one step at most and stays well below bf16's own rounding (2^-9 of a value).
 //
-// Layout: the planes of 32 consecutive elements of a row share a 128-byte line, 64 bytes of h and 64 of l, so a K step
-// of 32 elements of both planes is one line of every row.  Every operand has its contraction along the rows: X for
-// X X^T, X^T for B X, A and B as they are (symmetric).  So a step keeps X both ways, written by one epilogue.
-// Sides are padded to whole tiles with zeros, which are all in the workspace: the products read and write no edge.
+// Layout: with two planes the 32 consecutive elements of a row that make a line of 128 bytes are 64 bytes of h and 64 of
+// l; with one, a line is 64 elements.  A step of the products' loops is a line of every row.  Every operand has its
+// contraction along the rows: X for X X^T, X^T for B X, A and B as they are (symmetric).  So a step keeps X both ways,
+// written by one epilogue.  Sides are padded to whole tiles with zeros, which are all in the workspace: the products read
+// and write no edge.
 #include <type_traits>
 
-#include "s3r_internal.h"
+#include "rows8.h"
 #include "tile_ring.h"
 
 namespace s3r {
@@ -24,47 +27,58 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr float kUp = 4096.f, kDown = 1.f / 4096.f;      // the planes' scale
-constexpr int kLine = 128, kLineEl = 32;                 // bytes and elements of a line
+constexpr int kLine = 128;                               // bytes of a line
+constexpr int kLoose = 2;
+__host__ __device__ constexpr int line_el(int planes) { return 64 / planes; }
+__host__ __device__ constexpr int el_bytes(int planes) { return 2 * planes; }
 
 // ------------------------------------------------------------------ norm ----
-// Sum of squares in fp64: no square of an fp32 number leaves its range.  Partial sums of kNormBlocks workgroups a
-// matrix, added in a fixed order by whoever needs the norm.
-constexpr int kNormThreads = 256, kNormBlocks = 64;
-
-__device__ __forceinline__ float element(const float* p) { return *p; }
-__device__ __forceinline__ float element(const uint16_t* p) { return bf16_to_f32(*p); }
-
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double red[kNormThreads / 64];
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double s = 0.;
-#pragma unroll
-  for (int w = 0; w < kNormThreads / 64; ++w) s += red[w];
-  return s;
-}
+// Sum of squares in fp64: no square of an fp32 number leaves its range.  A matrix is cut into runs of 2048 elements of a
+// row, dealt evenly to `parts` workgroups; whoever needs the norm adds their sums in a fixed order.  Bound by its bytes:
+// 4096 x 14336 fp32 in 64 parts took 1495 us.
+constexpr int kNormThreads = 256, kNormRun = kNormThreads * 8, kNormMost = 1024;
 
 template <typename TIn>
-__global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(OrthArgs a, double* part) {
+__global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(OrthArgs a, double* part, int parts) {
+  __shared__ double red[kNormThreads / 64];
   const TIn* G = (const TIn*)a.G + (int64_t)blockIdx.y * a.g_stride;
+  const int64_t per_row = (a.K + kNormRun - 1) / kNormRun, runs = a.N * per_row;
+  const int64_t u0 = runs * blockIdx.x / parts, u1 = runs * (blockIdx.x + 1) / parts;
   double s = 0.;
-  const int64_t rows = (a.N + kNormBlocks - 1) / kNormBlocks;
-  const int64_t r0 = blockIdx.x * rows, r1 = min(r0 + rows, a.N);
-  for (int64_t r = r0; r < r1; ++r)
-    for (int64_t c = threadIdx.x; c < a.K; c += kNormThreads) {
-      const double v = element(G + r * a.ld + c);
-      s += v * v;
+  constexpr int kBatch = 4;
+  for (int64_t u = u0; u < u1; u += kBatch) {
+    Raw8<TIn> v[kBatch];
+    int64_t left[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {             // every load before the first sum
+      const int64_t r = (u + q) / per_row, c = (u + q - r * per_row) * kNormRun + threadIdx.x * 8;
+      left[q] = u + q < u1 ? a.K - c : 0;
+      v[q] = mr_load8<TIn, false>(G + r * a.ld + c, left[q], a.K);
     }
-  s = block_sum(s);
-  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * kNormBlocks + blockIdx.x] = s;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      mr_tail<false>(v[q], left[q], a.K);
+      const Raw8<float> f = mr_float8(v[q]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s += (double)f.w[x] * (double)f.w[x];
+    }
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  s = 0.;
+#pragma unroll
+  for (int w = 0; w < kNormThreads / 64; ++w) s += red[w];
+  part[(int64_t)blockIdx.y * parts + blockIdx.x] = s;
 }
 
 // 2^12 / (norm + eps) from the partial sums, by one wave; NaN for a matrix that is not finite, 0 for one of zeros
 // without an eps.
-__device__ __forceinline__ float orth_factor(const double* part, float eps) {
-  static_assert(kNormBlocks == 64, "a partial sum a lane");
-  const double s = wave_sum(part[threadIdx.x & 63]);
+__device__ __forceinline__ float orth_factor(const double* part, int parts, float eps) {
+  double s = 0.;
+  for (int i = threadIdx.x & 63; i < parts; i += 64) s += part[i];
+  s = wave_sum(s);
   const double d = sqrt(s) + (double)eps;
   if (!(s < __builtin_inf())) return __builtin_nanf("");
   return d > 0. ? (float)((double)kUp / d) : 0.f;
@@ -78,10 +92,12 @@ __device__ __forceinline__ void split(float v, _Float16& h, _Float16& l) {
   h = (_Float16)v;
   l = (_Float16)(v - (float)h);
 }
+template <int P>
 __device__ __forceinline__ int64_t plane_off(int64_t row, int64_t col, int64_t ld) {        // ld in bytes
-  return row * ld + (col / kLineEl) * kLine + (col % kLineEl) * 2;
+  return P == 1 ? row * ld + col * 2 : row * ld + (col >> 5) * kLine + (col & 31) * 2;
 }
 // 8 consecutive values (col a multiple of 8) to their planes.
+template <int P>
 __device__ __forceinline__ void store_planes(uint8_t* p, const float (&v)[8]) {
   v8h h, l;
 #pragma unroll
@@ -92,28 +108,40 @@ __device__ __forceinline__ void store_planes(uint8_t* p, const float (&v)[8]) {
     l[i] = y;
   }
   *reinterpret_cast<v8h*>(p) = h;
-  *reinterpret_cast<v8h*>(p + kLine / 2) = l;
+  if constexpr (P == 2) *reinterpret_cast<v8h*>(p + kLine / 2) = l;
 }
 
 // G, scaled, to its planes as it lies (`own`) and transposed (`other`), 64 x 64 elements a workgroup, zeros past its
-// edges.  rows x cols: the padded sizes, G's orientation.
+// edges.  rows x cols: the padded sizes (multiples of 32), G's orientation.
 constexpr int kPrepThreads = 256, kPrepTile = 64;
-template <typename TIn>
-__global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, const double* part, uint8_t* own,
+template <typename TIn, int P>
+__global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, const double* part, int parts, uint8_t* own,
                                                                     int64_t own_stride, uint8_t* other, int64_t other_stride,
                                                                     int64_t rows, int64_t cols) {
   __shared__ float tile[kPrepTile][kPrepTile + 1];
   __shared__ float factor;
   const int64_t e = blockIdx.z;
   if (threadIdx.x < 64) {
-    const float f = orth_factor(part + e * kNormBlocks, a.eps);
+    const float f = orth_factor(part + e * parts, parts, a.eps);
     if (threadIdx.x == 0) factor = f;
   }
   const TIn* G = (const TIn*)a.G + e * a.g_stride;
   const int64_t r0 = (int64_t)blockIdx.y * kPrepTile, c0 = (int64_t)blockIdx.x * kPrepTile;
-  for (int i = threadIdx.x; i < kPrepTile * kPrepTile; i += kPrepThreads) {
-    const int64_t r = r0 + i / kPrepTile, c = c0 + i % kPrepTile;
-    tile[i / kPrepTile][i % kPrepTile] = r < a.N && c < a.K ? element(G + r * a.ld + c) : 0.f;
+  constexpr int kPer = kPrepTile / 8, kPasses = kPrepTile * kPer / kPrepThreads;       // threads of a row, rows of a thread
+  const int q0 = threadIdx.x / kPer, p0 = threadIdx.x % kPer * 8;
+  Raw8<TIn> g[kPasses];
+#pragma unroll
+  for (int x = 0; x < kPasses; ++x) {
+    const int64_t r = r0 + q0 + x * (kPrepThreads / kPer);
+    g[x] = mr_load8<TIn, false>(G + (r < a.N ? r : 0) * a.ld + c0 + p0, r < a.N ? a.K - c0 - p0 : 0, a.K);
+  }
+#pragma unroll
+  for (int x = 0; x < kPasses; ++x) {
+    const int64_t r = r0 + q0 + x * (kPrepThreads / kPer);
+    mr_tail<false>(g[x], r < a.N ? a.K - c0 - p0 : 0, a.K);
+    const Raw8<float> v = mr_float8(g[x]);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) tile[q0 + x * (kPrepThreads / kPer)][p0 + y] = v.w[y];
   }
   __syncthreads();
   const float f = factor;
@@ -127,19 +155,20 @@ __global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, 
       v[x] = tile[q][p + x] * f;
       w[x] = tile[p + x][q] * f;
     }
-    store_planes(own + plane_off(r0 + q, c0 + p, cols * 4), v);
-    store_planes(other + plane_off(c0 + q, r0 + p, rows * 4), w);
+    if (r0 + q < rows && c0 + p < cols) store_planes<P>(own + plane_off<P>(r0 + q, c0 + p, cols * el_bytes(P)), v);
+    if (c0 + q < cols && r0 + p < rows) store_planes<P>(other + plane_off<P>(c0 + q, r0 + p, rows * el_bytes(P)), w);
   }
 }
 
 // -------------------------------------------------------------- products ----
 // Tiles of BM x BN, WM x WN waves of (32 MI) x (32 NI) each, operands staged through LDS by buffer-load DMA in a ring
-// of NS steps of one line (32 elements, both planes) of every row, the eight 16-byte chunks of a line at permuted places
-// (chunk q of row r at q ^ ((r >> 1) & 7): a quarter-wave's reads hit 16 bank groups).
+// of NS steps of one line of every row, the eight 16-byte chunks of a line at permuted places (chunk q of row r at
+// q ^ ((r >> 1) & 7): a quarter-wave's reads hit 16 bank groups).  P: planes; a line has Parts parts of 16 elements.
 // v_mfma_f32_32x32x16_f16: lane l holds row or column l % 32, elements 8 (l / 32) .. + 7 of 16; result register r is
 // row (r / 4) 8 + (l / 32) 4 + r % 4, column l % 32.
-template <int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
+template <int P_, int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
 struct OrthGeo {
+  static constexpr int P = P_, Parts = line_el(P) / 16, Products = P == 2 ? 3 : 1;
   static constexpr int WavesPerSimd = WavesPerSimd_;
   static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr int Waves = WM * WN, Threads = 64 * Waves;
@@ -199,9 +228,9 @@ __device__ __forceinline__ void orth_load(const OrthSrc<T>& s, uint8_t* st, int 
 }
 
 template <typename T>
-struct OrthFrag { v8h ah[T::MI], al[T::MI], bh[T::NI], bl[T::NI]; };
+struct OrthFrag { v8h a[T::P][T::MI], b[T::P][T::NI]; };
 
-// The fragments of half h (16 elements) of a stage.
+// The fragments of part h (16 elements) of a stage.
 template <typename T>
 __device__ __forceinline__ void orth_frag(const uint8_t* st, int h, OrthFrag<T>& f) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -210,54 +239,62 @@ __device__ __forceinline__ void orth_frag(const uint8_t* st, int h, OrthFrag<T>&
 #pragma unroll
   for (int i = 0; i < T::MI; ++i) {
     const int r = (wm * T::MI + i) * 32 + r31;
-    f.ah[i] = *reinterpret_cast<const v8h*>(st + r * kLine + (chunk_place(r, c) << 4));
-    f.al[i] = *reinterpret_cast<const v8h*>(st + r * kLine + (chunk_place(r, c + 4) << 4));
+#pragma unroll
+    for (int l = 0; l < T::P; ++l) f.a[l][i] = *reinterpret_cast<const v8h*>(st + r * kLine + (chunk_place(r, c + 4 * l) << 4));
   }
 #pragma unroll
   for (int j = 0; j < T::NI; ++j) {
     const int r = (wn * T::NI + j) * 32 + r31;
-    f.bh[j] = *reinterpret_cast<const v8h*>(st + T::OffB + r * kLine + (chunk_place(r, c) << 4));
-    f.bl[j] = *reinterpret_cast<const v8h*>(st + T::OffB + r * kLine + (chunk_place(r, c + 4) << 4));
+#pragma unroll
+    for (int l = 0; l < T::P; ++l)
+      f.b[l][j] = *reinterpret_cast<const v8h*>(st + T::OffB + r * kLine + (chunk_place(r, c + 4 * l) << 4));
   }
 }
 
 template <typename T>
 __device__ __forceinline__ void orth_mfma(const OrthFrag<T>& f, v16f (&acc)[T::MI][T::NI]) {
 #pragma unroll
-  for (int i = 0; i < T::MI; ++i)
+  for (int l = T::Products - 1; l >= 0; --l)             // l h', h l', h h'
 #pragma unroll
-    for (int j = 0; j < T::NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.al[i], f.bh[j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-  for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-    for (int j = 0; j < T::NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.ah[i], f.bl[j], acc[i][j], 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-    for (int j = 0; j < T::NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.ah[i], f.bh[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < T::NI; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[l == 2][i], f.b[l == 1][j], acc[i][j], 0, 0, 0);
 }
 
-// Step kt on stage S = kt % NS, the fragments of its first half in f.  The first half's products cover the reads of the
-// second half; the barrier between them makes step kt + 1 visible and retires stage S, which takes step kt + NS.
+// Part h of step kt on stage S, its fragments in f: its products cover the reads of part h + 1.
+template <typename T, int S, int H>
+__device__ __forceinline__ void orth_parts(OrthFrag<T>& f, v16f (&acc)[T::MI][T::NI]) {
+  if constexpr (H + 1 < T::Parts) {
+    constexpr int kReads = T::P * (T::MI + T::NI), kProducts = T::Products * T::MI * T::NI;
+    OrthFrag<T> n;
+    orth_frag<T>(ring<T, S>(), H + 1, n);
+    orth_mfma<T>(f, acc);
+#pragma unroll
+    for (int x = 0; x < kProducts; ++x) {
+      __builtin_amdgcn_sched_group_barrier(kSgDsRead, (kReads + kProducts - 1) / kProducts, 0);
+      __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    f = n;
+    orth_parts<T, S, H + 1>(f, acc);
+  }
+}
+
+// Step kt on stage S = kt % NS, the fragments of its first part in f.  Before the last part's products every read of the
+// stage has arrived; the barrier there makes step kt + 1 visible and retires stage S, which takes step kt + NS.
 template <typename T, int S>
 __device__ __forceinline__ void orth_step(const OrthSrc<T>& src, int kt, OrthFrag<T>& f, v16f (&acc)[T::MI][T::NI]) {
-  constexpr int kReads = 2 * (T::MI + T::NI), kProducts = 3 * T::MI * T::NI;
-  OrthFrag<T> n;
-  orth_frag<T>(ring<T, S>(), 1, n);
-  orth_mfma<T>(f, acc);
-#pragma unroll
-  for (int x = 0; x < kProducts; ++x) {
-    __builtin_amdgcn_sched_group_barrier(kSgDsRead, (kReads + kProducts - 1) / kProducts, 0);
-    __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
-  }
-  __builtin_amdgcn_sched_barrier(0);
+  constexpr int kReads = T::P * (T::MI + T::NI), kProducts = T::Products * T::MI * T::NI;
+  orth_parts<T, S, 0>(f, acc);
   S3R_WAIT_VM(T::Loads * (T::NS - 2));
   S3R_WAIT_LGKM0();
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
+  OrthFrag<T> n;
   orth_load<T>(src, ring<T, S>(), kt + T::NS);
-  orth_frag<T>(ring<T, (S + 1) % T::NS>(), 0, f);
-  orth_mfma<T>(n, acc);
+  orth_frag<T>(ring<T, (S + 1) % T::NS>(), 0, n);
+  orth_mfma<T>(f, acc);
 #pragma unroll
   for (int x = 0; x < kProducts; ++x) {
     __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
@@ -265,6 +302,7 @@ __device__ __forceinline__ void orth_step(const OrthSrc<T>& src, int kt, OrthFra
     __builtin_amdgcn_sched_group_barrier(kSgVmem, (T::Loads + kProducts - 1) / kProducts, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
+  f = n;
 }
 
 template <typename T, int S>
@@ -355,9 +393,10 @@ __device__ __forceinline__ void store_one(uint16_t* p, float v, float keep) {
 }
 
 // A tile's results, 32 rows of a wave at a time through its own part of the (free) ring, read from there along the rows
-// and along the columns.
-template <typename T, OrthEpi EPI>
-__device__ __forceinline__ void orth_store(const OrthGemm& p, const OrthTile& t, const v16f (&acc)[T::MI][T::NI]) {
+// and along the columns.  OP: the results' planes (of kEpiBoth, those of the next step).
+// This does rows 32 i .. of every wave.
+template <typename T, OrthEpi EPI, int OP>
+__device__ __forceinline__ void orth_store_rows(const OrthGemm& p, const OrthTile& t, int i, const v16f (&acc)[T::NI]) {
   constexpr int kBuf = 32 * T::EpiLd * 4;
   constexpr int kPer = T::StageBytes / kBuf;                  // waves' buffers in one stage
   static_assert(kPer > 0 && kPer * T::NS >= T::Waves, "the epilogue's staging fits the ring");
@@ -371,67 +410,72 @@ __device__ __forceinline__ void orth_store(const OrthGemm& p, const OrthTile& t,
   constexpr int W = 32 * T::NI, LR = W / 8;                   // columns of a wave; lanes of a row, 8 columns each
   const int64_t col0 = (int64_t)t.tn * T::BN + wn * W;
   const bool turned = EPI == kEpiBoth || (symmetric(EPI) && t.tm != t.tn);
+  const int64_t row0 = (int64_t)t.tm * T::BM + (wm * T::MI + i) * 32;
 #pragma unroll
-  for (int i = 0; i < T::MI; ++i) {
-    const int64_t row0 = (int64_t)t.tm * T::BM + (wm * T::MI + i) * 32;
+  for (int j = 0; j < T::NI; ++j)
 #pragma unroll
-    for (int j = 0; j < T::NI; ++j)
+    for (int r = 0; r < 16; ++r)
+      buf[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * T::EpiLd + j * 32 + (lane & 31)] = acc[j][r] * kDown;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  for (int q = 0; q < 32; q += 64 / LR) {
+    const int rr = q + lane / LR, cc = lane % LR * 8;
+    const int64_t row = row0 + rr, col = col0 + cc;
+    float v[8];
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        buf[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * T::EpiLd + j * 32 + (lane & 31)] = acc[i][j][r] * kDown;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    for (int q = 0; q < 32; q += 64 / LR) {
-      const int rr = q + lane / LR, cc = lane % LR * 8;
-      const int64_t row = row0 + rr, col = col0 + cc;
-      float v[8];
+    for (int x = 0; x < 8; x += 4) {
+      const v4f w = *reinterpret_cast<const v4f*>(buf + rr * T::EpiLd + cc + x);
 #pragma unroll
-      for (int x = 0; x < 8; x += 4) {
-        const v4f w = *reinterpret_cast<const v4f*>(buf + rr * T::EpiLd + cc + x);
+      for (int y = 0; y < 4; ++y) v[x + y] = w[y];
+    }
+    if constexpr (EPI == kEpiPoly) {
+      const uint8_t* at = p.addend + t.e * p.d_stride + plane_off<T::P>(row, col, p.ld_direct);
+      v8h h[T::P];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) v[x + y] = w[y];
+      for (int l = 0; l < T::P; ++l) h[l] = *reinterpret_cast<const v8h*>(at + l * (kLine / 2));
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        v[x] = p.c * v[x] + p.b * (T::P == 2 ? (float)h[0][x] + (float)h[T::P - 1][x] : (float)h[0][x]);
+        if (row == col + x) v[x] += p.a * kUp;
       }
-      if constexpr (EPI == kEpiPoly) {
-        const uint8_t* at = p.addend + t.e * p.d_stride + plane_off(row, col, p.ld_direct);
-        const v8h h = *reinterpret_cast<const v8h*>(at), l = *reinterpret_cast<const v8h*>(at + kLine / 2);
+      if (turned) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          v[x] = p.c * v[x] + p.b * ((float)h[x] + (float)l[x]);
-          if (row == col + x) v[x] += p.a * kUp;
-        }
-        if (turned) {
-#pragma unroll
-          for (int x = 0; x < 8; x += 4)
-            *reinterpret_cast<v4f*>(buf + rr * T::EpiLd + cc + x) = v4f{v[x], v[x + 1], v[x + 2], v[x + 3]};
-        }
-      }
-      if constexpr (EPI == kEpiOutF32 || EPI == kEpiOutBf16) {
-        using TOut = std::conditional_t<EPI == kEpiOutF32, float, uint16_t>;
-        TOut* out = (TOut*)p.out + t.e * p.out_stride + row * p.ld_out + col;
-        if (row < p.rows) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (col + x < p.cols) store_one(out + x, v[x] * (kDown * p.scale), p.keep);
-        }
-      } else {
-        store_planes(p.direct + t.e * p.d_stride + plane_off(row, col, p.ld_direct), v);
+        for (int x = 0; x < 8; x += 4)
+          *reinterpret_cast<v4f*>(buf + rr * T::EpiLd + cc + x) = v4f{v[x], v[x + 1], v[x + 2], v[x + 3]};
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if constexpr (EPI == kEpiBoth || symmetric(EPI)) {
-      if (turned)
-        for (int q = 0; q < 4 * W; q += 64) {                 // a column's 8 rows a lane
-          const int cc = (q + lane) >> 2, rr = (lane & 3) * 8;
-          float v[8];
+    if constexpr (EPI == kEpiOutF32 || EPI == kEpiOutBf16) {
+      using TOut = std::conditional_t<EPI == kEpiOutF32, float, uint16_t>;
+      TOut* out = (TOut*)p.out + t.e * p.out_stride + row * p.ld_out + col;
+      if (row < p.rows) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = buf[(rr + x) * T::EpiLd + cc];
-          store_planes(p.turned + t.e * p.t_stride + plane_off(col0 + cc, row0 + rr, p.ld_turned), v);
-        }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+        for (int x = 0; x < 8; ++x)
+          if (col + x < p.cols) store_one(out + x, v[x] * (kDown * p.scale), p.keep);
+      }
+    } else {
+      store_planes<OP>(p.direct + t.e * p.d_stride + plane_off<OP>(row, col, p.ld_direct), v);
     }
   }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if constexpr (EPI == kEpiBoth || symmetric(EPI)) {
+    if (turned)
+      for (int q = 0; q < 4 * W; q += 64) {                 // a column's 8 rows a lane
+        const int cc = (q + lane) >> 2, rr = (lane & 3) * 8;
+        float v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = buf[(rr + x) * T::EpiLd + cc];
+        store_planes<OP>(p.turned + t.e * p.t_stride + plane_off<OP>(col0 + cc, row0 + rr, p.ld_turned), v);
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <typename T, OrthEpi EPI, int OP>
+__device__ __forceinline__ void orth_store(const OrthGemm& p, const OrthTile& t, const v16f (&acc)[T::MI][T::NI]) {
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i) orth_store_rows<T, EPI, OP>(p, t, i, acc[i]);
 }
 
 // The steps of all shared tiles in a row, dealt to the workers evenly: worker w has [first(w), first(w + 1)).
@@ -442,28 +486,23 @@ __device__ __forceinline__ int64_t first_step(const OrthGemm& p, int w) {
 // Workgroups 0 .. full - 1 take a tile each.  What does not fill the GPU evenly, the last `rest` tiles, is dealt to
 // `workers` workgroups by steps: each leaves the sums of its part of a tile in memory (at most two tiles are partly its
 // own; tiles wholly its own go straight to their results) and orth_join_kernel adds them up, in the order of K.
-template <typename T, OrthEpi EPI>
+template <typename T, OrthEpi EPI, int OP>
 __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_gemm_kernel(OrthGemm p) {
   v16f acc[T::MI][T::NI];
-  int bid = blockIdx.x;
-  if (bid < p.full) {
-    if (p.full % 8 == 0) bid = (bid % 8) * (p.full / 8) + bid / 8;       // a contiguous range of tiles per XCD
-    const OrthTile t = orth_tile<EPI>(p, bid);
-    orth_sums<T>(p, t, 0, p.steps, acc);
-    orth_store<T, EPI>(p, t, acc);
-    return;
-  }
-  int w = bid - p.full;
-  if (p.workers % 8 == 0) w = (w % 8) * (p.workers / 8) + w / 8;
-  const int64_t s1 = first_step(p, w + 1);
-  int slot = 0;
-  for (int64_t s = first_step(p, w); s < s1;) {
+  const bool whole = (int)blockIdx.x < p.full;
+  int w = whole ? blockIdx.x : blockIdx.x - p.full;
+  const int n = whole ? p.full : p.workers;
+  if (n % 8 == 0) w = (w % 8) * (n / 8) + w / 8;                // a contiguous range of tiles per XCD
+  // from the first of the whole tiles' steps, or the shared ones'
+  int64_t s = whole ? (int64_t)w * p.steps : first_step(p, w);
+  const int64_t s1 = whole ? s + p.steps : first_step(p, w + 1);
+  for (int slot = 0; s < s1;) {
     const int tile = (int)(s / p.steps), k0 = (int)(s - (int64_t)tile * p.steps);
     const int k1 = (int)min((int64_t)p.steps, k0 + (s1 - s));
-    const OrthTile t = orth_tile<EPI>(p, p.full + tile);
+    const OrthTile t = orth_tile<EPI>(p, whole ? tile : p.full + tile);
     orth_sums<T>(p, t, k0, k1, acc);
     if (k1 - k0 == p.steps) {
-      orth_store<T, EPI>(p, t, acc);
+      orth_store<T, EPI, OP>(p, t, acc);
     } else {
       v4f* part = reinterpret_cast<v4f*>(p.partial) + (int64_t)(2 * w + slot) * (T::BM * T::BN / 4) + threadIdx.x;
       slot = 1;
@@ -476,73 +515,186 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_gemm_kernel(
             part[((i * T::NI + j) * 4 + r) * T::Threads] =
                 v4f{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
     }
+    s += k1 - k0;
+    if (s >= s1) return;
     S3R_WAIT_VM(0);
     __syncthreads();                   // the ring is free again, and the next loads are counted from none
-    s += k1 - k0;
   }
 }
 
-template <typename T, OrthEpi EPI>
+// Tile blockIdx.x of the shared ones, rows 32 blockIdx.y .. of every wave (a workgroup for a whole tile of 256 took twice
+// as long, few of them adding up in a row what many had left).
+template <typename T, OrthEpi EPI, int OP>
 __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_join_kernel(OrthGemm p) {
-  const int tile = blockIdx.x;
+  const int tile = blockIdx.x, i = blockIdx.y;
   const int64_t s0 = (int64_t)tile * p.steps, s1 = s0 + p.steps, all = (int64_t)p.rest * p.steps;
   int w = (int)(s0 * p.workers / all);
   while (first_step(p, w + 1) <= s0) ++w;
   while (first_step(p, w) > s0) --w;
   if (first_step(p, w + 1) >= s1) return;              // one worker had all of it
-  v16f acc[T::MI][T::NI];
+  v16f acc[T::NI];
 #pragma unroll
-  for (int i = 0; i < T::MI; ++i)
+  for (int j = 0; j < T::NI; ++j)
 #pragma unroll
-    for (int j = 0; j < T::NI; ++j)
+    for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
+  constexpr int kBatch = 4;
+  while (first_step(p, w) < s1) {
+    v4f v[kBatch][T::NI * 4];
+    bool some[kBatch];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  for (; first_step(p, w) < s1; ++w) {
-    // a worker's second part follows a tile's end; its first one is the tile that its range begins in
-    const int64_t b = first_step(p, w);
-    if (b == first_step(p, w + 1)) continue;
-    const int slot = b < s0 && b % p.steps != 0 ? 1 : 0;
-    const v4f* part = reinterpret_cast<const v4f*>(p.partial) + (int64_t)(2 * w + slot) * (T::BM * T::BN / 4) + threadIdx.x;
+    for (int q = 0; q < kBatch; ++q, ++w) {              // every load before the first sum
+      // a worker's second part follows a tile's end; its first one is the tile that its range begins in
+      const int64_t b = first_step(p, w);
+      some[q] = b < s1 && b != first_step(p, w + 1);
+      if (!some[q]) continue;
+      const int slot = b < s0 && b % p.steps != 0 ? 1 : 0;
+      const v4f* part = reinterpret_cast<const v4f*>(p.partial) + (int64_t)(2 * w + slot) * (T::BM * T::BN / 4) +
+                        (int64_t)i * T::NI * 4 * T::Threads + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < T::MI; ++i)
+      for (int x = 0; x < T::NI * 4; ++x) v[q][x] = part[x * T::Threads];
+    }
 #pragma unroll
-      for (int j = 0; j < T::NI; ++j)
+    for (int q = 0; q < kBatch; ++q)
+      if (some[q])
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const v4f v = part[((i * T::NI + j) * 4 + r) * T::Threads];
+        for (int x = 0; x < T::NI * 4; ++x)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) acc[i][j][4 * r + y] += v[y];
-        }
+          for (int y = 0; y < 4; ++y) acc[x / 4][4 * (x % 4) + y] += v[q][x][y];
   }
-  orth_store<T, EPI>(p, orth_tile<EPI>(p, p.full + tile), acc);
+  orth_store_rows<T, EPI, OP>(p, orth_tile<EPI>(p, p.full + tile), i, acc);
+}
+
+// Small matrices: 32 x 32 results a workgroup, whose eight waves deal the contraction's steps of 32 elements among them and
+// join their sums in LDS.  Fragments go straight from the caches to the matrix cores, kBatch steps of a wave at a time, so
+// a product of a few hundred elements is one round of loads.
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64, kFewLd = 36;
+
+template <int P, OrthEpi EPI, int OP>
+__global__ __launch_bounds__(kFewThreads) void orth_few_kernel(OrthGemm p) {
+  __shared__ float part[kFewWaves][32 * kFewLd];
+  constexpr int kBatch = 4 / P, kProducts = P == 2 ? 3 : 1;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const OrthTile t = orth_tile<EPI>(p, blockIdx.x);
+  const int r31 = lane & 31, half = (lane >> 5) * 16;
+  const uint8_t* A = p.A + t.e * p.a_stride + ((int64_t)t.tm * 32 + r31) * p.lda + half;
+  const uint8_t* B = p.B + t.e * p.b_stride + ((int64_t)t.tn * 32 + r31) * p.ldb + half;
+  v16f acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  for (int k0 = wave; k0 < p.steps; k0 += kFewWaves * kBatch) {
+    v8h a[kBatch][2][P], b[kBatch][2][P];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int k = k0 + q * kFewWaves;
+      if (k < p.steps) {                               // the same in the whole wave
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int l = 0; l < P; ++l) {
+            a[q][h][l] = *reinterpret_cast<const v8h*>(A + (int64_t)k * 64 * P + h * 32 + l * 64);
+            b[q][h][l] = *reinterpret_cast<const v8h*>(B + (int64_t)k * 64 * P + h * 32 + l * 64);
+          }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      if (k0 + q * kFewWaves >= p.steps) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int l = kProducts - 1; l >= 0; --l)
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[q][h][l == 2], b[q][h][l == 1], acc, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) part[wave][((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * kFewLd + r31] = acc[r];
+  __syncthreads();
+  // 8 results a thread, 128 threads; where they are written transposed as well, 128 others do that
+  const bool turned = threadIdx.x >= 128;
+  if (threadIdx.x >= 256) return;
+  if (turned && !(EPI == kEpiBoth || (symmetric(EPI) && t.tm != t.tn))) return;
+  const int at = threadIdx.x & 127, major = at >> 2, minor = (at & 3) * 8;
+  float v[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int i = turned ? (minor + x) * kFewLd + major : major * kFewLd + minor + x;
+    v[x] = part[0][i];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v[x] += part[w][i];
+    v[x] *= kDown;
+  }
+  const int64_t row = (int64_t)t.tm * 32 + (turned ? minor : major), col = (int64_t)t.tn * 32 + (turned ? major : minor);
+  if constexpr (EPI == kEpiPoly) {
+    // transposed: the addend's other triangle, which its product wrote as a copy of this one
+    const uint8_t* add = p.addend + t.e * p.d_stride + (turned ? plane_off<P>(col, row, p.ld_direct) : plane_off<P>(row, col, p.ld_direct));
+    v8h h[P];
+#pragma unroll
+    for (int l = 0; l < P; ++l) h[l] = *reinterpret_cast<const v8h*>(add + l * (kLine / 2));
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      v[x] = p.c * v[x] + p.b * (P == 2 ? (float)h[0][x] + (float)h[P - 1][x] : (float)h[0][x]);
+      if (!turned && row == col + x) v[x] += p.a * kUp;
+    }
+  }
+  if constexpr (EPI == kEpiOutF32 || EPI == kEpiOutBf16) {
+    using TOut = std::conditional_t<EPI == kEpiOutF32, float, uint16_t>;
+    TOut* out = (TOut*)p.out + t.e * p.out_stride + row * p.ld_out + col;
+    if (row < p.rows) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (col + x < p.cols) store_one(out + x, v[x] * (kDown * p.scale), p.keep);
+    }
+  } else if (turned) {
+    store_planes<OP>(p.turned + t.e * p.t_stride + plane_off<OP>(col, row, p.ld_turned), v);
+  } else {
+    store_planes<OP>(p.direct + t.e * p.d_stride + plane_off<OP>(row, col, p.ld_direct), v);
+  }
 }
 
 // -------------------------------------------------------------- launches ----
-using Orth256 = OrthGeo<4, 2, 2, 4, 2, 2>;       // 256 x 256, 8 waves, a workgroup per CU
-using Orth128 = OrthGeo<2, 2, 2, 2, 2, 2>;       // 128 x 128, 4 waves, two per CU
-using Orth64 = OrthGeo<1, 1, 2, 2, 4, 2>;        // 64 x 64, 4 waves, two per CU
-template <typename T> constexpr int kSlots = std::is_same<T, Orth256>::value ? 256 : 512;
-// Steps of a tile that sharing the last tiles has to save to be worth a launch and the way through memory (~10 us).
-template <typename T> constexpr int kShareGain = T::BM == 256 ? 4 : T::BM == 128 ? 8 : 32;
+// Tiles by their side, in two forms: with a deep ring, one workgroup a CU, for products that have no more tiles than that (a
+// step then takes the loads' latency over the ring's depth), and with several workgroups a CU.
+template <int P_, int Side, bool Deep> struct OrthPick;
+template <int P_, bool Deep> struct OrthPick<P_, 32, Deep> { static constexpr int P = P_, BM = 32, Threads = kFewThreads, PerCu = 1; };
+template <int P, bool Deep> struct OrthPick<P, 256, Deep> : OrthGeo<P, 4, 2, 2, 4, 2, 2> { static constexpr int PerCu = 1; };
+template <int P> struct OrthPick<P, 128, false> : OrthGeo<P, 2, 2, 2, 2, 2, 2> { static constexpr int PerCu = 2; };
+template <int P> struct OrthPick<P, 128, true> : OrthGeo<P, 2, 2, 2, 2, 4, 1> { static constexpr int PerCu = 1; };
+template <int P> struct OrthPick<P, 64, false> : OrthGeo<P, 1, 1, 2, 2, 3, 3> { static constexpr int PerCu = 3; };
+template <int P> struct OrthPick<P, 64, true> : OrthGeo<P, 1, 1, 2, 2, 4, 1> { static constexpr int PerCu = 1; };
+constexpr int kCus = 256, kMostSlots = 3 * kCus;
+// Steps of a tile that sharing the last tiles has to save to be worth a launch and the way through memory.
+constexpr int share_gain(int side) { return side == 256 ? 16 : side == 128 ? 16 : 40; }
 constexpr int kShareLeast = 4;                   // steps of a worker, at least
 
+// The tiles' side.  us for five steps of fp32 results with sides of 32, 64, 128 and 256:
+//   256 x 512       104   110   193          2048 x 2048         2490   834   823  1633
+//   512 x 512       135   143   246          1500 x 4000         2230   845   784  1956
+//   768 x 768       263   172   303          8 x 1024 x 4096     7760  2730  2117  2430
+//   64 x 8192       353   189   296          4096 x 4096           -   5690  4080  4080
+//   16 x 200 x 300  176   118   188          4096 x 14336          -  15900 11100 10370
+//   3 x 1283 x 701  587   290   400          64 x 1408 x 2048      -  20400 15400 16280 (256 x 256 tiles: 1408 padded to 1536)
+// So the smallest tiles are for matrices that do not fill the GPU with them and whose sums are short, and a larger tile for
+// those that give every CU one of it, the largest where it pads little.
 int tile_side(const OrthArgs& a) {
   const int64_t m = std::min(a.N, a.K), n = std::max(a.N, a.K);
-  auto tiles = [&](int64_t side) { return a.E * ((m + side - 1) / side) * ((n + side - 1) / side); };
-  if (tiles(128) < 256) return 64;
-  const int64_t m128 = (m + 127) / 128 * 128, m256 = (m + 255) / 256 * 256;
-  const int64_t n128 = (n + 127) / 128 * 128, n256 = (n + 255) / 256 * 256;
-  return tiles(256) >= 256 && (double)m256 * n256 <= 1.05 * (double)m128 * n128 ? 256 : 128;
+  auto padded = [](int64_t x, int64_t side) { return (x + side - 1) / side * side; };
+  auto tiles = [&](int64_t side) { return a.E * (padded(m, side) / side) * (padded(n, side) / side); };
+  if (tiles(32) <= kCus && n <= 1024) return 32;
+  if (tiles(128) < kCus) return 64;
+  return tiles(256) >= kCus && (double)padded(m, 256) * padded(n, 256) <= 1.05 * (double)padded(m, 128) * padded(n, 128) ? 256 : 128;
 }
 
 struct OrthLayout {
-  int side;
+  int side, parts;
   int64_t m, n, mp, np;
   size_t part, x, xt[2], A, B, partial, total;
 };
 OrthLayout orth_layout(const OrthArgs& a) {
   OrthLayout l{};
   l.side = tile_side(a);
+  // workgroups for the norm: enough for the GPU, of four runs at least (every workgroup that writes the planes adds them up)
+  const int64_t runs = a.N * ((a.K + kNormRun - 1) / kNormRun);
+  l.parts = (int)std::max<int64_t>(1, std::min<int64_t>({kNormMost, (2048 + a.E - 1) / a.E, runs / 4}));
   l.m = std::min(a.N, a.K);
   l.n = std::max(a.N, a.K);
   l.mp = (l.m + l.side - 1) / l.side * l.side;
@@ -553,87 +705,118 @@ OrthLayout orth_layout(const OrthArgs& a) {
     at += align_up(bytes, 256);
     return here;
   };
-  const size_t xs = (size_t)a.E * l.mp * l.np * 4, as = (size_t)a.E * l.mp * l.mp * 4;
-  l.part = take((size_t)a.E * kNormBlocks * 8);
+  const size_t xs = (size_t)a.E * l.mp * l.np * el_bytes(2), as = (size_t)a.E * l.mp * l.mp * el_bytes(2);
+  l.part = take((size_t)a.E * l.parts * 8);
   l.x = take(xs);
   l.xt[0] = take(xs);
   l.xt[1] = take(xs);
   l.A = take(as);
   l.B = take(as);
-  l.partial = take((size_t)(l.side == 256 ? 256 : 512) * 2 * l.side * l.side * 4);
+  if (l.side > 32) l.partial = take((size_t)(l.side == 256 ? kCus : kMostSlots) * 2 * l.side * l.side * 4);
   l.total = at;
   return l;
 }
 
-template <typename T, OrthEpi EPI>
+template <typename T, OrthEpi EPI, int OP>
+hipError_t run_orth_tiles(OrthGemm p, int64_t tiles, hipStream_t st) {
+  constexpr int kSlots = kCus * T::PerCu;
+  if (tiles >= (int64_t)1 << 31 || (tiles + kSlots) * T::Threads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+  if constexpr (T::BM == 32) {
+    hipLaunchKernelGGL((orth_few_kernel<T::P, EPI, OP>), dim3((unsigned)tiles), dim3(T::Threads), 0, st, p);
+  } else {
+    const int rest = (int)(tiles % kSlots);
+    const int64_t workers = std::min<int64_t>(kSlots, (int64_t)rest * p.steps / kShareLeast);
+    const bool share = workers > rest && (double)p.steps * (1.0 - (double)rest / workers) >= share_gain(T::BM);
+    p.rest = share ? rest : 0;
+    p.workers = share ? (int)workers : 0;
+    p.full = (int)tiles - p.rest;
+    hipLaunchKernelGGL((orth_gemm_kernel<T, EPI, OP>), dim3((unsigned)(p.full + p.workers)), dim3(T::Threads), 0, st, p);
+    if (share) hipLaunchKernelGGL((orth_join_kernel<T, EPI, OP>), dim3((unsigned)p.rest, T::MI), dim3(T::Threads), 0, st, p);
+  }
+  return hipGetLastError();
+}
+
+template <int P, int Side, OrthEpi EPI, int OP>
 hipError_t run_orth_gemm(OrthGemm p, int64_t E, hipStream_t st) {
   p.per_matrix = symmetric(EPI) ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
   const int64_t tiles = E * p.per_matrix;
-  if (tiles >= (int64_t)1 << 31 || (tiles + kSlots<T>) * T::Threads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-  const int rest = (int)(tiles % kSlots<T>);
-  const int64_t workers = std::min<int64_t>(kSlots<T>, (int64_t)rest * p.steps / kShareLeast);
-  const bool share = workers > rest && (double)p.steps * (1.0 - (double)rest / workers) >= kShareGain<T>;
-  p.rest = share ? rest : 0;
-  p.workers = share ? (int)workers : 0;
-  p.full = (int)tiles - p.rest;
-  hipLaunchKernelGGL((orth_gemm_kernel<T, EPI>), dim3((unsigned)(p.full + p.workers)), dim3(T::Threads), 0, st, p);
-  if (share) hipLaunchKernelGGL((orth_join_kernel<T, EPI>), dim3((unsigned)p.rest), dim3(T::Threads), 0, st, p);
-  return hipGetLastError();
+  if constexpr (Side == 64 || Side == 128)
+    if (tiles <= kCus) return run_orth_tiles<OrthPick<P, Side, true>, EPI, OP>(p, tiles, st);
+  return run_orth_tiles<OrthPick<P, Side, false>, EPI, OP>(p, tiles, st);
 }
 
-template <typename T>
-hipError_t run_orth_steps(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
+// Step s, whose operands have P planes; OP: the next one's.
+template <int P, int Side, int OP>
+hipError_t run_orth_step(const OrthArgs& a, const OrthLayout& l, int s, hipStream_t st) {
   char* ws = (char*)a.ws;
+  constexpr int el = el_bytes(P);
   uint8_t* x = (uint8_t*)ws + l.x;
   uint8_t *A = (uint8_t*)ws + l.A, *B = (uint8_t*)ws + l.B;
-  const int64_t ld_x = l.np * 4, ld_t = l.mp * 4, xs = l.mp * l.np * 4, as = l.mp * l.mp * 4;
-  const int tm = (int)(l.mp / T::BM), tn = (int)(l.np / T::BM);
-  const int along_n = (int)((l.n + kLineEl - 1) / kLineEl), along_m = (int)((l.m + kLineEl - 1) / kLineEl);
-  hipError_t err = hipSuccess;
-  for (int s = 0; s < a.steps && err == hipSuccess; ++s) {
-    const uint8_t* xt = (uint8_t*)ws + l.xt[s & 1];
-    OrthGemm p{};
-    p.partial = (float*)(ws + l.partial);
-    p.a = a.a; p.b = a.b; p.c = a.c;
-    p.A = p.B = x; p.lda = p.ldb = ld_x; p.a_stride = p.b_stride = xs;
-    p.tiles_m = p.tiles_n = tm; p.steps = along_n;
-    p.direct = p.turned = A; p.ld_direct = p.ld_turned = ld_t; p.d_stride = p.t_stride = as;
-    if ((err = run_orth_gemm<T, kEpiGram>(p, a.E, st)) != hipSuccess) break;
-    p.A = p.B = A; p.lda = p.ldb = ld_t; p.a_stride = p.b_stride = as;
-    p.steps = along_m;
-    p.addend = A;
-    p.direct = p.turned = B;
-    if ((err = run_orth_gemm<T, kEpiPoly>(p, a.E, st)) != hipSuccess) break;
-    const bool last = s + 1 == a.steps, wide = a.N <= a.K;
-    const uint8_t* first = last && wide ? B : xt;             // the tiles' rows: m's or n's
-    p.A = first; p.a_stride = first == xt ? xs : as;
-    p.B = first == xt ? B : xt; p.b_stride = first == xt ? as : xs;
-    p.lda = p.ldb = ld_t;
-    p.tiles_m = first == xt ? tn : tm; p.tiles_n = first == xt ? tm : tn;
-    if (!last) {
-      p.direct = (uint8_t*)ws + l.xt[~s & 1]; p.ld_direct = ld_t; p.d_stride = xs;
-      p.turned = x; p.ld_turned = ld_x; p.t_stride = xs;
-      err = run_orth_gemm<T, kEpiBoth>(p, a.E, st);
-    } else {
-      p.out = a.out; p.ld_out = a.ld_out; p.out_stride = a.out_stride; p.rows = a.N; p.cols = a.K;
-      p.scale = a.scale; p.keep = a.keep;
-      err = a.out_dt == S3R_BF16 ? run_orth_gemm<T, kEpiOutBf16>(p, a.E, st) : run_orth_gemm<T, kEpiOutF32>(p, a.E, st);
-    }
+  const uint8_t* xt = (uint8_t*)ws + l.xt[s & 1];
+  const int64_t ld_x = l.np * el, ld_t = l.mp * el, xs = l.mp * ld_x, as = l.mp * ld_t;
+  const int tm = (int)(l.mp / Side), tn = (int)(l.np / Side);
+  constexpr int el_step = Side == 32 ? 32 : line_el(P);       // elements of a step of the products' loops
+  const int along_n = (int)((l.n + el_step - 1) / el_step), along_m = (int)((l.m + el_step - 1) / el_step);
+  OrthGemm p{};
+  p.partial = (float*)(ws + l.partial);
+  p.a = a.a; p.b = a.b; p.c = a.c;
+  p.A = p.B = x; p.lda = p.ldb = ld_x; p.a_stride = p.b_stride = xs;
+  p.tiles_m = p.tiles_n = tm; p.steps = along_n;
+  p.direct = p.turned = A; p.ld_direct = p.ld_turned = ld_t; p.d_stride = p.t_stride = as;
+  hipError_t err = run_orth_gemm<P, Side, kEpiGram, P>(p, a.E, st);
+  if (err != hipSuccess) return err;
+  p.A = p.B = A; p.lda = p.ldb = ld_t; p.a_stride = p.b_stride = as;
+  p.steps = along_m;
+  p.addend = A;
+  p.direct = p.turned = B;
+  if ((err = run_orth_gemm<P, Side, kEpiPoly, P>(p, a.E, st)) != hipSuccess) return err;
+  const bool last = s + 1 == a.steps, wide = a.N <= a.K;
+  const uint8_t* first = last && wide ? B : xt;             // the tiles' rows: m's or n's
+  p.A = first; p.a_stride = first == xt ? xs : as;
+  p.B = first == xt ? B : xt; p.b_stride = first == xt ? as : xs;
+  p.lda = p.ldb = ld_t;
+  p.tiles_m = first == xt ? tn : tm; p.tiles_n = first == xt ? tm : tn;
+  if (!last) {
+    p.direct = (uint8_t*)ws + l.xt[~s & 1]; p.ld_direct = l.mp * el_bytes(OP); p.d_stride = l.np * p.ld_direct;
+    p.turned = x; p.ld_turned = l.np * el_bytes(OP); p.t_stride = l.mp * p.ld_turned;
+    return run_orth_gemm<P, Side, kEpiBoth, OP>(p, a.E, st);
   }
+  p.out = a.out; p.ld_out = a.ld_out; p.out_stride = a.out_stride; p.rows = a.N; p.cols = a.K;
+  p.scale = a.scale; p.keep = a.keep;
+  if constexpr (P == 1) return run_orth_gemm<P, Side, kEpiOutBf16, P>(p, a.E, st);
+  else return run_orth_gemm<P, Side, kEpiOutF32, P>(p, a.E, st);
+}
+
+// Steps that take both planes.
+int exact_steps(const OrthArgs& a) { return a.out_dt == S3R_BF16 ? std::max(0, a.steps - kLoose) : a.steps; }
+
+template <int Side>
+hipError_t run_orth_steps(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
+  const int exact = exact_steps(a);
+  hipError_t err = hipSuccess;
+  for (int s = 0; s < a.steps && err == hipSuccess; ++s)
+    err = s + 1 < exact || (s < exact && exact == a.steps) ? run_orth_step<2, Side, 2>(a, l, s, st)
+          : s < exact                                       ? run_orth_step<2, Side, 1>(a, l, s, st)
+                                                            : run_orth_step<1, Side, 1>(a, l, s, st);
   return err;
 }
 
-template <typename TIn>
+template <typename TIn, int P>
 hipError_t run_orth_prepare(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
   char* ws = (char*)a.ws;
   double* part = (double*)(ws + l.part);
-  hipLaunchKernelGGL((orth_norm_kernel<TIn>), dim3(kNormBlocks, (unsigned)a.E), dim3(kNormThreads), 0, st, a, part);
+  hipLaunchKernelGGL((orth_norm_kernel<TIn>), dim3((unsigned)l.parts, (unsigned)a.E), dim3(kNormThreads), 0, st, a, part, l.parts);
   const bool wide = a.N <= a.K;
-  const int64_t rows = wide ? l.mp : l.np, cols = wide ? l.np : l.mp, xs = l.mp * l.np * 4;
+  const int64_t rows = wide ? l.mp : l.np, cols = wide ? l.np : l.mp, xs = l.mp * l.np * el_bytes(P);
   uint8_t *x = (uint8_t*)ws + l.x, *xt = (uint8_t*)ws + l.xt[0];
-  hipLaunchKernelGGL((orth_prepare_kernel<TIn>), dim3((unsigned)(cols / kPrepTile), (unsigned)(rows / kPrepTile), (unsigned)a.E),
-                     dim3(kPrepThreads), 0, st, a, part, wide ? x : xt, xs, wide ? xt : x, xs, rows, cols);
+  hipLaunchKernelGGL((orth_prepare_kernel<TIn, P>),
+                     dim3((unsigned)((cols + kPrepTile - 1) / kPrepTile), (unsigned)((rows + kPrepTile - 1) / kPrepTile), (unsigned)a.E),
+                     dim3(kPrepThreads), 0, st, a, part, l.parts, wide ? x : xt, xs, wide ? xt : x, xs, rows, cols);
   return hipGetLastError();
+}
+template <typename TIn>
+hipError_t run_orth_prepare(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
+  return exact_steps(a) > 0 ? run_orth_prepare<TIn, 2>(a, l, st) : run_orth_prepare<TIn, 1>(a, l, st);
 }
 }  // namespace
 
@@ -644,8 +827,9 @@ hipError_t launch_orthogonalize(const OrthArgs& a, hipStream_t st) {
   const OrthLayout l = orth_layout(a);
   const hipError_t e = a.g_dtype == S3R_BF16 ? run_orth_prepare<uint16_t>(a, l, st) : run_orth_prepare<float>(a, l, st);
   if (e != hipSuccess) return e;
-  if (l.side == 256) return run_orth_steps<Orth256>(a, l, st);
-  return l.side == 128 ? run_orth_steps<Orth128>(a, l, st) : run_orth_steps<Orth64>(a, l, st);
+  if (l.side == 256) return run_orth_steps<256>(a, l, st);
+  if (l.side == 128) return run_orth_steps<128>(a, l, st);
+  return l.side == 64 ? run_orth_steps<64>(a, l, st) : run_orth_steps<32>(a, l, st);
 }
 
 }  // namespace s3r

@@ -69,25 +69,27 @@ def test_sizes_of_values(size):
 
 def test_several_matrices_strides_scale_and_keep():
     G = gradient((5, 70, 133), torch.float32, 1)
-    each = torch.stack([s3r.orthogonalize(g) for g in G])
     for dtype in BOTH:
+        each = torch.stack([s3r.orthogonalize(g, out_dtype=dtype) for g in G])
         wide = torch.full((5, 80, 140), 7.0, device=DEV).to(dtype)
         src = torch.full((5, 72, 150), float("nan"), device=DEV)
         src[:, 1:71, 3:136] = G
         out = wide[:, 5:75, 1:134]
         ws = s3r.orthogonalize_buffer(G)
         s3r.s3r_orthogonalize(src[:, 1:71, 3:136], out, ws=ws)
-        assert torch.equal(out, each.to(dtype))
+        assert torch.equal(out, each)
         s3r.s3r_orthogonalize(src[:, 1:71, 3:136], out, scale=-0.5, keep=0.25, ws=ws)
-        exp = 0.25 * each.to(dtype).double() - 0.5 * each.double()
-        # the results' own rounding, and those of the product and the sum in fp32
-        assert ((out.double() - exp).abs() <= HALF[dtype] * exp.abs() + 3 * 2.0 ** -24 * each.double().abs()).all()
+        exp, size = 0.25 * each.double() - 0.5 * each.double(), each.double().abs()
+        # X lies within half a step of `each`, which out held exactly: half of that, the result's own rounding (of a number
+        # that is at most half a step of X from exp), and those of two products and a sum in fp32
+        most = 0.5 * HALF[dtype] * size + HALF[dtype] * (exp.abs() + 0.5 * HALF[dtype] * size) + 3 * 2.0 ** -24 * size
+        assert ((out.double() - exp).abs() <= most).all()
         assert (wide[:, :5] == 7).all() and (wide[:, 75:] == 7).all() and (wide[..., 0] == 7).all() and (wide[..., 134:] == 7).all()
         H = G.to(dtype, copy=True)                    # (of the same type it would be G, which this changes)
         exp = s3r.orthogonalize(H)
         s3r.s3r_orthogonalize(H, H, ws=ws)
         assert torch.equal(H, exp)                    # in place
-    nan = torch.full((5, 70, 133), float("nan"), device=DEV)
+    nan = torch.full((5, 70, 133), float("nan"), dtype=torch.bfloat16, device=DEV)
     s3r.s3r_orthogonalize(G, nan, ws=ws)              # keep 0 reads nothing
     assert torch.equal(nan, each)
     tall = G.transpose(1, 2).contiguous()
