@@ -51,24 +51,42 @@ __device__ __forceinline__ uint2 i8_codes(const Raw8<float>& v, const Step& s) {
 template <typename TRaw>
 __device__ __forceinline__ Raw8<float> i8_swiglu(const TRaw& v, const TRaw& u) {
   const Raw8<float> x = mr_float8(v), y = mr_float8(u);
-  Raw8<float> h;
+  Raw8<float> d, s;
+  bool slow = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h.w[i] = mr_swiglu(x.w[i], y.w[i]);        // 0 * 0 past the end
-  return h;
+  for (int i = 0; i < 8; ++i) {
+    d.w[i] = 1.f + glue_exp32(-x.w[i]);
+    s.w[i] = glue_recip(d.w[i]);
+    slow |= glue_slow_recip(d.w[i]);
+  }
+  if (__builtin_amdgcn_ballot_w64(slow) != 0) {          // the rare reciprocal below 2^-126: one branch for the wave
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (glue_slow_recip(d.w[i])) s.w[i] = __fdiv_rn(1.f, d.w[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s.w[i] = (x.w[i] * s.w[i]) * y.w[i];       // 0 * 0 past the end
+  return s;
 }
 
 // Elements c, c + stride, ... (Pieces of them, 8 each) of a row.
 template <typename TIn, bool UP, bool Words, int Pieces>
 struct I8Pieces {
   std::conditional_t<UP, Raw8<float>, Raw8<TIn>> v[Pieces];
+  Raw8<TIn> a[Pieces], u[UP ? Pieces : 1];
   __device__ __forceinline__ void load(const I8Source<TIn, UP, Words>& s, int64_t c, int stride) {
-    Raw8<TIn> a[Pieces], u[UP ? Pieces : 1];
+    ask(s, c, stride);
+    take(s, c, stride);
+  }
+  __device__ __forceinline__ void ask(const I8Source<TIn, UP, Words>& s, int64_t c, int stride) {
 #pragma unroll
     for (int q = 0; q < Pieces; ++q) {           // every load before the first conversion
       const int64_t at = c + (int64_t)q * stride;
       a[q] = mr_load8<TIn, Words>(s.A + at, s.left(at), s.K);
       if constexpr (UP) u[q] = mr_load8<TIn, Words>(s.U + at, s.left(at), s.K);
     }
+  }
+  __device__ __forceinline__ void take(const I8Source<TIn, UP, Words>& s, int64_t c, int stride) {
 #pragma unroll
     for (int q = 0; q < Pieces; ++q) {
       const int64_t n = s.left(c + (int64_t)q * stride);
@@ -76,6 +94,7 @@ struct I8Pieces {
       if constexpr (UP) {
         mr_tail<Words>(u[q], n, s.K);
         v[q] = i8_swiglu(a[q], u[q]);
+        __builtin_amdgcn_sched_barrier(0);         // one piece's registers at a time
       } else {
         v[q] = a[q];
       }
@@ -94,10 +113,11 @@ struct I8Pieces {
   }
 };
 
+constexpr int ir_block(int threads) { return threads > kIrBlock ? threads : kIrBlock; }
 template <typename TIn, bool UP, bool Words, int Threads, int Pieces, bool Long>
-__global__ __launch_bounds__(kIrBlock) void i8_rows_kernel(I8RowsArgs a) {
-  constexpr int kRows = kIrBlock / Threads, kWaves = Threads / 64;
-  __shared__ uint32_t red[kIrBlock / 64];
+__global__ __launch_bounds__(ir_block(Threads)) void i8_rows_kernel(I8RowsArgs a) {
+  constexpr int kRows = ir_block(Threads) / Threads, kWaves = Threads / 64;
+  __shared__ uint32_t red[ir_block(Threads) / 64];
   const int sub = threadIdx.x % Threads, mine = threadIdx.x / Threads;
   const int64_t r = wide_block() * kRows + mine;
   const int64_t g = blockIdx.z;
@@ -192,19 +212,26 @@ __device__ __forceinline__ I8Tile i8_tile(const I8ProdK& p, int mt, int tile) {
   return I8Tile{h.r0, min(h.r1, h.r0 + tile), __builtin_amdgcn_readfirstlane(h.e), true};
 }
 
-// Up to four rows: byte dot products.  A wave takes kDotR weight rows, 1 KiB of each at a time (whole lines, 16 bytes a
-// lane), against the rows' codes in LDS; `split` of the workgroup's eight waves share weight rows and deal the 1 KiB
-// pieces of K among them.  The matrix cores would want a weight row in 4 lanes and 16 lines a quarter-wave.
-// With TIn the rows come unrounded: every workgroup rounds them while its first weights are on the way, so there is no
-// second launch and no codes go through memory.  TIn void: rows already in codes.
-constexpr int kDotThreads = 512, kDotWaves = kDotThreads / 64, kDotR = 4, kDotPiece = 1024;
+// Up to four rows: byte dot products.  A wave takes R weight rows, 1 KiB of each at a time (whole lines, 16 bytes a
+// lane), against the rows' codes in LDS; `split` of the workgroup's waves share weight rows and deal the 1 KiB pieces of K
+// among them.  (The matrix cores would want a weight row in 4 lanes and 16 lines a quarter-wave.)  Bound by the weights'
+// bytes: 1 x 14336 x 4096 12.7 - 13.3 us, 4.4 - 4.6 TB/s with the launch; 32 rows of 64 experts of 2816 x 2048 29.7.
+// With TIn the rows come unrounded: every workgroup rounds them while its weights are on the way, so there is no
+// second launch and no codes go through memory.  TIn void: rows already in codes.  Loads arrive in the order that they were
+// asked for, so the rows are asked for first, then kDepth pieces of the weights, always all of them, for the compiler to
+// know how many stand between (1 x 4096 x 14336 behind silu(gate) * up: 13.2 us, with the weights first 19.5).
+constexpr int kDotPiece = 1024;
+// silu(gate) * up of a whole row is 36 instructions an element for every workgroup: wider ones share it among more waves,
+// with half of the weights on the way, which is what memory moves meanwhile (and what the registers have room for).
+constexpr int dot_waves(bool up) { return up ? 16 : 8; }
 constexpr size_t kDotLdsMax = 60000;              // of the 64 KiB that a workgroup has without asking
 
-template <typename TOut, typename TIn, bool UP, bool Words, int MT>
-__global__ __launch_bounds__(kDotThreads) void i8_dot_kernel(I8ProdK p, I8RowsArgs q, int split) {
+template <typename TOut, typename TIn, bool UP, bool Words, int MT, int R, int kDepth>
+__global__ __launch_bounds__(64 * dot_waves(UP)) void i8_dot_kernel(I8ProdK p, I8RowsArgs q, int split) {
+  constexpr int kDotWaves = dot_waves(UP), kDotThreads = 64 * kDotWaves;
   constexpr bool kFused = !std::is_void<TIn>::value;
   __shared__ uint32_t red[kDotWaves];
-  __shared__ int part[kDotWaves][kDotR * MT];
+  __shared__ int part[kDotWaves][R * MT];
   extern __shared__ __attribute__((aligned(16))) int8_t rows[];         // MT rows of kpad codes
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
@@ -212,28 +239,35 @@ __global__ __launch_bounds__(kDotThreads) void i8_dot_kernel(I8ProdK p, I8RowsAr
   if (!t.some) return;
   const int rows_n = (int)(t.m1 - t.m0);
   const int slice = wave % split, group = wave / split;
-  const int64_t n0 = ((int64_t)nt * (kDotWaves / split) + group) * kDotR;
+  const int64_t n0 = ((int64_t)nt * (kDotWaves / split) + group) * R;
   const int pieces = (int)((p.K + kDotPiece - 1) / kDotPiece), kpad = pieces * kDotPiece;
   const __amdgpu_buffer_rsrc_t rb =
-      rows_rsrc(p.B + t.e * p.b_stride + (n0 < p.N ? n0 : 0) * p.ldb, min(p.N - n0, (int64_t)kDotR), p.ldb, p.K);
-  v4i cur[kDotR], nxt[kDotR];
-  auto load = [&](v4i (&w)[kDotR], int pc) {
-    if (pc < pieces) {                             // the same in the whole wave
+      rows_rsrc(p.B + t.e * p.b_stride + (n0 < p.N ? n0 : 0) * p.ldb, min(p.N - n0, (int64_t)R), p.ldb, p.K);
+  v4i w[kDepth][R];
+  // Past the last piece every load reads zeros: their number is the same for all, and the compiler can count to the row's.
+  const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc((void*)p.B, (short)0, 0, kRsrcWord3);
+  auto load = [&](int d, int pc) {
+    const __amdgpu_buffer_rsrc_t from = pc < pieces ? rb : none;
 #pragma unroll
-      for (int r = 0; r < kDotR; ++r)
-        w[r] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, (uint32_t)(pc * kDotPiece + lane * 16),
-                                                                             (uint32_t)r * (uint32_t)p.ldb, 0));
-    }
+    for (int r = 0; r < R; ++r)
+      w[d][r] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(from, (uint32_t)(pc * kDotPiece + lane * 16),
+                                                                              (uint32_t)r * (uint32_t)p.ldb, 0));
   };
-  load(cur, slice);
-  load(nxt, slice + split);
+  auto load_all = [&]() {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(d, slice + d * split);
+  };
   float sa[MT];
   if constexpr (kFused) {
-    constexpr int kPer = kDotThreads / MT, kStride = kPer * 8, kPieces = 4;
+    constexpr int kPer = kDotThreads / MT, kStride = kPer * 8, kPieces = UP ? 2 : 4;
     const int mine = threadIdx.x / kPer, c0 = (threadIdx.x % kPer) * 8;
     const I8Source<TIn, UP, Words> s(q, 0, mine < rows_n ? mr_source(q, t.m0 + mine) : -1);
     I8Pieces<TIn, UP, Words, kPieces> v;
-    v.load(s, c0, kStride);
+    v.ask(s, c0, kStride);
+    __builtin_amdgcn_sched_barrier(0);
+    load_all();                                    // after the row's: loads arrive in order, and the row is needed first
+    __builtin_amdgcn_sched_barrier(0);
+    v.take(s, c0, kStride);
     uint32_t m = v.amax();
     for (int64_t c = kPieces * kStride; c < p.K; c += kPieces * kStride) {
       I8Pieces<TIn, UP, Words, kPieces> more;
@@ -248,7 +282,7 @@ __global__ __launch_bounds__(kDotThreads) void i8_dot_kernel(I8ProdK p, I8RowsAr
     for (int i = 0; i < MT; ++i) {
       uint32_t a = 0;
 #pragma unroll
-      for (int w = 0; w < kDotWaves / MT; ++w) a = max(a, red[i * (kDotWaves / MT) + w]);
+      for (int x = 0; x < kDotWaves / MT; ++x) a = max(a, red[i * (kDotWaves / MT) + x]);
       const Step st = make_step(a);
       sa[i] = st.delta;
       flag |= st.flag;
@@ -256,8 +290,8 @@ __global__ __launch_bounds__(kDotThreads) void i8_dot_kernel(I8ProdK p, I8RowsAr
     }
     if (flag && nt == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, flag);
     const Step st = make_step(m);
-    auto store = [&](int64_t c, uint2 w) {
-      if (c < kpad) *reinterpret_cast<uint2*>(rows + mine * kpad + c) = w;
+    auto store = [&](int64_t c, uint2 q8) {
+      if (c < kpad) *reinterpret_cast<uint2*>(rows + mine * kpad + c) = q8;
     };
     v.codes(st, c0, kStride, store);
     for (int64_t c = kPieces * kStride; c < kpad; c += kPieces * kStride) {
@@ -266,54 +300,58 @@ __global__ __launch_bounds__(kDotThreads) void i8_dot_kernel(I8ProdK p, I8RowsAr
       more.codes(st, c + c0, kStride, store);
     }
   } else {
+    load_all();
     for (int at = threadIdx.x * 16; at < MT * kpad; at += kDotThreads * 16) {
       const int i = at / kpad, c = at - i * kpad;
-      v4i w = {0, 0, 0, 0};
+      v4i x = {0, 0, 0, 0};
       if (i < rows_n && c < p.K)
-        w = *reinterpret_cast<const v4i*>(p.A + (t.m0 + i) * p.lda + c) & tail_mask(c, p.K);
-      *reinterpret_cast<v4i*>(rows + at) = w;
+        x = *reinterpret_cast<const v4i*>(p.A + (t.m0 + i) * p.lda + c) & tail_mask(c, p.K);
+      *reinterpret_cast<v4i*>(rows + at) = x;
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) sa[i] = i < rows_n ? p.sa[t.m0 + i] : 0.f;
   }
   __syncthreads();
-  int acc[kDotR][MT];
+  int acc[R][MT];
 #pragma unroll
-  for (int r = 0; r < kDotR; ++r)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[r][i] = 0;
-  for (int pc = slice; pc < pieces; pc += split) {
+  for (int p0 = slice; p0 < pieces; p0 += kDepth * split) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const v4i x = *reinterpret_cast<const v4i*>(rows + i * kpad + pc * kDotPiece + lane * 16);
+    for (int d = 0; d < kDepth; ++d) {
+      const int pc = p0 + d * split;
+      if (pc >= pieces) break;
 #pragma unroll
-      for (int r = 0; r < kDotR; ++r)
+      for (int i = 0; i < MT; ++i) {
+        const v4i x = *reinterpret_cast<const v4i*>(rows + i * kpad + pc * kDotPiece + lane * 16);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) acc[r][i] = __builtin_amdgcn_sdot4(cur[r][w], x[w], acc[r][i], false);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) acc[r][i] = __builtin_amdgcn_sdot4(w[d][r][y], x[y], acc[r][i], false);
+      }
+      load(d, pc + kDepth * split);
     }
-#pragma unroll
-    for (int r = 0; r < kDotR; ++r) cur[r] = nxt[r];
-    load(nxt, pc + 2 * split);
   }
   // lane r * MT + i gets the sum of (weight row r, row i)
   int sum = 0;
 #pragma unroll
-  for (int r = 0; r < kDotR; ++r)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const int all = __builtin_amdgcn_readlane(wave_prefix(acc[r][i]), 63);
       sum = lane == r * MT + i ? all : sum;
     }
   if (split > 1) {
-    if (lane < kDotR * MT) part[wave][lane] = sum;
+    if (lane < R * MT) part[wave][lane] = sum;
     __syncthreads();
     if (slice > 0) return;
-    if (lane < kDotR * MT)
-      for (int w = 1; w < split; ++w) sum += part[wave + w][lane];
+    if (lane < R * MT)
+      for (int x = 1; x < split; ++x) sum += part[wave + x][lane];
   }
   const int i = lane % MT;
   const int64_t n = n0 + lane / MT;
-  if (lane >= kDotR * MT || i >= rows_n || n >= p.N) return;
+  if (lane >= R * MT || i >= rows_n || n >= p.N) return;
   float step = sa[0];
 #pragma unroll
   for (int x = 1; x < MT; ++x) step = i == x ? sa[x] : step;
@@ -321,102 +359,131 @@ __global__ __launch_bounds__(kDotThreads) void i8_dot_kernel(I8ProdK p, I8RowsAr
   store_out((TOut*)p.out + (t.m0 + i) * p.ld_out + n, i8_result(sum, step, p.sb[col], p.bias ? p.bias[col] : 0.f));
 }
 
-// Few rows: 16 MI rows x 16 NJ columns per workgroup, whose eight waves deal K's units of 128 bytes among them and
-// join their sums in LDS.  Fragments go straight from memory to the matrix cores (v_mfma_i32_16x16x64_i8: lane l holds
-// row or column l % 16, bytes 16 (l / 16) .. + 15 of 64; the result's register r is row 4 (l / 16) + r, column l % 16);
-// the weights' bytes are the bound, so a wave issues the loads of `Depth` units before its first product.
-constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;
+// Few rows: 16 MI rows x 16 NJ columns per workgroup, whose waves deal K's units of 128 bytes among them and join
+// their sums in LDS.  The weights' bytes are the bound, and how they are asked for: a load of 16 rows x 64 bytes (the matrix
+// cores' operand) is 64 requests, one of 8 whole lines 16, and the rows' codes cost as much as the weights (24 x 4096 x
+// 14336: 20.8 us straight into registers).  So every wave stages its units in LDS by buffer-load DMA, whole lines, in
+// a ring of its own of NS units: no wave waits for another before the end.  Chunks of a line as in the tiles below.
+// v_mfma_i32_16x16x64_i8: lane l holds row or column l % 16, bytes 16 (l / 16) .. + 15 of 64; the result's register r is
+// row 4 (l / 16) + r, column l % 16.
+__device__ __forceinline__ int chunk_pos8(int r, int q) { return q ^ ((r >> 1) & 7); }
 
-template <typename TOut, int MI, int NJ, int Depth>
-__global__ __launch_bounds__(kFewThreads) void i8_few_rows_kernel(I8ProdK p) {
-  __shared__ int part[kFewWaves - 1][MI * NJ][256];
+template <int MI_, int NJ_, int Waves_, int NS_>
+struct FewGeo {
+  static constexpr int MI = MI_, NJ = NJ_, Waves = Waves_, NS = NS_, Threads = 64 * Waves;
+  static constexpr int Loads = 2 * (MI + NJ);                             // 1 KiB pieces of a unit
+  static constexpr int UnitBytes = Loads * 1024, StageBytes = Waves * UnitBytes;
+};
+
+template <typename T>
+struct FewSrc {
+  __amdgpu_buffer_rsrc_t a, b, z;
+  uint32_t v[T::Loads];                       // this lane's byte offsets in unit 0
+  int units;
+};
+
+// Unit u into this wave's part of stage st; past the last unit every load reads zeros, so the wait counts stay the same.
+template <typename T>
+__device__ __forceinline__ void few_load(const FewSrc<T>& s, uint8_t* st, int u) {
+  const bool live = u < s.units;
+  const __amdgpu_buffer_rsrc_t ra = live ? s.a : s.z, rb = live ? s.b : s.z;
+#pragma unroll
+  for (int q = 0; q < T::Loads; ++q) dma16(q < 2 * T::MI ? ra : rb, st + q * 1024, s.v[q], (uint32_t)u * 128u);
+}
+
+template <typename T, int S>
+__device__ __forceinline__ void few_fill(const FewSrc<T>& s, int mine, int wave) {
+  if constexpr (S < T::NS) {
+    few_load<T>(s, ring<T, S>() + mine, wave + S * T::Waves);
+    few_fill<T, S + 1>(s, mine, wave);
+  }
+}
+
+// Units u, u + Waves, ... on the stages from S on.
+template <typename T, int S>
+__device__ __forceinline__ void few_units(const FewSrc<T>& s, int mine, int u, int64_t K, v4i (&acc)[T::MI][T::NJ]) {
+  if constexpr (S < T::NS) {
+    if (u >= s.units) return;
+    const int lane = threadIdx.x & 63, r15 = lane & 15, kb = lane >> 4;
+    uint8_t* st = ring<T, S>() + mine;
+    S3R_WAIT_VM(T::Loads * (T::NS - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    v4i x[2][T::MI], y[2][T::NJ];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = r15 * 128 + (chunk_pos8(r15, 4 * h + kb) << 4);
+#pragma unroll
+      for (int i = 0; i < T::MI; ++i) x[h][i] = *reinterpret_cast<const v4i*>(st + i * 2048 + at);
+#pragma unroll
+      for (int j = 0; j < T::NJ; ++j) y[h][j] = *reinterpret_cast<const v4i*>(st + (T::MI + j) * 2048 + at);
+    }
+    S3R_WAIT_LGKM0();
+    __builtin_amdgcn_sched_barrier(0);
+    few_load<T>(s, st, u + T::NS * T::Waves);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if ((u + 1) * 128 > K) {                 // the last unit of a K that fills none: the rows' codes past K count as 0
+        const v4i m = tail_mask(u * 128 + h * 64 + kb * 16, K);
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i) x[h][i] &= m;
+      }
+#pragma unroll
+      for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[h][i], y[h][j], acc[i][j], 0, 0, 0);
+    }
+    few_units<T, S + 1>(s, mine, u + T::Waves, K, acc);
+  }
+}
+
+template <typename TOut, typename T>
+__global__ __launch_bounds__(T::Threads) void i8_few_rows_kernel(I8ProdK p) {
   // The wave's index in a scalar register: the loop over its units has to branch, since the matrix instructions run
   // whatever the execution mask says.
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
-  const I8Tile t = i8_tile(p, mt, 16 * MI);
+  const I8Tile t = i8_tile(p, mt, 16 * T::MI);
   if (!t.some) return;
-  const int64_t n0 = (int64_t)nt * (16 * NJ);
-  const int r15 = lane & 15, kb = lane >> 4;
-  const int units = (int)((p.K + 127) / 128);
-  const __amdgpu_buffer_rsrc_t ra = rows_rsrc(p.A + t.m0 * p.lda, t.m1 - t.m0, p.lda, p.K);
-  const __amdgpu_buffer_rsrc_t rb = rows_rsrc(p.B + t.e * p.b_stride + n0 * p.ldb, min(p.N - n0, (int64_t)(16 * NJ)), p.ldb, p.K);
-  uint32_t va[MI], vb[NJ];
+  const int64_t n0 = (int64_t)nt * (16 * T::NJ);
+  FewSrc<T> s;
+  s.units = (int)((p.K + 127) / 128);
+  s.a = rows_rsrc(p.A + t.m0 * p.lda, t.m1 - t.m0, p.lda, p.K);
+  s.b = rows_rsrc(p.B + t.e * p.b_stride + n0 * p.ldb, min(p.N - n0, (int64_t)(16 * T::NJ)), p.ldb, p.K);
+  s.z = __builtin_amdgcn_make_buffer_rsrc((void*)p.A, (short)0, 0, kRsrcWord3);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) va[i] = (uint32_t)((16 * i + r15) * p.lda + kb * 16);
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) vb[j] = (uint32_t)((16 * j + r15) * p.ldb + kb * 16);
-  v4i acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-  v4i x[Depth][2][MI], y[Depth][2][NJ];
-  auto load = [&](int u0) {
-#pragma unroll
-    for (int d = 0; d < Depth; ++d) {
-      const int u = u0 + d * kFewWaves;
-      if (u < units) {                             // the same in the whole wave
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            y[d][h][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb[j] + h * 64, (uint32_t)u * 128u, 0));
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-            x[d][h][i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, va[i] + h * 64, (uint32_t)u * 128u, 0));
-        }
-      }
-    }
-  };
-  for (int u0 = wave; u0 < units; u0 += kFewWaves * Depth) {
-    load(u0);
-#pragma unroll
-    for (int d = 0; d < Depth; ++d) {
-      const int u = u0 + d * kFewWaves;
-      if (u >= units) break;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if ((u + 1) * 128 > p.K) {                 // the last unit of a K that fills none: the rows' codes past K count as 0
-          const v4i m = tail_mask(u * 128 + h * 64 + kb * 16, p.K);
-#pragma unroll
-          for (int i = 0; i < MI; ++i) x[d][h][i] &= m;
-        }
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[d][h][i], y[d][h][j], acc[i][j], 0, 0, 0);
-      }
-    }
+  for (int q = 0; q < T::Loads; ++q) {
+    const int r = (q < 2 * T::MI ? q : q - 2 * T::MI) * 8 + (lane >> 3);
+    s.v[q] = (uint32_t)(r * (q < 2 * T::MI ? p.lda : p.ldb) + chunk_pos8(r & 15, lane & 7) * 16);
   }
-  if (wave > 0) {
+  v4i acc[T::MI][T::NJ];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+  for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < T::NJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  const int mine = wave * T::UnitBytes;
+  few_fill<T, 0>(s, mine, wave);
+  for (int u = wave; u < s.units; u += T::NS * T::Waves) few_units<T, 0>(s, mine, u, p.K, acc);
+  S3R_WAIT_VM(0);
+  // the waves' sums over each other's: a wave's part of stage 0 is its own until here
+  static_assert(T::UnitBytes >= T::MI * T::NJ * 1024, "a wave's sums fit its unit");
+  int* part = reinterpret_cast<int*>(ring<T, 0>());
 #pragma unroll
-        for (int r = 0; r < 4; ++r) part[wave - 1][i * NJ + j][r * 64 + lane] = acc[i][j][r];
-  }
+  for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[(mine / 4) + ((i * T::NJ + j) * 4 + r) * 64 + lane] = acc[i][j][r];
   __syncthreads();
-  if (wave > 0) return;
+  // a register of the results (64 of them) a wave and turn
   TOut* out = (TOut*)p.out;
+  for (int x = wave; x < T::MI * T::NJ * 4; x += T::Waves) {
+    int v = 0;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int64_t n = n0 + 16 * j + r15;
-    if (n >= p.N) continue;
-    const float sb = p.sb[t.e * p.N + n], bias = p.bias ? p.bias[t.e * p.N + n] : 0.f;
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t m = t.m0 + 16 * i + 4 * kb + r;
-        if (m >= t.m1) continue;
-        int v = acc[i][j][r];
-#pragma unroll
-        for (int w = 0; w < kFewWaves - 1; ++w) v += part[w][i * NJ + j][r * 64 + lane];
-        store_out(out + m * p.ld_out + n, i8_result(v, p.sa[m], sb, bias));
-      }
+    for (int w = 0; w < T::Waves; ++w) v += part[w * (T::UnitBytes / 4) + x * 64 + lane];
+    const int i = x / (T::NJ * 4), j = x / 4 % T::NJ;
+    const int64_t m = t.m0 + 16 * i + 4 * (lane >> 4) + x % 4, n = n0 + 16 * j + (lane & 15);
+    if (m < t.m1 && n < p.N)
+      store_out(out + m * p.ld_out + n, i8_result(v, p.sa[m], p.sb[t.e * p.N + n], p.bias ? p.bias[t.e * p.N + n] : 0.f));
   }
 }
 
@@ -445,8 +512,6 @@ struct I8TileSrc {
   uint32_t va[T::PA], vb[T::PB];              // this lane's byte offsets in step 0
   int nk;
 };
-
-__device__ __forceinline__ int chunk_pos8(int r, int q) { return q ^ ((r >> 1) & 7); }
 
 // Step kt into stage st; past the last step every load reads zeros, so the wait counts stay the same.
 template <typename T>
@@ -771,20 +836,25 @@ bool i8_words(const I8RowsArgs& a) {       // rows in whole 16-byte words
 
 template <typename TIn, bool UP, bool Words, int Threads, int Pieces, bool Long>
 hipError_t run_i8_rows(const I8RowsArgs& a, hipStream_t st) {
-  dim3 grid = wide_grid((a.R + kIrBlock / Threads - 1) / (kIrBlock / Threads));
+  constexpr int kBlock = ir_block(Threads), kRows = kBlock / Threads;
+  dim3 grid = wide_grid((a.R + kRows - 1) / kRows);
   grid.z = (unsigned)a.G;
-  hipLaunchKernelGGL((i8_rows_kernel<TIn, UP, Words, Threads, Pieces, Long>), grid, dim3(kIrBlock), 0, st, a);
+  hipLaunchKernelGGL((i8_rows_kernel<TIn, UP, Words, Threads, Pieces, Long>), grid, dim3(kBlock), 0, st, a);
   return hipGetLastError();
 }
 
+// Rows from which a wave each is enough: 401 x 1999 fp32 and product 14.9 us with a workgroup each, 16.4 with a wave; 16384 x
+// 2048 47.7 and 43.6.
+constexpr int64_t kIrFill = 4096;
 template <typename TIn, bool UP, bool Words>
 hipError_t run_i8_rows(const I8RowsArgs& a, hipStream_t st) {
   if (a.K <= 512) return run_i8_rows<TIn, UP, Words, 64, 1, false>(a, st);
-  if (a.K <= 2048) return run_i8_rows<TIn, UP, Words, 64, 4, false>(a, st);
+  if (a.K <= 2048)
+    return a.R * a.G < kIrFill ? run_i8_rows<TIn, UP, Words, 256, 1, false>(a, st) : run_i8_rows<TIn, UP, Words, 64, 4, false>(a, st);
   if (a.K <= 4096) return run_i8_rows<TIn, UP, Words, 256, 2, false>(a, st);
-  if (a.K <= 8192) return run_i8_rows<TIn, UP, Words, 256, 4, false>(a, st);
-  if (a.K <= 16384) return run_i8_rows<TIn, UP, Words, 256, 8, false>(a, st);
-  return run_i8_rows<TIn, UP, Words, 256, 4, true>(a, st);
+  if (a.K <= 8192) return run_i8_rows<TIn, UP, Words, 512, 2, false>(a, st);
+  if (a.K <= 16384) return run_i8_rows<TIn, UP, Words, 512, 4, false>(a, st);
+  return run_i8_rows<TIn, UP, Words, 512, 4, true>(a, st);
 }
 
 template <typename TIn>
@@ -811,6 +881,17 @@ hipError_t launch_i8_colsum(const int64_t* offsets, int64_t G, int64_t R, int64_
 }
 
 namespace {
+// Few rows, of as many workgroups as the columns give: 32 columns each read the rows' codes half as often, 16 keep every CU
+// busy below kFewWide columns.  us with 32 and 16:  24 x 4096 x 14336 18.2 and 15.8, 32 x 14336 x 4096 20.9 and 25.4,
+// 16 x 14336 x 4096 18.9 and 21.8, 64 x 14336 x 4096 23.1 and 30.7, 64 x 4096 x 14336 23.6 and 20.9.
+constexpr int64_t kFewWide = 8192;
+using Few16 = FewGeo<1, 1, 8, 4>;
+using Few16Wide = FewGeo<1, 2, 4, 4>;
+using Few32 = FewGeo<2, 1, 8, 3>;
+using Few32Wide = FewGeo<2, 2, 4, 4>;
+using Few64 = FewGeo<4, 1, 8, 2>;
+using Few64Wide = FewGeo<4, 2, 4, 3>;
+using FewGrouped = FewGeo<1, 2, 4, 3>;           // two workgroups a CU
 using I8Tile256 = I8Geo<4, 2, 2, 4, 2, 2>;        // 256 x 256, 8 waves
 using I8Tile256x128 = I8Geo<2, 2, 4, 2, 3, 2>;    // 8 waves
 using I8Tile128 = I8Geo<2, 2, 2, 2, 2, 2>;        // 4 waves, two workgroups per CU
@@ -851,36 +932,49 @@ hipError_t run_i8_tiles(const I8ProductArgs& a, hipStream_t st) {
   return a.out_dt == S3R_BF16 ? run_i8_tiles<T, uint16_t>(a, p, st) : run_i8_tiles<T, float>(a, p, st);
 }
 
-template <int MI, int NJ, int Depth>
+template <typename T>
 hipError_t run_i8_few(const I8ProductArgs& a, hipStream_t st) {
   I8ProdK p = product_params(a);
-  const int64_t mt = row_tiles(a, 16 * MI);
-  p.tiles_n = (int)((a.N + 16 * NJ - 1) / (16 * NJ));
-  if (mt * p.tiles_n * kFewThreads >= kMostItems) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(mt * p.tiles_n)), block(kFewThreads);
-  if (a.out_dt == S3R_BF16) hipLaunchKernelGGL((i8_few_rows_kernel<uint16_t, MI, NJ, Depth>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((i8_few_rows_kernel<float, MI, NJ, Depth>), grid, block, 0, st, p);
+  const int64_t mt = row_tiles(a, 16 * T::MI);
+  p.tiles_n = (int)((a.N + 16 * T::NJ - 1) / (16 * T::NJ));
+  if (mt * p.tiles_n * T::Threads >= kMostItems) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(mt * p.tiles_n)), block(T::Threads);
+  if (a.out_dt == S3R_BF16) hipLaunchKernelGGL((i8_few_rows_kernel<uint16_t, T>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((i8_few_rows_kernel<float, T>), grid, block, 0, st, p);
   return hipGetLastError();
 }
 
+constexpr int64_t kDotFill = 128, kDotRoom = 16 * 256;            // waves of these kernels that a GPU holds
 size_t dot_lds(int rows, int64_t K) { return (size_t)rows * (size_t)((K + kDotPiece - 1) / kDotPiece) * kDotPiece; }
 
-template <typename TIn, bool UP, bool Words, int MT>
+template <typename TIn, bool UP, bool Words, int MT, int R, int Depth>
 hipError_t run_i8_dot(const I8ProductArgs& a, const I8RowsArgs& q, hipStream_t st) {
+  constexpr int kDotWaves = dot_waves(UP), kDotThreads = 64 * kDotWaves;
   I8ProdK p = product_params(a);
-  const int64_t mt = row_tiles(a, MT), groups = (a.N + kDotR - 1) / kDotR;
-  // waves that share weight rows: enough for two workgroups a CU, where K has pieces for them
+  const int64_t mt = row_tiles(a, MT), groups = (a.N + R - 1) / R;
+  // waves that share weight rows: as many as the GPU has room for at once, where K has pieces for them
   int split = 1;
-  while (split < kDotWaves && mt * ((groups * split + kDotWaves - 1) / kDotWaves) < 512 && split * kDotPiece < a.K) split *= 2;
+  while (split < kDotWaves && mt * groups * split * 2 <= kDotRoom && split * kDotPiece < a.K) split *= 2;
   p.tiles_n = (int)((groups * split + kDotWaves - 1) / kDotWaves);
   if (mt * p.tiles_n * kDotThreads >= kMostItems) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(mt * p.tiles_n)), block(kDotThreads);
   const size_t lds = dot_lds(MT, a.K);
   if (a.out_dt == S3R_BF16)
-    hipLaunchKernelGGL((i8_dot_kernel<uint16_t, TIn, UP, Words, MT>), grid, block, lds, st, p, q, split);
+    hipLaunchKernelGGL((i8_dot_kernel<uint16_t, TIn, UP, Words, MT, R, Depth>), grid, block, lds, st, p, q, split);
   else
-    hipLaunchKernelGGL((i8_dot_kernel<float, TIn, UP, Words, MT>), grid, block, lds, st, p, q, split);
+    hipLaunchKernelGGL((i8_dot_kernel<float, TIn, UP, Words, MT, R, Depth>), grid, block, lds, st, p, q, split);
   return hipGetLastError();
+}
+template <typename TIn, bool UP, bool Words, int MT>
+hipError_t run_i8_dot(const I8ProductArgs& a, const I8RowsArgs& q, hipStream_t st) {
+  // one weight row a wave where four would leave half of the CUs without a workgroup
+  const int64_t pieces = (a.K + kDotPiece - 1) / kDotPiece;
+  const int64_t waves = row_tiles(a, MT) * ((a.N + 3) / 4) * std::max<int64_t>(1, pieces / 4);
+  const bool few = waves < kDotFill * dot_waves(UP);
+  // over experts, more workgroups on a CU hide the offsets' and the index' round trips better than deeper loads
+  if (a.G) return few ? run_i8_dot<TIn, UP, Words, MT, 1, 8>(a, q, st) : run_i8_dot<TIn, UP, Words, MT, 4, 2>(a, q, st);
+  if constexpr (UP) return few ? run_i8_dot<TIn, UP, Words, MT, 1, 8>(a, q, st) : run_i8_dot<TIn, UP, Words, MT, 4, 2>(a, q, st);
+  else return few ? run_i8_dot<TIn, UP, Words, MT, 1, 16>(a, q, st) : run_i8_dot<TIn, UP, Words, MT, 4, 4>(a, q, st);
 }
 // Rows of a workgroup: 1, 2 or 4.
 int dot_rows(const I8ProductArgs& a) { return a.M <= 2 ? (int)a.M : 4; }
@@ -902,8 +996,12 @@ constexpr int64_t kDotRows = 4, kDotGrouped = 1;
 bool takes_dots(const I8ProductArgs& a) {
   return mean_rows(a) <= (a.G ? kDotGrouped : kDotRows) && dot_lds(dot_rows(a), a.K) <= kDotLdsMax;
 }
-// Rows per weight, on average, up to which a grouped product takes the few-rows kernel.
-constexpr int64_t kFewGrouped = 16;
+// Rows per weight, on average, up to which a grouped product takes the few-rows kernel.  64 experts, N = 2816, K = 2048: 2 rows
+// 55 us against 60 in 128 x 128 tiles, 8 rows 83 against 88, 16 rows 108 against 94.5.
+constexpr int64_t kFewGrouped = 12;
+// From here on the larger tile: 64 experts, 512 rows each, N = 2816, K = 2048 357 us against 379 in 128 x 128 tiles, 8 experts,
+// 1024 rows each, N = K = 4096 216 against 222; 32 experts, 256 rows each, N = 2048, K = 1408 70.4 both.
+constexpr int64_t kTallGrouped = 384;
 
 template <typename T>
 int64_t tile_count(const I8ProductArgs& a) { return ((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN); }
@@ -914,12 +1012,18 @@ hipError_t launch_i8_product(const I8ProductArgs& a, hipStream_t st) {
   if (takes_dots(a)) return run_i8_dot<void, false, true>(a, I8RowsArgs{}, st);
   if (a.G) {
     const int64_t rows = mean_rows(a);
-    if (rows <= kFewGrouped) return run_i8_few<1, 2, 2>(a, st);
-    return rows < 1024 ? run_i8_tiles<I8Tile128>(a, st) : run_i8_tiles<I8Tile256x128>(a, st);
+    if (rows <= kFewGrouped) return run_i8_few<FewGrouped>(a, st);
+    return rows < kTallGrouped ? run_i8_tiles<I8Tile128>(a, st) : run_i8_tiles<I8Tile256>(a, st);
   }
-  if (a.M <= 16) return run_i8_few<1, 1, 4>(a, st);
-  if (a.M <= 32) return run_i8_few<2, 1, 4>(a, st);
-  if (a.M <= 64) return run_i8_few<4, 1, 2>(a, st);
+  const bool wide = a.N >= kFewWide;
+  if (a.M <= 16) return wide ? run_i8_few<Few16Wide>(a, st) : run_i8_few<Few16>(a, st);
+  if (a.M <= 32) return wide ? run_i8_few<Few32Wide>(a, st) : run_i8_few<Few32>(a, st);
+  if (a.M <= 64) return wide ? run_i8_few<Few64Wide>(a, st) : run_i8_few<Few64>(a, st);
+  // Sums that the few-rows kernel spreads over a workgroup's waves, where a tile would walk K alone: with no more than one
+  // workgroup a CU (two where K is long).  us of it and of tiles: 128 x 1000 x 8000 15.6 and 28.1, 192 x 1283 x 1999 11.3 and
+  // 14.6, 256 x 1283 x 1999 (324 workgroups) 15.2 and 14.0, 96 x 4096 x 14336 (512) 33.1 and 42.8, x 4096 17.5 and 16.8.
+  const int64_t few = (a.M + 63) / 64 * ((a.N + 15) / 16);
+  if (few <= 256 || (few <= 512 && a.K >= 8192)) return run_i8_few<Few64>(a, st);
   if (tile_count<I8Tile256>(a) >= kFillTiles) return run_i8_tiles<I8Tile256>(a, st);
   if (tile_count<I8Tile256x128>(a) >= kFillTiles) return run_i8_tiles<I8Tile256x128>(a, st);
   if (tile_count<I8Tile128>(a) >= kFillTiles) return run_i8_tiles<I8Tile128>(a, st);
@@ -931,6 +1035,8 @@ hipError_t launch_i8_product(const I8ProductArgs& a, hipStream_t st) {
 hipError_t launch_i8_linear(const I8RowsArgs& rows, const I8ProductArgs& prod, hipStream_t st) {
   if (prod.M == 0 || prod.N == 0) return launch_check_offsets(prod.offsets, prod.G, prod.M, prod.flags, st);
   if (takes_dots(prod)) return rows.dtype == S3R_BF16 ? run_i8_dot<uint16_t>(prod, rows, st) : run_i8_dot<float>(prod, rows, st);
+  // (Rounding rows that an index repeats once and gathering their codes in the product's loads: 371 us against 358 for 64
+  // experts' 32768 rows of 16384.)
   const hipError_t e = launch_i8_rows(rows, st);
   return e != hipSuccess ? e : launch_i8_product(prod, st);
 }
