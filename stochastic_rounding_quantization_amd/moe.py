@@ -1,9 +1,9 @@
-"""A mixture-of-experts SwiGLU layer on the library's calls: MXFP4 forward, S3R-EC INT8 backward.
+"""A mixture-of-experts SwiGLU layer on the library's calls: MXFP4 or INT8 forward, S3R-EC INT8 backward.
 
-    python -m stochastic_rounding_quantization_amd.moe [--tokens T] [--experts E] [--top-k K] [--width D] [--ff F]
+    python -m stochastic_rounding_quantization_amd.moe [--tokens T] [--experts E] [--top-k K] [--width D] [--ff F] [--int8] [--update]
 
-runs one training step (forward and backward) and one decoding step of a layer with random weights and prints
-their times.  ``MoeLayer`` is the path itself:
+runs one training step (forward and backward, with --update the weights' orthogonalised update as well) and one decoding
+step of a layer with random weights and prints their times.  ``MoeLayer`` is the path itself:
 
 forward   route the logits; the tokens' rows in the experts' order times the experts' gate and up weights (one
           stacked product, 4-bit weights and rows); silu(gate) * up rounded straight into the down product's
@@ -11,6 +11,8 @@ forward   route the logits; the tokens' rows in the experts' order times the exp
 backward  the sum's gradients; the router's; each projection as the grouped INT8 path takes it (G rounded with
           S3R-EC, dX and dW from one set of codes, up to its 131072 rows); the rows' gradients summed back into the
           tokens.  silu(gate) * up and the joining of the gate and up gradients are torch operations.
+With ``int8`` the forward products are INT8 too, and the backward takes their codes: of the weights, of the tokens' rows
+and of silu(gate) * up, which is then rounded once, straight to INT8.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ import argparse
 from dataclasses import dataclass
 
 from . import s3r
+from .optim import Muon
 
 
 @dataclass
@@ -28,6 +31,7 @@ class Saved:
     routed: s3r.Routed
     gate_up: object        # bf16 [R x 2 F]: the pre-activations, gate columns first
     rows: object           # bf16 [R x D]: the experts' outputs
+    codes: object = None   # an INT8 forward's rows: (of the tokens, of silu(gate) * up)
 
 
 class _Codes:
@@ -71,18 +75,19 @@ def _version(W):
 class MoeLayer:
     """gate_up: bf16 [E x 2F x D] (an expert's gate rows, then its up rows), down: bf16 [E x D x F].
 
-    The layer keeps codes of the weights: MXFP4 from the start, INT8 from the first backward pass.  It follows weights
+    The layer keeps codes of the weights: MXFP4 from the start and INT8 from the first backward pass, or with int8 those of
+    both passes from the start.  It follows weights
     that torch's operations change in place, as an optimizer's step does, or that other tensors replace.  After changes
     that torch does not count (through ``.data``, by a kernel that was given the address, by the replay of a graph, to
     inference tensors), and before the replay of a graph that holds the layer's own calls, call ``weights_changed``.
     """
 
-    def __init__(self, gate_up, down, top_k, **router):
-        self.gate_up, self.down, self.top_k, self.router = gate_up, down, top_k, router
+    def __init__(self, gate_up, down, top_k, *, int8=False, **router):
+        self.gate_up, self.down, self.top_k, self.router, self.int8 = gate_up, down, top_k, router, int8
         self.ff = down.shape[2]
         self._mx = _Codes(_mx_weights), _Codes(_mx_weights)
-        self._int8 = _Codes(_int8_gate_up), _Codes(_int8_weights)
-        for codes, W in zip(self._mx, (gate_up, down)):
+        self._int8 = (_Codes(_int_gate_up), _Codes(_int_weights)) if int8 else (_Codes(_int8_gate_up), _Codes(_int8_weights))
+        for codes, W in zip(self._int8 if int8 else self._mx, (gate_up, down)):
             codes.renew(W)
 
     @property
@@ -100,14 +105,29 @@ class MoeLayer:
                 if codes.weight is not None:
                     codes.renew(W)
 
-    def forward(self, x, logits, bias=None):
-        """(y, Saved) of tokens x [T x D] bf16 with router logits [T x E]."""
+    def forward(self, x, logits, bias=None, *, keep=True):
+        """(y, Saved) of tokens x [T x D] bf16 with router logits [T x E]; keep False: nothing for a backward pass, (y, None)."""
         import torch
         r = s3r.route(logits, self.top_k, bias=bias, **self.router)
+        if self.int8:
+            return self._forward_int8(x, logits, r, keep)
         a = s3r.mx_linear(x, self.mx_gate_up, offsets=r.offsets, index=r.row_slot, index_div=self.top_k)
         rows = s3r.mx_linear(a[:, :self.ff], self.mx_down, up=a[:, self.ff:], offsets=r.offsets,
                              out_dtype=torch.bfloat16)
-        return s3r.combine(rows, r), Saved(x, logits, r, a, rows)
+        return s3r.combine(rows, r), Saved(x, logits, r, a, rows) if keep else None
+
+    def _forward_int8(self, x, logits, r, keep):
+        import torch
+        gate_up, down = self._int8[0].of(self.gate_up).rows, self._int8[1].of(self.down).rows
+        at = dict(offsets=r.offsets, out_dtype=torch.bfloat16)
+        if not keep:
+            a = s3r.int_linear(x, gate_up, index=r.row_slot, index_div=self.top_k, **at)
+            return s3r.combine(s3r.int_linear(a[:, :self.ff], down, up=a[:, self.ff:], **at), r), None
+        xq = s3r.int_rows(x, index=r.row_slot, index_div=self.top_k)
+        a = s3r.int_product(xq, gate_up, **at)
+        hq = s3r.int_rows(a[:, :self.ff], up=a[:, self.ff:])
+        rows = s3r.int_product(hq, down, **at)
+        return s3r.combine(rows, r), Saved(x, logits, r, a, rows, (xq, hq))
 
     def backward(self, saved: Saved, dy, *, seed=0, layer_id=0):
         """(dx f32, dlogits, dgate_up f32, ddown f32) from dy [T x D] bf16."""
@@ -117,16 +137,20 @@ class MoeLayer:
             zeros = dict(dtype=torch.float32, device=dy.device)
             return (torch.zeros(dy.shape, **zeros), torch.empty_like(saved.logits),
                     torch.zeros(self.gate_up.shape, **zeros), torch.zeros(self.down.shape, **zeros))
-        gate_w, up_w = self._int8[0].of(self.gate_up)
-        down_w = self._int8[1].of(self.down)
+        gate_up_w, down_w = self._int8[0].of(self.gate_up), self._int8[1].of(self.down)
+        gate_w, up_w = gate_up_w.parts if self.int8 else gate_up_w
+        down_w = down_w.parts[0] if self.int8 else down_w
         gate, up = saved.gate_up[:, :F].contiguous(), saved.gate_up[:, F:].contiguous()
         drows, dweights = s3r.combine_backward(dy, saved.rows, r)
         dlogits = s3r.route_backward(r, saved.logits, dweights)
-        g = gate.float()
-        hidden = (g * torch.sigmoid(g) * up.float()).to(torch.bfloat16)
-        dh, ddown = _linear_backward(drows, _int8_rows(hidden, r.offsets), down_w, r.offsets, seed, 4 * layer_id)
+        if saved.codes:
+            xq, hq = ((q.Q, q.delta[0], s3r.int_colsum(q.Q, offsets=r.offsets)) for q in saved.codes)
+        else:
+            g = gate.float()
+            hq = _int8_rows((g * torch.sigmoid(g) * up.float()).to(torch.bfloat16), r.offsets)
+            xq = _int8_rows(s3r.dispatch(saved.x, r), r.offsets)
+        dh, ddown = _linear_backward(drows, hq, down_w, r.offsets, seed, 4 * layer_id)
         dgate, dup = s3r.swiglu_backward(dh, gate, up)
-        xq = _int8_rows(s3r.dispatch(saved.x, r), r.offsets)
         dxr, dwg = _linear_backward(dgate, xq, gate_w, r.offsets, seed, 4 * layer_id + 1)
         dxr, dwu = _linear_backward(dup, xq, up_w, r.offsets, seed, 4 * layer_id + 2, into=dxr)
         return s3r.combine(dxr, r, weighted=False), dlogits, torch.cat([dwg, dwu], dim=1), ddown
@@ -157,6 +181,33 @@ def _int8_gate_up(W, codes):
     """Those of the gate rows and those of the up rows."""
     F = W.shape[1] // 2
     return [_int8_weights(w, c) for w, c in zip((W[:, :F], W[:, F:]), codes or (None, None))]
+
+
+@dataclass
+class _IntWeights:
+    """INT8 codes of W [E x N x K] for the forward products, and (codes, s_w, r_W) of equal runs of N for the backward's."""
+    rows: s3r.IntRows
+    parts: list
+
+
+def _int_weights(W, codes, parts=1):
+    (E, N, K), F = W.shape, W.shape[1] // parts
+    w = s3r.int_rows_buffer(N, K, W.device, E) if codes is None else codes.rows
+    s3r.s3r_int_rows(W, w)
+    sums = s3r.int_colsum(w.codes[..., :K].flatten(0, 1), E * parts).unflatten(0, (E, parts))
+    new = [(w.codes[:, i * F:(i + 1) * F, :K], w.delta[:, i * F:(i + 1) * F].contiguous(), sums[:, i].contiguous())
+           for i in range(parts)]
+    if codes is None:
+        return _IntWeights(w, new)
+    for old, part in zip(codes.parts, new):
+        for a, b in zip(old[1:], part[1:]):
+            if a.data_ptr() != b.data_ptr():
+                a.copy_(b)
+    return codes
+
+
+def _int_gate_up(W, codes):
+    return _int_weights(W, codes, 2)
 
 
 def _int8_rows(X, offsets):
@@ -195,20 +246,26 @@ def main(argv=None) -> None:
     p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     for name, value in (("tokens", 16384), ("experts", 64), ("top-k", 2), ("width", 2048), ("ff", 1408), ("steps", 5)):
         p.add_argument("--" + name, type=int, default=value)
+    p.add_argument("--int8", action="store_true", help="INT8 forward products")
+    p.add_argument("--update", action="store_true", help="the weights' update after every training step")
     a = p.parse_args(argv)
     g = torch.Generator("cuda").manual_seed(0)
 
     def normal(*shape, std=1.0):
         return (torch.randn(*shape, generator=g, device="cuda") * std).to(torch.bfloat16)
 
-    layer = MoeLayer(normal(a.experts, 2 * a.ff, a.width, std=0.02), normal(a.experts, a.width, a.ff, std=0.02), a.top_k)
+    layer = MoeLayer(normal(a.experts, 2 * a.ff, a.width, std=0.02), normal(a.experts, a.width, a.ff, std=0.02), a.top_k,
+                     int8=a.int8)
+    update = Muon([layer.gate_up[:, :a.ff], layer.gate_up[:, a.ff:], layer.down], lr=1e-3) if a.update else None
     x, logits, dy = normal(a.tokens, a.width), normal(a.tokens, a.experts), normal(a.tokens, a.width, std=1e-4)
 
     def train():
         y, saved = layer.forward(x, logits)
-        return layer.backward(saved, dy)
+        dx, dlogits, dgate_up, ddown = layer.backward(saved, dy)
+        if update:
+            update.step([dgate_up[:, :a.ff], dgate_up[:, a.ff:], ddown])
 
-    for what, step in (("training step", train), ("decoding step, 16 tokens", lambda: layer.forward(x[:16], logits[:16]))):
+    for what, step in (("training step", train), ("decoding step, 16 tokens", lambda: layer.forward(x[:16], logits[:16], keep=False))):
         step()
         torch.cuda.synchronize()
         t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))

@@ -1,0 +1,175 @@
+"""The INT8 forward, the S3R-EC backward on its codes and the orthogonalised update together, on an MI355X.
+
+The forward pass is equal to the oracle's; the backward takes codes that are equal to those it would make itself; the
+update is within the oracle's bound of it (tests/test_gpu_orth.py).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int8, orth, route
+from stochastic_rounding_quantization_amd import moe, s3r
+from stochastic_rounding_quantization_amd.optim import Muon
+from tests._gpu import DEV, host
+
+pytestmark = pytest.mark.gpu
+T, E, K, D, F = 150, 6, 2, 250, 190
+
+
+def normal(g, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g, device=DEV) * std).to(torch.bfloat16)
+
+
+def f(t):
+    return host(t.float())
+
+
+def make(seed, **kw):
+    g = torch.Generator(DEV).manual_seed(seed)
+    layer = moe.MoeLayer(normal(g, E, 2 * F, D, std=0.1), normal(g, E, D, F, std=0.1), K, int8=True, **kw)
+    return layer, normal(g, T, D), normal(g, T, E), normal(g, T, D, std=1e-2)
+
+
+def test_forward():
+    layer, x, logits, _ = make(1)
+    y, saved = layer.forward(x, logits)
+    ids = route.choose(f(logits), K)
+    offsets, slot_row, row_slot = route.order(ids, E)
+    xq = int8.rows(f(x)[row_slot // K])
+    a, rows = f(saved.gate_up), f(saved.rows)
+    for e in range(E):
+        r = slice(offsets[e], offsets[e + 1])
+        w = int8.rows(f(layer.gate_up[e]))
+        np.testing.assert_array_equal(a[r], int8.product(xq[0][r], xq[1][r], w[0], w[1], bf16=True))
+        h, w = int8.rows(a[r, :F], a[r, F:]), int8.rows(f(layer.down[e]))
+        np.testing.assert_array_equal(rows[r], int8.product(h[0], h[1], w[0], w[1], bf16=True))
+    exp, _ = route.combine(rows, slot_row, route.weights(f(logits), ids))
+    assert (np.abs(f(y) - exp) <= 2.0 ** -8 * np.abs(exp) + 2.0 ** -18 * np.abs(exp).max()).all()
+    for n in (T, 3, 1, 0):                               # what keeps nothing, fused, has the same bits
+        full, nothing = layer.forward(x[:n], logits[:n], keep=False)
+        assert nothing is None and torch.equal(full, layer.forward(x[:n], logits[:n])[0])
+
+
+def test_gradients_point_the_unquantized_way():
+    layer, x, logits, dy = make(2)
+    _, saved = layer.forward(x, logits)
+    grads = layer.backward(saved, dy)
+    xs, ls, wg, wd = (t.float().detach().requires_grad_() for t in (x, logits, layer.gate_up, layer.down))
+    ids = saved.routed.ids.long()
+    p = torch.softmax(ls, 1).gather(1, ids)
+    p = p / p.sum(1, keepdim=True)
+    y = torch.zeros(T, D, device=DEV)
+    for e in range(E):
+        t, j = torch.where(ids == e)
+        a = xs[t] @ wg[e].t()
+        h = torch.nn.functional.silu(a[:, :F]) * a[:, F:]
+        y = y.index_add(0, t, p[t, j, None] * (h @ wd[e].t()))
+    y.backward(dy.float())
+    for got, exp in zip(grads, (xs.grad, ls.grad, wg.grad, wd.grad)):
+        got = got.float()
+        assert got.shape == exp.shape and torch.isfinite(got).all()
+        assert torch.nn.functional.cosine_similarity(got.flatten(), exp.flatten(), dim=0) > 0.95
+
+
+def test_backward_codes_are_its_own():
+    """Weights' codes, steps and column sums as the grouped quantizer makes them; the rows' as well."""
+    layer, x, logits, _ = make(3)
+    _, saved = layer.forward(x, logits)
+    gu, dn = layer._int8[0].of(layer.gate_up), layer._int8[1].of(layer.down)
+    for got, exp in ((gu.parts[0], moe._int8_weights(layer.gate_up[:, :F].contiguous(), None)),
+                     (gu.parts[1], moe._int8_weights(layer.gate_up[:, F:].contiguous(), None)),
+                     (dn.parts[0], moe._int8_weights(layer.down, None))):
+        assert all(torch.equal(a, b) for a, b in zip(got, exp))
+    off = saved.routed.offsets
+    q, s, xs = moe._int8_rows(s3r.dispatch(x, saved.routed), off)
+    mine = saved.codes[0]
+    assert torch.equal(q, mine.Q) and torch.equal(s, mine.delta[0]) and torch.equal(xs, s3r.int_colsum(mine.Q, offsets=off))
+
+
+def same_step(layer, x, logits, dy):
+    other = moe.MoeLayer(layer.gate_up.clone(), layer.down.clone(), layer.top_k, int8=True, **layer.router)
+    out = []
+    for m in (layer, other):
+        y, saved = m.forward(x, logits)
+        out.append((y, *m.backward(saved, dy)))
+    return all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_steps_of_training():
+    """Forward, backward, update, three times: the codes follow the weights, and each update is the formula's."""
+    layer, x, logits, dy = make(4)
+    halves = [layer.gate_up[:, :F], layer.gate_up[:, F:], layer.down]
+    opt = Muon(halves, lr=0.02, decay=0.1)
+    bufs = [0, 0, 0]
+    for _ in range(3):
+        _, saved = layer.forward(x, logits)
+        _, _, dgu, dd = layer.backward(saved, dy)
+        grads = [dgu[:, :F], dgu[:, F:], dd]
+        before = [W.double().cpu().numpy() for W in halves]
+        opt.step(grads)
+        for i, (W, W0, g) in enumerate(zip(halves, before, grads)):
+            g = host(g).astype(np.float64)
+            bufs[i] = 0.95 * bufs[i] + g
+            u = g + 0.95 * bufs[i]
+            scale = 0.02 * max(1.0, W.shape[1] / W.shape[2]) ** 0.5
+            for e in range(E):
+                # u itself is fp32's, and the steps multiply what is lost there as they do their own roundings
+                X, far = orth.newton_schulz(u[e]), orth.newton_schulz(u[e], noise=2.0 ** -20)
+                exp = (1 - 0.02 * 0.1) * W0[e] - scale * X
+                off = np.linalg.norm(host(W[e].double()) - exp)
+                # the sum rounded to bf16, and X: kept to bf16 by the last steps (half a step of X, as its own rounding)
+                assert off <= 2.0 ** -8 * np.linalg.norm(exp) + scale * (4 * np.linalg.norm(far - X) + 2.0 ** -8 * np.linalg.norm(X))
+        assert same_step(layer, x, logits, dy)
+
+
+def test_update_of_plain_matrices_and_refusals():
+    g = torch.Generator(DEV).manual_seed(5)
+    W, dW = normal(g, 70, 30), torch.randn(70, 30, generator=g, device=DEV)
+    V = torch.randn(20, 50, generator=g, device=DEV)
+    opt = Muon([W, V], lr=0.1, momentum=0.0, nesterov=False)
+    W0, V0, version = W.clone(), V.clone(), W._version
+    opt.step([dW, V0.bfloat16()])
+    assert W._version > version
+    ws = s3r.orthogonalize_buffer(W)
+    s3r.s3r_orthogonalize(dW, W0, scale=-0.1 * (70 / 30) ** 0.5, keep=1.0, ws=ws)
+    assert torch.equal(W, W0)
+    V1 = V0.clone()
+    s3r.s3r_orthogonalize(V0.bfloat16().float(), V1, scale=-0.1, keep=1.0, ws=s3r.orthogonalize_buffer(V))
+    assert torch.equal(V, V1)
+    for bad in ([dW], [dW, dW], [dW, V.t()]):
+        with pytest.raises(ValueError):
+            opt.step(bad)
+
+
+def test_linear_layer_forward_backward_update():
+    """A dense layer: the forward's codes and sums are the operands that the backward would make, so its results are too."""
+    g = torch.Generator(DEV).manual_seed(6)
+    X, W, dY = normal(g, 96, 200), normal(g, 130, 200, std=0.1), normal(g, 96, 130, std=1e-2)
+    xq, wq = s3r.int_rows(X), s3r.int_rows(W)
+    y = s3r.int_product(xq, wq)
+    np.testing.assert_array_equal(host(y), int8.product(*int8.rows(f(X))[:2], *int8.rows(f(W))[:2]))
+    q = s3r.quantize(dY, ec=s3r.EC_TWO_WAY, row_scale=xq.delta[0], col_scale=wq.delta[0], rows_per_example=48)
+    dX = s3r.backward_dx(q, wq.Q, s_x=xq.delta[0], r_W=s3r.int_colsum(wq.Q)[0])
+    dW = s3r.backward_dw(q, xq.Q, s_w=wq.delta[0], xs_b=s3r.int_colsum(xq.Q, 2))
+    fx, fw = s3r.forward_operand(X, rows_per_example=48), s3r.forward_operand(W)
+    assert torch.equal(dX, s3r.backward_dx(q, fw.Q, s_x=fx.delta, r_W=fw.code_colsum[0]))
+    assert torch.equal(dW, s3r.backward_dw(q, fx.Q, s_w=fw.delta, xs_b=fx.code_colsum))
+    U = s3r.orthogonalize(dW)
+    exp = orth.newton_schulz(host(dW))
+    assert np.linalg.norm(host(U) - exp) <= 1e-5 * np.linalg.norm(exp)
+
+
+def test_graph_of_a_decoding_step():
+    layer, x, logits, _ = make(7)
+    layer.forward(x[:5], logits[:5], keep=False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, _ = layer.forward(x[:5], logits[:5], keep=False)
+    g = torch.Generator(DEV).manual_seed(8)
+    for _ in range(3):
+        x.copy_(normal(g, T, D))
+        logits.copy_(normal(g, T, E))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, layer.forward(x[:5], logits[:5], keep=False)[0])
