@@ -213,6 +213,37 @@ def test_groups(sizes, K):
     assert torch.equal(got, s3r.int_linear(tokens[perm.long() // 2].contiguous(), w, offsets=offsets, out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("M", [1, 2, 4, 9, 40, 100, 300])
+def test_dense_gathers(M):
+    """An index without groups, with places that name no row (zeros: the bias alone), and behind silu(gate) * up."""
+    X = matrix((37, 500), torch.bfloat16, M) * 0.1
+    w = s3r.int_rows(matrix((70, 250), torch.bfloat16, 3))
+    bias = matrix((1, 70), torch.float32, 4)[0]
+    index = torch.randint(0, 111, (M,), device=DEV).to(torch.int32)
+    index[M // 2] = -5
+    index[M // 3] = 111
+    src = X[(index.long() // 3).clamp(0, 36)].clone()
+    src[[M // 2, M // 3]] = 0
+    gate, up = X[:, :250], X[:, 250:]
+    flags = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = s3r.int_linear(gate, w, index=index, index_div=3, bias=bias, out_dtype=torch.float32, flags=flags)
+    same(y, expected(src[:, :250], w, bias))
+    assert torch.equal(y[M // 2], bias) and int(flags) == 0
+    same(s3r.int_linear(gate, w, up=up, index=index, index_div=3, out_dtype=torch.float32),
+         expected(src[:, :250], w, up=src[:, 250:]))
+
+
+@pytest.mark.parametrize("M", [1, 3, 4])
+def test_longest_rows_of_the_byte_products(M):
+    """Rows past the registers of their workgroup, and past its LDS."""
+    for K in (16384 // (4 if M > 2 else M), 4097, 13000, 15001, 17000, 59000, 60001):
+        for dtype in BOTH:
+            both = matrix((M, 2 * K), dtype, K) * 0.1
+            w = s3r.int_rows(matrix((9, K), torch.bfloat16, 1))
+            same(s3r.int_linear(both[:, :K], w, out_dtype=torch.float32), expected(both[:, :K], w))
+            same(s3r.int_linear(both[:, :K], w, up=both[:, K:], out_dtype=torch.float32), expected(both[:, :K], w, up=both[:, K:]))
+
+
 def test_groups_refuse_bad_offsets():
     w = s3r.int_rows(matrix((70, 20, 64), torch.bfloat16, 1))
     for R in (5, 70, 2000, 90000):

@@ -141,6 +141,30 @@ def test_large(shape):
     assert torch.equal(y, s3r.orthogonalize(G))
 
 
+@pytest.mark.parametrize("shape", [(2, 1500, 2600), (3, 2600, 1100), (2, 2304, 4352)])
+def test_several_large(shape):
+    """Shared tiles of more than one matrix; results in bf16, whose last steps take one plane."""
+    g = torch.Generator(DEV).manual_seed(3)
+    G = torch.randn(*shape, generator=g, device=DEV)
+    y, z = s3r.orthogonalize(G), s3r.orthogonalize(G, out_dtype=torch.bfloat16)
+    for e in range(shape[0]):
+        exp = exact64(G[e])
+        assert float((y[e].double() - exp).norm() / exp.norm()) <= 1e-5
+        # half a step of bf16, and as much again at most for what the last steps leave out
+        assert float((z[e].double() - exp).norm() / exp.norm()) <= 2 * 2.0 ** -8
+
+
+def test_smallest_values_are_kept():
+    """X far below 1 (eps is most of the norm): to 2^-37 absolute, through planes whose values are subnormal fp16."""
+    G = gradient((70, 90), torch.float32, 8, 1e-11)
+    for steps in (1, 3):
+        y = s3r.orthogonalize(G, steps=steps, coeffs=(1.0, 0.0, 0.0), eps=1e-2)
+        exp = host(G.double()) / (np.linalg.norm(host(G.double())) + float(np.float32(1e-2)))
+        off = np.abs(host(y.double()) - exp).max()
+        print(f"{off:.2e}, values to {np.abs(exp).max():.2e}")
+        assert off <= steps * 2.0 ** -37 + 2.0 ** -23 * np.abs(exp).max()
+
+
 def test_many_matrices_in_tiles_of_128():
     G = gradient((20, 300, 700), torch.bfloat16, 9)
     y = s3r.orthogonalize(G, out_dtype=torch.float32)
