@@ -666,39 +666,46 @@ constexpr int kCus = 256, kMostSlots = 3 * kCus;
 constexpr int share_gain(int side) { return side == 256 ? 16 : side == 128 ? 16 : 40; }
 constexpr int kShareLeast = 4;                   // steps of a worker, at least
 
-// The tiles' side.  us for five steps of fp32 results with sides of 32, 64, 128 and 256:
-//   256 x 512       104   110   193          2048 x 2048         2490   834   823  1633
-//   512 x 512       135   143   246          1500 x 4000         2230   845   784  1956
-//   768 x 768       263   172   303          8 x 1024 x 4096     7760  2730  2117  2430
-//   64 x 8192       353   189   296          4096 x 4096           -   5690  4080  4080
-//   16 x 200 x 300  176   118   188          4096 x 14336          -  15900 11100 10370
-//   3 x 1283 x 701  587   290   400          64 x 1408 x 2048      -  20400 15400 16280 (256 x 256 tiles: 1408 padded to 1536)
+// The tiles' sides, of the symmetric products and of B X.  us for five steps of fp32 results:
+//   sides            32    64   128        sides            64   128   128 and 256    256
+//   256 x 512       104   110   193        2048 x 2048     834   823
+//   512 x 512       135   143   246        4 x 2048 x 2048      2242   2136          2363
+//   768 x 768       263   172   303        4096 x 4096    5690  3955   3793          3867
+//   64 x 8192       353   189   296        2 x 3000 x 5000      5169   4777          4885
+//   16 x 200 x 300  176   118   188        2048 x 8192          2104   2085          1888
+//   3 x 1283 x 701  587   290   400        4096 x 14336   15900 10801  10362         10153
 // So the smallest tiles are for matrices that do not fill the GPU with them and whose sums are short, and a larger tile for
-// those that give every CU one of it, the largest where it pads little.
-int tile_side(const OrthArgs& a) {
+// those that give every CU one of it, the largest where it pads little; of the symmetric products' triangle only with
+// long sums, which the workgroups share.
+struct OrthSides { int symmetric, update; };
+OrthSides tile_sides(const OrthArgs& a) {
   const int64_t m = std::min(a.N, a.K), n = std::max(a.N, a.K);
   auto padded = [](int64_t x, int64_t side) { return (x + side - 1) / side * side; };
   auto tiles = [&](int64_t side) { return a.E * (padded(m, side) / side) * (padded(n, side) / side); };
-  if (tiles(32) <= kCus && n <= 1024) return 32;
-  if (tiles(128) < kCus) return 64;
-  return tiles(256) >= kCus && (double)padded(m, 256) * padded(n, 256) <= 1.05 * (double)padded(m, 128) * padded(n, 128) ? 256 : 128;
+  if (tiles(32) <= kCus && n <= 1024) return {32, 32};
+  if (tiles(128) < kCus) return {64, 64};
+  const bool most = tiles(256) >= kCus && (double)padded(m, 256) * padded(n, 256) <= 1.05 * (double)padded(m, 128) * padded(n, 128);
+  return {most && n >= 8000 ? 256 : 128, most ? 256 : 128};
 }
 
 struct OrthLayout {
-  int side, parts;
+  OrthSides sides;
+  int parts;
   int64_t m, n, mp, np;
   size_t part, x, xt[2], A, B, partial, total;
 };
 OrthLayout orth_layout(const OrthArgs& a) {
   OrthLayout l{};
-  l.side = tile_side(a);
+  l.sides = tile_sides(a);
+  const int side = l.sides.symmetric, update = l.sides.update;
   // workgroups for the norm: enough for the GPU, of four runs at least (every workgroup that writes the planes adds them up)
   const int64_t runs = a.N * ((a.K + kNormRun - 1) / kNormRun);
   l.parts = (int)std::max<int64_t>(1, std::min<int64_t>({kNormMost, (2048 + a.E - 1) / a.E, runs / 4}));
   l.m = std::min(a.N, a.K);
   l.n = std::max(a.N, a.K);
-  l.mp = (l.m + l.side - 1) / l.side * l.side;
-  l.np = (l.n + l.side - 1) / l.side * l.side;
+  // (the symmetric products leave what B's sides are padded with past their own tiles as it is: it reaches only padding)
+  l.mp = (l.m + update - 1) / update * update;
+  l.np = (l.n + update - 1) / update * update;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -712,7 +719,8 @@ OrthLayout orth_layout(const OrthArgs& a) {
   l.xt[1] = take(xs);
   l.A = take(as);
   l.B = take(as);
-  if (l.side > 32) l.partial = take((size_t)(l.side == 256 ? kCus : kMostSlots) * 2 * l.side * l.side * 4);
+  // two tiles of every worker's sums, of the larger of both sides' (256 x 256 x 256 CUs against 128 x 128 x 512)
+  if (side > 32) l.partial = take((size_t)(update == 256 ? kCus * 256 * 256 : kMostSlots * side * side) * 2 * 4);
   l.total = at;
   return l;
 }
@@ -746,7 +754,7 @@ hipError_t run_orth_gemm(OrthGemm p, int64_t E, hipStream_t st) {
 }
 
 // Step s, whose operands have P planes; OP: the next one's.
-template <int P, int Side, int OP>
+template <int P, int Side, int Update, int OP>
 hipError_t run_orth_step(const OrthArgs& a, const OrthLayout& l, int s, hipStream_t st) {
   char* ws = (char*)a.ws;
   constexpr int el = el_bytes(P);
@@ -754,14 +762,14 @@ hipError_t run_orth_step(const OrthArgs& a, const OrthLayout& l, int s, hipStrea
   uint8_t *A = (uint8_t*)ws + l.A, *B = (uint8_t*)ws + l.B;
   const uint8_t* xt = (uint8_t*)ws + l.xt[s & 1];
   const int64_t ld_x = l.np * el, ld_t = l.mp * el, xs = l.mp * ld_x, as = l.mp * ld_t;
-  const int tm = (int)(l.mp / Side), tn = (int)(l.np / Side);
+  const int tm = (int)(l.mp / Update), tn = (int)(l.np / Update);
   constexpr int el_step = Side == 32 ? 32 : line_el(P);       // elements of a step of the products' loops
   const int along_n = (int)((l.n + el_step - 1) / el_step), along_m = (int)((l.m + el_step - 1) / el_step);
   OrthGemm p{};
   p.partial = (float*)(ws + l.partial);
   p.a = a.a; p.b = a.b; p.c = a.c;
   p.A = p.B = x; p.lda = p.ldb = ld_x; p.a_stride = p.b_stride = xs;
-  p.tiles_m = p.tiles_n = tm; p.steps = along_n;
+  p.tiles_m = p.tiles_n = (int)((l.m + Side - 1) / Side); p.steps = along_n;
   p.direct = p.turned = A; p.ld_direct = p.ld_turned = ld_t; p.d_stride = p.t_stride = as;
   hipError_t err = run_orth_gemm<P, Side, kEpiGram, P>(p, a.E, st);
   if (err != hipSuccess) return err;
@@ -779,25 +787,25 @@ hipError_t run_orth_step(const OrthArgs& a, const OrthLayout& l, int s, hipStrea
   if (!last) {
     p.direct = (uint8_t*)ws + l.xt[~s & 1]; p.ld_direct = l.mp * el_bytes(OP); p.d_stride = l.np * p.ld_direct;
     p.turned = x; p.ld_turned = l.np * el_bytes(OP); p.t_stride = l.mp * p.ld_turned;
-    return run_orth_gemm<P, Side, kEpiBoth, OP>(p, a.E, st);
+    return run_orth_gemm<P, Update, kEpiBoth, OP>(p, a.E, st);
   }
   p.out = a.out; p.ld_out = a.ld_out; p.out_stride = a.out_stride; p.rows = a.N; p.cols = a.K;
   p.scale = a.scale; p.keep = a.keep;
-  if constexpr (P == 1) return run_orth_gemm<P, Side, kEpiOutBf16, P>(p, a.E, st);
-  else return run_orth_gemm<P, Side, kEpiOutF32, P>(p, a.E, st);
+  if constexpr (P == 1) return run_orth_gemm<P, Update, kEpiOutBf16, P>(p, a.E, st);
+  else return run_orth_gemm<P, Update, kEpiOutF32, P>(p, a.E, st);
 }
 
 // Steps that take both planes.
 int exact_steps(const OrthArgs& a) { return a.out_dt == S3R_BF16 ? std::max(0, a.steps - kLoose) : a.steps; }
 
-template <int Side>
+template <int Side, int Update = Side>
 hipError_t run_orth_steps(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
   const int exact = exact_steps(a);
   hipError_t err = hipSuccess;
   for (int s = 0; s < a.steps && err == hipSuccess; ++s)
-    err = s + 1 < exact || (s < exact && exact == a.steps) ? run_orth_step<2, Side, 2>(a, l, s, st)
-          : s < exact                                       ? run_orth_step<2, Side, 1>(a, l, s, st)
-                                                            : run_orth_step<1, Side, 1>(a, l, s, st);
+    err = s + 1 < exact || (s < exact && exact == a.steps) ? run_orth_step<2, Side, Update, 2>(a, l, s, st)
+          : s < exact                                       ? run_orth_step<2, Side, Update, 1>(a, l, s, st)
+                                                            : run_orth_step<1, Side, Update, 1>(a, l, s, st);
   return err;
 }
 
@@ -827,9 +835,10 @@ hipError_t launch_orthogonalize(const OrthArgs& a, hipStream_t st) {
   const OrthLayout l = orth_layout(a);
   const hipError_t e = a.g_dtype == S3R_BF16 ? run_orth_prepare<uint16_t>(a, l, st) : run_orth_prepare<float>(a, l, st);
   if (e != hipSuccess) return e;
-  if (l.side == 256) return run_orth_steps<256>(a, l, st);
-  if (l.side == 128) return run_orth_steps<128>(a, l, st);
-  return l.side == 64 ? run_orth_steps<64>(a, l, st) : run_orth_steps<32>(a, l, st);
+  if (l.sides.symmetric == 256) return run_orth_steps<256>(a, l, st);
+  if (l.sides.update == 256) return run_orth_steps<128, 256>(a, l, st);
+  if (l.sides.symmetric == 128) return run_orth_steps<128>(a, l, st);
+  return l.sides.symmetric == 64 ? run_orth_steps<64>(a, l, st) : run_orth_steps<32>(a, l, st);
 }
 
 }  // namespace s3r
