@@ -537,7 +537,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_join_kernel(
   for (int j = 0; j < T::NI; ++j)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 8 / T::NI;
   while (first_step(p, w) < s1) {
     v4f v[kBatch][T::NI * 4];
     bool some[kBatch];
@@ -664,7 +664,9 @@ template <int P> struct OrthPick<P, 64, true> : OrthGeo<P, 1, 1, 2, 2, 4, 1> { s
 constexpr int kCus = 256, kMostSlots = 3 * kCus;
 // Steps of a tile that sharing the last tiles has to save to be worth a launch and the way through memory.
 constexpr int share_gain(int side) { return side == 256 ? 16 : side == 128 ? 16 : 40; }
-constexpr int kShareLeast = 4;                   // steps of a worker, at least
+// Steps of a worker, at least, since a tile's join adds its workers' sums in turn.  us for five steps with these and with 4: 64 x 8192
+// 120 and 175 (the join of the one tile 6.5 and 22), 12 x 52 x 2723 158 and 176, 32 x 700 x 1400 1990 and 2056; others within 2 %.
+constexpr int share_least(int side) { return side == 64 ? 16 : 8; }
 
 // The tiles' sides, of the symmetric products and of B X.  us for five steps of fp32 results:
 //   sides            32    64   128        sides            64   128   128 and 256    256
@@ -675,16 +677,18 @@ constexpr int kShareLeast = 4;                   // steps of a worker, at least
 //   16 x 200 x 300  176   118   188        2048 x 8192          2104   2085          1888
 //   3 x 1283 x 701  587   290   400        4096 x 14336   15900 10801  10362         10153
 // So the smallest tiles are for matrices that do not fill the GPU with them and whose sums are short, and a larger tile for
-// those that give every CU one of it, the largest where it pads little; of the symmetric products' triangle only with
-// long sums, which the workgroups share.
+// those that give every CU one of it and that it pads no more than 1.4 times as far (12 x 52 x 2723, twice as far: 158 us in
+// tiles of 64, 247 of 128), the largest where it pads little; of the symmetric products' triangle only with long sums, which
+// the workgroups share.
 struct OrthSides { int symmetric, update; };
 OrthSides tile_sides(const OrthArgs& a) {
   const int64_t m = std::min(a.N, a.K), n = std::max(a.N, a.K);
   auto padded = [](int64_t x, int64_t side) { return (x + side - 1) / side * side; };
   auto tiles = [&](int64_t side) { return a.E * (padded(m, side) / side) * (padded(n, side) / side); };
   if (tiles(32) <= kCus && n <= 1024) return {32, 32};
-  if (tiles(128) < kCus) return {64, 64};
-  const bool most = tiles(256) >= kCus && (double)padded(m, 256) * padded(n, 256) <= 1.05 * (double)padded(m, 128) * padded(n, 128);
+  auto area = [&](int64_t side) { return (double)padded(m, side) * padded(n, side); };
+  if (tiles(128) < kCus || area(128) > 1.4 * area(64)) return {64, 64};
+  const bool most = tiles(256) >= kCus && area(256) <= 1.05 * area(128);
   return {most && n >= 8000 ? 256 : 128, most ? 256 : 128};
 }
 
@@ -733,7 +737,7 @@ hipError_t run_orth_tiles(OrthGemm p, int64_t tiles, hipStream_t st) {
     hipLaunchKernelGGL((orth_few_kernel<T::P, EPI, OP>), dim3((unsigned)tiles), dim3(T::Threads), 0, st, p);
   } else {
     const int rest = (int)(tiles % kSlots);
-    const int64_t workers = std::min<int64_t>(kSlots, (int64_t)rest * p.steps / kShareLeast);
+    const int64_t workers = std::min<int64_t>(kSlots, (int64_t)rest * p.steps / share_least(T::BM));
     const bool share = workers > rest && (double)p.steps * (1.0 - (double)rest / workers) >= share_gain(T::BM);
     p.rest = share ? rest : 0;
     p.workers = share ? (int)workers : 0;
