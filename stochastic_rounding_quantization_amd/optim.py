@@ -22,7 +22,6 @@ class Muon:
         self.weights, self.lr, self.momentum, self.nesterov, self.decay = list(weights), lr, momentum, nesterov, decay
         self.steps, self.coeffs, self.eps = steps, coeffs, eps
         self.buffers = [torch.zeros(W.shape, dtype=torch.float32, device=W.device) for W in self.weights]
-        self._ws = None
 
     def step(self, grads):
         """One update from the gradients, in the weights' order (f32 or bf16, of their shapes)."""
@@ -30,24 +29,14 @@ class Muon:
         grads = list(grads)
         if len(grads) != len(self.weights) or any(g.shape != W.shape for g, W in zip(grads, self.weights)):
             raise ValueError("a gradient for every weight, of its shape")
-        for W, g, buf in zip(self.weights, grads, self.buffers):
-            g = g.float()
-            buf.mul_(self.momentum).add_(g)
-            u = g.add(buf, alpha=self.momentum) if self.nesterov else buf
-            N, K = W.shape[-2:]
-            s3r.s3r_orthogonalize(u, W, steps=self.steps, coeffs=self.coeffs, eps=self.eps,
-                                  scale=-self.lr * max(1.0, N / max(K, 1)) ** 0.5, keep=1.0 - self.lr * self.decay,
-                                  ws=self._workspace(W))
-            if not W.is_inference():
-                torch.autograd.graph.increment_version(W)
-
-    def _workspace(self, W):
-        """One workspace for all weights, which are updated one after another on one stream."""
-        import torch
-        n = s3r.s3r_orthogonalize_workspace(s3r.orth_desc(W.shape))
-        if self._ws is None or self._ws.numel() < n or torch.cuda.is_current_stream_capturing():
-            ws = s3r.orthogonalize_buffer(W)
-            if torch.cuda.is_current_stream_capturing():
-                return ws
-            self._ws = ws
-        return self._ws
+        with torch.no_grad():
+            for W, g, buf in zip(self.weights, grads, self.buffers):
+                g = g.float()
+                buf.mul_(self.momentum).add_(g)
+                u = g.add(buf, alpha=self.momentum) if self.nesterov else buf
+                N, K = W.shape[-2:]
+                s3r.s3r_orthogonalize(u, W, steps=self.steps, coeffs=self.coeffs, eps=self.eps,
+                                      scale=-self.lr * max(1.0, N / max(K, 1)) ** 0.5, keep=1.0 - self.lr * self.decay,
+                                      ws=s3r.orthogonalize_buffer(W))
+                if not W.is_inference():
+                    torch.autograd.graph.increment_version(W)

@@ -173,3 +173,33 @@ def test_graph_of_a_decoding_step():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, layer.forward(x[:5], logits[:5], keep=False)[0])
+
+
+def test_optimizer_steps_on_other_streams_captured_and_without_a_graph():
+    g = torch.Generator(DEV).manual_seed(7)
+    shapes = ((3, 40, 90), (200, 70), (1, 1))
+    start = [torch.randn(*s, generator=g, device=DEV) for s in shapes]
+    grads = [torch.randn(*s, generator=g, device=DEV) for s in shapes]
+    plain = [W.clone() for W in start]
+    opt = Muon(plain, lr=0.1)
+    seen = []
+    for _ in range(4):
+        opt.step(grads)
+        seen.append([W.clone() for W in plain])
+
+    other = [W.clone() for W in start]
+    opt = Muon(other, lr=0.1)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        opt.step([(2 * x.clone().requires_grad_()) / 2 for x in grads])
+    torch.cuda.synchronize()
+    assert all(torch.equal(W, V) for W, V in zip(other, seen[0])) and not any(b.requires_grad for b in opt.buffers)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step(grads)
+    for after in seen[1:]:
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(W, V) for W, V in zip(other, after))
+        torch.randn(300, 300, device=DEV) @ torch.randn(300, 300, device=DEV)
