@@ -737,10 +737,10 @@ int s3r_int_linear(const s3r_int_pdesc* desc, const void* A, const void* up, int
  * The products keep values of 22 bits (two fp16 planes) and sum in fp32; results agree with
  * fp64 to about 1e-5 of the matrix (in the Frobenius norm) or better.  With S3R_BF16 results
  * the last two steps keep 11 bits, which adds less to the matrix than its rounding to bf16.
- * X itself is kept to 2^-37, so matrices far
- * smaller than eps lose digits, and below 2^-37 eps give zeros.  Every singular value of every X, A and b A +
- * c A A + a I has to stay below 16 (the usual coefficients stay below 4); past that, results
- * are infinite or NaN.  A matrix with a non-finite element gives NaN throughout; one of
+ * X itself is kept to 2^-37, so matrices far smaller than eps lose digits, and below
+ * 2^-37 eps give zeros.  Every singular value of every X, A and b A + c A A + a I has to
+ * stay below 16 (the usual coefficients stay below 4); past that, results are infinite or
+ * NaN.  A matrix with a non-finite element gives NaN throughout; one of
  * zeros gives zeros.
  *   groups  matrices of rows x cols (0 .. 65535; rows and cols below 2^20), g_stride and
  *           out_stride elements apart;
