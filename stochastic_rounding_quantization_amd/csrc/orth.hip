@@ -676,7 +676,7 @@ constexpr int share_least(int side) { return side == 64 ? 16 : 8; }
 //   256 x 512       104   110   193        2048 x 2048     834   823
 //   512 x 512       135   143   246        4 x 2048 x 2048      2242   2136          2363
 //   768 x 768       263   172   303        4096 x 4096    5690  3955   3793          3867
-//   64 x 8192       353   189   296        2 x 3000 x 5000      5169   4777          4885
+//   64 x 8192       353   120   296        2 x 3000 x 5000      5169   4777          4885
 //   16 x 200 x 300  176   118   188        2048 x 8192          2104   2085          1888
 //   3 x 1283 x 701  587   290   400        4096 x 14336   15900 10801  10362         10153
 // So the smallest tiles are for matrices that do not fill the GPU with them and whose sums are short, and a larger tile for
