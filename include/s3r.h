@@ -734,9 +734,9 @@ int s3r_int_linear(const s3r_int_pdesc* desc, const void* A, const void* up, int
  *   `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X    (X^T X from the other side
  *                   where G has more rows than columns: the same values)
  *   out <- keep out + scale X   (keep 0: out is not read; fp32, rounded once for S3R_BF16)
- * The products keep values of 22 bits (two fp16 planes) and sum in fp32; results agree with
- * fp64 to about 1e-5 of the matrix (in the Frobenius norm) or better.  With S3R_BF16 results
- * the last two steps keep 11 bits, which adds less to the matrix than its rounding to bf16.
+ * The products keep values of 22 bits (two fp16 planes) and sum in fp32, whatever the results'
+ * type; results agree with fp64 to about 1e-5 of the matrix (in the Frobenius norm) or better,
+ * before their rounding to S3R_BF16.
  * X itself is kept to 2^-37, so matrices far smaller than eps lose digits, and below
  * 2^-37 eps give zeros.  Every singular value of every X, A and b A + c A A + a I has to
  * stay below 16 (the usual coefficients stay below 4); past that, results are infinite or

@@ -6,11 +6,12 @@
 // products carry about 22 bits: a value is kept as two fp16 planes, v 2^12 = h + l with h and l the nearest fp16, and
 // a product is h h' + h l' + l h' in fp32 (three matrix instructions; l l' is below 2^-22).  The factor 2^12 keeps l of
 // entries down to 2^-15 normal; entries up to 16 fit, and the singular values of X, A and B stay below 4.
-// Where the result is bf16, the last kLoose steps take h alone (a third of the work): what they lose, a few 2^-12 of the
-// matrix, is multiplied by one step at most and stays well below bf16's own rounding (up to 2^-8 of a value).
+// A result in bf16 takes both planes in every step too: h alone loses 2^-12 of X, which fills the directions that a gradient of
+// few tokens leaves empty, and one step multiplies it there by a (two steps: by a^2, 0.0023 - 0.0029 of the matrix at ranks 1 to
+// 64, where rounding to bf16 is 0.0017).
 //
-// Layout: with two planes the 32 consecutive elements of a row that make a line of 128 bytes are 64 bytes of h and 64 of
-// l; with one, a line is 64 elements.  A step of the products' loops is a line of every row.  Every operand has its
+// Layout: the 32 consecutive elements of a row that make a line of 128 bytes are 64 bytes of h and 64 of l.  A step of the
+// products' loops is a line of every row.  Every operand has its
 // contraction along the rows: X for X X^T, X^T for B X, A and B as they are (symmetric).  So a step keeps X both ways,
 // written by one epilogue.  The matrix cores keep fp16's subnormals, so small h and l lose nothing more.  Sides are padded to whole tiles with zeros, which are all in the workspace: the products read
 // and write no edge.
@@ -28,9 +29,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr float kUp = 4096.f, kDown = 1.f / 4096.f;      // the planes' scale
 constexpr int kLine = 128;                               // bytes of a line
-constexpr int kLoose = 2;
-__host__ __device__ constexpr int line_el(int planes) { return 64 / planes; }
-__host__ __device__ constexpr int el_bytes(int planes) { return 2 * planes; }
+constexpr int kLineEl = 32, kElBytes = 4;                // elements of a line, bytes of an element
 
 // ------------------------------------------------------------------ norm ----
 // Sum of squares in fp64: no square of an fp32 number leaves its range.  A matrix is cut into runs of 2048 elements of a
@@ -92,12 +91,10 @@ __device__ __forceinline__ void split(float v, _Float16& h, _Float16& l) {
   h = (_Float16)v;
   l = (_Float16)(v - (float)h);
 }
-template <int P>
 __device__ __forceinline__ int64_t plane_off(int64_t row, int64_t col, int64_t ld) {        // ld in bytes
-  return P == 1 ? row * ld + col * 2 : row * ld + (col >> 5) * kLine + (col & 31) * 2;
+  return row * ld + (col >> 5) * kLine + (col & 31) * 2;
 }
 // 8 consecutive values (col a multiple of 8) to their planes.
-template <int P>
 __device__ __forceinline__ void store_planes(uint8_t* p, const float (&v)[8]) {
   v8h h, l;
 #pragma unroll
@@ -108,14 +105,14 @@ __device__ __forceinline__ void store_planes(uint8_t* p, const float (&v)[8]) {
     l[i] = y;
   }
   *reinterpret_cast<v8h*>(p) = h;
-  if constexpr (P == 2) *reinterpret_cast<v8h*>(p + kLine / 2) = l;
+  *reinterpret_cast<v8h*>(p + kLine / 2) = l;
 }
 
 // G, scaled, to its planes as it lies (`own`) and transposed (`other`), 64 x 64 elements a workgroup, zeros past its
 // edges.  rows x cols: the padded sizes (multiples of 32), G's orientation.  Bound by its bytes: 4 read and 8 written an
 // element, 4096 x 14336 146 - 149 us, 4.7 TB/s.
 constexpr int kPrepThreads = 256, kPrepTile = 64;
-template <typename TIn, int P>
+template <typename TIn>
 __global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, const double* part, int parts, uint8_t* own,
                                                                     int64_t own_stride, uint8_t* other, int64_t other_stride,
                                                                     int64_t rows, int64_t cols) {
@@ -156,22 +153,22 @@ __global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, 
       v[x] = tile[q][p + x] * f;
       w[x] = tile[p + x][q] * f;
     }
-    if (r0 + q < rows && c0 + p < cols) store_planes<P>(own + plane_off<P>(r0 + q, c0 + p, cols * el_bytes(P)), v);
-    if (c0 + q < cols && r0 + p < rows) store_planes<P>(other + plane_off<P>(c0 + q, r0 + p, rows * el_bytes(P)), w);
+    if (r0 + q < rows && c0 + p < cols) store_planes(own + plane_off(r0 + q, c0 + p, cols * kElBytes), v);
+    if (c0 + q < cols && r0 + p < rows) store_planes(other + plane_off(c0 + q, r0 + p, rows * kElBytes), w);
   }
 }
 
 // -------------------------------------------------------------- products ----
 // Tiles of BM x BN, WM x WN waves of (32 MI) x (32 NI) each, operands staged through LDS by buffer-load DMA in a ring
 // of NS steps of one line of every row, the eight 16-byte chunks of a line at permuted places (chunk q of row r at
-// q ^ ((r >> 1) & 7): a quarter-wave's reads hit 16 bank groups).  P: planes; a line has Parts parts of 16 elements.
+// q ^ ((r >> 1) & 7): a quarter-wave's reads hit 16 bank groups).  A line has kParts parts of 16 elements.
 // v_mfma_f32_32x32x16_f16: lane l holds row or column l % 32, elements 8 (l / 32) .. + 7 of 16; result register r is
 // row (r / 4) 8 + (l / 32) 4 + r % 4, column l % 32.
-// Bound by the matrix cores and power.  B X of 4096 x 14336 in tiles of 256, two planes: 1.10 - 1.15 ms, 1.3 PFLOP/s counting the
-// three products; one plane 460 - 518 us, 0.93 - 1.05.  64 x 1408 x 2048 in tiles of 128: 1445 us, 1.08 PFLOP/s.
-template <int P_, int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
+// Bound by the matrix cores and power.  B X of 4096 x 14336 in tiles of 256: 1.10 - 1.15 ms, 1.3 PFLOP/s counting the three
+// products.  64 x 1408 x 2048 in tiles of 128: 1445 us, 1.08 PFLOP/s.
+constexpr int kParts = kLineEl / 16, kPlanes = 2, kProducts = 3;
+template <int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
 struct OrthGeo {
-  static constexpr int P = P_, Parts = line_el(P) / 16, Products = P == 2 ? 3 : 1;
   static constexpr int WavesPerSimd = WavesPerSimd_;
   static constexpr int MI = MI_, NI = NI_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr int Waves = WM * WN, Threads = 64 * Waves;
@@ -231,7 +228,7 @@ __device__ __forceinline__ void orth_load(const OrthSrc<T>& s, uint8_t* st, int 
 }
 
 template <typename T>
-struct OrthFrag { v8h a[T::P][T::MI], b[T::P][T::NI]; };
+struct OrthFrag { v8h a[kPlanes][T::MI], b[kPlanes][T::NI]; };
 
 // The fragments of part h (16 elements) of a stage.
 template <typename T>
@@ -243,13 +240,13 @@ __device__ __forceinline__ void orth_frag(const uint8_t* st, int h, OrthFrag<T>&
   for (int i = 0; i < T::MI; ++i) {
     const int r = (wm * T::MI + i) * 32 + r31;
 #pragma unroll
-    for (int l = 0; l < T::P; ++l) f.a[l][i] = *reinterpret_cast<const v8h*>(st + r * kLine + (chunk_place(r, c + 4 * l) << 4));
+    for (int l = 0; l < kPlanes; ++l) f.a[l][i] = *reinterpret_cast<const v8h*>(st + r * kLine + (chunk_place(r, c + 4 * l) << 4));
   }
 #pragma unroll
   for (int j = 0; j < T::NI; ++j) {
     const int r = (wn * T::NI + j) * 32 + r31;
 #pragma unroll
-    for (int l = 0; l < T::P; ++l)
+    for (int l = 0; l < kPlanes; ++l)
       f.b[l][j] = *reinterpret_cast<const v8h*>(st + T::OffB + r * kLine + (chunk_place(r, c + 4 * l) << 4));
   }
 }
@@ -257,7 +254,7 @@ __device__ __forceinline__ void orth_frag(const uint8_t* st, int h, OrthFrag<T>&
 template <typename T>
 __device__ __forceinline__ void orth_mfma(const OrthFrag<T>& f, v16f (&acc)[T::MI][T::NI]) {
 #pragma unroll
-  for (int l = T::Products - 1; l >= 0; --l)             // l h', h l', h h'
+  for (int l = kProducts - 1; l >= 0; --l)               // l h', h l', h h'
 #pragma unroll
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
@@ -268,14 +265,14 @@ __device__ __forceinline__ void orth_mfma(const OrthFrag<T>& f, v16f (&acc)[T::M
 // Part h of step kt on stage S, its fragments in f: its products cover the reads of part h + 1.
 template <typename T, int S, int H>
 __device__ __forceinline__ void orth_parts(OrthFrag<T>& f, v16f (&acc)[T::MI][T::NI]) {
-  if constexpr (H + 1 < T::Parts) {
-    constexpr int kReads = T::P * (T::MI + T::NI), kProducts = T::Products * T::MI * T::NI;
+  if constexpr (H + 1 < kParts) {
+    constexpr int kReads = kPlanes * (T::MI + T::NI), kMfmas = kProducts * T::MI * T::NI;
     OrthFrag<T> n;
     orth_frag<T>(ring<T, S>(), H + 1, n);
     orth_mfma<T>(f, acc);
 #pragma unroll
-    for (int x = 0; x < kProducts; ++x) {
-      __builtin_amdgcn_sched_group_barrier(kSgDsRead, (kReads + kProducts - 1) / kProducts, 0);
+    for (int x = 0; x < kMfmas; ++x) {
+      __builtin_amdgcn_sched_group_barrier(kSgDsRead, (kReads + kMfmas - 1) / kMfmas, 0);
       __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -288,7 +285,7 @@ __device__ __forceinline__ void orth_parts(OrthFrag<T>& f, v16f (&acc)[T::MI][T:
 // stage has arrived; the barrier there makes step kt + 1 visible and retires stage S, which takes step kt + NS.
 template <typename T, int S>
 __device__ __forceinline__ void orth_step(const OrthSrc<T>& src, int kt, OrthFrag<T>& f, v16f (&acc)[T::MI][T::NI]) {
-  constexpr int kReads = T::P * (T::MI + T::NI), kProducts = T::Products * T::MI * T::NI;
+  constexpr int kReads = kPlanes * (T::MI + T::NI), kMfmas = kProducts * T::MI * T::NI;
   orth_parts<T, S, 0>(f, acc);
   S3R_WAIT_VM(T::Loads * (T::NS - 2));
   S3R_WAIT_LGKM0();
@@ -299,10 +296,10 @@ __device__ __forceinline__ void orth_step(const OrthSrc<T>& src, int kt, OrthFra
   orth_frag<T>(ring<T, (S + 1) % T::NS>(), 0, n);
   orth_mfma<T>(f, acc);
 #pragma unroll
-  for (int x = 0; x < kProducts; ++x) {
+  for (int x = 0; x < kMfmas; ++x) {
     __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kSgDsRead, (kReads + kProducts - 1) / kProducts, 0);
-    __builtin_amdgcn_sched_group_barrier(kSgVmem, (T::Loads + kProducts - 1) / kProducts, 0);
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, (kReads + kMfmas - 1) / kMfmas, 0);
+    __builtin_amdgcn_sched_group_barrier(kSgVmem, (T::Loads + kMfmas - 1) / kMfmas, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
   f = n;
@@ -396,9 +393,9 @@ __device__ __forceinline__ void store_one(uint16_t* p, float v, float keep) {
 }
 
 // A tile's results, 32 rows of a wave at a time through its own part of the (free) ring, read from there along the rows
-// and along the columns.  OP: the results' planes (of kEpiBoth, those of the next step).
+// and along the columns.
 // This does rows 32 i .. of every wave.
-template <typename T, OrthEpi EPI, int OP>
+template <typename T, OrthEpi EPI>
 __device__ __forceinline__ void orth_store_rows(const OrthGemm& p, const OrthTile& t, int i, const v16f (&acc)[T::NI]) {
   constexpr int kBuf = 32 * T::EpiLd * 4;
   constexpr int kPer = T::StageBytes / kBuf;                  // waves' buffers in one stage
@@ -432,13 +429,13 @@ __device__ __forceinline__ void orth_store_rows(const OrthGemm& p, const OrthTil
       for (int y = 0; y < 4; ++y) v[x + y] = w[y];
     }
     if constexpr (EPI == kEpiPoly) {
-      const uint8_t* at = p.addend + t.e * p.d_stride + plane_off<T::P>(row, col, p.ld_direct);
-      v8h h[T::P];
+      const uint8_t* at = p.addend + t.e * p.d_stride + plane_off(row, col, p.ld_direct);
+      v8h h[kPlanes];
 #pragma unroll
-      for (int l = 0; l < T::P; ++l) h[l] = *reinterpret_cast<const v8h*>(at + l * (kLine / 2));
+      for (int l = 0; l < kPlanes; ++l) h[l] = *reinterpret_cast<const v8h*>(at + l * (kLine / 2));
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        v[x] = p.c * v[x] + p.b * (T::P == 2 ? (float)h[0][x] + (float)h[T::P - 1][x] : (float)h[0][x]);
+        v[x] = p.c * v[x] + p.b * ((float)h[0][x] + (float)h[1][x]);
         if (row == col + x) v[x] += p.a * kUp;
       }
       if (turned) {
@@ -456,7 +453,7 @@ __device__ __forceinline__ void orth_store_rows(const OrthGemm& p, const OrthTil
           if (col + x < p.cols) store_one(out + x, v[x] * (kDown * p.scale), p.keep);
       }
     } else {
-      store_planes<OP>(p.direct + t.e * p.d_stride + plane_off<OP>(row, col, p.ld_direct), v);
+      store_planes(p.direct + t.e * p.d_stride + plane_off(row, col, p.ld_direct), v);
     }
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -468,17 +465,17 @@ __device__ __forceinline__ void orth_store_rows(const OrthGemm& p, const OrthTil
         float v[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) v[x] = buf[(rr + x) * T::EpiLd + cc];
-        store_planes<OP>(p.turned + t.e * p.t_stride + plane_off<OP>(col0 + cc, row0 + rr, p.ld_turned), v);
+        store_planes(p.turned + t.e * p.t_stride + plane_off(col0 + cc, row0 + rr, p.ld_turned), v);
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <typename T, OrthEpi EPI, int OP>
+template <typename T, OrthEpi EPI>
 __device__ __forceinline__ void orth_store(const OrthGemm& p, const OrthTile& t, const v16f (&acc)[T::MI][T::NI]) {
 #pragma unroll
-  for (int i = 0; i < T::MI; ++i) orth_store_rows<T, EPI, OP>(p, t, i, acc[i]);
+  for (int i = 0; i < T::MI; ++i) orth_store_rows<T, EPI>(p, t, i, acc[i]);
 }
 
 // The steps of all shared tiles in a row, dealt to the workers evenly: worker w has [first(w), first(w + 1)).
@@ -489,7 +486,7 @@ __device__ __forceinline__ int64_t first_step(const OrthGemm& p, int w) {
 // Workgroups 0 .. full - 1 take a tile each.  What does not fill the GPU evenly, the last `rest` tiles, is dealt to
 // `workers` workgroups by steps: each leaves the sums of its part of a tile in memory (at most two tiles are partly its
 // own; tiles wholly its own go straight to their results) and orth_join_kernel adds them up, in the order of K.
-template <typename T, OrthEpi EPI, int OP>
+template <typename T, OrthEpi EPI>
 __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_gemm_kernel(OrthGemm p) {
   v16f acc[T::MI][T::NI];
   const bool whole = (int)blockIdx.x < p.full;
@@ -505,7 +502,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_gemm_kernel(
     const OrthTile t = orth_tile<EPI>(p, whole ? tile : p.full + tile);
     orth_sums<T>(p, t, k0, k1, acc);
     if (k1 - k0 == p.steps) {
-      orth_store<T, EPI, OP>(p, t, acc);
+      orth_store<T, EPI>(p, t, acc);
     } else {
       v4f* part = reinterpret_cast<v4f*>(p.partial) + (int64_t)(2 * w + slot) * (T::BM * T::BN / 4) + threadIdx.x;
       slot = 1;
@@ -527,7 +524,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_gemm_kernel(
 
 // Tile blockIdx.x of the shared ones, rows 32 blockIdx.y .. of every wave (a workgroup for a whole tile of 256 took twice
 // as long, few of them adding up in a row what many had left).  136 tiles of 256, 256 workers: 36 - 41 us.
-template <typename T, OrthEpi EPI, int OP>
+template <typename T, OrthEpi EPI>
 __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_join_kernel(OrthGemm p) {
   const int tile = blockIdx.x, i = blockIdx.y;
   const int64_t s0 = (int64_t)tile * p.steps, s1 = s0 + p.steps, all = (int64_t)p.rest * p.steps;
@@ -564,7 +561,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_join_kernel(
 #pragma unroll
           for (int y = 0; y < 4; ++y) acc[x / 4][4 * (x % 4) + y] += v[q][x][y];
   }
-  orth_store_rows<T, EPI, OP>(p, orth_tile<EPI>(p, p.full + tile), i, acc);
+  orth_store_rows<T, EPI>(p, orth_tile<EPI>(p, p.full + tile), i, acc);
 }
 
 // Small matrices: 32 x 32 results a workgroup, whose eight waves deal the contraction's steps of 32 elements among them and
@@ -572,10 +569,10 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_join_kernel(
 // a product of a few hundred elements is one round of loads.  Bound by latency: 256 x 512 4.9 - 5.8 us a product.
 constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64, kFewLd = 36;
 
-template <int P, OrthEpi EPI, int OP>
+template <OrthEpi EPI>
 __global__ __launch_bounds__(kFewThreads) void orth_few_kernel(OrthGemm p) {
   __shared__ float part[kFewWaves][32 * kFewLd];
-  constexpr int kBatch = 4 / P, kProducts = P == 2 ? 3 : 1;
+  constexpr int kBatch = 2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const OrthTile t = orth_tile<EPI>(p, blockIdx.x);
   const int r31 = lane & 31, half = (lane >> 5) * 16;
@@ -585,7 +582,7 @@ __global__ __launch_bounds__(kFewThreads) void orth_few_kernel(OrthGemm p) {
 #pragma unroll
   for (int r = 0; r < 16; ++r) acc[r] = 0.f;
   for (int k0 = wave; k0 < p.steps; k0 += kFewWaves * kBatch) {
-    v8h a[kBatch][2][P], b[kBatch][2][P];
+    v8h a[kBatch][2][kPlanes], b[kBatch][2][kPlanes];
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       const int k = k0 + q * kFewWaves;
@@ -593,9 +590,9 @@ __global__ __launch_bounds__(kFewThreads) void orth_few_kernel(OrthGemm p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int l = 0; l < P; ++l) {
-            a[q][h][l] = *reinterpret_cast<const v8h*>(A + (int64_t)k * 64 * P + h * 32 + l * 64);
-            b[q][h][l] = *reinterpret_cast<const v8h*>(B + (int64_t)k * 64 * P + h * 32 + l * 64);
+          for (int l = 0; l < kPlanes; ++l) {
+            a[q][h][l] = *reinterpret_cast<const v8h*>(A + (int64_t)k * kLine + h * 32 + l * 64);
+            b[q][h][l] = *reinterpret_cast<const v8h*>(B + (int64_t)k * kLine + h * 32 + l * 64);
           }
       }
     }
@@ -629,13 +626,13 @@ __global__ __launch_bounds__(kFewThreads) void orth_few_kernel(OrthGemm p) {
   const int64_t row = (int64_t)t.tm * 32 + (turned ? minor : major), col = (int64_t)t.tn * 32 + (turned ? major : minor);
   if constexpr (EPI == kEpiPoly) {
     // transposed: the addend's other triangle, which its product wrote as a copy of this one
-    const uint8_t* add = p.addend + t.e * p.d_stride + (turned ? plane_off<P>(col, row, p.ld_direct) : plane_off<P>(row, col, p.ld_direct));
-    v8h h[P];
+    const uint8_t* add = p.addend + t.e * p.d_stride + (turned ? plane_off(col, row, p.ld_direct) : plane_off(row, col, p.ld_direct));
+    v8h h[kPlanes];
 #pragma unroll
-    for (int l = 0; l < P; ++l) h[l] = *reinterpret_cast<const v8h*>(add + l * (kLine / 2));
+    for (int l = 0; l < kPlanes; ++l) h[l] = *reinterpret_cast<const v8h*>(add + l * (kLine / 2));
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      v[x] = p.c * v[x] + p.b * (P == 2 ? (float)h[0][x] + (float)h[P - 1][x] : (float)h[0][x]);
+      v[x] = p.c * v[x] + p.b * ((float)h[0][x] + (float)h[1][x]);
       if (!turned && row == col + x) v[x] += p.a * kUp;
     }
   }
@@ -648,22 +645,22 @@ __global__ __launch_bounds__(kFewThreads) void orth_few_kernel(OrthGemm p) {
         if (col + x < p.cols) store_one(out + x, v[x] * (kDown * p.scale), p.keep);
     }
   } else if (turned) {
-    store_planes<OP>(p.turned + t.e * p.t_stride + plane_off<OP>(col, row, p.ld_turned), v);
+    store_planes(p.turned + t.e * p.t_stride + plane_off(col, row, p.ld_turned), v);
   } else {
-    store_planes<OP>(p.direct + t.e * p.d_stride + plane_off<OP>(row, col, p.ld_direct), v);
+    store_planes(p.direct + t.e * p.d_stride + plane_off(row, col, p.ld_direct), v);
   }
 }
 
 // -------------------------------------------------------------- launches ----
 // Tiles by their side, in two forms: with a deep ring, one workgroup a CU, for products that have no more tiles than that (a
 // step then takes the loads' latency over the ring's depth), and with several workgroups a CU.
-template <int P_, int Side, bool Deep> struct OrthPick;
-template <int P_, bool Deep> struct OrthPick<P_, 32, Deep> { static constexpr int P = P_, BM = 32, Threads = kFewThreads, PerCu = 1; };
-template <int P, bool Deep> struct OrthPick<P, 256, Deep> : OrthGeo<P, 4, 2, 2, 4, 2, 2> { static constexpr int PerCu = 1; };
-template <int P> struct OrthPick<P, 128, false> : OrthGeo<P, 2, 2, 2, 2, 2, 2> { static constexpr int PerCu = 2; };
-template <int P> struct OrthPick<P, 128, true> : OrthGeo<P, 2, 2, 2, 2, 4, 1> { static constexpr int PerCu = 1; };
-template <int P> struct OrthPick<P, 64, false> : OrthGeo<P, 1, 1, 2, 2, 3, 3> { static constexpr int PerCu = 3; };
-template <int P> struct OrthPick<P, 64, true> : OrthGeo<P, 1, 1, 2, 2, 4, 1> { static constexpr int PerCu = 1; };
+template <int Side, bool Deep> struct OrthPick;
+template <bool Deep> struct OrthPick<32, Deep> { static constexpr int BM = 32, Threads = kFewThreads, PerCu = 1; };
+template <bool Deep> struct OrthPick<256, Deep> : OrthGeo<4, 2, 2, 4, 2, 2> { static constexpr int PerCu = 1; };
+template <> struct OrthPick<128, false> : OrthGeo<2, 2, 2, 2, 2, 2> { static constexpr int PerCu = 2; };
+template <> struct OrthPick<128, true> : OrthGeo<2, 2, 2, 2, 4, 1> { static constexpr int PerCu = 1; };
+template <> struct OrthPick<64, false> : OrthGeo<1, 1, 2, 2, 3, 3> { static constexpr int PerCu = 3; };
+template <> struct OrthPick<64, true> : OrthGeo<1, 1, 2, 2, 4, 1> { static constexpr int PerCu = 1; };
 constexpr int kCus = 256, kMostSlots = 3 * kCus;
 // Steps of a tile that sharing the last tiles has to save to be worth a launch and the way through memory.
 constexpr int share_gain(int side) { return side == 256 ? 16 : side == 128 ? 16 : 40; }
@@ -719,7 +716,7 @@ OrthLayout orth_layout(const OrthArgs& a) {
     at += align_up(bytes, 256);
     return here;
   };
-  const size_t xs = (size_t)a.E * l.mp * l.np * el_bytes(2), as = (size_t)a.E * l.mp * l.mp * el_bytes(2);
+  const size_t xs = (size_t)a.E * l.mp * l.np * kElBytes, as = (size_t)a.E * l.mp * l.mp * kElBytes;
   l.part = take((size_t)a.E * l.parts * 8);
   l.x = take(xs);
   l.xt[0] = take(xs);
@@ -732,12 +729,12 @@ OrthLayout orth_layout(const OrthArgs& a) {
   return l;
 }
 
-template <typename T, OrthEpi EPI, int OP>
+template <typename T, OrthEpi EPI>
 hipError_t run_orth_tiles(OrthGemm p, int64_t tiles, hipStream_t st) {
   constexpr int kSlots = kCus * T::PerCu;
   if (tiles >= (int64_t)1 << 31 || (tiles + kSlots) * T::Threads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   if constexpr (T::BM == 32) {
-    hipLaunchKernelGGL((orth_few_kernel<T::P, EPI, OP>), dim3((unsigned)tiles), dim3(T::Threads), 0, st, p);
+    hipLaunchKernelGGL((orth_few_kernel<EPI>), dim3((unsigned)tiles), dim3(T::Threads), 0, st, p);
   } else {
     const int rest = (int)(tiles % kSlots);
     const int64_t workers = std::min<int64_t>(kSlots, (int64_t)rest * p.steps / share_least(T::BM));
@@ -745,46 +742,43 @@ hipError_t run_orth_tiles(OrthGemm p, int64_t tiles, hipStream_t st) {
     p.rest = share ? rest : 0;
     p.workers = share ? (int)workers : 0;
     p.full = (int)tiles - p.rest;
-    hipLaunchKernelGGL((orth_gemm_kernel<T, EPI, OP>), dim3((unsigned)(p.full + p.workers)), dim3(T::Threads), 0, st, p);
-    if (share) hipLaunchKernelGGL((orth_join_kernel<T, EPI, OP>), dim3((unsigned)p.rest, T::MI), dim3(T::Threads), 0, st, p);
+    hipLaunchKernelGGL((orth_gemm_kernel<T, EPI>), dim3((unsigned)(p.full + p.workers)), dim3(T::Threads), 0, st, p);
+    if (share) hipLaunchKernelGGL((orth_join_kernel<T, EPI>), dim3((unsigned)p.rest, T::MI), dim3(T::Threads), 0, st, p);
   }
   return hipGetLastError();
 }
 
-template <int P, int Side, OrthEpi EPI, int OP>
+template <int Side, OrthEpi EPI>
 hipError_t run_orth_gemm(OrthGemm p, int64_t E, hipStream_t st) {
   p.per_matrix = symmetric(EPI) ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
   const int64_t tiles = E * p.per_matrix;
   if constexpr (Side == 64 || Side == 128)
-    if (tiles <= kCus) return run_orth_tiles<OrthPick<P, Side, true>, EPI, OP>(p, tiles, st);
-  return run_orth_tiles<OrthPick<P, Side, false>, EPI, OP>(p, tiles, st);
+    if (tiles <= kCus) return run_orth_tiles<OrthPick<Side, true>, EPI>(p, tiles, st);
+  return run_orth_tiles<OrthPick<Side, false>, EPI>(p, tiles, st);
 }
 
-// Step s, whose operands have P planes; OP: the next one's.
-template <int P, int Side, int Update, int OP>
+template <int Side, int Update>
 hipError_t run_orth_step(const OrthArgs& a, const OrthLayout& l, int s, hipStream_t st) {
   char* ws = (char*)a.ws;
-  constexpr int el = el_bytes(P);
   uint8_t* x = (uint8_t*)ws + l.x;
   uint8_t *A = (uint8_t*)ws + l.A, *B = (uint8_t*)ws + l.B;
   const uint8_t* xt = (uint8_t*)ws + l.xt[s & 1];
-  const int64_t ld_x = l.np * el, ld_t = l.mp * el, xs = l.mp * ld_x, as = l.mp * ld_t;
+  const int64_t ld_x = l.np * kElBytes, ld_t = l.mp * kElBytes, xs = l.mp * ld_x, as = l.mp * ld_t;
   const int tm = (int)(l.mp / Update), tn = (int)(l.np / Update);
-  constexpr int el_step = Side == 32 ? 32 : line_el(P);       // elements of a step of the products' loops
-  const int along_n = (int)((l.n + el_step - 1) / el_step), along_m = (int)((l.m + el_step - 1) / el_step);
+  const int along_n = (int)((l.n + kLineEl - 1) / kLineEl), along_m = (int)((l.m + kLineEl - 1) / kLineEl);      // lines
   OrthGemm p{};
   p.partial = (float*)(ws + l.partial);
   p.a = a.a; p.b = a.b; p.c = a.c;
   p.A = p.B = x; p.lda = p.ldb = ld_x; p.a_stride = p.b_stride = xs;
   p.tiles_m = p.tiles_n = (int)((l.m + Side - 1) / Side); p.steps = along_n;
   p.direct = p.turned = A; p.ld_direct = p.ld_turned = ld_t; p.d_stride = p.t_stride = as;
-  hipError_t err = run_orth_gemm<P, Side, kEpiGram, P>(p, a.E, st);
+  hipError_t err = run_orth_gemm<Side, kEpiGram>(p, a.E, st);
   if (err != hipSuccess) return err;
   p.A = p.B = A; p.lda = p.ldb = ld_t; p.a_stride = p.b_stride = as;
   p.steps = along_m;
   p.addend = A;
   p.direct = p.turned = B;
-  if ((err = run_orth_gemm<P, Side, kEpiPoly, P>(p, a.E, st)) != hipSuccess) return err;
+  if ((err = run_orth_gemm<Side, kEpiPoly>(p, a.E, st)) != hipSuccess) return err;
   const bool last = s + 1 == a.steps, wide = a.N <= a.K;
   const uint8_t* first = last && wide ? B : xt;             // the tiles' rows: m's or n's
   p.A = first; p.a_stride = first == xt ? xs : as;
@@ -792,46 +786,34 @@ hipError_t run_orth_step(const OrthArgs& a, const OrthLayout& l, int s, hipStrea
   p.lda = p.ldb = ld_t;
   p.tiles_m = first == xt ? tn : tm; p.tiles_n = first == xt ? tm : tn;
   if (!last) {
-    p.direct = (uint8_t*)ws + l.xt[~s & 1]; p.ld_direct = l.mp * el_bytes(OP); p.d_stride = l.np * p.ld_direct;
-    p.turned = x; p.ld_turned = l.np * el_bytes(OP); p.t_stride = l.mp * p.ld_turned;
-    return run_orth_gemm<P, Update, kEpiBoth, OP>(p, a.E, st);
+    p.direct = (uint8_t*)ws + l.xt[~s & 1]; p.ld_direct = ld_t; p.d_stride = xs;
+    p.turned = x; p.ld_turned = ld_x; p.t_stride = xs;
+    return run_orth_gemm<Update, kEpiBoth>(p, a.E, st);
   }
   p.out = a.out; p.ld_out = a.ld_out; p.out_stride = a.out_stride; p.rows = a.N; p.cols = a.K;
   p.scale = a.scale; p.keep = a.keep;
-  if constexpr (P == 1) return run_orth_gemm<P, Update, kEpiOutBf16, P>(p, a.E, st);
-  else return run_orth_gemm<P, Update, kEpiOutF32, P>(p, a.E, st);
+  return a.out_dt == S3R_BF16 ? run_orth_gemm<Update, kEpiOutBf16>(p, a.E, st) : run_orth_gemm<Update, kEpiOutF32>(p, a.E, st);
 }
-
-// Steps that take both planes.
-int exact_steps(const OrthArgs& a) { return a.out_dt == S3R_BF16 ? std::max(0, a.steps - kLoose) : a.steps; }
 
 template <int Side, int Update = Side>
 hipError_t run_orth_steps(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
-  const int exact = exact_steps(a);
   hipError_t err = hipSuccess;
-  for (int s = 0; s < a.steps && err == hipSuccess; ++s)
-    err = s + 1 < exact || (s < exact && exact == a.steps) ? run_orth_step<2, Side, Update, 2>(a, l, s, st)
-          : s < exact                                       ? run_orth_step<2, Side, Update, 1>(a, l, s, st)
-                                                            : run_orth_step<1, Side, Update, 1>(a, l, s, st);
+  for (int s = 0; s < a.steps && err == hipSuccess; ++s) err = run_orth_step<Side, Update>(a, l, s, st);
   return err;
 }
 
-template <typename TIn, int P>
+template <typename TIn>
 hipError_t run_orth_prepare(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
   char* ws = (char*)a.ws;
   double* part = (double*)(ws + l.part);
   hipLaunchKernelGGL((orth_norm_kernel<TIn>), dim3((unsigned)l.parts, (unsigned)a.E), dim3(kNormThreads), 0, st, a, part, l.parts);
   const bool wide = a.N <= a.K;
-  const int64_t rows = wide ? l.mp : l.np, cols = wide ? l.np : l.mp, xs = l.mp * l.np * el_bytes(P);
+  const int64_t rows = wide ? l.mp : l.np, cols = wide ? l.np : l.mp, xs = l.mp * l.np * kElBytes;
   uint8_t *x = (uint8_t*)ws + l.x, *xt = (uint8_t*)ws + l.xt[0];
-  hipLaunchKernelGGL((orth_prepare_kernel<TIn, P>),
+  hipLaunchKernelGGL((orth_prepare_kernel<TIn>),
                      dim3((unsigned)((cols + kPrepTile - 1) / kPrepTile), (unsigned)((rows + kPrepTile - 1) / kPrepTile), (unsigned)a.E),
                      dim3(kPrepThreads), 0, st, a, part, l.parts, wide ? x : xt, xs, wide ? xt : x, xs, rows, cols);
   return hipGetLastError();
-}
-template <typename TIn>
-hipError_t run_orth_prepare(const OrthArgs& a, const OrthLayout& l, hipStream_t st) {
-  return exact_steps(a) > 0 ? run_orth_prepare<TIn, 2>(a, l, st) : run_orth_prepare<TIn, 1>(a, l, st);
 }
 }  // namespace
 

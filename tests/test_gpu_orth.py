@@ -207,3 +207,92 @@ def test_streams_and_graph_replays():
         step()
         torch.cuda.synchronize()
         assert torch.equal(got[0], out) and torch.equal(got[1], long_out)
+
+
+def low_rank(shape, rank, seed=0, size=1e-4):
+    r = np.random.default_rng(seed)
+    return torch.from_numpy(r.normal(size=(shape[0], rank)) @ r.normal(size=(rank, shape[1])) * size).float().to(DEV)
+
+
+def lost(shape, steps=5, a=orth.COEFFS[0]):
+    """How far a result may be off where G has few directions, of its norm: (2^-22 + 2^-24 sqrt(n / 16)) a^steps, n the longer side.
+
+    A value is kept to 2^-24 of itself and a product leaves out 2^-24 of its terms.  A sum of n terms of one sign is made by
+    3 n / 16 additions to a running sum that grows evenly, each off by 2^-24 of it at most and 2^-24 / sqrt(3) in the mean, all
+    together 2^-24 sqrt(n / 16) / sqrt(3).  What falls into a direction that G lacks is multiplied there by a in every later
+    step, as A's errors are in their own: by sqrt((b + c)^2 + c^2) = 3.4 for singular values near 1, which is a.  The later steps' own
+    errors are a, a^2, .. times smaller: 1 / (1 - 1 / a) = 1.41 altogether, and 1.41 / sqrt(3) < 1.  The result's norm
+    is that of G's directions, whose values stay near 1.
+    """
+    return (2.0 ** -22 + 2.0 ** -24 * np.sqrt(max(shape) / 16)) * max(1.0, a) ** steps
+
+
+def bf16_rounding(exp):
+    """How far the nearest bf16 values of a matrix are from it."""
+    return np.linalg.norm(host(torch.from_numpy(exp).bfloat16().double()) - exp)
+
+
+@pytest.mark.parametrize("rank", [1, 4, 8, 64, None])
+@pytest.mark.parametrize("shape", [(100, 90), (256, 512), (700, 300)])
+def test_results_in_bf16_lose_their_rounding_only(shape, rank):
+    """A value's distance from its nearest bf16 moves by no more than the value does: off by d before the rounding, the
+    result is off by the exact result's own rounding and 2 d at most."""
+    for steps, coeffs in ((5, orth.COEFFS), (1, orth.COEFFS), (2, orth.COEFFS), (3, (1.5, -0.5, 0.0)), (6, (1.875, -1.25, 0.375))):
+        G = gradient(shape, torch.float32, 3) if rank is None else low_rank(shape, rank)
+        exp = orth.newton_schulz(host(G.double()), steps=steps, coeffs=coeffs)
+        for H in (G, G.t().contiguous()):
+            y = s3r.orthogonalize(H, steps=steps, coeffs=coeffs, out_dtype=torch.bfloat16)
+            y = host((y if H is G else y.t()).double())
+            most = bf16_rounding(exp) + 2 * lost(shape, steps, coeffs[0]) * np.linalg.norm(exp)
+            off = np.linalg.norm(y - exp)
+            print(f"{shape} rank {rank}, {steps} steps: {off / np.linalg.norm(exp):.2e} of {most / np.linalg.norm(exp):.2e}")
+            assert off <= most
+
+
+def into(G, out_dtype):
+    """The steps' result through a workspace of NaN (every plane's fp16, every sum): what is read has been written."""
+    out, ws = torch.empty(G.shape, dtype=out_dtype, device=DEV), s3r.orthogonalize_buffer(G)
+    s3r.s3r_orthogonalize(G, out, ws=ws.fill_(255))
+    return out
+
+
+@pytest.mark.parametrize("shape", [*SHAPES, (3, 70, 133), (5, 130, 50), (20, 300, 700), (2, 1500, 2600)])
+def test_workspaces_that_hold_anything(shape):
+    G = gradient(shape, torch.float32, 6)
+    for out in BOTH:
+        assert torch.equal(into(G, out), s3r.orthogonalize(G, out_dtype=out))
+
+
+# tiles of 256 for both kinds of product (and sides that fill none), of 128 and 256 (padding of X that no product writes)
+WIDEST = [(4090, 8190), (8190, 4090), (2, 2300, 8100), (5220, 6100), (6100, 5220)]
+
+
+@pytest.mark.parametrize("shape", WIDEST)
+def test_widest_tiles(shape):
+    """Errors as of the other large matrices, and the result's own rounding in bf16 (twice the error at most beside it)."""
+    g = torch.Generator(DEV).manual_seed(4)
+    G = torch.randn(*shape, generator=g, device=DEV)
+    y, z = into(G, torch.float32), into(G, torch.bfloat16)
+    for e in range(shape[0] if len(shape) == 3 else 1):
+        at = (lambda t: t[e]) if len(shape) == 3 else (lambda t: t)
+        exp = exact64(at(G))
+        n = float(exp.norm())
+        off, off16 = float((at(y).double() - exp).norm()), float((at(z).double() - exp).norm())
+        rounding = float((exp.bfloat16().double() - exp).norm())
+        print(f"{shape}: {off / n:.2e}, bf16 {off16 / n:.2e} of {rounding / n:.2e}")
+        assert off <= 1e-5 * n and off16 <= rounding + 2e-5 * n
+
+
+@pytest.mark.parametrize("rank", [1, 8])
+@pytest.mark.parametrize("shape", [(2048, 1408), (1500, 4000), (4090, 8190), (5220, 6100)])
+def test_low_rank_in_large_tiles(shape, rank):
+    """Rounding errors fill the directions that G leaves empty, and each step multiplies them by a."""
+    g = torch.Generator(DEV).manual_seed(rank)
+    G = torch.randn(shape[0], rank, generator=g, device=DEV) @ torch.randn(rank, shape[1], generator=g, device=DEV) * 1e-4
+    exp = exact64(G)
+    most = lost(shape) * float(exp.norm())
+    off = float((into(G, torch.float32).double() - exp).norm())
+    off16 = float((into(G, torch.bfloat16).double() - exp).norm())
+    rounding = float((exp.bfloat16().double() - exp).norm())
+    print(f"{shape} rank {rank}: {off / float(exp.norm()):.2e} of {lost(shape):.2e}, bf16 {off16 / float(exp.norm()):.2e} of {rounding / float(exp.norm()):.2e}")
+    assert off <= most and off16 <= rounding + 2 * most
