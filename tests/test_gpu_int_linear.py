@@ -339,3 +339,45 @@ def test_streams_and_graph_replays():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (*outs, sums)))
+
+
+# few rows of wide weights (to 16, 32 and 64 rows, 8192 columns and more), and tiles of 128 x 64
+WIDE = [(5, 8195, 300), (9, 8192, 64), (16, 14336, 129), (24, 8192, 1000), (32, 8449, 127), (33, 8200, 129), (50, 9001, 700),
+        (64, 14336, 260), (512, 3100, 200), (500, 3333, 1029)]
+
+
+@pytest.mark.parametrize("out", BOTH)
+@pytest.mark.parametrize("M, N, K", WIDE)
+def test_wide_products(M, N, K, out):
+    test_products(M, N, K, out)
+
+
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("K", [256, 2043])
+@pytest.mark.parametrize("N", [9, 8200])
+def test_byte_products_of_every_kind(N, K, dtype, up):
+    """One and four weight rows a wave; dense and over experts; rows rounded by the product itself and before it."""
+    def both(rows, seed):
+        x = matrix((rows, 2 * K), dtype, seed) * 0.1
+        return (x[:, :K].contiguous(), x[:, K:].contiguous()) if up else (x[:, :K].contiguous(), None)
+
+    def results(x, u, w, **kw):
+        yield s3r.int_linear(x, w, up=u, out_dtype=torch.float32, **kw)
+        yield s3r.int_product(s3r.int_rows(x, up=u), w, **kw)
+    w = s3r.int_rows(matrix((N, K), torch.bfloat16, N))
+    for M in (1, 2, 3, 4):
+        x, u = both(M, M)
+        exp = expected(x, w, up=u)
+        for y in results(x, u, w):
+            same(y, exp)
+        same(s3r.int_linear(x, w, up=u, out_dtype=torch.bfloat16), expected(x, w, up=u, out=torch.bfloat16))
+    sizes = [2, 0, 1, 0, 1]
+    E, R, offsets = len(sizes), sum(sizes), grouped(sizes)
+    N = min(N, 1700)                                # four rows a wave from here on, with the groups' five row tiles
+    w = s3r.int_rows(matrix((E, N, K), torch.bfloat16, N + 1))
+    x, u = both(R, 9)
+    o = offsets.tolist()
+    exp = np.concatenate([expected(x[a:b], w, up=None if u is None else u[a:b], group=e) for e, (a, b) in enumerate(zip(o, o[1:]))])
+    for y in results(x, u, w, offsets=offsets):
+        same(y, exp)
