@@ -296,3 +296,15 @@ def test_low_rank_in_large_tiles(shape, rank):
     rounding = float((exp.bfloat16().double() - exp).norm())
     print(f"{shape} rank {rank}: {off / float(exp.norm()):.2e} of {lost(shape):.2e}, bf16 {off16 / float(exp.norm()):.2e} of {rounding / float(exp.norm()):.2e}")
     assert off <= most and off16 <= rounding + 2 * most
+
+
+@pytest.mark.parametrize("rank", [1, 2, 8, 32, None])
+@pytest.mark.parametrize("steps", [3, 5, 8, 10])
+def test_errors_by_rank_and_steps(rank, steps):
+    for shape in ((256, 512), (64, 90), (300, 129)):
+        G = gradient(shape, torch.float32, steps) if rank is None else low_rank(shape, rank, steps)
+        exp = orth.newton_schulz(host(G.double()), steps=steps)
+        off = np.linalg.norm(host(s3r.orthogonalize(G, steps=steps).double()) - exp) / np.linalg.norm(exp)
+        most = lost(shape, steps)
+        print(f"{shape} rank {rank}, {steps} steps: {off:.2e} of {most:.2e}")
+        assert off <= most
