@@ -73,14 +73,21 @@ __global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(OrthArgs a, dou
 }
 
 // 2^12 / (norm + eps) from the partial sums, by one wave; NaN for a matrix that is not finite, 0 for one of zeros
-// without an eps.
-__device__ __forceinline__ float orth_factor(const double* part, int parts, float eps) {
+// without an eps.  As power * rest: norms from 2^-149 on put the factor up to 2^161, which fp32 does not hold, and those
+// above 2^138 among its subnormal numbers; the power of two brings elements so small or large to where the rest is normal.
+struct OrthFactor {
+  float power, rest;
+  __device__ __forceinline__ float operator()(float v) const { return v * power * rest; }
+};
+__device__ __forceinline__ OrthFactor orth_factor(const double* part, int parts, float eps) {
   double s = 0.;
   for (int i = threadIdx.x & 63; i < parts; i += 64) s += part[i];
   s = wave_sum(s);
   const double d = sqrt(s) + (double)eps;
-  if (!(s < __builtin_inf())) return __builtin_nanf("");
-  return d > 0. ? (float)((double)kUp / d) : 0.f;
+  if (!(s < __builtin_inf())) return OrthFactor{1.f, __builtin_nanf("")};
+  const double f = d > 0. ? (double)kUp / d : 0.;
+  const float power = f > 0x1p100 ? 0x1p40f : f < 0x1p-100 ? 0x1p-40f : 1.f;
+  return OrthFactor{power, (float)(f / (double)power)};
 }
 
 // ---------------------------------------------------------------- planes ----
@@ -117,10 +124,10 @@ __global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, 
                                                                     int64_t own_stride, uint8_t* other, int64_t other_stride,
                                                                     int64_t rows, int64_t cols) {
   __shared__ float tile[kPrepTile][kPrepTile + 1];
-  __shared__ float factor;
+  __shared__ OrthFactor factor;
   const int64_t e = blockIdx.z;
   if (threadIdx.x < 64) {
-    const float f = orth_factor(part + e * parts, parts, a.eps);
+    const OrthFactor f = orth_factor(part + e * parts, parts, a.eps);
     if (threadIdx.x == 0) factor = f;
   }
   const TIn* G = (const TIn*)a.G + e * a.g_stride;
@@ -142,7 +149,7 @@ __global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, 
     for (int y = 0; y < 8; ++y) tile[q0 + x * (kPrepThreads / kPer)][p0 + y] = v.w[y];
   }
   __syncthreads();
-  const float f = factor;
+  const OrthFactor f = factor;
   own += e * own_stride;
   other += e * other_stride;
   for (int i = threadIdx.x; i < kPrepTile * kPrepTile / 8; i += kPrepThreads) {
@@ -150,8 +157,8 @@ __global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, 
     float v[8], w[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      v[x] = tile[q][p + x] * f;
-      w[x] = tile[p + x][q] * f;
+      v[x] = f(tile[q][p + x]);
+      w[x] = f(tile[p + x][q]);
     }
     if (r0 + q < rows && c0 + p < cols) store_planes(own + plane_off(r0 + q, c0 + p, cols * kElBytes), v);
     if (c0 + q < cols && r0 + p < rows) store_planes(other + plane_off(c0 + q, r0 + p, rows * kElBytes), w);

@@ -308,3 +308,13 @@ def test_errors_by_rank_and_steps(rank, steps):
         most = lost(shape, steps)
         print(f"{shape} rank {rank}, {steps} steps: {off:.2e} of {most:.2e}")
         assert off <= most
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("size", [1e-35, 1e-37, 1e-38, 1e-40, 2e37])
+def test_norms_whose_inverse_leaves_fp32(size, dtype):
+    """Without an eps every matrix is brought to norm 1, down to subnormal elements and up to the largest."""
+    for shape in ((70, 90), (90, 70), (1, 1), (300, 700)):
+        G = gradient(shape, dtype, 3, size)
+        assert bool(G.isfinite().all()) and bool(G.any())
+        check(s3r.orthogonalize(G, eps=0.0, out_dtype=torch.float32), G, eps=0.0)
