@@ -81,3 +81,106 @@ def test_oracle_follows_the_singular_values():
             s = a * s + b * s ** 3 + c * s ** 5
         np.testing.assert_allclose(orth.newton_schulz(G), (U * s) @ V, atol=1e-12)
     assert not orth.newton_schulz(np.zeros((3, 4)), eps=0.0).any()
+
+
+@pytest.fixture
+def launches(L, monkeypatch):
+    """The binding up to the launch, which does nothing here: (u, W, arguments) of each."""
+    import torch
+    seen, real = [], s3r.s3r_orthogonalize
+
+    def call(u, W, **kw):
+        seen.append((u.clone(), W, kw))
+        assert real(u, W, **kw, stream=0, rc_only=True) in PAST
+        W.add_(1)                                  # as if written
+    monkeypatch.setattr(s3r, "s3r_orthogonalize", call)
+
+    def aligned(nbytes, device):
+        ws = torch.empty(nbytes + 256, dtype=torch.uint8)
+        return ws[-ws.data_ptr() % 256:][:nbytes]
+    monkeypatch.setattr(s3r, "_scratch", aligned)
+    return seen
+
+
+def muon(nesterov=True, **kw):
+    import torch
+    from stochastic_rounding_quantization_amd.optim import Muon
+    g = torch.Generator().manual_seed(1)
+    weights = [torch.randn(4, 6, generator=g), torch.randn(2, 5, 3, generator=g).bfloat16()]
+    grads = [torch.randn(W.shape, generator=g) for W in weights]
+    return Muon(weights, lr=0.1, nesterov=nesterov, **kw), weights, grads
+
+
+def column_major(t):
+    return t.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+
+@pytest.mark.parametrize("nesterov", [True, False])
+def test_optimizer_takes_gradients_of_any_layout(launches, nesterov):
+    """A column-major gradient, a bf16 one and a slice give the update of the same numbers in a row."""
+    import torch
+    for other in (column_major, lambda g: torch.cat([g, g], -1)[..., :g.shape[-1]], lambda g: g):
+        for dtype in (torch.float32, torch.bfloat16):
+            del launches[:]
+            for layout in (lambda g: g, other):
+                opt, _, grads = muon(nesterov)
+                for _ in range(2):
+                    opt.step([layout(g.to(dtype)) for g in grads])
+                launches.append(opt.buffers)
+            half = len(launches) // 2
+            assert half == 5
+            for a, b in zip(launches[:4], launches[half:-1]):
+                assert torch.equal(a[0], b[0]) and a[0].is_contiguous()
+            assert all(torch.equal(a, b) for a, b in zip(launches[4], launches[-1]))
+    opt, _, grads = muon(nesterov)
+    del launches[:]
+    opt.step(grads)
+    opt.step([2 * g for g in grads])
+    buf = 0.95 * grads[0] + 2 * grads[0]
+    torch.testing.assert_close(launches[2][0], 2 * grads[0] + 0.95 * buf if nesterov else buf)
+
+
+@pytest.mark.parametrize("what", ["gradient shape", "one gradient", "gradient device", "rate", "decay", "steps",
+                                  "coefficients", "weight layout", "weight type", "weight device"])
+def test_refused_steps_change_nothing(launches, what):
+    import torch
+    opt, weights, grads = muon()
+    opt.step(grads)
+    del launches[:]
+    before = [t.clone() for t in (*weights, *opt.buffers)]
+    if what == "gradient shape":
+        grads[1] = grads[1].transpose(1, 2)
+    elif what == "one gradient":
+        grads.pop()
+    elif what == "gradient device":
+        grads[1] = grads[1].to("meta")
+    elif what == "rate":
+        opt.lr = NAN
+    elif what == "decay":
+        opt.decay = 1e300
+    elif what == "steps":
+        opt.steps = 65
+    elif what == "coefficients":
+        opt.coeffs = (1.0, INF, 0.0)
+    elif what == "weight layout":
+        opt.weights[1] = column_major(weights[1])
+    elif what == "weight type":
+        opt.weights[1] = weights[1].half()
+    else:
+        opt.weights[1] = weights[1].to("meta")
+    with pytest.raises(ValueError):
+        opt.step(grads)
+    assert not launches
+    assert all(torch.equal(a, b) for a, b in zip(before, (*weights, *opt.buffers)))
+
+
+def test_optimizer_refuses_weights_that_no_step_takes():
+    import torch
+    from stochastic_rounding_quantization_amd.optim import Muon
+    W = torch.zeros(4, 6)
+    for bad in (W.t(), W[0], W.half(), W.double(), torch.zeros(2, 2, 4, 6), W[:, ::2], W[:1].expand(4, 6), torch.zeros(1, 4, 6).expand(2, 4, 6)):
+        with pytest.raises(ValueError):
+            Muon([W.clone(), bad], lr=0.1)
+    Muon([], lr=0.1).step([])
+    for good in (W, W[:, 1:4], torch.zeros(2, 4, 6)[:, 1:3], torch.zeros(0, 6), torch.zeros(3, 0, 2)):
+        Muon([good], lr=0.1)
