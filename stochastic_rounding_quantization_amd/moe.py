@@ -256,7 +256,7 @@ def main(argv=None) -> None:
 
     layer = MoeLayer(normal(a.experts, 2 * a.ff, a.width, std=0.02), normal(a.experts, a.width, a.ff, std=0.02), a.top_k,
                      int8=a.int8)
-    update = Muon([layer.gate_up[:, :a.ff], layer.gate_up[:, a.ff:], layer.down], lr=1e-3) if a.update else None
+    update = Muon([layer.gate_up[:, :a.ff], layer.gate_up[:, a.ff:], layer.down], lr=0.02) if a.update else None
     x, logits, dy = normal(a.tokens, a.width), normal(a.tokens, a.experts), normal(a.tokens, a.width, std=1e-4)
 
     def train():

@@ -15,6 +15,10 @@ class Muon:
     step   buf <- momentum buf + dW,  u = dW + momentum buf (Nesterov) or buf,  X = u orthogonalised,
            W <- (1 - lr decay) W - lr sqrt(max(1, N / K)) X, rounded once for bf16 weights.
     The momentum is kept in f32.  torch sees the weights change, as after an operation in place.
+
+    bf16 weights are rounded to nearest after each step, so steps that are small beside 2^-9 of a weight are lost in part: of
+    lr 0.02 on weights of 0.02 (1408 x 2048) all arrives, with an error of 0.08 of the step by rounding, of lr 0.001 only 0.56.
+    Where steps are so small, keep the weights in f32, update those, and copy them into the layer's bf16 tensors after each step.
     """
 
     def __init__(self, weights, lr, *, momentum=0.95, nesterov=True, decay=0.0, steps=5, coeffs=s3r.NS_COEFFS, eps=1e-7):

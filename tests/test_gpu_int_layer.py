@@ -203,3 +203,24 @@ def test_optimizer_steps_on_other_streams_captured_and_without_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(W, V) for W, V in zip(other, after))
         torch.randn(300, 300, device=DEV) @ torch.randn(300, 300, device=DEV)
+
+
+def test_small_steps_of_f32_weights_arrive_whole():
+    """f32 weights, copied into the layer's after every step: the codes follow, and twenty steps of lr 0.0001 sum up."""
+    layer, x, logits, dy = make(8)
+    halves = [layer.gate_up[:, :F], layer.gate_up[:, F:], layer.down]
+    masters = [W.float() for W in halves]
+    start = [W.double() for W in masters]
+    opt, lr, seen = Muon(masters, lr=1e-4, nesterov=False, momentum=0.5), 1e-4, [0, 0, 0]
+    for _ in range(20):
+        _, saved = layer.forward(x, logits)
+        _, _, dgu, dd = layer.backward(saved, dy)
+        opt.step([dgu[:, :F], dgu[:, F:], dd])
+        for i, (W, M, buf) in enumerate(zip(halves, masters, opt.buffers)):
+            W.copy_(M)
+            seen[i] = seen[i] + s3r.orthogonalize(buf).double() * lr * max(1.0, W.shape[1] / W.shape[2]) ** 0.5
+    for M, W0, total in zip(masters, start, seen):
+        # each step rounds X, the product and the sum in fp32: three times 2^-24 of the step or of the weight
+        most = 20 * 3 * 2.0 ** -24 * (M.double().abs() + lr * 2)
+        assert ((M.double() - (W0 - total)).abs() <= most).all()
+    assert same_step(layer, x, logits, dy)
