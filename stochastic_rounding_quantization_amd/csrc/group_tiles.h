@@ -33,7 +33,7 @@ __device__ __forceinline__ GroupRound group_round(const int64_t* __restrict__ of
   r.o0 = in ? offsets[g] : 0;
   r.o1 = in ? offsets[g + 1] : 0;
   r.bad = in && (r.o1 < r.o0 || r.o0 < 0 || r.o1 > R || (g == 0 && r.o0 != 0) || (g == G - 1 && r.o1 != R));
-  r.n = r.bad ? 0 : ((int)(r.o1 - r.o0) + tile - 1) / tile;
+  r.n = r.bad ? 0 : (int)(((uint32_t)(r.o1 - r.o0) + (uint32_t)tile - 1u) / (uint32_t)tile);   // rows below 2^31
   r.s = wave_prefix(r.n);
   return r;
 }

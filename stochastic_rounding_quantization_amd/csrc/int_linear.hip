@@ -201,7 +201,8 @@ __device__ __forceinline__ v4i tail_mask(int64_t c, int64_t K) {
 // The rows [m0, m1) of tile mt and its weight, or nothing to do.
 struct I8Tile { int64_t m0, m1; int e; bool some; };
 __device__ __forceinline__ I8Tile i8_tile(const I8ProdK& p, int mt, int tile) {
-  if (!p.G) return I8Tile{(int64_t)mt * tile, min(p.M, (int64_t)(mt + 1) * tile), 0, true};
+  const int64_t m0 = (int64_t)mt * tile;
+  if (!p.G) return I8Tile{m0, min(p.M, m0 + tile), 0, m0 < p.M};
   GroupRound first;
   bool bad;
   const int total = group_total(p.offsets, p.G, p.M, tile, first, bad);
@@ -236,7 +237,8 @@ __global__ __launch_bounds__(64 * dot_waves(UP)) void i8_dot_kernel(I8ProdK p, I
   __shared__ int part[kDotWaves][R * MT];
   extern __shared__ __attribute__((aligned(16))) int8_t rows[];         // MT rows of kpad codes
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
+  const unsigned block = (unsigned)wide_block();
+  const int mt = block / p.tiles_n, nt = block - mt * p.tiles_n;
   const I8Tile t = i8_tile(p, mt, MT);
   if (!t.some) return;
   const int rows_n = (int)(t.m1 - t.m0);
@@ -444,7 +446,8 @@ __global__ __launch_bounds__(T::Threads) void i8_few_rows_kernel(I8ProdK p) {
   // The wave's index in a scalar register: the loop over its units has to branch, since the matrix instructions run
   // whatever the execution mask says.
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int mt = blockIdx.x / p.tiles_n, nt = blockIdx.x - mt * p.tiles_n;
+  const unsigned block = (unsigned)wide_block();
+  const int mt = block / p.tiles_n, nt = block - mt * p.tiles_n;
   const I8Tile t = i8_tile(p, mt, 16 * T::MI);
   if (!t.some) return;
   const int64_t n0 = (int64_t)nt * (16 * T::NJ);
@@ -716,7 +719,7 @@ template <typename T, typename TOut>
 __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void i8_tile_kernel(I8ProdK p, int tiles_m) {
   // A contiguous range of tiles per XCD (workgroups go to the 8 XCDs in turn).  Grouped: of the tiles that the
   // groups have, not of the grid's bound on them, whose surplus would all be the last XCD's.
-  int bid = blockIdx.x;
+  int bid = (int)wide_block();
   GroupRound first;
   if (p.G) {
     bool bad;
@@ -726,10 +729,12 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void i8_tile_kernel(I8
       return;
     }
     const int nblocks = tiles_m * p.tiles_n, per = (nblocks + 7) / 8;
-    bid = (blockIdx.x % 8) * per + blockIdx.x / 8;
-    if ((int)blockIdx.x / 8 >= per || bid >= nblocks) return;
+    const int at = bid / 8;
+    bid = (bid % 8) * per + at;
+    if (at >= per || bid >= nblocks) return;
   } else {
     const int nblocks = tiles_m * p.tiles_n;
+    if (bid >= nblocks) return;
     if (nblocks % 8 == 0) bid = (bid % 8) * (nblocks / 8) + bid / 8;
   }
   const int group = 8 * p.tiles_n;
@@ -921,15 +926,16 @@ int64_t mean_rows(const I8ProductArgs& a) { return a.G ? (a.M + a.G - 1) / a.G :
 int64_t row_tiles(const I8ProductArgs& a, int tile) {
   return a.G ? a.M / tile + std::min(a.G, a.M) : (a.M + tile - 1) / tile;
 }
-constexpr int64_t kMostItems = (int64_t)1 << 32;
+// Workgroups of a grid: numbers of 31 bits, and what a second dimension adds to whole rows of it.
+constexpr int64_t kMostBlocks = ((int64_t)1 << 31) - ((int64_t)1 << kWideShift);
 
 template <typename T, typename TOut>
 hipError_t run_i8_tiles(const I8ProductArgs& a, I8ProdK p, hipStream_t st) {
   const int64_t mt = row_tiles(a, T::BM);
   p.tiles_n = (int)((a.N + T::BN - 1) / T::BN);
-  if ((mt * p.tiles_n + 7) * T::Threads >= kMostItems) return hipErrorInvalidConfiguration;
   const int64_t blocks = a.G ? (mt * p.tiles_n + 7) / 8 * 8 : mt * p.tiles_n;
-  hipLaunchKernelGGL((i8_tile_kernel<T, TOut>), dim3((unsigned)blocks), dim3(T::Threads), 0, st, p, (int)mt);
+  if (blocks > kMostBlocks) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((i8_tile_kernel<T, TOut>), wide_grid(blocks), dim3(T::Threads), 0, st, p, (int)mt);
   return hipGetLastError();
 }
 template <typename T>
@@ -943,8 +949,8 @@ hipError_t run_i8_few(const I8ProductArgs& a, hipStream_t st) {
   I8ProdK p = product_params(a);
   const int64_t mt = row_tiles(a, 16 * T::MI);
   p.tiles_n = (int)((a.N + 16 * T::NJ - 1) / (16 * T::NJ));
-  if (mt * p.tiles_n * T::Threads >= kMostItems) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(mt * p.tiles_n)), block(T::Threads);
+  if (mt * p.tiles_n > kMostBlocks) return hipErrorInvalidConfiguration;
+  const dim3 grid = wide_grid(mt * p.tiles_n), block(T::Threads);
   if (a.out_dt == S3R_BF16) hipLaunchKernelGGL((i8_few_rows_kernel<uint16_t, T>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((i8_few_rows_kernel<float, T>), grid, block, 0, st, p);
   return hipGetLastError();
@@ -962,8 +968,8 @@ hipError_t run_i8_dot(const I8ProductArgs& a, const I8RowsArgs& q, hipStream_t s
   int split = 1;
   while (split < kDotWaves && mt * groups * split * 2 <= kDotRoom && split * kDotPiece < a.K) split *= 2;
   p.tiles_n = (int)((groups * split + kDotWaves - 1) / kDotWaves);
-  if (mt * p.tiles_n * kDotThreads >= kMostItems) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(mt * p.tiles_n)), block(kDotThreads);
+  if (mt * p.tiles_n > kMostBlocks) return hipErrorInvalidConfiguration;
+  const dim3 grid = wide_grid(mt * p.tiles_n), block(kDotThreads);
   const size_t lds = dot_lds(MT, a.K);
   if (a.out_dt == S3R_BF16)
     hipLaunchKernelGGL((i8_dot_kernel<uint16_t, TIn, UP, Words, MT, R, Depth>), grid, block, lds, st, p, q, split);

@@ -381,3 +381,68 @@ def test_byte_products_of_every_kind(N, K, dtype, up):
     exp = np.concatenate([expected(x[a:b], w, up=None if u is None else u[a:b], group=e) for e, (a, b) in enumerate(zip(o, o[1:]))])
     for y in results(x, u, w, offsets=offsets):
         same(y, exp)
+
+
+def random_rows(rows, K, groups=1):
+    """Codes and steps without the rows behind them."""
+    w = s3r.int_rows_buffer(rows, K, DEV, groups)
+    w.codes.random_(-127, 128)
+    w.delta.uniform_(0.5, 1.0)
+    return w
+
+
+def part(a, w, rows, cols, e=0):
+    """Results of a slice of rows and columns: sums of 16 products are exact in fp32."""
+    acc = a.Q[rows].float() @ w.codes[e, cols, :w.K].float().t()
+    return (a.delta[0, rows, None] * w.delta[e, None, cols]) * acc
+
+
+# more workgroups than a grid of one dimension has threads for
+@pytest.mark.parametrize("M, N, out", [(2, (1 << 28) + 5, torch.float32), (9, (1 << 29) + 3, torch.bfloat16)])
+def test_products_of_very_many_columns(M, N, out):
+    a, w = random_rows(M, 16), random_rows(N, 16)
+    y = torch.full((M, N), float("nan"), dtype=out, device=DEV)
+    s3r.s3r_int_product(a, w, y)
+    for cols in (slice(0, 1 << 22), slice(N // 2, N // 2 + (1 << 22)), slice(N - (1 << 22), N)):
+        assert torch.equal(y[:, cols], part(a, w, slice(None), cols).to(out))
+    assert not any(y[:, c:c + (1 << 27)].isnan().any() for c in range(0, N, 1 << 27))
+
+
+def test_products_of_gate_and_up_with_very_many_columns():
+    M, N = 2, (1 << 28) + 5
+    w = random_rows(N, 16)
+    both = matrix((M, 32), torch.bfloat16, 1)
+    gate, up = both[:, :16], both[:, 16:]
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    s3r.s3r_int_linear(gate, w, y, up=up, ws=s3r.int_linear_buffer(M, 16, DEV))
+    a = s3r.int_rows(gate, up=up)
+    for cols in (slice(0, 1 << 22), slice(N - (1 << 22), N)):
+        assert torch.equal(y[:, cols], part(a, w, slice(None), cols).bfloat16())
+    assert not any(y[:, c:c + (1 << 27)].isnan().any() for c in range(0, N, 1 << 27))
+
+
+@pytest.mark.parametrize("per, N", [(1, 60000), (2, 120000)])
+def test_products_of_very_many_columns_of_groups(per, N):
+    E = 4096
+    a, w = random_rows(per * E, 16), random_rows(N, 16, E)
+    y = torch.full((per * E, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    s3r.s3r_int_product(a, w, y, offsets=torch.arange(E + 1, device=DEV) * per)
+    for e in (0, 1, 2047, 4094, 4095):
+        rows = slice(per * e, per * e + per)
+        assert torch.equal(y[rows], part(a, w, rows, slice(None), e).bfloat16())
+    assert not any(y[r:r + 512].isnan().any() for r in range(0, per * E, 512))
+
+
+@pytest.mark.parametrize("groups", [0, 2])
+def test_products_of_the_most_rows(groups):
+    M = (1 << 31) - 1
+    a, w = random_rows(M, 5), random_rows(3, 5, max(groups, 1))
+    a.codes[..., 5:] = 0
+    offsets = torch.tensor([0, 7, M], device=DEV) if groups else None
+    y = torch.full((M, 3), float("nan"), dtype=torch.bfloat16, device=DEV)
+    s3r.s3r_int_product(a, w, y, offsets=offsets)
+    e = 1 if groups else 0
+    for rows in (slice(7, 1 << 20), slice(M // 2, M // 2 + (1 << 20)), slice(M - (1 << 20), M)):
+        assert torch.equal(y[rows], part(a, w, rows, slice(None), e).bfloat16())
+    assert torch.equal(y[:7], part(a, w, slice(0, 7), slice(None)).bfloat16())
+    assert not any(y[r:r + (1 << 26)].isnan().any() for r in range(0, M, 1 << 26))
