@@ -43,7 +43,7 @@ class Muon:
             *_, N, K = W.shape
             if W.numel() and (W.stride(-1) != 1 or W.stride(-2) < K or
                               (W.dim() == 3 and W.shape[0] > 1 and W.stride(0) < (N - 1) * W.stride(-2) + K)):
-                raise ValueError("expected weights with unit column stride whose rows do not overlap")
+                raise ValueError("expected weights with unit column stride, row after row and matrix after matrix")
             need = s3r.s3r_orthogonalize_workspace(s3r.orth_desc(W.shape, s3r.S3R_F32, s3r._gdtype(W), **self._update(W)))
             if not need:
                 raise ValueError("weights or settings out of the update's range")

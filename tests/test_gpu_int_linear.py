@@ -446,3 +446,24 @@ def test_products_of_the_most_rows(groups):
         assert torch.equal(y[rows], part(a, w, rows, slice(None), e).bfloat16())
     assert torch.equal(y[:7], part(a, w, slice(0, 7), slice(None)).bfloat16())
     assert not any(y[r:r + (1 << 26)].isnan().any() for r in range(0, M, 1 << 26))
+
+
+@pytest.mark.parametrize("M, N, K", [(1, 40, 2000), (4, 70, 300), (40, 60, 1100), (300, 270, 500)])
+def test_rows_far_apart(M, N, K):
+    """The largest leading dimensions (through the C ABI): codes of 2 GiB a tile."""
+    ld = (1 << 23) - 16
+    far_a, far_w = (torch.full((r, ld), 55, dtype=torch.int8, device=DEV) for r in (M, N))
+    x, W = matrix((M, K), torch.float32, 1), matrix((N, K), torch.bfloat16, 2)
+    w = s3r.int_rows(W)
+    far_w[:, :K] = w.codes[0, :, :K]
+    sa, y = torch.empty(M, device=DEV), torch.full((M, N), float("nan"), device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    L = s3r.lib()
+    assert L.s3r_int_rows(1, M, K, x.data_ptr(), None, s3r.S3R_F32, K, 0, M, None, 1, far_a.data_ptr(), ld, 0, sa.data_ptr(),
+                          None, stream) == 0
+    d = s3r.IntPDesc(M, N, K, 0, ld, N * ld, s3r.S3R_F32, 0)
+    assert L.s3r_int_product(d, far_a.data_ptr(), ld, sa.data_ptr(), None, far_w.data_ptr(), w.delta.data_ptr(), None,
+                             y.data_ptr(), N, None, stream) == 0
+    same(y, expected(x, w))
+    pad = (K + 15) // 16 * 16
+    assert not far_a[:, K:pad].any() and (far_a[:, pad:] == 55).all()

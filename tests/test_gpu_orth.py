@@ -318,3 +318,12 @@ def test_norms_whose_inverse_leaves_fp32(size, dtype):
         G = gradient(shape, dtype, 3, size)
         assert bool(G.isfinite().all()) and bool(G.any())
         check(s3r.orthogonalize(G, eps=0.0, out_dtype=torch.float32), G, eps=0.0)
+
+
+@pytest.mark.parametrize("shape", [(1, (1 << 20) - 1), ((1 << 20) - 1, 3), (2, 5, 700001)])
+def test_longest_sides(shape):
+    G = gradient(shape, torch.float32, 7)
+    y = into(G, torch.float32)
+    for g, u in ((G, y),) if len(shape) == 2 else zip(G, y):
+        exp = orth.newton_schulz(host(g.double()))
+        assert np.linalg.norm(host(u.double()) - exp) <= lost(shape) * np.linalg.norm(exp)
