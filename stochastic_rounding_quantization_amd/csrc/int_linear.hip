@@ -892,10 +892,14 @@ hipError_t launch_i8_colsum(const int64_t* offsets, int64_t G, int64_t R, int64_
 }
 
 namespace {
-// Few rows, of as many workgroups as the columns give: 32 columns each read the rows' codes half as often, 16 keep every CU
-// busy below kFewWide columns.  us with 32 and 16:  24 x 4096 x 14336 18.2 and 15.8, 32 x 14336 x 4096 20.9 and 25.4,
-// 16 x 14336 x 4096 18.9 and 21.8, 64 x 14336 x 4096 23.1 and 30.7, 64 x 4096 x 14336 23.6 and 20.9.
-constexpr int64_t kFewWide = 8192;
+// Few rows, in one round of workgroups where that can be: 16 columns each give every CU one up to kFewWide columns, past that
+// 32 columns read the rows' codes half as often and take one round instead of two.  us with 32 and 16:
+//   rows  K        N = 4096       5120         6144         8192         10240        14336
+//   16    4096      6.8   6.2    7.3   9.3    8.4   9.8    9.9  10.8   15.1  14.8   18.6  21.6
+//   64    4096      9.5   8.6    9.8  13.9   10.4  14.3   11.8  15.0   20.1  21.2   24.2  32.1
+//   16    14336    19.2  14.5   20.1  24.1   20.9  25.7   23.5  27.0   38.5  37.4   42.5  49.8
+//   64    14336    29.7  24.0   30.4  42.8   31.2  43.4   32.9  45.4   58.2  64.7   61.3  85.9
+constexpr int64_t kFewWide = 16 * 256;
 using Few16 = FewGeo<1, 1, 8, 4>;
 using Few16Wide = FewGeo<1, 2, 4, 4>;
 using Few32 = FewGeo<2, 1, 8, 3>;
@@ -1027,7 +1031,7 @@ hipError_t launch_i8_product(const I8ProductArgs& a, hipStream_t st) {
     if (rows <= kFewGrouped) return run_i8_few<FewGrouped>(a, st);
     return rows < kTallGrouped ? run_i8_tiles<I8Tile128>(a, st) : run_i8_tiles<I8Tile256>(a, st);
   }
-  const bool wide = a.N >= kFewWide;
+  const bool wide = a.N > kFewWide;
   if (a.M <= 16) return wide ? run_i8_few<Few16Wide>(a, st) : run_i8_few<Few16>(a, st);
   if (a.M <= 32) return wide ? run_i8_few<Few32Wide>(a, st) : run_i8_few<Few32>(a, st);
   if (a.M <= 64) return wide ? run_i8_few<Few64Wide>(a, st) : run_i8_few<Few64>(a, st);

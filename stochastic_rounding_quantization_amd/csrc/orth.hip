@@ -683,6 +683,8 @@ constexpr int share_least(int side) { return side == 64 ? 16 : 8; }
 //   64 x 8192       353   120   296        2 x 3000 x 5000      5169   4777          4885
 //   16 x 200 x 300  176   118   188        2048 x 8192          2104   2085          1888
 //   3 x 1283 x 701  587   290   400        4096 x 14336   15900 10801  10362         10153
+// and of the symmetric products' 128 and 256 (B X in 256): 4096 x 5120 4706 4794, 4096 x 6144 5348 5432, 4096 x 8192 6557 6520,
+// 2560 x 7168 2721 2643, 2 x 2048 x 6144 3226 3000, 2048 x 8192 2119 1943, 2048 x 10240 2666 2430.
 // So the smallest tiles are for matrices that do not fill the GPU with them and whose sums are short, and a larger tile for
 // those that give every CU one of it and that it pads no more than 1.4 times as far (12 x 52 x 2723, twice as far: 158 us in
 // tiles of 64, 247 of 128), the largest where it pads little; of the symmetric products' triangle only with long sums, which

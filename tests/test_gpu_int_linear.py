@@ -341,8 +341,9 @@ def test_streams_and_graph_replays():
         assert all(torch.equal(a, b) for a, b in zip(got, (*outs, sums)))
 
 
-# few rows of wide weights (to 16, 32 and 64 rows, 8192 columns and more), and tiles of 128 x 64
-WIDE = [(5, 8195, 300), (9, 8192, 64), (16, 14336, 129), (24, 8192, 1000), (32, 8449, 127), (33, 8200, 129), (50, 9001, 700),
+# few rows of wide weights (to 16, 32 and 64 rows) on both sides of 4096 columns, and tiles of 128 x 64
+WIDE = [(7, 4096, 200), (16, 4097, 130), (20, 4090, 300), (30, 5000, 77), (60, 4095, 128), (40, 4100, 1000),
+        (5, 8195, 300), (9, 8192, 64), (16, 14336, 129), (24, 8192, 1000), (32, 8449, 127), (33, 8200, 129), (50, 9001, 700),
         (64, 14336, 260), (512, 3100, 200), (500, 3333, 1029)]
 
 
