@@ -19,7 +19,7 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 // Threads threads take a row of up to 8 * Threads * Pieces elements, which stay in registers between the maximum and
 // the codes; longer rows (Long) are read again for the codes.  Codes are written up to the next multiple of 16
 // columns (zeros past K).  With `up` the element is silu(A) * up in fp32, not rounded in between.
-// Bound by bytes without `up` (8192 x 4096 bf16 16.6 - 17.0 us, 5.9 - 6.1 TB/s with the last-level cache's help; 64 experts' 32768
+// Bound by bytes without `up` (8192 x 4096 bf16 16.6 - 17.3 us, 5.8 - 6.1 TB/s with the last-level cache's help; 64 experts' 32768
 // gathered rows of 2048 31.7), by vector instructions with it: 36 an element, 8192 x 14336 142 - 150 us, 3.9 - 4.1 TB/s.
 constexpr int kIrBlock = 256;
 
@@ -218,7 +218,7 @@ __device__ __forceinline__ I8Tile i8_tile(const I8ProdK& p, int mt, int tile) {
 // Up to four rows: byte dot products.  A wave takes R weight rows, 1 KiB of each at a time (whole lines, 16 bytes a
 // lane), against the rows' codes in LDS; `split` of the workgroup's waves share weight rows and deal the 1 KiB pieces of K
 // among them.  (The matrix cores would want a weight row in 4 lanes and 16 lines a quarter-wave.)  Bound by the weights'
-// bytes: 1 x 14336 x 4096 11.6 - 13.6 us, 4.3 - 5.1 TB/s with the launch; 32 rows of 64 experts of 2816 x 2048 25.4 - 25.8.
+// bytes: 1 x 14336 x 4096 11.6 - 13.6 us, 4.3 - 5.1 TB/s with the launch; 32 rows of 64 experts of 2816 x 2048 25.4 - 26.0.
 // With TIn the rows come unrounded: every workgroup rounds them while its weights are on the way, so there is no
 // second launch and no codes go through memory.  TIn void: rows already in codes.  Loads arrive in the order that they were
 // asked for, so the rows are asked for first, then kDepth pieces of the weights, always all of them, for the compiler to
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(64 * dot_waves(UP)) void i8_dot_kernel(I8ProdK p, I
 // their sums in LDS.  The weights' bytes are the bound, and how they are asked for: a load of 16 rows x 64 bytes (the matrix
 // cores' operand) is 64 requests, one of 8 whole lines 16, and the rows' codes cost as much as the weights (24 x 4096 x
 // 14336: 20.8 us straight into registers).  So every wave stages its units in LDS by buffer-load DMA, whole lines, in
-// a ring of its own of NS units: no wave waits for another before the end (12.6 us, 4.7 TB/s).  Chunks of a line as in the
+// a ring of its own of NS units: no wave waits for another before the end (12.0 - 13.2 us, 4.5 - 4.9 TB/s).  Chunks of a line as in the
 // tiles below.
 // v_mfma_i32_16x16x64_i8: lane l holds row or column l % 16, bytes 16 (l / 16) .. + 15 of 64; the result's register r is
 // row 4 (l / 16) + r, column l % 16.
@@ -498,8 +498,8 @@ __global__ __launch_bounds__(T::Threads) void i8_few_rows_kernel(I8ProdK p) {
 // whole line), the eight 16-byte chunks of a row at permuted places (chunk q of row r at q ^ ((r >> 1) & 7), so a
 // quarter-wave's reads hit 16 bank groups).  v_mfma_i32_32x32x32_i8: lane l holds row or column l % 32, bytes
 // 16 (l / 32) .. + 15 of 32; result register r is row (r / 4) 8 + (l / 32) 4 + r % 4, column l % 32.
-// Bound by power where the tiles are large: 8192 x 14336 x 4096 405 - 439 us, 2.2 - 2.4 POP/s (the whole call with operands of
-// zeros 339 us against 487 on one box), 8192 x 4096 x 14336 390 - 421.  64 experts' 32768 x 2816 x 2048 294 - 298 us, 1.3 POP/s:
+// Bound by power where the tiles are large: 8192 x 14336 x 4096 411 - 439 us, 2.2 - 2.3 POP/s (the whole call with operands of
+// zeros 336 us against 418 - 430, in turn on one box, and 448 - 467 over longer runs), 8192 x 4096 x 14336 400 - 421.  64 experts' 32768 x 2816 x 2048 295 - 300 us, 1.3 POP/s:
 // partial tiles, 16 steps of K and 185 MB of results.
 template <int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
 struct I8Geo {
@@ -789,7 +789,8 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void i8_tile_kernel(I8
 
 // ----------------------------------------------------------- column sums ----
 // A workgroup adds 64 rows of 1024 columns, four columns a thread; integer sums, so the order of its additions into
-// memory does not change them.  Bound by the codes' bytes.
+// memory does not change them.  32768 x 2048 in 64 groups 21.8 us, 8192 x 14336 33 us, 3.1 - 3.6 TB/s, of the codes and the additions;
+// 8192 x 4096 19.8 us: 512 workgroups do not fill the GPU.  The clearing before it 1.5 - 4.8 us.
 constexpr int kCsRows = 64;
 __global__ __launch_bounds__(256) void i8_colsum_clear_kernel(const int64_t* offsets, int64_t G, int64_t R, int64_t K,
                                                               int32_t* sums, uint32_t* flags) {

@@ -172,7 +172,7 @@ __global__ __launch_bounds__(kPrepThreads) void orth_prepare_kernel(OrthArgs a, 
 // v_mfma_f32_32x32x16_f16: lane l holds row or column l % 32, elements 8 (l / 32) .. + 7 of 16; result register r is
 // row (r / 4) 8 + (l / 32) 4 + r % 4, column l % 32.
 // Bound by the matrix cores and power.  B X of 4096 x 14336 in tiles of 256: 1.10 - 1.15 ms, 1.3 PFLOP/s counting the three
-// products.  64 x 1408 x 2048 in tiles of 128: 1445 us, 1.08 PFLOP/s.
+// products.  64 x 1408 x 2048 in tiles of 128: 1445 - 1500 us, 1.04 - 1.08.
 constexpr int kParts = kLineEl / 16, kPlanes = 2, kProducts = 3;
 template <int MI_, int NI_, int WM_, int WN_, int NS_, int WavesPerSimd_>
 struct OrthGeo {
@@ -530,7 +530,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_gemm_kernel(
 }
 
 // Tile blockIdx.x of the shared ones, rows 32 blockIdx.y .. of every wave (a workgroup for a whole tile of 256 took twice
-// as long, few of them adding up in a row what many had left).  136 tiles of 256, 256 workers: 36 - 41 us.
+// as long, few of them adding up in a row what many had left).  136 tiles of 256, 256 workers: 35 - 41 us.
 template <typename T, OrthEpi EPI>
 __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_join_kernel(OrthGemm p) {
   const int tile = blockIdx.x, i = blockIdx.y;
@@ -573,7 +573,7 @@ __global__ __launch_bounds__(T::Threads, T::WavesPerSimd) void orth_join_kernel(
 
 // Small matrices: 32 x 32 results a workgroup, whose eight waves deal the contraction's steps of 32 elements among them and
 // join their sums in LDS.  Fragments go straight from the caches to the matrix cores, kBatch steps of a wave at a time, so
-// a product of a few hundred elements is one round of loads.  Bound by latency: 256 x 512 4.9 - 5.8 us a product.
+// a product of a few hundred elements is one round of loads.  Bound by latency: 256 x 512 4.2 - 5.8 us a product.
 constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64, kFewLd = 36;
 
 template <OrthEpi EPI>
