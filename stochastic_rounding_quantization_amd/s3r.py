@@ -925,7 +925,8 @@ def orth_desc(shape, g_dtype=S3R_F32, out_dtype=S3R_F32, *, steps=5, coeffs=NS_C
               keep=0.0) -> OrthDesc:
     """Of matrices [rows x cols] or [groups x rows x cols]."""
     groups, rows, cols = (1, *shape) if len(shape) == 2 else shape
-    return OrthDesc(groups, rows, cols, g_dtype, out_dtype, steps, *coeffs, eps, scale, keep, 0)
+    a, b, c = coeffs
+    return OrthDesc(groups, rows, cols, g_dtype, out_dtype, steps, a, b, c, eps, scale, keep, 0)
 
 
 def s3r_orthogonalize_workspace(desc: OrthDesc) -> int:

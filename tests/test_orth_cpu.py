@@ -184,3 +184,15 @@ def test_optimizer_refuses_weights_that_no_step_takes():
     Muon([], lr=0.1).step([])
     for good in (W, W[:, 1:4], torch.zeros(2, 4, 6)[:, 1:3], torch.zeros(0, 6), torch.zeros(3, 0, 2)):
         Muon([good], lr=0.1)
+
+
+@pytest.mark.parametrize("coeffs", [(1.0, -0.5), (1.0, 2.0, 3.0, 4.0), ()])
+def test_binding_takes_three_coefficients(L, coeffs):
+    """Two would have left the others a place off: eps as c, scale as eps, a result of zeros."""
+    import torch
+    from stochastic_rounding_quantization_amd.optim import Muon
+    G = torch.zeros(4, 6)
+    for call in (lambda: s3r.orth_desc((4, 6), coeffs=coeffs), lambda: s3r.s3r_orthogonalize(G, G.clone(), coeffs=coeffs, stream=0),
+                 lambda: Muon([G], lr=0.1, coeffs=coeffs)):
+        with pytest.raises(ValueError):
+            call()
